@@ -416,13 +416,143 @@ int kvattn_decode_window_tail_direct(const void* q, const void* k_win, const voi
                                      float scale, float* out, float* lse, void* ws,
                                      size_t ws_bytes, void* stream);
 
+/*
+ * Prompt-side operators: what puts a prompt into the caches above and attends over it.  Rows are
+ * half [n_tok] rows of heads x head_dim elements whose tokens lie `stride` elements apart (a
+ * multiple of 8, at least heads x head_dim: a slice of a fused projection is fine); row pointers
+ * are 16-byte aligned.  head_dim 128 or 256 (UNSUPPORTED otherwise).  Attention results are half,
+ * the type that the next layer's product reads.
+ */
+
+/* Pair layouts of the rotated part of a head: (i, i + n_rot / 2), or (2i, 2i + 1). */
+#define KVATTN_ROPE_HALF 0
+#define KVATTN_ROPE_INTERLEAVED 1
+/* Context scalings of kvattn_rope_table. */
+#define KVATTN_ROPE_PLAIN 0
+#define KVATTN_ROPE_LINEAR 1
+#define KVATTN_ROPE_YARN 2
+
+/*
+ * kvattn_rope_table -- host.  The angle per position of each of n_rot / 2 pairs, theta_i =
+ * base^(-2i / n_rot), as a 64-bit fixed-point fraction of a turn: turns[i] = 2^64 theta_i / (2 pi).
+ *  scaling  PLAIN; LINEAR: theta_i / factor; YARN (Peng et al. 2023, "NTK-by-parts"): with r_i =
+ *           original_len theta_i / (2 pi) turns over the original context and keep = clamp((r_i - 1)
+ *           / 31, 0, 1), theta_i (keep + (1 - keep) / factor), and *gain = 0.1 ln(factor) + 1.
+ *  turns    host uint64 [n_rot / 2];  gain  host float (1 but for YARN), kvattn_rope's gain.
+ * Errors: INVALID_ARG (n_rot odd or below 2, base not above 1, factor below 1 where it is used,
+ * original_len below 1 with YARN, null outputs).
+ */
+int kvattn_rope_table(int n_rot, double base, int scaling, double factor, int64_t original_len, uint64_t* turns,
+                      float* gain);
+
+/*
+ * kvattn_rope -- device.  Rotary positions of q and k in one launch: pair (a, b) number i of a
+ * head's first n_rot elements becomes gain (a cos - b sin, a sin + b cos) with the angle
+ * positions[t] x theta_i; elements from n_rot on are copied.  The angle is an integer product
+ * modulo whole turns, so every int32 position is exact to 2^-32 turns; sums are fp32, rounded to
+ * half once.
+ *  q, k      half rows of n_head / n_head_kv heads (a count of 0: that tensor is not used).
+ *  positions device int32 [n_tok], any values.   turns  device uint64 [n_rot / 2].
+ *  n_rot     a multiple of 16, at most head_dim (UNSUPPORTED / INVALID_ARG otherwise).
+ *  q_out, k_out  half rows with strides of their own; q_out == q with the same stride (and k_out
+ *            == k) works in place; other overlaps do not.
+ * Errors: INVALID_ARG, UNSUPPORTED (before any launch); CUDA.
+ */
+int kvattn_rope(const void* q, int64_t q_stride, int n_head, const void* k, int64_t k_stride, int n_head_kv,
+                const int32_t* positions, const uint64_t* turns, float gain, int n_rot, int layout, int64_t n_tok,
+                int head_dim, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * kvattn_cache_write -- device.  New K and V rows into cells of a cache of any kv_type: token t's
+ * rows into cell slots[t].
+ *  k, v      half rows of n_head_kv heads.
+ *  slots     device int32 [n_tok]; -1: the token is not written; other values outside
+ *            [0, n_cells) are skipped and or KVATTN_DEVICE_BAD_PLAN_ENTRY into *status.  NULL:
+ *            cell t (n_tok <= n_cells).  Two tokens of one call must not name the same cell (its
+ *            contents are then unspecified; other cells are not affected).
+ *  status    NULL, or a device uint32 (a decode workspace's first word is one).
+ * f16 rows are copied.  In quantised rows each 32 elements share the scale d, the half next to
+ * amax / 127 (Q8_0) or m / -8 (Q4_0; m the element of largest magnitude, the lowest index of
+ * equals) away from zero; codes are x / d rounded to nearest, ties to even (Q4_0: +8 becomes 7).
+ * So no Q8_0 element is off by more than |d| / 2.  32 elements with an infinity or a NaN among
+ * them get the scale NaN and read back as NaN.  Cells not named keep their bytes.
+ * Limits: n_tok x n_head_kv x head_dim / 16 below 2^31 (UNSUPPORTED).
+ * Errors: INVALID_ARG, UNSUPPORTED (before any launch); CUDA.
+ */
+int kvattn_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots,
+                       int64_t n_tok, int n_head_kv, int head_dim, int kv_type, void* k_cache, void* v_cache,
+                       void* k_scales, void* v_scales, int64_t n_cells, uint32_t* status, void* stream);
+
+/*
+ * kvattn_cache_read -- device.  The cells slots[t] back as half rows: scale x code rounded once to
+ * half and kept within +-65504 (a scale that is not finite makes its 32 elements NaN); f16 cells
+ * are copied.  slots as in kvattn_cache_write, but a cell may be named more than once, and -1 (and
+ * an entry outside the cache, flagged in *status) gives a row of zeros -- a row of a cell plan is a
+ * valid argument.
+ * Limits and errors: as kvattn_cache_write.
+ */
+int kvattn_cache_read(const void* k_cache, const void* v_cache, const void* k_scales, const void* v_scales, int kv_type,
+                      int64_t n_cells, const int32_t* slots, int64_t n_tok, int n_head_kv, int head_dim, void* k,
+                      int64_t k_stride, void* v, int64_t v_stride, uint32_t* status, void* stream);
+
+/* Bytes of workspace kvattn_prefill needs (its status word); 0 on invalid arguments. */
+size_t kvattn_prefill_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim);
+
+/*
+ * kvattn_prefill -- device.  Causal attention of whole packed prompts over their own keys and
+ * values: token t of sequence s (rows offsets[s] .. offsets[s + 1]) attends to its sequence's
+ * tokens 0 .. t, by the definition at the top of this file.
+ *  q         half rows of n_head heads;  k, v  half rows of n_head_kv heads (n_head a multiple,
+ *            at most 128 times).
+ *  offsets   device int32 [n_seq + 1], non-decreasing, within [0, n_tok] (values outside are
+ *            clamped).  Tokens in front of the first sequence and behind the last are neither read
+ *            nor written; sequences may be empty.
+ *  out       device half [n_tok][n_head][head_dim];  lse  NULL or device float [n_tok][n_head].
+ *  ws        at least kvattn_prefill_workspace_bytes(...) bytes, 256-byte aligned, zeroed once
+ *            after allocation; its first word is the sticky status word.  Calls may share it.
+ * Values that are not finite reach the rows that see them only.
+ * Errors: INVALID_ARG, UNSUPPORTED (n_tok x n_head rows or the work units beyond 32 bits),
+ * WORKSPACE (before any launch); CUDA.
+ */
+int kvattn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                   const int32_t* offsets, int n_seq, int64_t n_tok, int n_head, int n_head_kv, int head_dim, float scale,
+                   void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace kvattn_prefill_chunk needs (status word and partials; split 0: for the split
+ * that the call selects on the current device); 0 on invalid arguments. */
+size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim,
+                                            int64_t max_len, int split);
+
+/*
+ * kvattn_prefill_chunk -- device.  Causal attention of each sequence's new tokens over its cache,
+ * which holds their own cells already: kvattn_decode_multi without its limit on rows and with a
+ * token count for each sequence (from one token, so that prompts' chunks and single-token decodes
+ * share a call).  With n_q = offsets[s + 1] - offsets[s] and L = seq_lens[s], token t attends to
+ * the logical positions 0 .. L - n_q + t; a token that sees no cell gets O = 0, LSE = -inf.
+ *  q, offsets, out, lse  as kvattn_prefill (n_tok rows of all sequences, packed).
+ *  k_cache .. seq_lens, n_seq, max_len, scale  as kvattn_decode; any kv_type, contiguous caches or
+ *            a cell plan.  The values of quantised caches enter the matrix products rounded to half
+ *            (2^-11 of each value).
+ *  split     cells per partial, a multiple of 128, or 0 to choose it from the shapes and the
+ *            device's SM count (a call with enough rows is not split).
+ *  ws        kvattn_prefill_chunk_workspace_bytes(...) bytes, 256-byte aligned, zeroed once after
+ *            allocation; work that shares one is ordered by the caller.
+ * Errors: INVALID_ARG, UNSUPPORTED (also max_len beyond 2^31, a split that is not a multiple of
+ * 128), WORKSPACE (before any launch); CUDA.
+ */
+int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets, int64_t n_tok, const void* k_cache,
+                         const void* v_cache, const void* k_scales, const void* v_scales, int kv_type, int64_t n_cells,
+                         const int32_t* cell_plan, int64_t plan_stride, const int32_t* seq_lens, int n_seq,
+                         int64_t max_len, int n_head, int n_head_kv, int head_dim, int split, float scale, void* out,
+                         float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Wait (host, bounded) until everything the last kvattn_decode_window_tail on this ctx
  * enqueued has finished.  Polls an event; returns TIMEOUT after timeout_ms, CUDA if the
  * work failed. */
 int kvattn_tail_wait(kvattn_tail_ctx* ctx, int timeout_ms);
 
-/* Read (and optionally clear) the sticky KVATTN_DEVICE_* bits of a decode or window+tail
- * workspace.  Synchronises `stream`. */
+/* Read (and optionally clear) the sticky KVATTN_DEVICE_* bits of a decode, window+tail or
+ * prefill workspace.  Synchronises `stream`. */
 int kvattn_workspace_status(void* ws, uint32_t* flags, int clear, void* stream);
 
 #ifdef __cplusplus

@@ -1,0 +1,81 @@
+// Prompt-side operators: rotary positions (rope.cu), the cache written in its stored type and
+// read back (cache_io.cu), and causal attention of many query tokens per sequence (prefill.cu).
+// prompt_api.cu holds their C entry points.
+#pragma once
+
+#include "kvattn_internal.cuh"
+
+namespace kvattn {
+
+// ---- rotary positions ----
+struct RopeParams {
+    const __half* src[2];     // q, k: half [n_tok] rows of n_head[i] x head_dim, token stride[i]
+    __half* dst[2];
+    int64_t src_stride[2], dst_stride[2];
+    int n_head[2];
+    const int32_t* pos;       // [n_tok]
+    const uint64_t* turns;    // [n_rot / 2]: the angle per position of each pair, in 2^-64 turns
+    int64_t n_tok;
+    int head_dim, n_rot, interleaved;
+    float gain;               // multiplies cosine and sine
+};
+cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream, bool pdl);
+
+// ---- cache rows in their stored type ----
+struct CacheIoParams {
+    const __half* src[2];     // write: new k, v rows, token stride
+    __half* dst[2];           // read: half rows, token stride
+    int64_t stride[2];
+    void* rows[2];            // the cache's K and V planes
+    __half* scales[2];        // null for f16
+    const int32_t* slots;     // [n_tok], or null: cell t
+    uint32_t* status;         // nullable: KVATTN_DEVICE_BAD_PLAN_ENTRY is or-ed in
+    int64_t n_tok, n_cells;
+    int n_head_kv, head_dim;
+};
+cudaError_t launch_cache_write(const CacheIoParams& p, int kv_type, cudaStream_t stream, bool pdl);
+cudaError_t launch_cache_read(const CacheIoParams& p, int kv_type, cudaStream_t stream, bool pdl);
+
+// ---- causal attention of packed query tokens ----
+struct PrefillParams {
+    CUtensorMap tmap_k, tmap_v;  // 3-D {head_dim, KV heads, cells}, boxes {64, 1, 128} (use_tma)
+    const __half* q;          // [n_tok] rows of n_head x head_dim, token stride q_stride
+    const void* k;            // f16: rows k_stride elements apart; quantised: dense planes
+    const void* v;
+    const __half* k_scale;
+    const __half* v_scale;
+    const int32_t* offsets;   // [n_seq + 1]
+    const int32_t* plan;      // nullable: [n_seq][plan_stride]
+    const int32_t* seq_lens;  // null: a sequence's cells are its own tokens
+    __half* out;              // [n_tok][n_head][head_dim]
+    float* lse;               // nullable: [n_tok][n_head]
+    float* part_o;            // [n_split][n_tok * n_head][head_dim], when n_split > 1
+    float* part_lse;          // [n_split][n_tok * n_head]
+    uint32_t* status;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t n_tok, n_cells, plan_stride, max_len;
+    uint64_t wait_limit_ns;
+    uint32_t stall_tx;        // test hook: extra bytes expected on the first slot (never arrive)
+    int n_seq, n_head, n_head_kv, group;
+    int n_split, split_tiles; // partials per row and 128-cell tiles per partial
+    int n_blocks;             // upper bound of the row blocks of all sequences
+    int use_tma;
+    float scale_log2;         // scale * log2(e)
+};
+constexpr int kPrefillTile = 128;  // cells per tile
+// query rows (token, query head of the KV head) of one work unit
+inline int prefill_block_rows(int head_dim) { return head_dim == 128 ? 256 : 128; }
+cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, cudaStream_t stream, bool pdl);
+cudaError_t launch_prefill_merge(const PrefillParams& p, int head_dim, cudaStream_t stream, bool pdl);
+
+// From api.cu: the 3-D map of half rows for launch_prefill, SM count, log switch and line,
+// the programmatic-launch switch.
+bool encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int head_dim,
+                        int64_t row_stride);
+int device_sms();
+bool log_enabled();
+void log_text(const char* text);
+bool pdl_enabled();
+void debug_waits(uint64_t* wait_limit_ns, uint32_t* stall_tx);
+
+}  // namespace kvattn

@@ -37,6 +37,11 @@ KVATTN_KV_Q4_0 = 3
 KVATTN_DEVICE_WAIT_TIMEOUT = 1
 KVATTN_DEVICE_BAD_PLAN_ENTRY = 2
 KVATTN_TAIL_PREFETCH = 1
+KVATTN_ROPE_HALF = 0
+KVATTN_ROPE_INTERLEAVED = 1
+KVATTN_ROPE_PLAIN = 0
+KVATTN_ROPE_LINEAR = 1
+KVATTN_ROPE_YARN = 2
 
 EXPORTED = (
     "kvattn_status_string", "kvattn_version", "kvattn_build_cell_plan", "kvattn_build_descriptors",
@@ -46,7 +51,9 @@ EXPORTED = (
     "kvattn_tail_wait", "kvattn_workspace_status", "kvattn_decode_noalloc",
     "kvattn_window_tail_direct_workspace_bytes", "kvattn_decode_window_tail_direct",
     "kvattn_select_split_for", "kvattn_select_split", "kvattn_decode_multi_workspace_bytes",
-    "kvattn_decode_multi", "kvattn_tail_ctx_set_flags",
+    "kvattn_decode_multi", "kvattn_tail_ctx_set_flags", "kvattn_rope_table", "kvattn_rope", "kvattn_cache_write",
+    "kvattn_cache_read", "kvattn_prefill_workspace_bytes", "kvattn_prefill", "kvattn_prefill_chunk_workspace_bytes",
+    "kvattn_prefill_chunk",
 )
 
 _P = ctypes.c_void_p
@@ -105,6 +112,23 @@ lib.kvattn_tail_wait.argtypes = [_P, _I]
 lib.kvattn_tail_wait.restype = _I
 lib.kvattn_workspace_status.argtypes = [_P, ctypes.POINTER(ctypes.c_uint32), _I, _P]
 lib.kvattn_workspace_status.restype = _I
+lib.kvattn_rope_table.argtypes = [_I, ctypes.c_double, _I, ctypes.c_double, _I64, _P, ctypes.POINTER(_F)]
+lib.kvattn_rope_table.restype = _I
+lib.kvattn_rope.argtypes = [_P, _I64, _I, _P, _I64, _I, _P, _P, _F, _I, _I, _I64, _I, _P, _I64, _P, _I64, _P]
+lib.kvattn_rope.restype = _I
+lib.kvattn_cache_write.argtypes = [_P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P, _P, _P, _P, _I64, _P, _P]
+lib.kvattn_cache_write.restype = _I
+lib.kvattn_cache_read.argtypes = [_P, _P, _P, _P, _I, _I64, _P, _I64, _I, _I, _P, _I64, _P, _I64, _P, _P]
+lib.kvattn_cache_read.restype = _I
+lib.kvattn_prefill_workspace_bytes.argtypes = [_I64, _I, _I, _I, _I]
+lib.kvattn_prefill_workspace_bytes.restype = _SZ
+lib.kvattn_prefill.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]
+lib.kvattn_prefill.restype = _I
+lib.kvattn_prefill_chunk_workspace_bytes.argtypes = [_I64, _I, _I, _I, _I, _I64, _I]
+lib.kvattn_prefill_chunk_workspace_bytes.restype = _SZ
+lib.kvattn_prefill_chunk.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _I,
+                                     _F, _P, _P, _P, _SZ, _P]
+lib.kvattn_prefill_chunk.restype = _I
 
 
 class KvattnError(RuntimeError):
@@ -313,6 +337,62 @@ def kvattn_workspace_status(ws, clear: bool = False, stream=None) -> int:
     return flags.value
 
 
+def kvattn_rope_table(n_rot, base, scaling, factor, original_len, turns) -> float:
+    """``turns``: host uint64 [n_rot // 2] (numpy).  Returns the gain."""
+    gain = _F(0.0)
+    _check(lib.kvattn_rope_table(n_rot, base, scaling, factor, original_len, _ptr(turns), ctypes.byref(gain)),
+           "kvattn_rope_table")
+    return gain.value
+
+
+def kvattn_rope(q, q_stride, n_head, k, k_stride, n_head_kv, positions, turns, gain, n_rot, layout, n_tok, head_dim, q_out,
+                q_out_stride, k_out, k_out_stride, stream=None):
+    rc = lib.kvattn_rope(_ptr(q), q_stride, n_head, _ptr(k), k_stride, n_head_kv, _ptr(positions), _ptr(turns), gain, n_rot,
+                         layout, n_tok, head_dim, _ptr(q_out), q_out_stride, _ptr(k_out), k_out_stride, _stream(stream))
+    _check(rc, "kvattn_rope")
+
+
+def kvattn_cache_write(k, k_stride, v, v_stride, slots, n_tok, n_head_kv, head_dim, kv_type, k_cache, v_cache, k_scales,
+                       v_scales, n_cells, status, stream=None):
+    rc = lib.kvattn_cache_write(_ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), n_tok, n_head_kv, head_dim, kv_type,
+                                _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), n_cells, _ptr(status),
+                                _stream(stream))
+    _check(rc, "kvattn_cache_write")
+
+
+def kvattn_cache_read(k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, slots, n_tok, n_head_kv, head_dim, k, k_stride,
+                      v, v_stride, status, stream=None):
+    rc = lib.kvattn_cache_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), kv_type, n_cells, _ptr(slots),
+                               n_tok, n_head_kv, head_dim, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(status),
+                               _stream(stream))
+    _check(rc, "kvattn_cache_read")
+
+
+def kvattn_prefill_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim) -> int:
+    return lib.kvattn_prefill_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim)
+
+
+def kvattn_prefill(q, q_stride, k, k_stride, v, v_stride, offsets, n_seq, n_tok, n_head, n_head_kv, head_dim, scale, out, lse,
+                   ws, ws_bytes, stream=None):
+    rc = lib.kvattn_prefill(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(offsets), n_seq, n_tok, n_head,
+                            n_head_kv, head_dim, scale, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+    _check(rc, "kvattn_prefill")
+
+
+def kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split) -> int:
+    return lib.kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split)
+
+
+def kvattn_prefill_chunk(q, q_stride, offsets, n_tok, k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, cell_plan,
+                         plan_stride, seq_lens, n_seq, max_len, n_head, n_head_kv, head_dim, split, scale, out, lse, ws,
+                         ws_bytes, stream=None):
+    rc = lib.kvattn_prefill_chunk(_ptr(q), q_stride, _ptr(offsets), n_tok, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                                  _ptr(v_scales), kv_type, n_cells, _ptr(cell_plan), plan_stride, _ptr(seq_lens), n_seq,
+                                  max_len, n_head, n_head_kv, head_dim, split, scale, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                  _stream(stream))
+    _check(rc, "kvattn_prefill_chunk")
+
+
 # ----------------------------- torch conveniences -----------------------------
 
 def decode_workspace(n_seq, n_head, head_dim, max_len, split, device="cuda"):
@@ -421,6 +501,212 @@ def build_cell_plan(encoded_per_seq, capacity_cells, plan_stride=None):
     plan = np.full((max(n_seq, 1), max(plan_stride, 1)), -1, dtype=np.int32)
     kvattn_build_cell_plan(cells, offsets, n_seq, capacity_cells, plan, plan_stride, lens)
     return plan[:n_seq, :plan_stride], lens[:n_seq]
+
+
+def _rows(x, name):
+    """(heads, head_dim, token stride) of half rows [T][heads][D]; the heads of a token must be
+    contiguous, the tokens may be strided (a slice of a fused projection)."""
+    import torch
+    if x.dim() != 3 or x.dtype != torch.float16:
+        raise ValueError(f"{name}: half rows [tokens][heads][head_dim] are wanted")
+    t, h, d = x.shape
+    if x.numel() and (x.stride(2) != 1 or (h > 1 and x.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return h, d, (x.stride(0) if t > 1 else h * d)
+
+
+def _ints(x, name, n=None):
+    import torch
+    if x.dtype != torch.int32 or not x.is_contiguous() or (n is not None and x.numel() != n):
+        raise ValueError(f"{name}: contiguous int32" + ("" if n is None else f" of {n} values") + " is wanted")
+    return x
+
+
+def _new_out(out, name, shape, like, dtype=None):
+    """A contiguous result tensor: the caller's, checked, or a new one."""
+    import torch
+    dtype = torch.float16 if dtype is None else dtype
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} of shape {tuple(shape)} is wanted")
+    return out
+
+
+def _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim):
+    """kv_type from the row widths, as in decode; checks the planes' shapes and layout."""
+    import torch
+    widths = k_cache.shape[-1], v_cache.shape[-1]
+    planes = [k_cache, v_cache]
+    if k_scales is None and v_scales is None:
+        kv_type, want, kinds = KVATTN_KV_F16, (head_dim, head_dim), (torch.float16, torch.float16)
+    elif k_scales is None or v_scales is None:
+        raise ValueError("k_scales and v_scales go together")
+    else:
+        kv_type = {(1, 1): KVATTN_KV_Q8_0, (1, 2): KVATTN_KV_Q8_0_Q4_0, (2, 2): KVATTN_KV_Q4_0}.get(
+            tuple(head_dim // w if w else 0 for w in widths))
+        if kv_type is None:
+            raise ValueError("no cache type has rows of these widths")
+        bits = {KVATTN_KV_Q8_0: (8, 8), KVATTN_KV_Q8_0_Q4_0: (8, 4), KVATTN_KV_Q4_0: (4, 4)}[kv_type]
+        want = tuple(head_dim * b // 8 for b in bits)
+        kinds = tuple(torch.int8 if b == 8 else torch.uint8 for b in bits)
+        for s in (k_scales, v_scales):
+            if s.dtype != torch.float16 or s.shape[:-1] != k_cache.shape[:-1] or s.shape[-1] * 32 != head_dim:
+                raise ValueError("scale planes are half [cells][kv heads][head_dim / 32]")
+        planes += [k_scales, v_scales]
+    if widths != want or k_cache.dtype != kinds[0] or v_cache.dtype != kinds[1] or k_cache.shape[:-1] != v_cache.shape[:-1]:
+        raise ValueError("the cache planes do not agree with each other or with head_dim")
+    if not all(x.is_contiguous() for x in planes):
+        raise ValueError("cache planes are contiguous")
+    return kv_type
+
+
+class RopeTable:
+    """Angles per position of a model's rotary pairs (``turns``, device uint64 kept as int64) and
+    the gain on cosine and sine; made by :func:`rope_table`."""
+
+    def __init__(self, turns, gain, n_rot):
+        self.turns, self.gain, self.n_rot = turns, gain, n_rot
+
+
+def rope_table(n_rot, *, base=10000.0, scaling="none", factor=1.0, original=0, device="cuda"):
+    """``scaling``: "none", "linear" or "yarn" (``factor`` times the ``original`` context)."""
+    import torch
+    kind = {"none": KVATTN_ROPE_PLAIN, "linear": KVATTN_ROPE_LINEAR, "yarn": KVATTN_ROPE_YARN}[scaling]
+    host = np.zeros(n_rot // 2, dtype=np.uint64)
+    gain = kvattn_rope_table(n_rot, base, kind, factor, original, host)
+    return RopeTable(torch.from_numpy(host.view(np.int64)).to(device), gain, n_rot)
+
+
+def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, stream=None):
+    """q: half [T][H][D], k: half [T][Hk][D] (either may be None), positions int32 [T].  Rotated rows
+    go to new tensors, or to ``q_out`` / ``k_out`` (which may be q and k themselves).  Returns (q, k)."""
+    import torch
+    code = {"half": KVATTN_ROPE_HALF, "interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
+    some = q if q is not None else k
+    T, D = some.shape[0], some.shape[-1]
+    args, outs = [], []
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            args.append((None, 0, 0, None, 0))
+            outs.append(None)
+            continue
+        h, d, st = _rows(x, name)
+        if y is None:
+            y = torch.empty((T, h, d), dtype=torch.float16, device=x.device)
+        if x.shape[0] != T or d != D or y.shape != x.shape:
+            raise ValueError(f"{name}: shapes do not agree")
+        args.append((x, st, h, y, _rows(y, name + "_out")[2]))
+        outs.append(y)
+    _ints(positions, "positions", T)
+    (q, qs, H, qo, qos), (k, ks, Hk, ko, kos) = args
+    kvattn_rope(q, qs, H, k, ks, Hk, positions, table.turns, table.gain, table.n_rot, code, T, D, qo, qos, ko, kos, stream)
+    return tuple(outs)
+
+
+def cache_write(k, v, slots, k_cache, v_cache, *, k_scales=None, v_scales=None, status=None, stream=None):
+    """k, v: half [T][Hk][D] into cells ``slots`` (int32 [T], -1: skipped; None: cells 0 .. T - 1) of a
+    cache whose type follows from its planes.  ``status``: an int32 tensor whose first word collects
+    the KVATTN_DEVICE_* bits."""
+    Hk, D, ks = _rows(k, "k")
+    Hv, Dv, vs = _rows(v, "v")
+    T = k.shape[0]
+    if (Hv, Dv, v.shape[0]) != (Hk, D, T) or k_cache.shape[-2] != Hk:
+        raise ValueError("k, v and the cache do not agree")
+    kv_type = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
+    n_cells = k_cache.numel() // max(Hk * k_cache.shape[-1], 1)
+    if slots is not None:
+        _ints(slots, "slots", T)
+    kvattn_cache_write(k, ks, v, vs, slots, T, Hk, D, kv_type, k_cache, v_cache, k_scales, v_scales, n_cells, status, stream)
+
+
+def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scales=None, k_out=None, v_out=None, status=None,
+               stream=None):
+    """Cells ``slots`` (int32 [T], e.g. a row of a cell plan; -1 gives zeros; None: every cell) as
+    half [T][Hk][head_dim] rows.  Returns (k, v)."""
+    import torch
+    Hk = k_cache.shape[-2]
+    kv_type = _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim)
+    n_cells = k_cache.numel() // max(Hk * k_cache.shape[-1], 1)
+    T = n_cells if slots is None else _ints(slots, "slots").numel()
+    if k_out is None:
+        k_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
+    hk, dk, ks = _rows(k_out, "k_out")
+    hv, dv, vs = _rows(v_out, "v_out")
+    if (hk, dk, k_out.shape[0]) != (Hk, head_dim, T) or (hv, dv, v_out.shape[0]) != (Hk, head_dim, T):
+        raise ValueError("k_out and v_out are half [slots][kv heads][head_dim]")
+    kvattn_cache_read(k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, slots, T, Hk, head_dim, k_out, ks, v_out, vs,
+                      status, stream)
+    return k_out, v_out
+
+
+def prefill_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, device="cuda"):
+    import torch
+    nbytes = kvattn_prefill_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim)
+    return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream=None):
+    """Causal attention of packed prompts: q half [T][H][D], k and v half [T][Hk][D], offsets int32
+    [S + 1].  Returns (out half [T][H][D], lse float [T][H])."""
+    import torch
+    H, D, qs = _rows(q, "q")
+    Hk, Dk, ks = _rows(k, "k")
+    Hv, Dv, vs = _rows(v, "v")
+    T = q.shape[0]
+    if (Dk, Dv, Hv) != (D, D, Hk) or k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v do not agree")
+    S = _ints(offsets, "offsets").numel() - 1
+    out = _new_out(out, "out", (T, H, D), q)
+    lse = _new_out(lse, "lse", (T, H), q, torch.float32)
+    if ws is None:
+        ws = prefill_workspace(T, S, H, Hk, D, q.device)
+    kvattn_prefill(q, qs, k, ks, v, vs, offsets, S, T, H, Hk, D, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws,
+                   ws.numel(), stream)
+    return out, lse
+
+
+def prefill_chunk_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split=0, device="cuda"):
+    import torch
+    nbytes = kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split)
+    return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cells=None, cell_plan=None, k_scales=None,
+                  v_scales=None, split=0, scale=None, out=None, lse=None, ws=None, stream=None):
+    """Causal attention of new tokens over caches that hold their cells: q half [T][H][D] (the
+    sequences' tokens packed, offsets int32 [S + 1]), the cache as in decode: one unified cache with
+    a ``cell_plan`` (int32 [S][stride]), a per-sequence [S][N][Hk][D] cache, or one [cells][Hk][D]
+    whose ``n_cells`` are each sequence's.  Returns (out half [T][H][D], lse: the given tensor or
+    None)."""
+    import torch
+    H, D, qs = _rows(q, "q")
+    T, Hk = q.shape[0], k_cache.shape[-2]
+    S = _ints(offsets, "offsets").numel() - 1
+    _ints(seq_lens, "seq_lens", S)
+    kv_type = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
+    if n_cells is None:
+        n_cells = k_cache.shape[1] if k_cache.dim() == 4 else k_cache.shape[0]
+    stride = 0
+    if cell_plan is not None:
+        stride = cell_plan.shape[-1]
+        _ints(cell_plan, "cell_plan", S * stride)
+    rows = k_cache.numel() // max(Hk * k_cache.shape[-1], 1)
+    if (n_cells if cell_plan is not None else n_cells * S) > rows:
+        raise ValueError("the cache has fewer cells than n_cells says")
+    if max_len is None:
+        max_len = stride if cell_plan is not None else n_cells
+    out = _new_out(out, "out", (T, H, D), q)
+    if lse is not None:
+        _new_out(lse, "lse", (T, H), q, torch.float32)
+    if ws is None:
+        ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, split, q.device)
+    kvattn_prefill_chunk(q, qs, offsets, T, k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, cell_plan, stride, seq_lens,
+                         S, max_len, H, Hk, D, split, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws, ws.numel(),
+                         stream)
+    return out, lse
 
 
 class WindowTail:
