@@ -518,10 +518,10 @@ int kvattn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_str
                    const int32_t* offsets, int n_seq, int64_t n_tok, int n_head, int n_head_kv, int head_dim, float scale,
                    void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace kvattn_prefill_chunk needs (status word and partials; split 0: for the split
- * that the call selects on the current device); 0 on invalid arguments. */
+/* Bytes of workspace kvattn_prefill_chunk needs on the current device (status word, and partials
+ * of at most two work units per SM: about 40 MB whatever the shapes); 0 on invalid arguments. */
 size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim,
-                                            int64_t max_len, int split);
+                                            int64_t max_len);
 
 /*
  * kvattn_prefill_chunk -- device.  Causal attention of each sequence's new tokens over its cache,
@@ -533,18 +533,18 @@ size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head
  *  k_cache .. seq_lens, n_seq, max_len, scale  as kvattn_decode; any kv_type, contiguous caches or
  *            a cell plan.  The values of quantised caches enter the matrix products rounded to half
  *            (2^-11 of each value).
- *  split     cells per partial, a multiple of 128, or 0 to choose it from the shapes and the
- *            device's SM count (a call with enough rows is not split).
+ * Few rows over long caches are cut over the cells too, into equal shares for the device's SMs
+ * that follow from the lengths alone (the result does not depend on timing), and merged.
  *  ws        kvattn_prefill_chunk_workspace_bytes(...) bytes, 256-byte aligned, zeroed once after
  *            allocation; work that shares one is ordered by the caller.
- * Errors: INVALID_ARG, UNSUPPORTED (also max_len beyond 2^31, a split that is not a multiple of
- * 128), WORKSPACE (before any launch); CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (also max_len of 2^31 or more), WORKSPACE (before any launch);
+ * CUDA.
  */
 int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets, int64_t n_tok, const void* k_cache,
                          const void* v_cache, const void* k_scales, const void* v_scales, int kv_type, int64_t n_cells,
                          const int32_t* cell_plan, int64_t plan_stride, const int32_t* seq_lens, int n_seq,
-                         int64_t max_len, int n_head, int n_head_kv, int head_dim, int split, float scale, void* out,
-                         float* lse, void* ws, size_t ws_bytes, void* stream);
+                         int64_t max_len, int n_head, int n_head_kv, int head_dim, float scale, void* out, float* lse,
+                         void* ws, size_t ws_bytes, void* stream);
 
 /* Wait (host, bounded) until everything the last kvattn_decode_window_tail on this ctx
  * enqueued has finished.  Polls an event; returns TIMEOUT after timeout_ms, CUDA if the

@@ -275,19 +275,20 @@ bool kvattn::encode_kv_tensor_map(CUtensorMap* map, const void* base, int kv_typ
 
 // ---- shared with the prompt-side entry points (prompt_api.cu) ----
 
-bool kvattn::encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int head_dim,
-                                int64_t row_stride) {
+bool kvattn::encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head, int head_dim,
+                                int64_t row_stride, int box_heads, int box_rows) {
     EncodeTiledFn enc = tensor_map_encoder();
-    if (enc == nullptr || !use_tma_env() || rows < 1 || rows > (int64_t)INT32_MAX || !aligned(base, 16)) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)n_head_kv, (cuuint64_t)rows};
+    if (enc == nullptr || rows < 1 || rows > (int64_t)INT32_MAX || !aligned(base, 16)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)n_head, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)row_stride * 2};
-    const cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kPrefillTile};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool kvattn::tma_enabled() { return use_tma_env(); }
 int kvattn::device_sms() { return sm_count(); }
 bool kvattn::log_enabled() { return log_on(); }
 void kvattn::log_text(const char* text) { log_line("%s", text); }

@@ -2,45 +2,58 @@
 // whole packed prompts over their own K and V, and chunks of new tokens over a cache that
 // already holds them (f16, Q8_0, Q8_0 + Q4_0, Q4_0; contiguous or through a cell plan).
 //
-// For each KV head the G x n_q query rows of a sequence are packed flat (row = token x G +
-// query head), so that every row of a work unit reads the same K and V.  Row r sees the cells
-// below lim(r) = L - n_q + 1 + r / G.  A unit is a block of rows (256 at head_dim 128, 128 at
-// 256), a KV head and a range of 128-cell tiles (all of them, or one of n_split parts):
+// Rows.  For each KV head the G query heads of a token are neighbouring rows, so that every row
+// of a work unit reads the same K and V: a row group is floor(128 / G) tokens x G rows (at most
+// the 128 TMEM lanes), a block is two groups at head_dim 128 and one at 256, and a unit is a
+// block and a KV head.  Token t of a sequence sees the cells below lim(t) = L - n_q + 1 + t.
 //
 //     S = Q K^T,  x = scale S (masked: -inf),  m = max x,  p = exp(x - m),
 //     l = sum p,  O = sum p V,  out = O / l,  lse = m + ln l,
 //
-// one pass over the cells with a running m and l per row (kept in 32 bits; p is rounded to f16
-// for the matrix product only, l sums the unrounded p).  Sixteen warps with fixed roles:
+// one pass over the cells in tiles of 128 with a running m and l per row (32 bits; p is rounded
+// to f16 for the matrix product only, l sums the unrounded p).
+//
+// Work.  The kernel is persistent, one CTA per SM.  Its schedulers cut the work in one of two
+// ways: whole units dealt out longest first, in alternating directions (prompts, where units
+// are many); or (chunks) the concatenation of all units' tiles cut into equal contiguous shares,
+// one per CTA, wherever the cuts fall.  A unit that is cut leaves partials (O_p, lse_p) in the
+// workspace, two at most per CTA, and the merge kernel joins them.  The shares follow from the
+// lengths alone, so results do not depend on timing.
+//
+// Sixteen warps with fixed roles:
 //
 //  * softmax (warps 0-3 and 4-7, 128 threads each): thread t holds row t, which is TMEM lane
 //    t: a row's maximum and sum need no exchange between threads.  At head_dim 128 each group
-//    has its own 128 rows; at 256 the first group has the unit's 128 rows and the second is
-//    idle.  The thread reads its row of S from tensor memory, masks, and writes p over it as
-//    f16 pairs.  p is scaled by 2^7 (it cancels in O / l): with the lazily moved maximum below
-//    p stays under 2^15, and p of 2^-21 of a row's largest still has all its f16 bits.
-//  * loader (warps 8-11): fills a ring of five 32 KB slots, each 128 cells x 128 dims of K or
-//    V in two 128-byte-swizzled planes.  A tile of f16 cells that are one physical run comes
-//    by TMA; other tiles by 16-byte cp.async per row with zeros for missing cells; quantised
-//    tiles are read into registers one slot ahead, turned into f16 there and stored.
+//    has its own row group; at 256 the first has the unit's and the second is idle.  The thread
+//    reads its row of S from tensor memory, masks, and writes p over it as f16 pairs.  p is
+//    scaled by 2^7 (it cancels in O / l): with the lazily moved maximum below p stays under
+//    2^15, and p of 2^-21 of a row's largest still has all its f16 bits.
+//  * loader (warps 8-11): fills a ring of 32 KB slots, each 128 cells x 128 dims of K or V in
+//    two 128-byte-swizzled planes.  f16: warp 8 issues TMA boxes for tiles whose cells are one
+//    physical run (holes and the end of a sequence included), warps 9-11 mend V tiles that need
+//    it, and all four copy tiles that are no run.  Quantised: every thread brings raw bytes into
+//    a ring of its own by cp.async, two slots ahead, and turns them into f16 in its slot.
 //  * MMA (warp 12): one elected lane issues tcgen05.mma.  S of one row group is computed while
 //    the softmax of the other runs (head_dim 128: two S and two O accumulators fill the 512
 //    TMEM columns), or S of the next tile while the softmax of this one runs (256: two S and
 //    a 256-column O).
+//  * scheduler (warp 13): finds the next unit's sequence, block and tiles while the others work,
+//    and issues the TMA of its query rows once the last S of the unit before is complete.
 //
 // The running maximum moves only when it grows by more than 2^8 (in p), so that O is rescaled
 // a few times per row at most; the softmax thread does it in tensor memory itself.
 //
-// Masked places: a score is masked before it is used, so whatever K holds there is dropped.  V
-// is multiplied by p = 0 there, and 0 x inf is NaN on the tensor cores, so cells that no row
-// may see are zeros in shared memory (a tile with any is not loaded by TMA), and in a tile that
-// only some rows see, elements of V that are not finite become zeros too and are added at the
-// end to the rows that do see the cell (any p > 0 times an infinity is that infinity).
+// Masked places: a score is replaced (not added to) before it is used, so whatever K holds there
+// is dropped.  V is multiplied by p = 0 there, and 0 x inf is NaN on the tensor cores, so V rows
+// that no row may see are zeroed in shared memory, and in a tile that only some rows see whole,
+// elements of V that are not finite become zeros too and are added at the end to the rows that
+// do see the cell (any p > 0 times an infinity is that infinity).
 //
 // Every wait is bounded, as in the decode kernels; a wait that gives up sets a flag that the
 // others see, and KVATTN_DEVICE_WAIT_TIMEOUT in the workspace.
 #include <climits>
 #include <cmath>
+#include <cstddef>
 #include <mutex>
 
 #include "prompt.cuh"
@@ -50,33 +63,61 @@ namespace kvattn {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kSlots = 5;
 constexpr int kPlaneBytes = 128 * 128;        // 128 cells (or rows) x 128 bytes
 constexpr int kSlotBytes = 2 * kPlaneBytes;   // 128 cells x 128 dims of f16
 constexpr int kQTileBytes = 2 * kPlaneBytes;  // 128 rows x 128 dims of f16
+constexpr int kMaxSlots = 5;
 constexpr int kHeaderBytes = 3072;
-constexpr int kRing = 4;                      // tiles whose masks are kept
-constexpr int kSmemBytes = 2 * kQTileBytes + kSlots * kSlotBytes + kHeaderBytes;  // all of the 227 KB
+constexpr int kRing = 4;                      // tiles whose masks, and units whose plans, are kept
+constexpr int kRawStages = 3;                 // quantised: slots of raw bytes in flight
+constexpr int kCutTiles = 3;                  // tiles that only some of a unit's (<= 256) tokens see whole
 constexpr float kSlack = 8.f;                 // lazy maximum
 constexpr float kLift = 7.f;                  // p is scaled by 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int64_t kUnitCost = 2;              // a unit's fixed cost in tiles, for the equal shares
+
+// f16 slots in the ring: what the 227 KB hold beside the queries (64 KB) and, for quantised
+// caches, the raw ring (17 KB a stage with 8-bit rows, 9 KB with 4-bit ones)
+template <int KBITS>
+struct Memory {
+    static constexpr int kSlots = KBITS == 16 ? 5 : (KBITS == 8 ? 3 : 4);
+    static constexpr int kRawBytes = KBITS == 16 ? 0 : 128 * 8 * KBITS * 2 + 1024;  // codes, then scales
+    static constexpr int kBytes = 2 * kQTileBytes + kSlots * kSlotBytes + kRawStages * kRawBytes + kHeaderBytes;
+    static_assert(kBytes <= 232448, "227 KB");
+};
+
+// What the scheduler tells the others of a piece of work.
+struct Seg {
+    long long q_tok;     // first token of the block, in the packed rows
+    long long cell0;     // first cell of the sequence (no plan)
+    long long len;       // cells of the sequence
+    long long lim0;      // lim of the block's first token
+    int seq, g;
+    int n_tok;           // tokens of the block; < 0: no more work
+    int j0, n[2];        // first tile; tiles of the row groups from there
+    int first_cut;       // from this tile on (from j0) some row does not see the tile whole
+    int part;            // partial slot, or -1: the whole unit
+};
 
 struct Header {
-    uint64_t full[kSlots], empty[kSlots];
-    uint64_t q_full;       // the unit's query rows are in shared memory
-    uint64_t s_full[2];    // S is in TMEM (of row group t, or of buffer b)
-    uint64_t p_full[2];    // p is
-    uint64_t pv_done;      // head_dim 256: P V of a tile is complete
-    uint64_t o_full[2];    // a row group's last P V is complete
-    uint64_t mask_full[kRing];  // through a plan: a tile's bias and holes are written
-    uint64_t load_done;    // every slot is filled, bad_cells is complete
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t landed[kMaxSlots];  // the TMA of a V tile that is mended afterwards
+    uint64_t q_full, q_empty;    // the unit's query rows; its last S is complete
+    uint64_t s_full[2];          // S is in TMEM (of row group t, or of buffer b)
+    uint64_t p_full[2];          // p is
+    uint64_t pv_done;            // head_dim 256: P V of a tile is complete
+    uint64_t o_full[2];          // a row group's last P V is complete
+    uint64_t mask_full[kRing];   // through a plan: a tile's bias and holes are written
+    uint64_t load_done[kRing];   // every slot of a unit is filled, its bad_cells are complete
+    uint64_t seg_full[kRing], seg_empty[kRing];
     uint32_t tmem;
     int abort_flag;
-    uint32_t bad_cells[4][4];              // cells of the last (partly seen) tiles with non-finite V
-    float bias[kRing][kPrefillTile];       // through a plan: 0, or -inf for a hole
-    uint32_t holes[kRing];                 // whether the tile has any
+    uint32_t bad_cells[kRing][kCutTiles][4];  // of a unit: cells of its cut tiles with V that is not finite
+    uint32_t holes[kRing];                    // whether the tile has any
+    Seg seg[kRing];
+    alignas(16) float bias[kRing][kPrefillTile];  // through a plan: +inf, or -inf for a hole
 };
-static_assert(sizeof(Header) <= kHeaderBytes, "header");
+static_assert(sizeof(Header) <= kHeaderBytes && offsetof(Header, bias) % 16 == 0, "header");
 
 // Shared-memory matrix descriptor: start address, leading and stride byte offsets, the
 // descriptor version of this architecture family, 128-byte swizzle.
@@ -159,11 +200,6 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// arrives on bar when this thread's cp.async so far are complete (adds itself to the phase's
-// pending arrivals first: the phase must be held open by an arrival that comes later)
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -193,111 +229,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-
-// A work unit, the same in every thread of the CTA.
-struct Unit {
-    int64_t q0;        // first token of the sequence
-    int64_t cell0;     // its first cell (no plan)
-    int64_t len;       // its cells
-    int64_t lim0;      // lim of row r = lim0 + r / G
-    int64_t rows;      // its rows for a KV head
-    int64_t row0;      // first row of the unit
-    int seq, g, split;
-    int j0;            // first tile of the split
-    int n[2];          // tiles of the row groups (from j0)
-    int n_max;
-    bool any;
-};
-
-__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
-
-// Finds block number `b` of the sequences' row blocks counted from the last sequence's last
-// block (the longest rows of a prompt come first), a warp at a time.
-template <int D>
-__device__ __forceinline__ Unit find_unit(const PrefillParams& p) {
-    constexpr int kRows = D == 128 ? 256 : 128, kGroups = D == 128 ? 2 : 1;
-    Unit u = {};
-    const int lane = threadIdx.x & 31;
-    uint32_t id = blockIdx.x, b;
-    if (p.n_split == 1) {  // KV heads side by side: the longest units first
-        u.g = (int)(id % (uint32_t)p.n_head_kv);
-        b = id / (uint32_t)p.n_head_kv;
-    } else {               // the row blocks that read the same cells side by side
-        b = id % (uint32_t)p.n_blocks;
-        id /= (uint32_t)p.n_blocks;
-        u.g = (int)(id % (uint32_t)p.n_head_kv);
-        u.split = (int)(id / (uint32_t)p.n_head_kv);
-    }
-    const int G = p.group;
-    uint32_t seen = 0;
-    u.seq = -1;
-    for (int top = p.n_seq; top > 0; top -= 32) {
-        const int s = top - 1 - lane;
-        int64_t a = 0, e = 0;
-        if (s >= 0) {
-            a = clamp64(__ldg(p.offsets + s), 0, p.n_tok);
-            e = clamp64(__ldg(p.offsets + s + 1), a, p.n_tok);
-        }
-        const uint32_t blocks = (uint32_t)(((e - a) * G + kRows - 1) / kRows);
-        uint32_t sum = blocks;  // inclusive over the lanes so far
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        const uint32_t hit = __ballot_sync(0xffffffffu, b < seen + sum);
-        if (hit != 0u) {
-            const int l = __ffs(hit) - 1;
-            u.seq = top - 1 - l;
-            u.q0 = __shfl_sync(0xffffffffu, a, l);
-            const int64_t end = __shfl_sync(0xffffffffu, e, l);
-            const uint32_t n_blocks = __shfl_sync(0xffffffffu, blocks, l);
-            const uint32_t before = seen + __shfl_sync(0xffffffffu, sum, l) - n_blocks;
-            u.rows = (end - u.q0) * G;
-            u.row0 = (int64_t)(n_blocks - 1 - (b - before)) * kRows;
-            break;
-        }
-        seen += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (u.seq < 0) return u;
-    const int64_t nq = u.rows / G;
-    if (p.seq_lens != nullptr) {
-        const int64_t cap = p.plan != nullptr ? p.plan_stride : p.n_cells;
-        int64_t L = clamp64(__ldg(p.seq_lens + u.seq), 0, p.max_len);
-        u.len = L < cap ? L : cap;
-        u.cell0 = (int64_t)u.seq * p.n_cells;
-    } else {
-        u.len = nq;
-        u.cell0 = u.q0;
-    }
-    u.lim0 = u.len - nq + 1;
-    u.j0 = u.split * p.split_tiles;
-#pragma unroll
-    for (int t = 0; t < kGroups; ++t) {
-        const int64_t first = u.row0 + 128 * t;
-        const int64_t last = (first + 127 < u.rows ? first + 127 : u.rows - 1);
-        int64_t tiles = 0;
-        if (first < u.rows) {
-            const int64_t lim = u.lim0 + last / G;  // (at most len)
-            tiles = lim > 0 ? (lim + kPrefillTile - 1) / kPrefillTile : 0;
-        }
-        if (p.n_split > 1 && tiles > u.j0 + p.split_tiles) tiles = u.j0 + p.split_tiles;
-        u.n[t] = tiles > u.j0 ? (int)(tiles - u.j0) : 0;
-    }
-    if (kGroups == 1) u.n[1] = 0;
-    u.n_max = u.n[0] > u.n[1] ? u.n[0] : u.n[1];
-    u.any = true;
-    return u;
-}
-
-// ------------------------------- quantised rows in registers -------------------------------
-
-// The raw bytes of a thread's part of a slot.  8-bit: 8 cells' 16-byte pieces (half a block
-// each); 4-bit: 4 cells' 16-byte blocks.  scale: the halves of their blocks, two per word.
-struct Raw {
-    uint4 w[8];
-    uint32_t d[4];
-};
 
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -335,19 +266,266 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w, bool& bad) {
     return w;
 }
 
+__device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+// ------------------------------------ work ------------------------------------
+
+template <int D>
+struct Geometry {
+    static constexpr int kGroups = D == 128 ? 2 : 1;
+    static constexpr int kHalves = D / 128;     // slots per tile of K or V
+};
+
+// A sequence as the schedulers see it.
+struct Sequence {
+    int64_t q0, n_q, len;
+    int64_t blocks;
+};
+template <int D>
+__device__ __forceinline__ Sequence read_sequence(const PrefillParams& p, int s) {
+    Sequence x = {};
+    if (s < 0 || s >= p.n_seq) return x;
+    x.q0 = clamp64(__ldg(p.offsets + s), 0, p.n_tok);
+    x.n_q = clamp64(__ldg(p.offsets + s + 1), x.q0, p.n_tok) - x.q0;
+    if (p.seq_lens != nullptr) {
+        const int64_t cap = p.plan != nullptr ? p.plan_stride : p.n_cells;
+        const int64_t L = clamp64(__ldg(p.seq_lens + s), 0, p.max_len);
+        x.len = L < cap ? L : cap;
+    } else {
+        x.len = x.n_q;
+    }
+    x.blocks = (x.n_q + p.block_tokens - 1) / p.block_tokens;
+    return x;
+}
+// Tiles that the block's first n tokens see.
+__device__ __forceinline__ int64_t tiles_seen(int64_t lim0, int64_t n) {
+    const int64_t lim = n > 0 ? lim0 + n - 1 : 0;
+    return lim > 0 ? (lim + kPrefillTile - 1) / kPrefillTile : 0;
+}
+
+// The units of all sequences in one line, each as long as its work in cells (rounded to a rule
+// that is linear in the block's number, so that sums have a closed form), plus its fixed cost;
+// CTA c of n takes the part [share(c), share(c + 1)).  Order: sequence, KV head, block.
+struct Line {
+    int64_t a, step;   // length of block b: a + step b
+    __device__ __forceinline__ int64_t upto(int64_t b) const { return a * b + step * (b * (b - 1) / 2); }
+};
+__device__ __forceinline__ Line line_of(const PrefillParams& p, const Sequence& x) {
+    const int64_t lim = x.len - x.n_q + 1;
+    return Line{kPrefillTile * kUnitCost + (lim > 1 ? lim : 1) + p.block_tokens - 1, p.block_tokens};
+}
+__device__ __forceinline__ int64_t share_of(int64_t total, int c, int n) {
+    return total / n * c + total % n * c / n;
+}
+__device__ __forceinline__ int64_t shfl64(int64_t v, int l) { return (int64_t)__shfl_sync(0xffffffffu, (long long)v, l); }
+template <int D>
+__device__ __forceinline__ int64_t total_of(const PrefillParams& p) {
+    const int lane = threadIdx.x & 31;
+    int64_t sum = 0;
+    for (int s = lane; s < p.n_seq; s += 32) {
+        const Sequence x = read_sequence<D>(p, s);
+        sum += line_of(p, x).upto(x.blocks) * p.n_head_kv;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += (int64_t)__shfl_xor_sync(0xffffffffu, (long long)sum, o);
+    return sum;
+}
+// The unit that holds position `at` of the line (at < total), the same in all lanes.
+struct Place {
+    Sequence x;
+    Line line;
+    int seq, g;
+    int64_t block, start, end;  // the unit's part of the line
+};
+template <int D>
+__device__ __forceinline__ Place place_of(const PrefillParams& p, int64_t at) {
+    const int lane = threadIdx.x & 31;
+    Place r = {};
+    int64_t base = 0;
+    for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
+        const Sequence x = read_sequence<D>(p, s0 + lane);
+        const Line line = line_of(p, x);
+        int64_t sum = x.blocks > 0 ? line.upto(x.blocks) * p.n_head_kv : 0;
+        const int64_t own = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = (int64_t)__shfl_up_sync(0xffffffffu, (long long)sum, o);
+            if (lane >= o) sum += v;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, at < base + sum);
+        if (hit != 0u) {
+            const int l = __ffs(hit) - 1;
+            r.seq = s0 + l;
+            r.x.q0 = shfl64(x.q0, l);
+            r.x.n_q = shfl64(x.n_q, l);
+            r.x.len = shfl64(x.len, l);
+            r.x.blocks = shfl64(x.blocks, l);
+            r.line.a = shfl64(line.a, l);
+            r.line.step = shfl64(line.step, l);
+            base += shfl64(sum - own, l);
+            break;
+        }
+        base += shfl64(sum, 31);
+    }
+    const int64_t per = r.line.upto(r.x.blocks);
+    int64_t y = at - base;
+    r.g = (int)(y / per);
+    y -= (int64_t)r.g * per;
+    int64_t lo = 0, hi = r.x.blocks - 1;  // the last block that starts at or before y
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (r.line.upto(mid) <= y)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    r.block = lo;
+    r.start = at - (y - r.line.upto(lo));
+    r.end = r.start + r.line.a + r.line.step * lo;
+    return r;
+}
+// Tiles [first, last) of a unit of `tiles` tiles that the part [a, b) of its line stands for.
+__device__ __forceinline__ void tiles_between(const Place& r, int64_t a, int64_t b, int64_t tiles, int64_t& first, int64_t& last) {
+    const int64_t w = r.end - r.start;
+    first = (a - r.start) * tiles / w;
+    last = (b - r.start) * tiles / w;
+}
+
+// Fills in a piece of work: tiles [first, last) of a block.
+template <int D>
+__device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence& x, int seq, int g, int64_t block, int64_t first,
+                                         int64_t last, int part, Seg& s) {
+    constexpr int kGroups = Geometry<D>::kGroups;
+    const int64_t tok0 = block * p.block_tokens;
+    const int64_t left = x.n_q - tok0;
+    s.seq = seq;
+    s.g = g;
+    s.n_tok = (int)(left < p.block_tokens ? left : p.block_tokens);
+    s.q_tok = x.q0 + tok0;
+    s.cell0 = p.seq_lens != nullptr ? (int64_t)seq * p.n_cells : x.q0;
+    s.len = x.len;
+    s.lim0 = x.len - x.n_q + 1 + tok0;
+    s.j0 = (int)first;
+    s.part = part;
+    int n_max = 0;
+    s.n[1] = 0;
+#pragma unroll
+    for (int t = 0; t < kGroups; ++t) {
+        const int64_t in = (int64_t)s.n_tok < (int64_t)(t + 1) * p.group_tokens ? s.n_tok : (int64_t)(t + 1) * p.group_tokens;
+        int64_t tiles = in > (int64_t)t * p.group_tokens ? tiles_seen(s.lim0, in) : 0;
+        tiles = tiles < last ? tiles : last;
+        s.n[t] = tiles > first ? (int)(tiles - first) : 0;
+        n_max = s.n[t] > n_max ? s.n[t] : n_max;
+    }
+    // (one token: all its rows see the same cells)
+    const int64_t cut = (s.lim0 > 0 ? s.lim0 : 0) / kPrefillTile - first;
+    s.first_cut = (s.n_tok == 1 || cut > n_max) ? n_max : (cut < 0 ? 0 : (int)cut);
+}
+
+// A warp's walk over its CTA's pieces.
+template <int D>
+struct Walk {
+    // whole units
+    uint32_t round;
+    // shares
+    int64_t at, end;
+    Place r;
+    bool started;
+
+    __device__ __forceinline__ void begin(const PrefillParams& p) {
+        round = 0;
+        started = false;
+        if (p.shares) {
+            const int64_t total = total_of<D>(p);
+            at = share_of(total, blockIdx.x, gridDim.x);
+            end = share_of(total, blockIdx.x + 1, gridDim.x);
+        }
+    }
+    // The next piece in s; false: none left.
+    __device__ __forceinline__ bool next(const PrefillParams& p, Seg& s) { return p.shares ? next_share(p, s) : next_whole(p, s); }
+
+    // Unit number i counts from the last sequence's last block (the longest rows of a prompt
+    // first), KV heads fastest; round r deals them out forwards or backwards.
+    __device__ __forceinline__ bool next_whole(const PrefillParams& p, Seg& s) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t n = gridDim.x, c = blockIdx.x;
+        const uint32_t i = round * n + ((round & 1u) ? n - 1u - c : c);
+        if (i < round * n) return false;  // (beyond 32 bits)
+        ++round;
+        const uint32_t g = i % (uint32_t)p.n_head_kv, b = i / (uint32_t)p.n_head_kv;
+        uint32_t seen = 0;
+        for (int top = p.n_seq; top > 0; top -= 32) {
+            const Sequence x = read_sequence<D>(p, top - 1 - lane);
+            uint32_t sum = (uint32_t)x.blocks;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, b < seen + sum);
+            if (hit != 0u) {
+                const int l = __ffs(hit) - 1;
+                Sequence y;
+                y.q0 = shfl64(x.q0, l);
+                y.n_q = shfl64(x.n_q, l);
+                y.len = shfl64(x.len, l);
+                y.blocks = shfl64(x.blocks, l);
+                const uint32_t before = seen + __shfl_sync(0xffffffffu, sum, l) - (uint32_t)y.blocks;
+                make_seg<D>(p, y, top - 1 - l, (int)g, y.blocks - 1 - (int64_t)(b - before), 0, INT_MAX, -1, s);
+                return true;
+            }
+            seen += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        return false;
+    }
+
+    __device__ __forceinline__ bool next_share(const PrefillParams& p, Seg& s) {
+        while (at < end) {
+            if (!started) {
+                r = place_of<D>(p, at);
+                started = true;
+            } else {  // the next unit of the line
+                r.start = r.end;
+                ++r.block;
+                if (r.block == r.x.blocks) {
+                    r.block = 0;
+                    ++r.g;
+                    if (r.g == p.n_head_kv) {
+                        r = place_of<D>(p, at);
+                    }
+                }
+                r.end = r.start + r.line.a + r.line.step * r.block;
+            }
+            const int64_t a = at, b = r.end < end ? r.end : end;
+            at = b;
+            const int64_t tok0 = r.block * p.block_tokens;
+            const int64_t left = r.x.n_q - tok0;
+            const int64_t tiles = tiles_seen(r.x.len - r.x.n_q + 1 + tok0, left < p.block_tokens ? left : p.block_tokens);
+            int64_t first, last;
+            tiles_between(r, a, b, tiles, first, last);
+            if (tiles == 0 ? a != r.start : first == last) continue;  // (a unit that sees nothing: its first piece)
+            const bool whole = first == 0 && last == tiles;
+            make_seg<D>(p, r.x, r.seq, r.g, r.block, first, last, whole ? -1 : 2 * (int)blockIdx.x + (a > r.start ? 0 : 1), s);
+            return true;
+        }
+        return false;
+    }
+};
+
 // ------------------------------------- the kernel -------------------------------------
 
 template <int D, int KBITS, int VBITS>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
-    constexpr int kGroups = D == 128 ? 2 : 1;   // row groups of 128
-    constexpr int kHalves = D / 128;            // slots per tile of K or V
+    constexpr int kGroups = Geometry<D>::kGroups, kHalves = Geometry<D>::kHalves;
     constexpr bool kQuant = KBITS != 16;
+    constexpr int kSlots = Memory<KBITS>::kSlots;
     constexpr uint32_t kColS1 = 128, kColO = 256;
     // the swizzled planes want a 1024-byte aligned base; with no static shared memory the window
     // starts on one, and nothing is left to align it with
     extern __shared__ __align__(1024) unsigned char q_tiles[];
     unsigned char* slots = q_tiles + 2 * kQTileBytes;
-    Header* h = reinterpret_cast<Header*>(slots + kSlots * kSlotBytes);
+    unsigned char* raws = slots + kSlots * kSlotBytes;
+    Header* h = reinterpret_cast<Header*>(raws + kRawStages * Memory<KBITS>::kRawBytes);
     volatile int* abort_flag = &h->abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -356,21 +534,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(smem_addr(&h->full[i]), 4);   // a lane of each loader warp (and its copies)
             mbar_init(smem_addr(&h->empty[i]), 1);  // the MMA lane's commit
+            mbar_init(smem_addr(&h->landed[i]), 1);
         }
-        mbar_init(smem_addr(&h->q_full), 128 * kGroups);
+        mbar_init(smem_addr(&h->q_full), 1);
+        mbar_init(smem_addr(&h->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&h->s_full[i]), 1);
             mbar_init(smem_addr(&h->p_full[i]), 128);
             mbar_init(smem_addr(&h->o_full[i]), 1);
         }
         mbar_init(smem_addr(&h->pv_done), 1);
-        for (int i = 0; i < kRing; ++i) mbar_init(smem_addr(&h->mask_full[i]), 1);
-        mbar_init(smem_addr(&h->load_done), 4);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(smem_addr(&h->mask_full[i]), 1);
+            mbar_init(smem_addr(&h->load_done[i]), 4);
+            mbar_init(smem_addr(&h->seg_full[i]), 1);
+            mbar_init(smem_addr(&h->seg_empty[i]), 5 + 4 * kGroups);  // loader, MMA and softmax warps
+        }
         h->abort_flag = 0;
-        for (int i = 0; i < 16; ++i) h->bad_cells[i >> 2][i & 3] = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
@@ -385,177 +568,359 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tc_fence_after();
     const uint32_t tmem = h->tmem;
     pdl_wait();
-    const Unit u = find_unit<D>(p);
     const int G = p.group;
-    // first tile (of the unit) that some row of it does not see whole: from here V's elements
-    // that are not finite are kept apart
-    const int64_t lim_first = u.lim0 + u.row0 / G;
-    const int64_t first_cut64 = (lim_first > 0 ? lim_first : 0) / kPrefillTile - u.j0;
-    const int first_cut = first_cut64 < 0 ? 0 : (first_cut64 > u.n_max ? u.n_max : (int)first_cut64);
-    // (at most 256 rows: with G = 1 a unit's limits lie in up to 256 cells, 3 tiles)
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), parity, abort_flag, p.wait_limit_ns));
+    };
+    // piece number i (in the order of the scheduler); false: no more, or a wait that gave up
+    auto take = [&](uint32_t i, Seg& s) -> bool {
+        if (!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u)) return false;
+        s = h->seg[i % kRing];
+        return s.n_tok >= 0;
+    };
+    auto give_back = [&](uint32_t i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&h->seg_empty[i % kRing]));
+    };
 
     if (warp >= 8 && warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ------------------------------------ loader ------------------------------------
         const int lt = tid - 256;       // 0 .. 127
         const int64_t Hk = p.n_head_kv;
-        bool bad_entry = false;
-        if (u.any && u.n_max > 0) {
-            const int32_t* prow = p.plan != nullptr ? p.plan + (int64_t)u.seq * p.plan_stride : nullptr;
-            // plan entries of a tile: lane l holds those of cells l, l + 32, l + 64, l + 96
-            struct Tile {
-                int32_t e[4];     // physical cells, -1: none
-                int64_t base;     // first physical cell when whole
-                bool whole;       // 128 cells in one run
-            };
-            auto read_tile = [&](int j) {
-                Tile t;
-                const int64_t i0 = (int64_t)(u.j0 + j) * kPrefillTile;
-                t.whole = i0 + kPrefillTile <= u.len;
-                t.base = u.cell0 + i0;
+        bool bad_entry = false, ok = true;
+        uint32_t n = 0;                 // slots filled
+        uint32_t T = 0;                 // tiles begun
+        uint32_t landed_use = 0;        // a bit per slot: parity of its landed barrier
+        Seg s = {};
+        // plan entries of a tile: lane l holds those of cells l, l + 32, l + 64, l + 96
+        struct Tile {
+            int32_t e[4];     // physical cells, -1: none; no plan: from the sequence's first
+            int64_t base;     // first physical cell when a run
+            bool run, holes;  // the cells that are there lie at base + their number; some are not
+        };
+        auto read_tile = [&](int j) {
+            Tile t;
+            const int64_t i0 = (int64_t)(s.j0 + j) * kPrefillTile;
+            const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+            const int32_t* prow = p.plan != nullptr ? p.plan + (int64_t)s.seq * p.plan_stride : nullptr;
+            t.run = true;
+            t.holes = i0 + kPrefillTile > s.len;
+            t.base = s.cell0 + i0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int64_t i = i0 + 32 * k + lane;
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = i0 + 32 * k + lane;
+                t.e[k] = -1;
+                if (j < n_max && i < s.len) t.e[k] = prow != nullptr ? __ldg(prow + i) : 32 * k + lane;
+            }
+            return t;
+        };
+        // checks a plan tile's entries and whether they are one run; writes its holes
+        auto settle = [&](Tile& t) {
+            if (p.plan == nullptr) return;
+            int lo = INT_MAX, hi = INT_MIN;
+            bool hole = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (t.e[k] < -1 || (int64_t)t.e[k] >= p.n_cells) {
+                    bad_entry = true;
                     t.e[k] = -1;
-                    if (j < u.n_max && i < u.len) t.e[k] = prow != nullptr ? __ldg(prow + i) : 32 * k + lane;
                 }
-                return t;
-            };
-            // checks a plan tile's entries and whether they are one run; writes its holes
-            auto settle = [&](Tile& t, int j) {
-                if (prow == nullptr) return;
-                bool run = t.whole, hole = false;
-                const int32_t first = __shfl_sync(0xffffffffu, t.e[0], 0);
+                if (t.e[k] >= 0) {
+                    const int d = t.e[k] - (32 * k + lane);
+                    lo = min(lo, d);
+                    hi = max(hi, d);
+                } else {
+                    hole = true;
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            t.run = lo >= hi;   // (no cell at all: lo > hi)
+            t.base = lo <= hi ? lo : 0;
+            t.holes = __any_sync(0xffffffffu, hole);
+            if (warp == 8) {
+                const uint32_t r = T % kRing;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (t.e[k] < -1 || (int64_t)t.e[k] >= p.n_cells) {
-                        bad_entry = true;
-                        t.e[k] = -1;
+                for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = t.e[k] < 0 ? -INFINITY : INFINITY;
+                if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
+            }
+        };
+        // physical cell of the tile's cell c (any lane's), -1: none
+        auto cell_of = [&](const Tile& t, int c) -> int64_t {
+            const int32_t v0 = __shfl_sync(0xffffffffu, t.e[0], c & 31);
+            const int32_t v1 = __shfl_sync(0xffffffffu, t.e[1], c & 31);
+            const int32_t v2 = __shfl_sync(0xffffffffu, t.e[2], c & 31);
+            const int32_t v3 = __shfl_sync(0xffffffffu, t.e[3], c & 31);
+            const int32_t v = (c & 64) ? ((c & 32) ? v3 : v2) : ((c & 32) ? v1 : v0);
+            return (p.plan == nullptr && v >= 0) ? t.base + v : v;
+        };
+        // Cells with V that is not finite, of a cut tile (unit number i's).
+        auto note = [&](uint32_t i, int j, int c, bool bad) {
+            if (bad) atomicOr(&h->bad_cells[i % kRing][(j - s.first_cut) % kCutTiles][c >> 5], 1u << (c & 31));
+        };
+        auto wait_slot_empty = [&]() -> bool {
+            const uint32_t use = n / kSlots;
+            return use == 0 || wait_all(&h->empty[n % kSlots], (use - 1) & 1u);
+        };
+        auto slot_ready = [&](uint64_t* bar) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(bar));
+            ++n;
+        };
+        auto stall_hook = [&](uint64_t* bar) {
+            if (n == 0 && p.stall_tx != 0u && lt == 0) mbar_expect_tx(smem_addr(bar), p.stall_tx);
+        };
+
+        if constexpr (!kQuant) {
+            // ---- f16 ----
+            // f16 rows of a slot by all four warps: 16 lanes a row, 8 rows at a time
+            auto copy_rows = [&](unsigned char* slot, const Tile& t, bool v_side, int half, bool cut, uint32_t i, int j) {
+                const int64_t stride = v_side ? p.v_stride : p.k_stride;
+                const __half* rows = static_cast<const __half*>(v_side ? p.v : p.k) + (int64_t)s.g * D + half * 128;
+                const int b = (lt & 15) * 16;
+                unsigned char* plane = slot + (b >> 7) * kPlaneBytes;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 16; i0 += 8) {
+                    uint4 w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int64_t cell = cell_of(t, (lt >> 4) + 8 * (i0 + k));
+                        w[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (cell >= 0) w[k] = __ldg(reinterpret_cast<const uint4*>(rows + cell * stride + b / 2));
                     }
-                    run = run && t.e[k] >= 0 && t.e[k] - first == 32 * k + lane;
-                    hole = hole || t.e[k] < 0;
-                }
-                t.whole = __all_sync(0xffffffffu, run);
-                t.base = first;
-                const bool holes = __any_sync(0xffffffffu, hole);
-                if (warp == 8) {
-                    const int r = j % kRing;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = t.e[k] < 0 ? -INFINITY : 0.f;
-                    if (lane == 0) h->holes[r] = holes ? 1u : 0u;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
+                    for (int k = 0; k < 8; ++k) {
+                        const int c = (lt >> 4) + 8 * (i0 + k);
+                        if (cut) {
+                            bool bad = false;
+                            w[k].x = finite2(w[k].x, bad);
+                            w[k].y = finite2(w[k].y, bad);
+                            w[k].z = finite2(w[k].z, bad);
+                            w[k].w = finite2(w[k].w, bad);
+                            note(i, j, c, bad);
+                        }
+                        *reinterpret_cast<uint4*>(plane + swz(c, b & 127)) = w[k];
+                    }
                 }
+                fence_async();
             };
-            // physical cell of the tile's cell c (any lane's), -1: none
-            auto cell_of = [&](const Tile& t, int c) -> int64_t {
-                if (prow == nullptr) {
-                    const int64_t i = (int64_t)c;
-                    return i < u.len - (t.base - u.cell0) ? t.base + i : -1;
+            // V rows that landed: zeros for cells that are not there and, in a cut tile, for what
+            // is not finite (warps 9-11, 16 lanes a row)
+            auto mend = [&](unsigned char* slot, const Tile& t, bool cut, uint32_t i, int j) {
+                const int sub = lane >> 4, b = (lane & 15) * 16;
+                unsigned char* plane = slot + (b >> 7) * kPlaneBytes;
+                for (int r = 2 * (warp - 9); r < 128; r += 6) {
+                    const int c = r + sub;   // (r is even: both rows in one word of entries)
+                    const int32_t v = __shfl_sync(0xffffffffu, (r & 64) ? ((r & 32) ? t.e[3] : t.e[2]) : ((r & 32) ? t.e[1] : t.e[0]),
+                                                  c & 31);
+                    uint4* at = reinterpret_cast<uint4*>(plane + swz(c, b & 127));
+                    if (v < 0) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (cut) {
+                        uint4 w = *at;
+                        bool bad = false;
+                        w.x = finite2(w.x, bad);
+                        w.y = finite2(w.y, bad);
+                        w.z = finite2(w.z, bad);
+                        w.w = finite2(w.w, bad);
+                        if (bad) *at = w;
+                        note(i, j, c, bad);
+                    }
                 }
-                int32_t v = __shfl_sync(0xffffffffu, t.e[0], c & 31);
-                const int32_t v1 = __shfl_sync(0xffffffffu, t.e[1], c & 31);
-                const int32_t v2 = __shfl_sync(0xffffffffu, t.e[2], c & 31);
-                const int32_t v3 = __shfl_sync(0xffffffffu, t.e[3], c & 31);
-                v = (c & 64) ? ((c & 32) ? v3 : v2) : ((c & 32) ? v1 : v);
-                return v;
+                fence_async();
             };
-            // The raw bytes of this thread's part of a slot (bits of the side, half of the dims)
-            auto fetch = [&](const Tile& t, bool v_side, int half, Raw& raw) {
+            auto fill = [&](const Tile& t, bool v_side, int half, uint32_t i, int j) {
+                if (!(ok = wait_slot_empty())) return;
+                const int st = (int)(n % kSlots);
+                unsigned char* slot = slots + st * kSlotBytes;
+                const bool cut = v_side && j >= s.first_cut;
+                uint64_t* bar = &h->full[st];
+                stall_hook(bar);
+                if (t.run && p.use_tma != 0) {
+                    const bool later = v_side && (cut || t.holes);
+                    if (warp == 8) {
+                        if (lane == 0) {
+                            const uint32_t b = smem_addr(later ? &h->landed[st] : bar);
+                            mbar_expect_tx(b, (uint32_t)kSlotBytes);
+                            const CUtensorMap* map = v_side ? &p.tmap_v : &p.tmap_k;
+                            tma_box(smem_addr(slot), map, half * 128, s.g, (int)t.base, b);
+                            tma_box(smem_addr(slot) + kPlaneBytes, map, half * 128 + 64, s.g, (int)t.base, b);
+                            if (later) mbar_arrive(b);
+                        }
+                    } else if (later) {
+                        if (!(ok = wait_all(&h->landed[st], (landed_use >> st) & 1u))) return;
+                        mend(slot, t, cut, i, j);
+                    }
+                    if (later) landed_use ^= 1u << st;
+                } else {
+                    copy_rows(slot, t, v_side, half, cut, i, j);
+                }
+                slot_ready(bar);
+            };
+            for (uint32_t i = 0; ok; ++i) {
+                if (!take(i, s)) break;
+                const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+                if (warp == 8 && lane < 4 * kCutTiles) h->bad_cells[i % kRing][lane >> 2][lane & 3] = 0u;
+                asm volatile("bar.sync 1, 128;" ::: "memory");   // (before any of them is set)
+                if (n_max > 0) {
+                    Tile tk = read_tile(0), tv = tk, next = read_tile(1);
+                    settle(tk);
+                    ++T;
+                    if (kHalves == 1) {
+                        for (int j = 0; j < n_max; ++j) {
+                            fill(tk, false, 0, i, j);
+                            if (!ok) break;
+                            tv = tk;
+                            if (j + 1 < n_max) {
+                                tk = next;
+                                settle(tk);
+                                ++T;
+                                next = read_tile(j + 2);
+                            }
+                            fill(tv, true, 0, i, j);
+                            if (!ok) break;
+                        }
+                    } else {   // K of tile j + 1 before V of tile j; each in two halves
+                        for (int j = -1; j < n_max && ok; ++j) {
+                            if (j >= 0) {
+                                tv = tk;
+                                if (j + 1 < n_max) {
+                                    tk = next;
+                                    settle(tk);
+                                    ++T;
+                                    next = read_tile(j + 2);
+                                }
+                            }
+#pragma unroll 1
+                            for (int half = 0; half < 2 && ok && j + 1 < n_max; ++half) fill(tk, false, half, i, j + 1);
+#pragma unroll 1
+                            for (int half = 0; half < 2 && ok && j >= 0; ++half) fill(tv, true, half, i, j);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&h->load_done[i % kRing]));
+                give_back(i);
+            }
+        } else {
+            // ---- quantised ----
+            constexpr int kStage = Memory<KBITS>::kRawBytes;
+            // A slot to come: its tile's cells (this thread's of the copies), side and half.
+            // Slots are fetched two ahead of the one that is turned into f16, so the walk over
+            // them runs ahead too; what turning needs of a slot is kept in three small words.
+            uint32_t ahead = 0;            // slots fetched
+            uint32_t what[kRawStages];     // v_side | cut << 1 | last of its unit << 2 | (j - first_cut) << 3 | unit << 8
+            auto fetch = [&](const Tile& t, bool v_side, int half, uint32_t word) {
                 const int bits = v_side ? VBITS : KBITS;
+                unsigned char* stage = raws + (ahead % kRawStages) * kStage;
                 const char* rows = static_cast<const char*>(v_side ? p.v : p.k);
-                const __half* scales = v_side ? p.v_scale : p.k_scale;
+                const char* scales = reinterpret_cast<const char*>(v_side ? p.v_scale : p.k_scale);
                 if (bits == 8) {
                     const int piece = lt & 7;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t c = cell_of(t, (lt >> 3) + 16 * i);
-                        raw.w[i] = make_uint4(0u, 0u, 0u, 0u);
-                        uint32_t d = 0u;
-                        if (c >= 0) {
-                            const int64_t row = c * Hk + u.g;
-                            raw.w[i] = __ldg(reinterpret_cast<const uint4*>(rows + row * D + half * 128 + 16 * piece));
-                            d = __ldg(reinterpret_cast<const unsigned short*>(scales) + row * (D / 32) + half * 4 + (piece >> 1));
-                        }
-                        raw.d[i >> 1] = (i & 1) ? (raw.d[i >> 1] | (d << 16)) : d;
+                    for (int k = 0; k < 8; ++k) {
+                        const int c = (lt >> 3) + 16 * k;
+                        const int64_t cell = cell_of(t, c);
+                        if (cell >= 0)
+                            cp_async_16_cg(smem_addr(stage + c * 128 + piece * 16), rows + (cell * Hk + s.g) * D + half * 128 + 16 * piece);
                     }
-                } else if (bits == 4) {
+                } else {
                     const int piece = lt & 3;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t c = cell_of(t, (lt >> 2) + 32 * i);
-                        raw.w[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-                        uint32_t d = 0u;
-                        if (c >= 0) {
-                            const int64_t row = c * Hk + u.g;
-                            raw.w[i] = __ldg(reinterpret_cast<const uint4*>(rows + row * (D / 2) + half * 64 + 16 * piece));
-                            d = __ldg(reinterpret_cast<const unsigned short*>(scales) + row * (D / 32) + half * 4 + piece);
-                        }
-                        raw.d[i] = d;
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = (lt >> 2) + 32 * k;
+                        const int64_t cell = cell_of(t, c);
+                        if (cell >= 0)
+                            cp_async_16_cg(smem_addr(stage + c * 64 + piece * 16),
+                                           rows + (cell * Hk + s.g) * (D / 2) + half * 64 + 16 * piece);
                     }
                 }
+                // scales: cell lt's four blocks; zeros where there is no cell, so that whatever
+                // its codes are it stands for zeros
+                const int64_t cell = cell_of(t, lt);
+                const uint32_t dst = smem_addr(stage + kStage - 1024 + 8 * lt);
+                if (cell >= 0)
+                    cp_async_8(dst, scales + ((cell * Hk + s.g) * (D / 32) + half * 4) * 2);
+                else
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                what[kRawStages - 1] = word;
+                ++ahead;
             };
-            // Bits of V that are not finite are dropped from the slot and their cells noted.
-            auto note = [&](int j, int c, bool bad) {
-                if (bad) atomicOr(&h->bad_cells[(j - first_cut) & 3][c >> 5], 1u << (c & 31));
-            };
-            auto store_raw = [&](unsigned char* slot, const Raw& raw, bool v_side, bool cut, int j) {
+            // Turns raw slot number n into f16 (its copies are complete and visible).
+            auto turn = [&](uint32_t word) {
+                const bool v_side = word & 1u, cut = (word >> 1) & 1u;
                 const int bits = v_side ? VBITS : KBITS;
+                const unsigned char* stage = raws + (n % kRawStages) * kStage;
+                const unsigned short* scales = reinterpret_cast<const unsigned short*>(stage + kStage - 1024);
+                unsigned char* slot = slots + (n % kSlots) * kSlotBytes;
+                uint32_t* bad_row = h->bad_cells[(word >> 8) % kRing][(word >> 3) & 3u];
                 if (bits == 8) {
                     const int piece = lt & 7;  // halves 16 piece .. of the row: bytes 32 piece ..
                     unsigned char* plane = slot + (piece >> 2) * kPlaneBytes;
                     const int b = (piece & 3) * 32;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int c = (lt >> 3) + 16 * i;
-                        const uint32_t ds = (raw.d[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+                    for (int k = 0; k < 8; ++k) {
+                        const int c = (lt >> 3) + 16 * k;
+                        const uint4 w = *reinterpret_cast<const uint4*>(stage + c * 128 + piece * 16);
+                        const uint32_t ds = scales[4 * c + (piece >> 1)];
                         const __half2 d = scale2(ds);
-                        const bool big = big_scale(ds);
-                        const uint32_t x[4] = {raw.w[i].x ^ 0x80808080u, raw.w[i].y ^ 0x80808080u,
-                                               raw.w[i].z ^ 0x80808080u, raw.w[i].w ^ 0x80808080u};
+                        const uint32_t x[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
                         uint32_t o[8];
+                        if (!big_scale(ds)) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            o[2 * k] = dequant(i8x2_lo(x[k]), d, big);
-                            o[2 * k + 1] = dequant(i8x2_hi(x[k]), d, big);
+                            for (int q = 0; q < 4; ++q) {
+                                o[2 * q] = dequant(i8x2_lo(x[q]), d, false);
+                                o[2 * q + 1] = dequant(i8x2_hi(x[q]), d, false);
+                            }
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                o[2 * q] = dequant(i8x2_lo(x[q]), d, true);
+                                o[2 * q + 1] = dequant(i8x2_hi(x[q]), d, true);
+                            }
                         }
                         if (cut) {
                             bool bad = false;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = finite2(o[k], bad);
-                            note(j, c, bad);
+                            for (int q = 0; q < 8; ++q) o[q] = finite2(o[q], bad);
+                            if (bad) atomicOr(&bad_row[c >> 5], 1u << (c & 31));
                         }
                         *reinterpret_cast<uint4*>(plane + swz(c, b)) = make_uint4(o[0], o[1], o[2], o[3]);
                         *reinterpret_cast<uint4*>(plane + swz(c, b + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                } else if (bits == 4) {
+                } else {
                     const int piece = lt & 3;  // block `piece`: halves 32 piece .., bytes 64 piece ..
                     unsigned char* plane = slot + (piece >> 1) * kPlaneBytes;
                     const int b = (piece & 1) * 64;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = (lt >> 2) + 32 * i;
-                        const uint32_t ds = raw.d[i];
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = (lt >> 2) + 32 * k;
+                        const uint4 w = *reinterpret_cast<const uint4*>(stage + c * 64 + piece * 16);
+                        const uint32_t ds = scales[4 * c + piece];
                         const __half2 d = scale2(ds);
                         const bool big = big_scale(ds);
-                        const uint32_t x[4] = {raw.w[i].x, raw.w[i].y, raw.w[i].z, raw.w[i].w};
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
                         uint32_t lo[8], hi[8];  // elements 0-15 and 16-31 of the block
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t a = prmt_b32(x[k], 0u, 0x4140u), e = prmt_b32(x[k], 0u, 0x4342u);
-                            lo[2 * k] = dequant(nib2(a & 0x000f000fu), d, big);
-                            lo[2 * k + 1] = dequant(nib2(e & 0x000f000fu), d, big);
-                            hi[2 * k] = dequant(nib2((a >> 4) & 0x000f000fu), d, big);
-                            hi[2 * k + 1] = dequant(nib2((e >> 4) & 0x000f000fu), d, big);
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t a = prmt_b32(x[q], 0u, 0x4140u), e = prmt_b32(x[q], 0u, 0x4342u);
+                            lo[2 * q] = dequant(nib2(a & 0x000f000fu), d, big);
+                            lo[2 * q + 1] = dequant(nib2(e & 0x000f000fu), d, big);
+                            hi[2 * q] = dequant(nib2((a >> 4) & 0x000f000fu), d, big);
+                            hi[2 * q + 1] = dequant(nib2((e >> 4) & 0x000f000fu), d, big);
                         }
                         if (cut) {
                             bool bad = false;
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                lo[k] = finite2(lo[k], bad);
-                                hi[k] = finite2(hi[k], bad);
+                            for (int q = 0; q < 8; ++q) {
+                                lo[q] = finite2(lo[q], bad);
+                                hi[q] = finite2(hi[q], bad);
                             }
-                            note(j, c, bad);
+                            if (bad) atomicOr(&bad_row[c >> 5], 1u << (c & 31));
                         }
                         *reinterpret_cast<uint4*>(plane + swz(c, b)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         *reinterpret_cast<uint4*>(plane + swz(c, b + 16)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
@@ -563,162 +928,162 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         *reinterpret_cast<uint4*>(plane + swz(c, b + 48)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
                     }
                 }
+                fence_async();
             };
-            // f16 rows of a slot by the whole group: 16 lanes a row, one row per 8 cells and warp half
-            auto copy_rows = [&](unsigned char* slot, const Tile& t, bool v_side, int half) {
-                const int64_t stride = v_side ? p.v_stride : p.k_stride;
-                const __half* rows = static_cast<const __half*>(v_side ? p.v : p.k) + (int64_t)u.g * D + half * 128;
-                const int b = (lt & 15) * 16;
-                const uint32_t plane = smem_addr(slot) + (b >> 7) * kPlaneBytes;
-                for (int i = 0; i < 16; ++i) {
-                    const int c = (lt >> 4) + 8 * i;
-                    const int64_t cell = cell_of(t, c);
-                    const uint32_t dst = plane + swz(c, b & 127);
-                    if (cell >= 0)
-                        cp_async_16_cg(dst, rows + cell * stride + b / 2);
-                    else
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u) : "memory");
-                }
-            };
-            // ... V of a tile that only some rows see whole: through registers
-            auto copy_rows_finite = [&](unsigned char* slot, const Tile& t, int half, int j) {
-                const __half* rows = static_cast<const __half*>(p.v) + (int64_t)u.g * D + half * 128;
-                const int b = (lt & 15) * 16;
-                unsigned char* plane = slot + (b >> 7) * kPlaneBytes;
-#pragma unroll 1
-                for (int i0 = 0; i0 < 16; i0 += 8) {
-                    uint4 w[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t cell = cell_of(t, (lt >> 4) + 8 * (i0 + i));
-                        w[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (cell >= 0) w[i] = __ldg(reinterpret_cast<const uint4*>(rows + cell * p.v_stride + b / 2));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int c = (lt >> 4) + 8 * (i0 + i);
-                        bool bad = false;
-                        w[i].x = finite2(w[i].x, bad);
-                        w[i].y = finite2(w[i].y, bad);
-                        w[i].z = finite2(w[i].z, bad);
-                        w[i].w = finite2(w[i].w, bad);
-                        note(j, c, bad);
-                        *reinterpret_cast<uint4*>(plane + swz(c, b & 127)) = w[i];
-                    }
-                }
-            };
-
-            // The order in which the MMA warp needs the slots: at head_dim 128 K0 V0 K1 V1 ..,
-            // at 256 K0 K1 V0 K2 V1 .. (two slots each).
-            uint32_t n = 0;  // slots filled
-            bool ok = true;
-            Raw cur, nxt;
-            Tile tk = read_tile(0), tv = tk, tnext = read_tile(1);
-            settle(tk, 0);
-            tv = tk;
-            auto fill = [&](const Tile& t, bool v_side, int half, int j) {
-                const int st = (int)(n % kSlots);
-                const uint32_t use = n / kSlots;
-                if (use > 0) {
-                    const bool got = mbar_wait_bounded(smem_addr(&h->empty[st]), (use - 1) & 1u, abort_flag, p.wait_limit_ns);
-                    if (!__all_sync(0xffffffffu, got)) {
-                        ok = false;
+            // The slots in the ring's order, one per call: side, half and tile of the next one.
+            // (At head_dim 128 K0 V0 K1 V1 .., at 256 K0 K1 V0 K2 V1 .., two slots each.)
+            uint32_t unit = 0;             // the unit that is being fetched
+            int step = 0, steps = 0;       // its slots so far and in all
+            Tile tk, tv, next;
+            bool more = true;
+            auto open_unit = [&]() {       // the next unit with tiles; those without are given back
+                for (;;) {
+                    if (!take(unit, s)) {
+                        more = false;
                         return;
                     }
-                }
-                unsigned char* slot = slots + st * kSlotBytes;
-                const uint32_t bar = smem_addr(&h->full[st]);
-                const bool cut = v_side && j >= first_cut;
-                if (n == 0 && p.stall_tx != 0u && lt == 0) mbar_expect_tx(bar, p.stall_tx);
-                if (kQuant) {
-                    store_raw(slot, cur, v_side, cut, j);
-                    fence_async();
-                } else if (cut) {
-                    copy_rows_finite(slot, t, half, j);
-                    fence_async();
-                } else if (t.whole && p.use_tma != 0) {
-                    if (lt == 0) {
-                        mbar_expect_tx(bar, (uint32_t)kSlotBytes);
-                        const CUtensorMap* map = v_side ? &p.tmap_v : &p.tmap_k;
-                        tma_box(smem_addr(slot), map, half * 128, u.g, (int)t.base, bar);
-                        tma_box(smem_addr(slot) + kPlaneBytes, map, half * 128 + 64, u.g, (int)t.base, bar);
-                    }
-                } else {
-                    copy_rows(slot, t, v_side, half);
-                    cp_async_arrive(bar);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar);
-                ++n;
-            };
-            if (kHalves == 1) {
-                if (kQuant) fetch(tk, false, 0, cur);
-                for (int j = 0; j < u.n_max && ok; ++j) {
-                    if (kQuant) fetch(tk, true, 0, nxt);
-                    fill(tk, false, 0, j);
-                    if (!ok) break;
-                    tv = tk;
-                    if (j + 1 < u.n_max) {
-                        tk = tnext;
-                        settle(tk, j + 1);
-                        tnext = read_tile(j + 2);
-                    }
-                    if (kQuant) {
-                        cur = nxt;
-                        if (j + 1 < u.n_max) fetch(tk, false, 0, nxt);
-                    }
-                    fill(tv, true, 0, j);
-                    if (kQuant) cur = nxt;
-                }
-            } else {
-                // (K of tile j + 1 before V of tile j; each in two halves)
-                if (kQuant) fetch(tk, false, 0, cur);
-                for (int j = -1; j < u.n_max && ok; ++j) {
-                    const int jk = j + 1;
-                    if (jk < u.n_max) {
-                        if (jk > 0) {
-                            tv = tk;
-                            tk = tnext;
-                            settle(tk, jk);
-                            tnext = read_tile(jk + 1);
-                            if (kQuant) fetch(tk, false, 0, cur);
-                        }
-#pragma unroll 1
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            if (kQuant && half == 0) fetch(tk, false, 1, nxt);
-                            fill(tk, false, half, jk);
-                            if (kQuant) cur = nxt;
-                        }
-                    } else {
+                    // (every warp is here: no bit of the unit four before is set any more)
+                    if (warp == 8 && lane < 4 * kCutTiles) h->bad_cells[unit % kRing][lane >> 2][lane & 3] = 0u;
+                    const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+                    if (n_max > 0) {
+                        step = 0;
+                        steps = 2 * kHalves * n_max;
+                        tk = read_tile(0);
+                        next = read_tile(1);
+                        settle(tk);
+                        ++T;
                         tv = tk;
+                        return;
                     }
-                    if (j >= 0 && ok) {
-                        if (kQuant) fetch(tv, true, 0, cur);
-#pragma unroll 1
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            if (kQuant && half == 0) fetch(tv, true, 1, nxt);
-                            fill(tv, true, half, j);
-                            if (kQuant) cur = nxt;
-                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&h->load_done[unit % kRing]));
+                    give_back(unit);
+                    ++unit;
+                }
+            };
+            auto fetch_next = [&]() {      // (a group is committed either way, so that they count)
+                if (more && step == steps) open_unit();
+                if (!more) {
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    what[kRawStages - 1] = 0xffffffffu;
+                    return;
+                }
+                const int n_max = steps / (2 * kHalves);
+                bool v_side;
+                int j, half;
+                if (kHalves == 1) {
+                    v_side = step & 1;
+                    j = step >> 1;
+                    half = 0;
+                } else {   // K0 then, for each j, K of j + 1 (if any) and V of j
+                    const int q = step >> 1;
+                    half = step & 1;
+                    if (q == 0) {
+                        v_side = false;
+                        j = 0;
+                    } else if (q == 2 * n_max - 1) {
+                        v_side = true;
+                        j = n_max - 1;
+                    } else {
+                        v_side = !(q & 1);
+                        j = v_side ? (q >> 1) - 1 : (q >> 1) + 1;
                     }
+                }
+                if (!v_side && half == 0 && j > 0) {   // a new tile
+                    tv = tk;
+                    tk = next;
+                    settle(tk);
+                    ++T;
+                    next = read_tile(j + 1);
+                }
+                if (kHalves == 2 && v_side && half == 0 && j == n_max - 1) tv = tk;
+                if (kHalves == 1) tv = tk;
+                ++step;
+                const bool cut = v_side && j >= s.first_cut;
+                const uint32_t word = (v_side ? 1u : 0u) | (cut ? 2u : 0u) | (step == steps ? 4u : 0u) |
+                                      ((uint32_t)(cut ? j - s.first_cut : 0) << 3) | ((unit & 0xffffu) << 8);
+                fetch(v_side ? tv : tk, v_side, half, word);
+                if (step == steps) ++unit;
+            };
+            uint32_t handed = 0;           // units given back (16 bits are compared with the words')
+            auto shift = [&]() {
+#pragma unroll
+                for (int k = 0; k + 1 < kRawStages; ++k) what[k] = what[k + 1];
+            };
+            step = steps = 0;
+#pragma unroll
+            for (int k = 0; k < kRawStages - 1; ++k) {
+                shift();
+                fetch_next();
+            }
+            // what[1], what[2]: the two slots in flight
+            for (;;) {
+                shift();                   // what[0]: the slot to turn
+                const uint32_t word = what[0];
+                what[kRawStages - 1] = 0xffffffffu;
+                if (word == 0xffffffffu) break;
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRawStages - 2) : "memory");
+                asm volatile("bar.sync 1, 128;" ::: "memory");   // everyone's copies; the stage before is free
+                fetch_next();
+                if (!(ok = wait_slot_empty())) break;
+                stall_hook(&h->full[n % kSlots]);
+                turn(word);
+                slot_ready(&h->full[(n) % kSlots]);
+                if (word & 4u) {           // the unit's last slot
+                    handed = (word >> 8) & 0xffffu;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&h->load_done[handed % kRing]));
+                    give_back(handed);
                 }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&h->load_done));
         if (__any_sync(0xffffffffu, bad_entry) && lane == 0 && warp == 8) atomicOr(p.status, KVATTN_DEVICE_BAD_PLAN_ENTRY);
     } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 12 && u.any && u.n_max > 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 13) {
+            // ---------------------------------- scheduler ----------------------------------
+            Walk<D> walk;
+            walk.begin(p);
+            uint32_t q_uses = 0;
+            for (uint32_t i = 0;; ++i) {
+                Seg s;
+                if (!walk.next(p, s)) s.n_tok = -1;
+                if (i >= kRing && !wait_all(&h->seg_empty[i % kRing], ((i / kRing) - 1) & 1u)) break;
+                if (lane == 0) {
+                    h->seg[i % kRing] = s;
+                    mbar_arrive(smem_addr(&h->seg_full[i % kRing]));
+                }
+                __syncwarp();
+                if (s.n_tok < 0) break;
+                if (s.n[0] > 0 || s.n[1] > 0) {
+                    // its query rows, once the last S of the unit before is complete
+                    if (q_uses > 0 && !wait_all(&h->q_empty, (q_uses - 1) & 1u)) break;
+                    ++q_uses;
+                    if (lane == 0) {
+                        const uint32_t bar = smem_addr(&h->q_full);
+                        const uint32_t box = 128u * (uint32_t)(p.group_tokens * G);
+                        const int n_grp = (kGroups == 2 && s.n[1] > 0) ? 2 : 1;
+                        mbar_expect_tx(bar, box * 2u * (uint32_t)(kHalves * n_grp));
+                        for (int t = 0; t < n_grp * kHalves; ++t)
+                            for (int pl = 0; pl < 2; ++pl)
+                                tma_box(smem_addr(q_tiles) + t * kQTileBytes + pl * kPlaneBytes, &p.tmap_q,
+                                        (kGroups == 2 ? 0 : t * 128) + pl * 64, s.g * G,
+                                        (int)s.q_tok + (kGroups == 2 ? t * p.group_tokens : 0), bar);
+                        mbar_arrive(bar);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (warp == 12) {
             // ------------------------------------- MMA -------------------------------------
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), parity, abort_flag, p.wait_limit_ns));
-            };
-            uint32_t n = 0;  // slots consumed
+            uint32_t n = 0;                   // slots consumed
+            uint32_t done[2] = {0u, 0u};      // head_dim 128: tiles of the row groups so far; 256: [0] tiles
+            uint32_t q_uses = 0;
             auto wait_slot = [&](uint32_t s) -> bool {
                 if (!wait_all(&h->full[s % kSlots], (s / kSlots) & 1u)) return false;
-                fence_async();  // rows that ordinary stores or cp.async wrote
+                fence_async();  // rows that ordinary stores wrote
                 tc_fence_after();
                 return true;
             };
@@ -740,85 +1105,103 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     mma_ts(d, a + 8 * k, vd + (uint64_t)((2048 * k) >> 4), kIdPV, (acc || k > 0) ? 1u : 0u);
             };
             const uint32_t q_addr = smem_addr(q_tiles);
-            bool ok = wait_all(&h->q_full, 0u);
-            tc_fence_after();
-            if (kGroups == 2) {
-                for (int j = 0; j <= u.n_max && ok; ++j) {
-                    const uint32_t ks = n, vs = n + 1, v_last = n - 1;
-                    if (j < u.n_max) {
-                        if (!(ok = wait_slot(ks))) break;
-                        if (j < u.n[0] && elect_one()) {
-                            issue_s(tm, q_addr, ks, false);
-                            mma_commit(smem_addr(&h->s_full[0]));
-                        }
-                        __syncwarp();
-                    }
-                    if (j > 0) {
-                        if (j - 1 < u.n[1] && !(ok = wait_all(&h->p_full[1], (j - 1) & 1u))) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            if (j - 1 < u.n[1]) {
-                                issue_pv(tm + kColO + 128, tm + kColS1, v_last, j > 1);
-                                if (j == u.n[1]) mma_commit(smem_addr(&h->o_full[1]));
+            bool ok = true;
+            Seg s;
+            for (uint32_t i = 0; ok; ++i) {
+                if (!take(i, s)) break;
+                give_back(i);
+                const int n0 = s.n[0], n1 = s.n[1], n_max = n0 > n1 ? n0 : n1;
+                if (n_max == 0) continue;
+                if (!(ok = wait_all(&h->q_full, q_uses & 1u))) break;
+                ++q_uses;
+                tc_fence_after();
+                if (kGroups == 2) {
+                    for (int j = 0; j <= n_max && ok; ++j) {
+                        const uint32_t ks = n, vs = n + 1, v_last = n - 1;
+                        if (j < n_max) {
+                            if (!(ok = wait_slot(ks))) break;
+                            if (j < n0 && elect_one()) {
+                                issue_s(tm, q_addr, ks, false);
+                                mma_commit(smem_addr(&h->s_full[0]));
                             }
-                            mma_commit(smem_addr(&h->empty[v_last % kSlots]));
+                            __syncwarp();
                         }
-                        __syncwarp();
-                    }
-                    if (j == u.n_max) break;
-                    if (elect_one()) {
-                        if (j < u.n[1]) {
-                            issue_s(tm + kColS1, q_addr + kQTileBytes, ks, false);
-                            mma_commit(smem_addr(&h->s_full[1]));
-                        }
-                        mma_commit(smem_addr(&h->empty[ks % kSlots]));
-                    }
-                    __syncwarp();
-                    if (!(ok = wait_slot(vs))) break;
-                    if (j < u.n[0]) {
-                        if (!(ok = wait_all(&h->p_full[0], j & 1u))) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            issue_pv(tm + kColO, tm, vs, j > 0);
-                            if (j + 1 == u.n[0]) mma_commit(smem_addr(&h->o_full[0]));
-                        }
-                        __syncwarp();
-                    }
-                    n += 2;
-                }
-            } else {
-                // S of a tile into buffer j & 1, its two halves of the dims in turn
-                auto issue_tile_s = [&](int j) -> bool {
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half, ++n) {
-                        if (!wait_slot(n)) return false;
-                        if (elect_one()) {
-                            issue_s(tm + kColS1 * (j & 1), q_addr + half * kQTileBytes, n, half > 0);
-                            mma_commit(smem_addr(&h->empty[n % kSlots]));
-                            if (half == 1) mma_commit(smem_addr(&h->s_full[j & 1]));
-                        }
-                        __syncwarp();
-                    }
-                    return true;
-                };
-                ok = ok && issue_tile_s(0);
-                for (int j = 0; j < u.n_max && ok; ++j) {
-                    if (j + 1 < u.n_max && !(ok = issue_tile_s(j + 1))) break;
-                    if (!(ok = wait_all(&h->p_full[j & 1], (j >> 1) & 1u))) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int half = 0; half < 2; ++half, ++n) {
-                        if (!(ok = wait_slot(n))) break;
-                        if (elect_one()) {
-                            issue_pv(tm + kColO + 128 * half, tm + kColS1 * (j & 1), n, j > 0);
-                            mma_commit(smem_addr(&h->empty[n % kSlots]));
-                            if (half == 1) {
-                                mma_commit(smem_addr(&h->pv_done));
-                                if (j + 1 == u.n_max) mma_commit(smem_addr(&h->o_full[0]));
+                        if (j > 0) {
+                            if (j - 1 < n1 && !(ok = wait_all(&h->p_full[1], (done[1] + j - 1) & 1u))) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                if (j - 1 < n1) {
+                                    issue_pv(tm + kColO + 128, tm + kColS1, v_last, j > 1);
+                                    if (j == n1) mma_commit(smem_addr(&h->o_full[1]));
+                                }
+                                mma_commit(smem_addr(&h->empty[v_last % kSlots]));
                             }
+                            __syncwarp();
+                        }
+                        if (j == n_max) break;
+                        if (elect_one()) {
+                            if (j < n1) {
+                                issue_s(tm + kColS1, q_addr + kQTileBytes, ks, false);
+                                mma_commit(smem_addr(&h->s_full[1]));
+                            }
+                            mma_commit(smem_addr(&h->empty[ks % kSlots]));
+                            if (j + 1 == n_max) mma_commit(smem_addr(&h->q_empty));
                         }
                         __syncwarp();
+                        if (!(ok = wait_slot(vs))) break;
+                        if (j < n0) {
+                            if (!(ok = wait_all(&h->p_full[0], (done[0] + j) & 1u))) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                issue_pv(tm + kColO, tm, vs, j > 0);
+                                if (j + 1 == n0) mma_commit(smem_addr(&h->o_full[0]));
+                            }
+                            __syncwarp();
+                        }
+                        n += 2;
                     }
+                    done[0] += n0;
+                    done[1] += n1;
+                } else {
+                    // S of a tile into buffer T & 1, its two halves of the dims in turn
+                    auto issue_tile_s = [&](int j) -> bool {
+                        const uint32_t buf = (done[0] + j) & 1u;
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half, ++n) {
+                            if (!wait_slot(n)) return false;
+                            if (elect_one()) {
+                                issue_s(tm + kColS1 * buf, q_addr + half * kQTileBytes, n, half > 0);
+                                mma_commit(smem_addr(&h->empty[n % kSlots]));
+                                if (half == 1) {
+                                    mma_commit(smem_addr(&h->s_full[buf]));
+                                    if (j + 1 == n_max) mma_commit(smem_addr(&h->q_empty));
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        return true;
+                    };
+                    ok = issue_tile_s(0);
+                    for (int j = 0; j < n_max && ok; ++j) {
+                        if (j + 1 < n_max && !(ok = issue_tile_s(j + 1))) break;
+                        const uint32_t t = done[0] + j, buf = t & 1u;
+                        if (!(ok = wait_all(&h->p_full[buf], (t >> 1) & 1u))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half, ++n) {
+                            if (!(ok = wait_slot(n))) break;
+                            if (elect_one()) {
+                                issue_pv(tm + kColO + 128 * half, tm + kColS1 * buf, n, j > 0);
+                                mma_commit(smem_addr(&h->empty[n % kSlots]));
+                                if (half == 1) {
+                                    mma_commit(smem_addr(&h->pv_done));
+                                    if (j + 1 == n_max) mma_commit(smem_addr(&h->o_full[0]));
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    done[0] += n0;
                 }
             }
         }
@@ -826,215 +1209,197 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------ softmax ------------------------------------
         const int grp = warp >> 2;                   // row group
-        const int row_in = tid & 127;                // TMEM lane
-        const int64_t row = u.row0 + 128 * grp + row_in;
-        if (u.any && grp < kGroups) {
-            const bool row_ok = row < u.rows;
-            const int64_t tok = row_ok ? row / G : 0;
-            const int head = u.g * G + (row_ok ? (int)(row - tok * G) : 0);
-            // Q rows in: each warp its 32 rows, 16 lanes a row of 128 dims
-            if (u.n_max > 0) {
-                const long long my_src = row_ok ? (long long)((u.q0 + tok) * p.q_stride + (int64_t)head * D) : -1ll;
-#pragma unroll 1
-                for (int half = 0; half < kHalves; ++half) {
-                    unsigned char* qt = q_tiles + (kGroups == 2 ? grp : half) * kQTileBytes;
-                    const int b = (lane & 15) * 16;
-                    const uint32_t plane = smem_addr(qt) + (b >> 7) * kPlaneBytes;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int rl = 2 * i + (lane >> 4);
-                        const long long src = __shfl_sync(0xffffffffu, my_src, rl);
-                        const uint32_t dst = plane + swz(32 * (warp & 3) + rl, b & 127);
-                        if (src >= 0)
-                            cp_async_16_cg(dst, p.q + src + half * 128 + b / 2);
-                        else
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u) : "memory");
-                    }
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_async();
-                mbar_arrive(smem_addr(&h->q_full));
-            }
+        if (grp < kGroups) {
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t t_o = tmem + lane_base + kColO + (kGroups == 2 ? 128u * grp : 0u);
-            const int n_tiles = u.n[grp];
-            // first cell of the split that this row does not see, from the split's first
-            const int64_t rel0 = row_ok ? u.lim0 + tok - (int64_t)u.j0 * kPrefillTile : 0;
-            float m_run = -INFINITY, l_run = 0.f;
-            bool ok = true;
             // (scale <= 0: scores are scaled before the maximum is taken)
             const bool pre = !(p.scale_log2 > 0.f);
             const float sc = pre ? 1.f : p.scale_log2;
-            for (int j = 0; j < n_tiles; ++j) {
-                const int buf = kGroups == 2 ? grp : (j & 1);
-                const uint32_t par = kGroups == 2 ? (j & 1u) : ((j >> 1) & 1u);
-                const uint32_t t_s = tmem + lane_base + kColS1 * buf;
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&h->s_full[buf]), par, abort_flag, p.wait_limit_ns))) {
-                    ok = false;
-                    break;
+            uint32_t done = 0;                       // tiles of this group so far
+            uint32_t masks = 0;                      // tiles of the CTA so far
+            uint32_t outs = 0;                       // units of this group with tiles so far
+            bool ok = true;
+            for (uint32_t i = 0; ok; ++i) {
+                if (!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u)) break;
+                const Seg& s = h->seg[i % kRing];        // (kept until it is given back)
+                if (s.n_tok < 0) break;
+                const int n_tiles = s.n[grp];
+                // first cell of the piece that this row does not see, from the piece's first
+                int rel0 = 0;
+                {
+                    const int tok_in = (tid & 127) / G, tok = grp * p.group_tokens + tok_in;
+                    if (tok_in < p.group_tokens && tok < s.n_tok)
+                        rel0 = (int)clamp64(s.lim0 + tok - (int64_t)s.j0 * kPrefillTile, 0, INT_MAX);
                 }
-                tc_fence_after();
-                uint32_t sv[128];
+                float m_run = -INFINITY, l_run = 0.f;
+                for (int j = 0; j < n_tiles; ++j, ++done) {
+                    const int buf = kGroups == 2 ? grp : (int)(done & 1u);
+                    const uint32_t par = kGroups == 2 ? (done & 1u) : ((done >> 1) & 1u);
+                    const uint32_t t_s = tmem + lane_base + kColS1 * buf;
+                    if (!(ok = wait_all(&h->s_full[buf], par))) break;
+                    tc_fence_after();
+                    uint32_t sv[128];
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) tmem_ld32(t_s + c, sv + c);
-                const int64_t rel = rel0 - (int64_t)j * kPrefillTile;
-                tc_wait_ld();
-                if (pre) {
-                    const uint64_t f = pack2(p.scale_log2, p.scale_log2);
+                    for (int c = 0; c < 128; c += 32) tmem_ld32(t_s + c, sv + c);
+                    const int rel = rel0 - j * kPrefillTile;
+                    tc_wait_ld();
+                    if (pre) {
+                        const uint64_t f = pack2(p.scale_log2, p.scale_log2);
 #pragma unroll
-                    for (int c = 0; c < 128; c += 2) {
-                        float a, b;
-                        unpack2(mul2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), f), a, b);
-                        sv[c] = __float_as_uint(a);
-                        sv[c + 1] = __float_as_uint(b);
+                        for (int c = 0; c < 128; c += 2) {
+                            float a, b;
+                            unpack2(mul2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), f), a, b);
+                            sv[c] = __float_as_uint(a);
+                            sv[c + 1] = __float_as_uint(b);
+                        }
                     }
-                }
-                if (!__all_sync(0xffffffffu, rel >= kPrefillTile)) {
-                    const int lim = rel < 0 ? 0 : (rel > 128 ? 128 : (int)rel);
+                    if (!__all_sync(0xffffffffu, rel >= kPrefillTile)) {
+                        const int lim = rel;
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= lim) sv[c] = 0xff800000u;
-                }
-                bool holes = false;
-                if (p.plan != nullptr) {
-                    // (the loader's write, ordered by a barrier of its own; the tile's V slot is
-                    // released after this thread's P, and the ring is deeper than the slots reach)
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&h->mask_full[j % kRing]), (j / kRing) & 1u,
-                                                                   abort_flag, p.wait_limit_ns))) {
-                        ok = false;
-                        break;
+                        for (int c = 0; c < 128; ++c)
+                            if (c >= lim) sv[c] = 0xff800000u;
                     }
-                    holes = h->holes[j % kRing] != 0u;
-                }
-                if (holes) {
-                    const float4* bias = reinterpret_cast<const float4*>(h->bias[j % kRing]);
+                    if (p.plan != nullptr) {
+                        // (the loader's write, ordered by a barrier of its own; the tile's V slot is
+                        // released after this thread's P, and the ring is deeper than the slots reach)
+                        const uint32_t t = masks + j;
+                        if (!(ok = wait_all(&h->mask_full[t % kRing], (t / kRing) & 1u))) break;
+                        if (h->holes[t % kRing] != 0u) {
+                            // the minimum of the score and -inf for a hole, +inf for a cell: a NaN that
+                            // stands in a hole goes too
+                            const float4* bias = reinterpret_cast<const float4*>(h->bias[t % kRing]);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const float4 f = bias[c];
-                        sv[4 * c] = __float_as_uint(__uint_as_float(sv[4 * c]) + f.x);
-                        sv[4 * c + 1] = __float_as_uint(__uint_as_float(sv[4 * c + 1]) + f.y);
-                        sv[4 * c + 2] = __float_as_uint(__uint_as_float(sv[4 * c + 2]) + f.z);
-                        sv[4 * c + 3] = __float_as_uint(__uint_as_float(sv[4 * c + 3]) + f.w);
-                    }
-                }
-                float mx[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
-#pragma unroll
-                for (int c = 8; c < 128; c += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx[k] = max3(mx[k], __uint_as_float(sv[c + 2 * k]), __uint_as_float(sv[c + 2 * k + 1]));
-                const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                const bool grow = tmax > m_run + kSlack;
-                if (__any_sync(0xffffffffu, grow)) {
-                    float alpha = 1.f;
-                    if (grow) {
-                        alpha = fast_exp2(m_run - tmax);  // (0 from a maximum of -inf)
-                        m_run = tmax;
-                        l_run *= alpha;
-                    }
-                    // rows whose maximum moved rescale their O once the last P V is complete
-                    // (head_dim 128: S of this tile came after it)
-                    if (j > 0) {
-                        if (kGroups == 1) {
-                            if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&h->pv_done), (j - 1) & 1u, abort_flag,
-                                                                           p.wait_limit_ns))) {
-                                ok = false;
-                                break;
+                            for (int c = 0; c < 32; ++c) {
+                                const float4 f = bias[c];
+                                sv[4 * c] = __float_as_uint(fminf(__uint_as_float(sv[4 * c]), f.x));
+                                sv[4 * c + 1] = __float_as_uint(fminf(__uint_as_float(sv[4 * c + 1]), f.y));
+                                sv[4 * c + 2] = __float_as_uint(fminf(__uint_as_float(sv[4 * c + 2]), f.z));
+                                sv[4 * c + 3] = __float_as_uint(fminf(__uint_as_float(sv[4 * c + 3]), f.w));
                             }
-                            tc_fence_after();
                         }
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
+#pragma unroll
+                    for (int c = 8; c < 128; c += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k] = max3(mx[k], __uint_as_float(sv[c + 2 * k]), __uint_as_float(sv[c + 2 * k + 1]));
+                    const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                    const bool grow = tmax > m_run + kSlack;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        float alpha = 1.f;
+                        if (grow) {
+                            alpha = fast_exp2(m_run - tmax);  // (0 from a maximum of -inf)
+                            m_run = tmax;
+                            l_run *= alpha;
+                        }
+                        // rows whose maximum moved rescale their O once the last P V is complete
+                        // (head_dim 128: S of this tile came after it)
+                        if (j > 0) {
+                            if (kGroups == 1) {
+                                if (!(ok = wait_all(&h->pv_done, (done - 1) & 1u))) break;
+                                tc_fence_after();
+                            }
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t ov[32];
-                            tmem_ld32(t_o + c0, ov);
-                            tc_wait_ld();
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                uint32_t ov[32];
+                                tmem_ld32(t_o + c0, ov);
+                                tc_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
-                            tmem_st32(t_o + c0, ov);
+                                for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+                                tmem_st32(t_o + c0, ov);
+                            }
                         }
                     }
-                }
-                const float nm = (m_run == -INFINITY) ? 0.f : kLift - m_run;
-                const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(nm, nm);
-                uint64_t sum[2] = {0ull, 0ull};
+                    const float nm = (m_run == -INFINITY) ? 0.f : kLift - m_run;
+                    const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(nm, nm);
+                    uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-                for (int c0 = 0; c0 < 128; c0 += 32) {
-                    uint32_t pw[16];
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        uint32_t pw[16];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        float a, b;
-                        unpack2(fma2(pack2(__uint_as_float(sv[c0 + c]), __uint_as_float(sv[c0 + c + 1])), sc2, nm2), a, b);
-                        a = fast_exp2(a);
-                        b = fast_exp2(b);
-                        sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
-                        pw[c >> 1] = pack_half2(a, b);
+                        for (int c = 0; c < 32; c += 2) {
+                            float a, b;
+                            unpack2(fma2(pack2(__uint_as_float(sv[c0 + c]), __uint_as_float(sv[c0 + c + 1])), sc2, nm2), a, b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
+                            pw[c >> 1] = pack_half2(a, b);
+                        }
+                        tmem_st16(t_s + (c0 >> 1), pw);
                     }
-                    tmem_st16(t_s + (c0 >> 1), pw);
+                    float s0, s1, s2, s3;
+                    unpack2(sum[0], s0, s1);
+                    unpack2(sum[1], s2, s3);
+                    l_run += (s0 + s1) + (s2 + s3);
+                    tc_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(smem_addr(&h->p_full[buf]));
                 }
-                float s0, s1, s2, s3;
-                unpack2(sum[0], s0, s1);
-                unpack2(sum[1], s2, s3);
-                l_run += (s0 + s1) + (s2 + s3);
-                tc_wait_st();
-                tc_fence_before();
-                mbar_arrive(smem_addr(&h->p_full[buf]));
-            }
-            // ---- the unit's result ----
-            if (ok && n_tiles > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&h->o_full[grp]), 0u, abort_flag, p.wait_limit_ns));
-                tc_fence_after();
-            }
-            if (ok) {
-                const bool none = n_tiles == 0 || l_run == 0.f;  // (a NaN sum stays)
-                const float inv = none ? 0.f : 1.f / l_run;
-                const bool split = p.n_split > 1;
-                const bool write = row_ok && !(split && n_tiles == 0);  // (the merge reads no such part)
-                const int64_t out_row = (u.q0 + tok) * p.n_head + head;
-                const int64_t part_row = (int64_t)u.split * p.n_tok * p.n_head + out_row;
+                if (!ok) break;
+                masks += s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+                // ---- the piece's result ----
+                const int row_in = tid & 127;
+                const int tok_in = row_in / G, head_in = row_in - tok_in * G;
+                const int tok = grp * p.group_tokens + tok_in;
+                const bool row_ok = tok_in < p.group_tokens && tok < s.n_tok;
                 // V that was kept apart: cells that this row sees
                 bool fix = false;
-                if (n_tiles > 0 && mbar_wait_bounded(smem_addr(&h->load_done), 0u, abort_flag, p.wait_limit_ns) && row_ok)
-                    for (int t = 0; t < 4; ++t)
-                        fix = fix || (h->bad_cells[t][0] | h->bad_cells[t][1] | h->bad_cells[t][2] | h->bad_cells[t][3]) != 0u;
+                if (n_tiles > 0) {
+                    if (!(ok = wait_all(&h->o_full[grp], outs & 1u))) break;
+                    ++outs;
+                    tc_fence_after();
+                    if (!(ok = wait_all(&h->load_done[i % kRing], (i / kRing) & 1u))) break;
+                    for (int t = 0; t < kCutTiles; ++t)
+                        for (int k = 0; k < 4; ++k) fix = fix || h->bad_cells[i % kRing][t][k] != 0u;
+                    fix = fix && row_ok;
+                }
+                const bool none = n_tiles == 0 || l_run == 0.f;  // (a NaN sum stays)
+                const float inv = none ? 0.f : 1.f / l_run;
+                const int64_t out_row = (s.q_tok + tok) * p.n_head + s.g * G + head_in;
+                const int64_t part_row = ((int64_t)s.part * kGroups + grp) * 128 + row_in;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
+                    if (s.part >= 0 && n_tiles == 0) break;      // (its lse says that nothing is there)
                     uint32_t ov[32];
                     if (n_tiles > 0) {
                         tmem_ld32(t_o + c0, ov);
                         tc_wait_ld();
+                    } else {   // (written on both ways: else its registers live through the tiles' loop)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) ov[k] = 0u;
                     }
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         ov[k] = none ? 0u : __float_as_uint(__uint_as_float(ov[k]) * inv);
                     if (fix) {
 #pragma unroll 1
-                        for (int t = 0; t < 4; ++t)
+                        for (int t = 0; t < kCutTiles; ++t)
 #pragma unroll 1
                             for (int c = 0; c < 128; ++c) {
-                                if (!((h->bad_cells[t][c >> 5] >> (c & 31)) & 1u)) continue;
-                                const int64_t at = (int64_t)(u.j0 + first_cut + t) * kPrefillTile + c;
-                                if (at >= u.lim0 + tok) continue;
-                                const int64_t cell = p.plan != nullptr ? (int64_t)__ldg(p.plan + (int64_t)u.seq * p.plan_stride + at)
-                                                                       : u.cell0 + at;
+                                if (!((h->bad_cells[i % kRing][t][c >> 5] >> (c & 31)) & 1u)) continue;
+                                const int64_t at = (int64_t)(s.j0 + s.first_cut + t) * kPrefillTile + c;
+                                if (at >= s.lim0 + tok) continue;
+                                const int64_t cell = p.plan != nullptr ? (int64_t)__ldg(p.plan + (int64_t)s.seq * p.plan_stride + at)
+                                                                       : s.cell0 + at;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
-                                    const int e = c0 + k;
+                                    const int d = c0 + k;
                                     __half x;
-                                    const int64_t vr = cell * p.n_head_kv + u.g;
                                     if (VBITS == 16) {
-                                        x = static_cast<const __half*>(p.v)[cell * p.v_stride + (int64_t)u.g * D + e];
+                                        x = static_cast<const __half*>(p.v)[cell * p.v_stride + (int64_t)s.g * D + d];
                                     } else {  // (only the scale is not finite)
-                                        x = p.v_scale[vr * (D / 32) + e / 32];
+                                        x = p.v_scale[(cell * p.n_head_kv + s.g) * (D / 32) + d / 32];
                                         if (__hisinf(x)) x = __ushort_as_half(0x7fffu);  // (as the loader has it)
                                     }
                                     if (__hisinf(x) || __hisnan(x)) ov[k] = __float_as_uint(__uint_as_float(ov[k]) + __half2float(x));
                                 }
                             }
                     }
-                    if (write) {
-                        if (split) {
+                    if (row_ok) {
+                        if (s.part >= 0) {
                             float4* d = reinterpret_cast<float4*>(p.part_o + part_row * D + c0);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
@@ -1046,20 +1411,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             for (int k = 0; k < 4; ++k) {
                                 uint32_t w[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    w[i] = pack_half2(__uint_as_float(ov[8 * k + 2 * i]), __uint_as_float(ov[8 * k + 2 * i + 1]));
+                                for (int q = 0; q < 4; ++q)
+                                    w[q] = pack_half2(__uint_as_float(ov[8 * k + 2 * q]), __uint_as_float(ov[8 * k + 2 * q + 1]));
                                 d[k] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         }
                     }
                 }
-                if (write) {
+                if (row_ok) {
                     const float v = none ? -INFINITY : (m_run - kLift + fast_log2(l_run)) * kLn2;
-                    if (split)
+                    if (s.part >= 0)
                         p.part_lse[part_row] = v;
                     else if (p.lse != nullptr)
                         p.lse[out_row] = v;
                 }
+                tc_fence_before();   // (O is read: the next unit's first P, which follows, lets it be written)
+                give_back(i);
             }
         }
     }
@@ -1077,61 +1444,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// Merges a row's partials: weights exp(lse_p - max lse).  A warp per row; the parts that a row
-// has follow from its limit, so nothing is read of the others.
+// Joins the partials of the units that were cut: weights exp(lse_p - max lse).  blockIdx.x + 1
+// is the boundary between two shares; the first boundary inside a unit does the unit, whose
+// parts are then known: one of each share that its line meets and that holds tiles of it.
+// blockIdx.y and the warps take its rows, the lanes a row's dims.
+constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(128) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const __grid_constant__ PrefillParams p, int n_ctas) {
+    constexpr int kGroups = Geometry<D>::kGroups;
     pdl_wait();
-    const int64_t rows = p.n_tok * p.n_head;
     const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    const int64_t tok = r / p.n_head;
-    // the token's sequence: the last one that starts at or before it and ends after it
-    int seq = -1;
-    int64_t q0 = 0, end = 0;
-    for (int s0 = 0; s0 < p.n_seq && seq < 0; s0 += 32) {
-        const int s = s0 + lane;
-        int64_t a = 0, e = 0;
-        if (s < p.n_seq) {
-            a = clamp64(__ldg(p.offsets + s), 0, p.n_tok);
-            e = clamp64(__ldg(p.offsets + s + 1), a, p.n_tok);
+    const int64_t total = total_of<D>(p);
+    const int c = blockIdx.x + 1;
+    const int64_t at = share_of(total, c, n_ctas);
+    if (at >= total) return;
+    const Place r = place_of<D>(p, at);
+    if (at == r.start || share_of(total, c - 1, n_ctas) > r.start) return;
+    Seg s;
+    const int64_t tok0 = r.block * p.block_tokens;
+    const int64_t left = r.x.n_q - tok0;
+    const int64_t tiles = tiles_seen(r.x.len - r.x.n_q + 1 + tok0, left < p.block_tokens ? left : p.block_tokens);
+    make_seg<D>(p, r.x, r.seq, r.g, r.block, 0, tiles, -1, s);
+    // the shares that meet the unit: c - 1 .. last
+    int last = c;
+    while (last + 1 < n_ctas && share_of(total, last + 1, n_ctas) < r.end) ++last;
+    const int n_parts = last - c + 2;
+    // part i's slot, -1: it holds no tile; whole: it holds them all and has written the result
+    bool whole = false;
+    auto slot_of = [&](int i) -> int {
+        const int cta = c - 1 + i;
+        const int64_t x0 = share_of(total, cta, n_ctas), x1 = share_of(total, cta + 1, n_ctas);
+        const int64_t a = x0 > r.start ? x0 : r.start, b = x1 < r.end ? x1 : r.end;
+        int64_t first, end;
+        tiles_between(r, a, b, tiles, first, end);
+        if (first == 0 && end == tiles) whole = true;
+        return first == end ? -1 : 2 * cta + (a > r.start ? 0 : 1);
+    };
+    for (int i = 0; i < n_parts; ++i) slot_of(i);
+    if (whole) return;
+    const int G = p.group;
+    const int step = kMergeWarps * gridDim.y;
+    for (int row = (int)blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < 128 * kGroups; row += step) {
+        const int grp = row >> 7, in = row & 127;
+        const int tok_in = in / G, tok = grp * p.group_tokens + tok_in;
+        if (tok_in >= p.group_tokens || tok >= s.n_tok) continue;
+        float m = -INFINITY;
+        for (int i = 0; i < n_parts; ++i) {
+            const int sl = slot_of(i);
+            if (sl < 0) continue;
+            const float v = p.part_lse[(int64_t)sl * kGroups * 128 + row];
+            m = v > m || v != v ? v : m;  // (a NaN stays)
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, tok >= a && tok < e);
-        if (hit != 0u) {
-            const int l = __ffs(hit) - 1;
-            seq = s0 + l;
-            q0 = __shfl_sync(0xffffffffu, a, l);
-            end = __shfl_sync(0xffffffffu, e, l);
-        }
-    }
-    if (seq < 0) return;  // a row behind the last sequence stays as it was
-    const int64_t cap = p.plan != nullptr ? p.plan_stride : p.n_cells;
-    int64_t L = clamp64(__ldg(p.seq_lens + seq), 0, p.max_len);
-    L = L < cap ? L : cap;
-    const int64_t lim = L - (end - q0) + 1 + (tok - q0);
-    int64_t parts = lim > 0 ? ((lim + kPrefillTile - 1) / kPrefillTile + p.split_tiles - 1) / p.split_tiles : 0;
-    if (parts > p.n_split) parts = p.n_split;
-    // maximum and weights' sum over the parts, a lane each
-    float m = -INFINITY;
-    for (int64_t i = lane; i < parts; i += 32) {
-        const float v = p.part_lse[i * rows + r];
-        m = v > m || v != v ? v : m;  // (a NaN stays)
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float v = __shfl_xor_sync(0xffffffffu, m, o);
-        m = v > m || v != v ? v : m;
-    }
-    float acc[D / 32] = {};
-    float total = 0.f;
-    if (m != -INFINITY) {
-        for (int64_t i = 0; i < parts; ++i) {
-            const float v = p.part_lse[i * rows + r];
+        float acc[D / 32] = {};
+        float sum = 0.f;
+        for (int i = 0; i < n_parts; ++i) {
+            const int sl = slot_of(i);
+            if (sl < 0) continue;
+            const float v = p.part_lse[(int64_t)sl * kGroups * 128 + row];
             if (v == -INFINITY) continue;
             const float w = exp2f((v - m) * 1.4426950408889634f);
-            total += w;
-            const float4* o = reinterpret_cast<const float4*>(p.part_o + (i * rows + r) * D);
+            sum += w;
+            const float4* o = reinterpret_cast<const float4*>(p.part_o + ((int64_t)sl * kGroups * 128 + row) * D);
 #pragma unroll
             for (int k = 0; k < D / 128; ++k) {
                 const float4 f = o[32 * k + lane];
@@ -1141,14 +1514,15 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const __grid_constan
                 acc[4 * k + 3] += w * f.w;
             }
         }
-    }
-    const float inv = m == -INFINITY ? 0.f : 1.f / total;
-    uint2* d = reinterpret_cast<uint2*>(p.out + r * D);
+        const float inv = m == -INFINITY ? 0.f : 1.f / sum;
+        const int64_t out_row = (s.q_tok + tok) * p.n_head + s.g * G + (in - tok_in * G);
+        uint2* d = reinterpret_cast<uint2*>(p.out + out_row * D);
 #pragma unroll
-    for (int k = 0; k < D / 128; ++k)
-        d[32 * k + lane] = make_uint2(pack_half2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
-                                      pack_half2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-    if (lane == 0 && p.lse != nullptr) p.lse[r] = m == -INFINITY ? -INFINITY : m + logf(total);
+        for (int k = 0; k < D / 128; ++k)
+            d[32 * k + lane] = make_uint2(pack_half2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                                          pack_half2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+        if (lane == 0 && p.lse != nullptr) p.lse[out_row] = m == -INFINITY ? -INFINITY : m + logf(sum);
+    }
 }
 
 template <int D>
@@ -1159,6 +1533,9 @@ const void* kernel_of(int kv_type) {
     case KVATTN_KV_Q8_0_Q4_0: return (const void*)prefill_kernel<D, 8, 4>;
     default: return (const void*)prefill_kernel<D, 4, 4>;
     }
+}
+int smem_of(int kv_type) {
+    return kv_type == KVATTN_KV_F16 ? Memory<16>::kBytes : (kv_type == KVATTN_KV_Q4_0 ? Memory<4>::kBytes : Memory<8>::kBytes);
 }
 
 // Per device and kernel, once: its shared memory.
@@ -1172,15 +1549,15 @@ cudaError_t prefill_setup(int kv_type, int head_dim) {
     bool& d = done[dev & 63][kv_type][head_dim == 256];
     if (!d) {
         e = cudaFuncSetAttribute(head_dim == 128 ? kernel_of<128>(kv_type) : kernel_of<256>(kv_type),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(kv_type));
         d = e == cudaSuccess;
     }
     return e;
 }
 
-cudaError_t launch(const void* f, unsigned grid, unsigned threads, size_t smem, void** args, cudaStream_t stream, bool pdl) {
+cudaError_t launch(const void* f, dim3 grid, unsigned threads, size_t smem, void** args, cudaStream_t stream, bool pdl) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1194,22 +1571,16 @@ cudaError_t launch(const void* f, unsigned grid, unsigned threads, size_t smem, 
 
 }  // namespace
 
-cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, cudaStream_t stream, bool pdl) {
-    const cudaError_t e = prefill_setup(kv_type, head_dim);
+cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl) {
+    cudaError_t e = prefill_setup(kv_type, head_dim);
     if (e != cudaSuccess) return e;
-    const int64_t grid = (int64_t)p.n_blocks * p.n_head_kv * p.n_split;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    void* args[] = {const_cast<PrefillParams*>(&p)};
-    return launch(head_dim == 128 ? kernel_of<128>(kv_type) : kernel_of<256>(kv_type), (unsigned)grid, kThreads, kSmemBytes,
-                  args, stream, pdl);
-}
-
-cudaError_t launch_prefill_merge(const PrefillParams& p, int head_dim, cudaStream_t stream, bool pdl) {
-    const int64_t grid = (p.n_tok * p.n_head + 3) / 4;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    void* args[] = {const_cast<PrefillParams*>(&p)};
+    void* args[] = {const_cast<PrefillParams*>(&p), &n_ctas};
+    e = launch(head_dim == 128 ? kernel_of<128>(kv_type) : kernel_of<256>(kv_type), dim3((unsigned)n_ctas), kThreads,
+               (size_t)smem_of(kv_type), args, stream, pdl);
+    if (e != cudaSuccess || !p.shares || n_ctas < 2) return e;
+    // eight CTAs per boundary: 32 or 16 rows each, so that a merge of a few units fills the device
     return launch(head_dim == 128 ? (const void*)prefill_merge_kernel<128> : (const void*)prefill_merge_kernel<256>,
-                  (unsigned)grid, 128, 0, args, stream, pdl);
+                  dim3((unsigned)n_ctas - 1u, 8), 32 * kMergeWarps, 0, args, stream, pdl);
 }
 
 }  // namespace kvattn

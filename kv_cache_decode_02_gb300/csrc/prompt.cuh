@@ -39,7 +39,7 @@ cudaError_t launch_cache_read(const CacheIoParams& p, int kv_type, cudaStream_t 
 // ---- causal attention of packed query tokens ----
 struct PrefillParams {
     CUtensorMap tmap_k, tmap_v;  // 3-D {head_dim, KV heads, cells}, boxes {64, 1, 128} (use_tma)
-    const __half* q;          // [n_tok] rows of n_head x head_dim, token stride q_stride
+    CUtensorMap tmap_q;       // 3-D {head_dim, heads, tokens}, boxes {64, group, group_tokens}
     const void* k;            // f16: rows k_stride elements apart; quantised: dense planes
     const void* v;
     const __half* k_scale;
@@ -49,29 +49,31 @@ struct PrefillParams {
     const int32_t* seq_lens;  // null: a sequence's cells are its own tokens
     __half* out;              // [n_tok][n_head][head_dim]
     float* lse;               // nullable: [n_tok][n_head]
-    float* part_o;            // [n_split][n_tok * n_head][head_dim], when n_split > 1
-    float* part_lse;          // [n_split][n_tok * n_head]
+    float* part_o;            // [2 CTAs][row groups][128][head_dim], when shares
+    float* part_lse;          // [2 CTAs][row groups][128]
     uint32_t* status;
-    int64_t q_stride, k_stride, v_stride;
+    int64_t k_stride, v_stride;
     int64_t n_tok, n_cells, plan_stride, max_len;
     uint64_t wait_limit_ns;
     uint32_t stall_tx;        // test hook: extra bytes expected on the first slot (never arrive)
     int n_seq, n_head, n_head_kv, group;
-    int n_split, split_tiles; // partials per row and 128-cell tiles per partial
-    int n_blocks;             // upper bound of the row blocks of all sequences
+    int group_tokens;         // tokens of a row group: floor(128 / group)
+    int block_tokens;         // tokens of a unit: two row groups at head_dim 128, one at 256
+    int shares;               // 1: equal shares of all units' tiles, cut anywhere; 0: whole units
     int use_tma;
     float scale_log2;         // scale * log2(e)
 };
 constexpr int kPrefillTile = 128;  // cells per tile
-// query rows (token, query head of the KV head) of one work unit
-inline int prefill_block_rows(int head_dim) { return head_dim == 128 ? 256 : 128; }
-cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, cudaStream_t stream, bool pdl);
-cudaError_t launch_prefill_merge(const PrefillParams& p, int head_dim, cudaStream_t stream, bool pdl);
+inline int prefill_groups(int head_dim) { return head_dim == 128 ? 2 : 1; }
+// The attention kernel on n_ctas CTAs (at most one per SM) and, with shares, the merge.
+cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl);
 
-// From api.cu: the 3-D map of half rows for launch_prefill, SM count, log switch and line,
-// the programmatic-launch switch.
-bool encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int head_dim,
-                        int64_t row_stride);
+// From api.cu: a 3-D map {head_dim, heads, rows} of half rows with boxes {64, box_heads, box_rows}
+// and the 128-byte swizzle, SM count, log switch and line, the programmatic-launch switch, the
+// limit on waits and its test hook.
+bool encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head, int head_dim, int64_t row_stride,
+                        int box_heads, int box_rows);
+bool tma_enabled();
 int device_sms();
 bool log_enabled();
 void log_text(const char* text);

@@ -1,8 +1,9 @@
-// C entry points of the prompt-side operators: host-side validation, the split choice of chunk
-// attention, workspace carving and launch order.
+// C entry points of the prompt-side operators: host-side validation, how attention's
+// work is cut, workspace carving and launches.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
 
 #include "prompt.cuh"
 
@@ -16,7 +17,6 @@ bool known_type(int t) { return t >= KVATTN_KV_F16 && t <= KVATTN_KV_Q4_0; }
 bool known_dim(int d) { return d == 128 || d == 256; }
 
 constexpr int kMaxPrefillGroup = 128;
-constexpr int64_t kMaxParts = 64;
 
 // Half rows of n_head x head_dim elements, `stride` elements apart: 16-byte pieces.
 bool row_ok(const void* p, int64_t stride, int64_t n_head, int head_dim) {
@@ -31,56 +31,76 @@ int check_cache(int kv_type, const void* k, const void* v, const void* ks, const
     return ks != nullptr && vs != nullptr && aligned(ks, sa) && aligned(vs, sa) ? KVATTN_OK : KVATTN_ERR_INVALID_ARG;
 }
 
-// Row blocks of the sequences together: at most one is part-filled per sequence.
-int64_t block_bound(int64_t n_tok, int n_seq, int group, int head_dim) {
-    const int64_t r = prefill_block_rows(head_dim);
-    return std::min((n_tok * group + r - 1) / r + std::max(n_seq - 1, 0), n_tok);
+// Units of all sequences together: at most one part-filled block per sequence.
+int64_t unit_bound(int64_t n_tok, int n_seq, int n_head_kv, int group, int head_dim) {
+    const int64_t per = (int64_t)(128 / group) * prefill_groups(head_dim);
+    return std::min((n_tok + per - 1) / per + std::max(n_seq - 1, 0), n_tok) * n_head_kv;
 }
 
-// Parts that the cells are cut into when the row blocks alone leave SMs idle, in 128-cell
-// tiles per part: the count whose waves x (tiles per part + a unit's fixed cost) is least,
-// where more parts also cost their partials' bytes.  In units of one tile's time (about 1.1 us
-// with 256 rows at head_dim 128): 3 tiles to start and end a unit, 4 for the merge's launch,
-// and the partials at about 4 MB per tile's time.
-int64_t choose_tiles(int64_t blocks, int n_head_kv, int64_t tiles, int64_t n_tok, int n_head, int head_dim, int sms) {
-    if (tiles <= 1) return std::max<int64_t>(tiles, 1);
-    double best = 0;
-    int64_t best_tiles = tiles;
-    for (int64_t parts = 1; parts <= std::min<int64_t>(tiles, kMaxParts); ++parts) {
-        const int64_t per = (tiles + parts - 1) / parts;
-        const int64_t n = (tiles + per - 1) / per;
-        if (n != parts) continue;
-        const int64_t waves = (blocks * n_head_kv * n + sms - 1) / sms;
-        double cost = (double)waves * (double)(per + 3);
-        if (n > 1) cost += 4.0 + (double)n * (double)n_tok * n_head * head_dim * 8.0 / 4.0e6;
-        if (parts == 1 || cost < best) {
-            best = cost;
-            best_tiles = per;
-        }
-    }
-    return best_tiles;
-}
-
-struct ChunkPlan {
-    int64_t blocks, tiles, n_split;
+// How a call's work is cut.  Units that are many and short are dealt out whole; few or long ones
+// (chunks over long caches) are cut into equal shares, one per CTA: 16 units of 1024 tiles would
+// otherwise keep 16 of 152 SMs busy.  A share costs its CTA a partial (written and read once
+// more) and the call a merge, so a CTA gets at least four tiles' worth of the bound below.
+struct Cut {
+    bool shares;
+    int n_ctas;
     size_t lse_off, o_off, total;
 };
 
-// (the arguments are valid)
-ChunkPlan chunk_plan(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim, int64_t max_len, int split) {
-    ChunkPlan c = {};
-    c.blocks = block_bound(n_tok, n_seq, n_head / n_head_kv, head_dim);
-    const int64_t all = std::max<int64_t>((max_len + kPrefillTile - 1) / kPrefillTile, 1);
-    c.tiles = split > 0 ? std::min<int64_t>(split / kPrefillTile, all)
-                        : choose_tiles(c.blocks, n_head_kv, all, n_tok, n_head, head_dim, device_sms());
-    c.n_split = (all + c.tiles - 1) / c.tiles;
+constexpr int64_t kMinShareTiles = 4;
+
+Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share) {
+    Cut c = {};
+    // (KVATTN_PREFILL_CTAS: the CTAs that share the work, for tests; 0: dealt out whole)
+    const char* env = std::getenv("KVATTN_PREFILL_CTAS");
+    const int sms = device_sms();
+    c.shares = may_share && tiles > kMinShareTiles && units < 8 * (int64_t)sms;
+    int64_t n = units;
+    if (c.shares) n = std::max(units, (units * tiles + kMinShareTiles - 1) / kMinShareTiles);
+    c.n_ctas = (int)std::max<int64_t>(std::min<int64_t>(n, sms), 1);
+    if (may_share && env != nullptr && *env != 0) {
+        const int want = std::atoi(env);
+        c.shares = want > 0;
+        c.n_ctas = std::max(std::min(want > 0 ? want : c.n_ctas, sms), 1);
+    }
+    if (c.n_ctas == 1) c.shares = false;
     size_t off = kStatusBytes;
+    const size_t rows = c.shares ? (size_t)c.n_ctas * 2 * (size_t)prefill_groups(head_dim) * 128 : 0;
     c.lse_off = off;
-    const size_t rows = c.n_split > 1 ? (size_t)c.n_split * (size_t)n_tok * (size_t)n_head : 0;
     off = align_up(off + rows * 4, kWsAlign);
     c.o_off = off;
     c.total = align_up(off + rows * (size_t)head_dim * 4, kWsAlign);
     return c;
+}
+
+Cut chunk_cut(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim, int64_t max_len) {
+    return cut_of(unit_bound(n_tok, n_seq, n_head_kv, n_head / n_head_kv, head_dim),
+                  (max_len + kPrefillTile - 1) / kPrefillTile, head_dim, true);
+}
+
+// What the two attention entry points have in common.
+int launch_attention(PrefillParams& p, const void* q, int64_t q_stride, int kv_type, int n_head, int n_head_kv, int head_dim,
+                     int64_t rows, float scale, const Cut& c, const char* name, void* stream) {
+    p.n_head = n_head;
+    p.n_head_kv = n_head_kv;
+    p.group = n_head / n_head_kv;
+    p.group_tokens = 128 / p.group;
+    p.block_tokens = p.group_tokens * prefill_groups(head_dim);
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    p.shares = c.shares ? 1 : 0;
+    debug_waits(&p.wait_limit_ns, &p.stall_tx);
+    if (!encode_prefill_map(&p.tmap_q, q, p.n_tok, n_head, head_dim, q_stride, p.group, p.group_tokens)) return KVATTN_ERR_CUDA;
+    p.use_tma = kv_type == KVATTN_KV_F16 && tma_enabled() &&
+                encode_prefill_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim, p.k_stride, 1, kPrefillTile) &&
+                encode_prefill_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim, p.v_stride, 1, kPrefillTile);
+    if (log_enabled()) {
+        char buf[256];
+        std::snprintf(buf, sizeof(buf), "%s kv_type=%d n_seq=%d n_tok=%lld n_head=%d/%d head_dim=%d plan=%d shares=%d grid=%d tma=%d",
+                      name, kv_type, p.n_seq, (long long)p.n_tok, n_head, n_head_kv, head_dim, p.plan != nullptr, p.shares,
+                      c.n_ctas, p.use_tma);
+        log_text(buf);
+    }
+    return cuda_status(launch_prefill(p, kv_type, head_dim, c.n_ctas, static_cast<cudaStream_t>(stream), pdl_enabled()));
 }
 
 int check_heads(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim) {
@@ -224,60 +244,41 @@ int kvattn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_str
         !aligned(out, 16) || !aligned(lse, 4) || ws == nullptr || !aligned(ws, kWsAlign))
         return KVATTN_ERR_INVALID_ARG;
     if (ws_bytes < kStatusBytes) return KVATTN_ERR_WORKSPACE;
+    const int64_t units = unit_bound(n_tok, n_seq, n_head_kv, n_head / n_head_kv, head_dim);
+    if (units > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
     PrefillParams p = {};
-    p.q = static_cast<const __half*>(q);
     p.k = k;
     p.v = v;
     p.offsets = offsets;
     p.out = static_cast<__half*>(out);
     p.lse = lse;
     p.status = static_cast<uint32_t*>(ws);
-    p.q_stride = q_stride;
     p.k_stride = k_stride;
     p.v_stride = v_stride;
     p.n_tok = n_tok;
     p.n_cells = n_tok;
     p.max_len = n_tok;
     p.n_seq = n_seq;
-    p.n_head = n_head;
-    p.n_head_kv = n_head_kv;
-    p.group = n_head / n_head_kv;
-    p.n_split = 1;
-    p.split_tiles = INT32_MAX / kPrefillTile;
-    const int64_t blocks = block_bound(n_tok, n_seq, p.group, head_dim);
-    if (blocks * n_head_kv > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
-    p.n_blocks = (int)blocks;
-    p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-    debug_waits(&p.wait_limit_ns, &p.stall_tx);
-    p.use_tma = encode_prefill_map(&p.tmap_k, k, n_tok, n_head_kv, head_dim, k_stride) &&
-                encode_prefill_map(&p.tmap_v, v, n_tok, n_head_kv, head_dim, v_stride);
-    if (log_enabled()) {
-        char buf[256];
-        std::snprintf(buf, sizeof(buf), "prefill n_seq=%d n_tok=%lld n_head=%d/%d head_dim=%d blocks=%d grid=%lld tma=%d", n_seq,
-                      (long long)n_tok, n_head, n_head_kv, head_dim, p.n_blocks, (long long)(blocks * n_head_kv), p.use_tma);
-        log_text(buf);
-    }
-    return cuda_status(launch_prefill(p, KVATTN_KV_F16, head_dim, static_cast<cudaStream_t>(stream), pdl_enabled()));
+    return launch_attention(p, q, q_stride, KVATTN_KV_F16, n_head, n_head_kv, head_dim, n_tok, scale,
+                            cut_of(units, 1, head_dim, false), "prefill", stream);
 }
 
 size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim,
-                                            int64_t max_len, int split) {
-    if (check_heads(n_tok, n_seq, n_head, n_head_kv, head_dim) != KVATTN_OK || max_len < 0 || max_len > INT32_MAX ||
-        split < 0 || split % kPrefillTile != 0)
-        return 0;
-    return chunk_plan(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split).total;
+                                            int64_t max_len) {
+    if (check_heads(n_tok, n_seq, n_head, n_head_kv, head_dim) != KVATTN_OK || max_len < 0 || max_len > INT32_MAX) return 0;
+    return chunk_cut(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len).total;
 }
 
 int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets, int64_t n_tok, const void* k_cache,
                          const void* v_cache, const void* k_scales, const void* v_scales, int kv_type, int64_t n_cells,
                          const int32_t* cell_plan, int64_t plan_stride, const int32_t* seq_lens, int n_seq,
-                         int64_t max_len, int n_head, int n_head_kv, int head_dim, int split, float scale, void* out,
-                         float* lse, void* ws, size_t ws_bytes, void* stream) {
+                         int64_t max_len, int n_head, int n_head_kv, int head_dim, float scale, void* out, float* lse,
+                         void* ws, size_t ws_bytes, void* stream) {
     int st = check_heads(n_tok, n_seq, n_head, n_head_kv, head_dim);
     if (st != KVATTN_OK) return st;
-    if (max_len < 0 || split < 0 || n_cells < 1 || !std::isfinite(scale) || (cell_plan != nullptr && plan_stride < 1))
+    if (max_len < 0 || n_cells < 1 || !std::isfinite(scale) || (cell_plan != nullptr && plan_stride < 1))
         return KVATTN_ERR_INVALID_ARG;
-    if (max_len > INT32_MAX || split % kPrefillTile != 0) return KVATTN_ERR_UNSUPPORTED;
+    if (max_len > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
     st = check_cache(kv_type, k_cache, v_cache, k_scales, v_scales, head_dim);
     if (st != KVATTN_OK) return st;
     if (n_tok == 0 || n_seq == 0) return KVATTN_OK;
@@ -285,11 +286,10 @@ int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets
         !aligned(seq_lens, 4) || !aligned(cell_plan, 4) || out == nullptr || !aligned(out, 16) || !aligned(lse, 4) ||
         ws == nullptr || !aligned(ws, kWsAlign))
         return KVATTN_ERR_INVALID_ARG;
-    const ChunkPlan c = chunk_plan(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split);
-    if (c.blocks * n_head_kv * c.n_split > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
+    const Cut c = chunk_cut(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len);
+    if (unit_bound(n_tok, n_seq, n_head_kv, n_head / n_head_kv, head_dim) > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
     if (ws_bytes < c.total) return KVATTN_ERR_WORKSPACE;
     PrefillParams p = {};
-    p.q = static_cast<const __half*>(q);
     p.k = k_cache;
     p.v = v_cache;
     p.k_scale = static_cast<const __half*>(k_scales);
@@ -303,40 +303,14 @@ int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets
     p.status = reinterpret_cast<uint32_t*>(wsb);
     p.part_lse = reinterpret_cast<float*>(wsb + c.lse_off);
     p.part_o = reinterpret_cast<float*>(wsb + c.o_off);
-    p.q_stride = q_stride;
     p.k_stride = p.v_stride = (int64_t)n_head_kv * head_dim;
     p.n_tok = n_tok;
     p.n_cells = n_cells;
     p.plan_stride = plan_stride;
     p.max_len = max_len;
     p.n_seq = n_seq;
-    p.n_head = n_head;
-    p.n_head_kv = n_head_kv;
-    p.group = n_head / n_head_kv;
-    p.n_split = (int)c.n_split;
-    p.split_tiles = (int)c.tiles;
-    p.n_blocks = (int)c.blocks;
-    p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-    debug_waits(&p.wait_limit_ns, &p.stall_tx);
-    if (kv_type == KVATTN_KV_F16) {
-        const int64_t cells = cell_plan != nullptr ? n_cells : n_cells * n_seq;
-        p.use_tma = encode_prefill_map(&p.tmap_k, k_cache, cells, n_head_kv, head_dim, p.k_stride) &&
-                    encode_prefill_map(&p.tmap_v, v_cache, cells, n_head_kv, head_dim, p.v_stride);
-    }
-    if (log_enabled()) {
-        char buf[256];
-        std::snprintf(buf, sizeof(buf),
-                      "prefill_chunk kv_type=%d n_seq=%d n_tok=%lld n_head=%d/%d head_dim=%d max_len=%lld split=%lld n_split=%d "
-                      "plan=%d blocks=%d grid=%lld tma=%d",
-                      kv_type, n_seq, (long long)n_tok, n_head, n_head_kv, head_dim, (long long)max_len,
-                      (long long)c.tiles * kPrefillTile, p.n_split, cell_plan != nullptr, p.n_blocks,
-                      (long long)(c.blocks * n_head_kv * c.n_split), p.use_tma);
-        log_text(buf);
-    }
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_prefill(p, kv_type, head_dim, s, pdl_enabled());
-    if (e == cudaSuccess && p.n_split > 1) e = launch_prefill_merge(p, head_dim, s, pdl_enabled());
-    return cuda_status(e);
+    return launch_attention(p, q, q_stride, kv_type, n_head, n_head_kv, head_dim, cell_plan != nullptr ? n_cells : n_cells * n_seq,
+                            scale, c, "prefill_chunk", stream);
 }
 
 }  // extern "C"

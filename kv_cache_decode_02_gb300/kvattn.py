@@ -124,10 +124,10 @@ lib.kvattn_prefill_workspace_bytes.argtypes = [_I64, _I, _I, _I, _I]
 lib.kvattn_prefill_workspace_bytes.restype = _SZ
 lib.kvattn_prefill.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]
 lib.kvattn_prefill.restype = _I
-lib.kvattn_prefill_chunk_workspace_bytes.argtypes = [_I64, _I, _I, _I, _I, _I64, _I]
+lib.kvattn_prefill_chunk_workspace_bytes.argtypes = [_I64, _I, _I, _I, _I, _I64]
 lib.kvattn_prefill_chunk_workspace_bytes.restype = _SZ
-lib.kvattn_prefill_chunk.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _I,
-                                     _F, _P, _P, _P, _SZ, _P]
+lib.kvattn_prefill_chunk.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _F,
+                                     _P, _P, _P, _SZ, _P]
 lib.kvattn_prefill_chunk.restype = _I
 
 
@@ -379,16 +379,16 @@ def kvattn_prefill(q, q_stride, k, k_stride, v, v_stride, offsets, n_seq, n_tok,
     _check(rc, "kvattn_prefill")
 
 
-def kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split) -> int:
-    return lib.kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split)
+def kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len) -> int:
+    return lib.kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len)
 
 
 def kvattn_prefill_chunk(q, q_stride, offsets, n_tok, k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, cell_plan,
-                         plan_stride, seq_lens, n_seq, max_len, n_head, n_head_kv, head_dim, split, scale, out, lse, ws,
+                         plan_stride, seq_lens, n_seq, max_len, n_head, n_head_kv, head_dim, scale, out, lse, ws,
                          ws_bytes, stream=None):
     rc = lib.kvattn_prefill_chunk(_ptr(q), q_stride, _ptr(offsets), n_tok, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
                                   _ptr(v_scales), kv_type, n_cells, _ptr(cell_plan), plan_stride, _ptr(seq_lens), n_seq,
-                                  max_len, n_head, n_head_kv, head_dim, split, scale, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                  max_len, n_head, n_head_kv, head_dim, scale, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
                                   _stream(stream))
     _check(rc, "kvattn_prefill_chunk")
 
@@ -668,14 +668,14 @@ def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream
     return out, lse
 
 
-def prefill_chunk_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split=0, device="cuda"):
+def prefill_chunk_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, device="cuda"):
     import torch
-    nbytes = kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, split)
+    nbytes = kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len)
     return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cells=None, cell_plan=None, k_scales=None,
-                  v_scales=None, split=0, scale=None, out=None, lse=None, ws=None, stream=None):
+                  v_scales=None, scale=None, out=None, lse=None, ws=None, stream=None):
     """Causal attention of new tokens over caches that hold their cells: q half [T][H][D] (the
     sequences' tokens packed, offsets int32 [S + 1]), the cache as in decode: one unified cache with
     a ``cell_plan`` (int32 [S][stride]), a per-sequence [S][N][Hk][D] cache, or one [cells][Hk][D]
@@ -702,9 +702,9 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     if lse is not None:
         _new_out(lse, "lse", (T, H), q, torch.float32)
     if ws is None:
-        ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, split, q.device)
+        ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, q.device)
     kvattn_prefill_chunk(q, qs, offsets, T, k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, cell_plan, stride, seq_lens,
-                         S, max_len, H, Hk, D, split, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws, ws.numel(),
+                         S, max_len, H, Hk, D, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws, ws.numel(),
                          stream)
     return out, lse
 

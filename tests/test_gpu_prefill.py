@@ -150,6 +150,17 @@ def make_chunk(kind, new, lens, H, Hk, D, plan, holes=0.0, seed=3, spare=2):
     return c
 
 
+@pytest.fixture
+def ctas(monkeypatch):
+    """Sets how many CTAs share a chunk call's work (None: the library's choice, 0: whole units)."""
+    def set_(n):
+        if n is None:
+            monkeypatch.delenv("KVATTN_PREFILL_CTAS", raising=False)
+        else:
+            monkeypatch.setenv("KVATTN_PREFILL_CTAS", str(n))
+    return set_
+
+
 def call_chunk(kv, c, lse=True, **kw):
     T, H, D = c["q"].shape
     out = torch.full((T, H, D), 7.0, dtype=torch.float16, device="cuda")
@@ -189,45 +200,88 @@ def check_chunk(kv, c, **kw):
     return out, lse
 
 
-@pytest.mark.parametrize("split", [0, 128, 384])
+@pytest.mark.parametrize("n", [None, 0, 5, 37])
 @pytest.mark.parametrize("plan,holes", [(False, 0.0), (True, 0.0), (True, 0.3)])
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("kind", KINDS)
-def test_chunk_kinds(kvattn, kind, D, plan, holes, split):
+def test_chunk_kinds(kvattn, ctas, kind, D, plan, holes, n):
     c = make_chunk(kind, [70, 1, 0, 33], [700, 513, 0, 33], 8, 2, D, plan, holes)
-    check_chunk(kvattn, c, split=split)
+    ctas(n)
+    check_chunk(kvattn, c)
 
 
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("new,lens", [([1], [1]), ([1], [128]), ([1], [129]), ([3], [2]), ([200], [150]), ([300], [300]),
                                       ([128, 128], [128, 256]), ([5, 6, 7], [0, 6, 1000]), ([260], [1500])])
-def test_chunk_lengths(kvattn, new, lens, D):
+def test_chunk_lengths(kvattn, ctas, new, lens, D):
     check_chunk(kvattn, make_chunk("f16", new, lens, 6, 2, D, False))
-    check_chunk(kvattn, make_chunk("q8_0", new, lens, 6, 2, D, True, 0.1), split=256)
+    ctas(11)
+    check_chunk(kvattn, make_chunk("q8_0", new, lens, 6, 2, D, True, 0.1))
 
 
 @pytest.mark.parametrize("H,Hk", [(1, 1), (5, 1), (16, 2), (7, 7), (48, 3)])
-def test_chunk_heads(kvattn, H, Hk):
+def test_chunk_heads(kvattn, ctas, H, Hk):
     check_chunk(kvattn, make_chunk("f16", [50, 90], [400, 90], H, Hk, 128, True, 0.1))
-    check_chunk(kvattn, make_chunk("q4_0", [50, 90], [400, 90], H, Hk, 128, False), split=128)
+    ctas(13)
+    check_chunk(kvattn, make_chunk("q4_0", [50, 90], [400, 90], H, Hk, 128, False))
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_chunk_all_holes_and_scales(kvattn, kind):
+def test_chunk_all_holes_and_scales(kvattn, ctas, kind):
     c = make_chunk(kind, [40], [600], 4, 2, 128, True, 0.2)
     c["plan"][0, :256] = -1          # whole tiles of holes
     check_chunk(kvattn, c)
-    check_chunk(kvattn, c, split=128, scale=-0.05)
+    ctas(9)
+    check_chunk(kvattn, c, scale=-0.05)
     c["plan"][:] = -1                # nothing to see at all
-    out, lse = call_chunk(kvattn, c)
-    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
-    out, lse = call_chunk(kvattn, c, split=128)
-    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    for n in (9, 0):
+        ctas(n)
+        out, lse = call_chunk(kvattn, c)
+        assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_chunk_cells_in_any_order(kvattn, ctas, D):
+    """Plans whose tiles are no run of cells: entries shuffled, with and without holes."""
+    g = U.gen(9)
+    for kind in ("f16", "q8_0"):
+        c = make_chunk(kind, [90, 5], [500, 300], 4, 2, D, True, 0.2)
+        for s, n in enumerate(c["L"]):
+            c["plan"][s, :n] = c["plan"][s, torch.randperm(n, generator=g, device="cuda")]
+        check_chunk(kvattn, c)
+        ctas(7)
+        check_chunk(kvattn, c)
+        ctas(None)
+
+
+def test_without_tensor_maps(kvattn):
+    """KVATTN_TMA=0: K and V by ordinary loads (read once per process, so in a child of its own)."""
+    import subprocess
+    import sys
+    code = ("from kv_cache_decode_02_gb300 import kvattn as K\n"
+            "from tests import test_gpu_prefill as t\n"
+            "t.check_prefill(K, [300, 70], 8, 2, 128)\n"
+            "t.check_chunk(K, t.make_chunk('f16', [60], [400], 4, 1, 256, True, 0.1))\n")
+    import os
+    r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, KVATTN_TMA="0"), capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_results_do_not_depend_on_how_the_work_is_cut(kvattn, ctas):
+    c = make_chunk("f16", [130, 1, 40], [3000, 2000, 40], 8, 2, 128, True, 0.1)
+    got = []
+    for n in (0, 2, 5, 40, 150):
+        ctas(n)
+        got.append(check_chunk(kvattn, c))
+        again = call_chunk(kvattn, c)
+        assert torch.equal(got[-1][0], again[0]) and torch.equal(got[-1][1], again[1])
 
 
 @pytest.mark.parametrize("kind", ["f16", "q8_0", "q4_0"])
-@pytest.mark.parametrize("split", [0, 128])
-def test_chunk_values_that_are_not_finite(kvattn, kind, split):
+@pytest.mark.parametrize("n", [0, 6])
+def test_chunk_values_that_are_not_finite(kvattn, ctas, kind, n):
+    ctas(n)
     # in cells that only the later new tokens see
     c = make_chunk(kind, [60], [500], 4, 1, 128, False)
     if kind == "f16":
@@ -236,7 +290,7 @@ def test_chunk_values_that_are_not_finite(kvattn, kind, split):
     else:
         c["vs"][470, 0, 1] = float("nan")
         c["vs"][495, 0, 3] = float("nan")
-    check_chunk(kvattn, c, split=split)
+    check_chunk(kvattn, c)
 
 
 def test_chunk_agrees_with_decode(kvattn):
@@ -251,14 +305,15 @@ def test_chunk_agrees_with_decode(kvattn):
     assert float((lse[some] - wl[some]).abs().max()) <= 2e-4
 
 
-def test_chunk_of_a_whole_prompt_agrees_with_prefill(kvattn):
+def test_chunk_of_a_whole_prompt_agrees_with_prefill(kvattn, ctas):
+    ctas(0)
     g = U.gen(5)
     T, H, Hk, D = 600, 8, 2, 128
     q, k, v = U.halves(g, T, H, D), U.halves(g, T, Hk, D), U.halves(g, T, Hk, D)
     off = U.ints([0, T])
     a, la = kvattn.prefill(q, k, v, off)
     lse = torch.empty((T, H), dtype=torch.float32, device="cuda")
-    b, lb = kvattn.prefill_chunk(q, off, k, v, U.ints([T]), split=640, lse=lse)
+    b, lb = kvattn.prefill_chunk(q, off, k, v, U.ints([T]), lse=lse)
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(la, lb)         # the same tiles in the same order
 
@@ -306,8 +361,8 @@ def test_prefill_in_a_graph_on_another_stream(kvattn):
     ws = kvattn.prefill_workspace(T, 2, H, Hk, D)
     want, _ = kvattn.prefill(q, k, v, off)
     c = make_chunk("q8_0", [70], [3000], 8, 2, 128, False)
-    cws = kvattn.prefill_chunk_workspace(70, 1, 8, 2, 128, 3000, 256)
-    cwant, clse = call_chunk(kvattn, c, split=256)
+    cws = kvattn.prefill_chunk_workspace(70, 1, 8, 2, 128, 3000)
+    cwant, clse = call_chunk(kvattn, c)
     out, lse = torch.zeros_like(want), torch.zeros((T, H), dtype=torch.float32, device="cuda")
     cout, cl = torch.zeros_like(cwant), torch.zeros_like(clse)
     side = torch.cuda.Stream()
@@ -316,7 +371,7 @@ def test_prefill_in_a_graph_on_another_stream(kvattn):
     with torch.cuda.graph(graph, stream=side):
         kvattn.prefill(q, k, v, off, out=out, lse=lse, ws=ws)
         kvattn.prefill_chunk(c["q"], c["offsets"], c["k"], c["v"], c["lens"], n_cells=c["n_cells"], k_scales=c["ks"],
-                             v_scales=c["vs"], max_len=3000, split=256, out=cout, lse=cl, ws=cws)
+                             v_scales=c["vs"], max_len=3000, out=cout, lse=cl, ws=cws)
     for _ in range(3):
         out.zero_()
         cout.zero_()
@@ -326,12 +381,12 @@ def test_prefill_in_a_graph_on_another_stream(kvattn):
     # two streams at once, a workspace each
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     outs = [torch.zeros_like(cwant) for _ in range(2)]
-    wss = [kvattn.prefill_chunk_workspace(70, 1, 8, 2, 128, 3000, 256) for _ in range(2)]
+    wss = [kvattn.prefill_chunk_workspace(70, 1, 8, 2, 128, 3000) for _ in range(2)]
     torch.cuda.synchronize()
     for _ in range(8):
         for st, o, w in ((s1, outs[0], wss[0]), (s2, outs[1], wss[1])):
             kvattn.prefill_chunk(c["q"], c["offsets"], c["k"], c["v"], c["lens"], n_cells=c["n_cells"], k_scales=c["ks"],
-                                 v_scales=c["vs"], max_len=3000, split=256, out=o, ws=w, stream=st)
+                                 v_scales=c["vs"], max_len=3000, out=o, ws=w, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(o, cwant) for o in outs)
 

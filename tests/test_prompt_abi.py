@@ -100,31 +100,30 @@ def test_prefill_refusals(kvattn, over, want):
 
 def chunk(kvattn, **over):
     a = dict(q=A, qs=4096, off=A, n_tok=100, k=A, v=A, ksc=None, vsc=None, kv_type=0, n_cells=4096, plan=None, stride=0, lens=A,
-             n_seq=2, max_len=4096, H=32, Hk=8, D=128, split=0, scale=0.1, out=A, lse=None, ws=A, ws_bytes=1 << 40, stream=None)
+             n_seq=2, max_len=4096, H=32, Hk=8, D=128, scale=0.1, out=A, lse=None, ws=A, ws_bytes=1 << 40, stream=None)
     a.update(over)
     return kvattn.lib.kvattn_prefill_chunk(*a.values())
 
 
 @pytest.mark.parametrize("over,want", [
-    (dict(D=64), UNS), (dict(H=30), INV), (dict(H=129, Hk=1), UNS), (dict(split=64), UNS), (dict(split=-128), INV),
+    (dict(D=64), UNS), (dict(H=30), INV), (dict(H=129, Hk=1), UNS), 
     (dict(max_len=-1), INV), (dict(max_len=1 << 31), UNS), (dict(n_cells=0), INV), (dict(plan=A), INV), (dict(plan=A + 2, stride=128), INV),
     (dict(kv_type=5), INV), (dict(kv_type=1), INV), (dict(ksc=A, vsc=A), INV), (dict(kv_type=1, ksc=A, vsc=A + 4), INV),
     (dict(k=None), INV), (dict(v=A + 8), INV), (dict(q=A + 2), INV), (dict(qs=4090), INV), (dict(off=None), INV),
     (dict(lens=None), INV), (dict(lens=A + 1), INV), (dict(out=A + 4), INV), (dict(ws=None), INV), (dict(scale=float("inf")), INV),
-    (dict(ws_bytes=0), WS), (dict(split=128, ws_bytes=100 * 32 * 128 * 4 * 32), WS), (dict(n_tok=0), 0), (dict(n_seq=0), 0),
+    (dict(ws_bytes=0), WS), (dict(n_tok=0), 0), (dict(n_seq=0), 0),
 ])
 def test_chunk_refusals(kvattn, over, want):
     assert chunk(kvattn, **over) == want
 
 
-def test_workspaces(kvattn):
+def test_workspaces(kvattn, monkeypatch):
     f, g = kvattn.kvattn_prefill_workspace_bytes, kvattn.kvattn_prefill_chunk_workspace_bytes
     assert f(100, 2, 32, 8, 128) == 256 and f(100, 2, 30, 8, 128) == 0 and f(100, 2, 32, 8, 96) == 0
-    assert g(100, 1, 32, 8, 128, 4096, 4096) == 256                  # one part: no partials
-    n = g(100, 1, 32, 8, 128, 4096, 128)                             # 32 parts of 3200 rows
-    assert n >= 32 * 3200 * (128 + 1) * 4 and n % 256 == 0
-    assert g(100, 1, 32, 8, 128, 4096, 64) == 0 and g(100, 1, 32, 8, 128, -1, 0) == 0
-    assert chunk(kvattn, n_seq=1, split=128, ws_bytes=n - 1) == WS
+    assert g(100, 1, 32, 8, 128, 128) == 256                         # units of one tile are not cut
+    assert g(100, 1, 32, 8, 128, -1) == 0 and g(100, 1, 32, 8, 128, 1 << 31) == 0 and g(100, 1, 31, 8, 128, 128) == 0
+    monkeypatch.setenv("KVATTN_PREFILL_CTAS", "0")
+    assert g(100, 1, 32, 8, 128, 1 << 20) == 256
 
 
 def test_wrapper_checks(kvattn):
