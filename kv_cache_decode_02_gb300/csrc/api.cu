@@ -288,6 +288,19 @@ bool kvattn::encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool kvattn::encode_codes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int row_bytes, int box_bytes,
+                              int box_rows) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (enc == nullptr || rows < 1 || rows > (int64_t)INT32_MAX || !aligned(base, 16)) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)n_head_kv, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)row_bytes * (cuuint64_t)n_head_kv};
+    const cuuint32_t box[3] = {(cuuint32_t)box_bytes, 1u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool kvattn::tma_enabled() { return use_tma_env(); }
 int kvattn::device_sms() { return sm_count(); }
 bool kvattn::log_enabled() { return log_on(); }

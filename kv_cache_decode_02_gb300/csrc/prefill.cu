@@ -31,8 +31,8 @@
 //  * loader (warps 8-11): fills a ring of 32 KB slots, each 128 cells x 128 dims of K or V in
 //    two 128-byte-swizzled planes.  f16: warp 8 issues TMA boxes for tiles whose cells are one
 //    physical run (holes and the end of a sequence included), warps 9-11 mend V tiles that need
-//    it, and all four copy tiles that are no run.  Quantised: every thread brings raw bytes into
-//    a ring of its own by cp.async, two slots ahead, and turns them into f16 in its slot.
+//    it, and all four copy tiles that are no run.  Quantised: warp 14 brings codes (TMA) and
+//    scales (cp.async) into a ring of raw bytes, and these four turn them into f16.
 //  * MMA (warp 12): one elected lane issues tcgen05.mma.  S of one row group is computed while
 //    the softmax of the other runs (head_dim 128: two S and two O accumulators fill the 512
 //    TMEM columns), or S of the next tile while the softmax of this one runs (256: two S and
@@ -74,7 +74,8 @@ constexpr int kCutTiles = 3;                  // tiles that only some of a unit'
 constexpr float kSlack = 8.f;                 // lazy maximum
 constexpr float kLift = 7.f;                  // p is scaled by 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int64_t kUnitCost = 2;              // a unit's fixed cost in tiles, for the equal shares
+constexpr uint32_t kNoMore = 0xffffffffu;
+constexpr int kUnitCost = 2;                  // a unit's fixed cost in tiles, for the equal shares
 
 // f16 slots in the ring: what the 227 KB hold beside the queries (64 KB) and, for quantised
 // caches, the raw ring (17 KB a stage with 8-bit rows, 9 KB with 4-bit ones)
@@ -102,6 +103,7 @@ struct Seg {
 struct Header {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t landed[kMaxSlots];  // the TMA of a V tile that is mended afterwards
+    uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // quantised: a slot's raw bytes; they are turned
     uint64_t q_full, q_empty;    // the unit's query rows; its last S is complete
     uint64_t s_full[2];          // S is in TMEM (of row group t, or of buffer b)
     uint64_t p_full[2];          // p is
@@ -114,6 +116,7 @@ struct Header {
     int abort_flag;
     uint32_t bad_cells[kRing][kCutTiles][4];  // of a unit: cells of its cut tiles with V that is not finite
     uint32_t holes[kRing];                    // whether the tile has any
+    uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | unit << 8
     Seg seg[kRing];
     alignas(16) float bias[kRing][kPrefillTile];  // through a plan: +inf, or -inf for a hole
 };
@@ -200,6 +203,32 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// arrives on bar when this thread's cp.async so far are complete (adds itself to the phase's
+// pending arrivals first: the phase must be held open by an arrival that comes later)
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Eight lanes that hold eight 16-byte pieces each of a row of their own: afterwards lane i of
+// them holds piece i of all eight rows (piece k from the k-th lane).
+__device__ __forceinline__ void turn_rows(uint32_t (&r)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k & s) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t& lo = r[4 * k + i];
+                uint32_t& hi = r[4 * (k | s) + i];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+                lo = up ? got : lo;
+                hi = up ? hi : got;
+            }
+        }
+    }
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -233,18 +262,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// Stored value = scale x code, rounded once to half: the type of an f16 cache (2^-11 of the
-// value, where the 8-bit code itself is off by up to 2^-8 of the block's largest).  Scales
-// above 515 could pass the largest half; those products are kept at it (as cache_read does).
-__device__ __forceinline__ uint32_t dequant(uint32_t codes, __half2 d, bool big) {
-    __half2 r = __hmul2_rn(as_h2(codes), d);
-    if (big) {
-        const __half2 top = __halves2half2(__ushort_as_half(0x7bffu), __ushort_as_half(0x7bffu));
-        r = __hmax2_nan(__hmin2_nan(r, top), __hneg2(top));
-    }
-    return as_u32(r);
-}
-__device__ __forceinline__ bool big_scale(uint32_t d) { return (d & 0x7fffu) > 0x6006u; }  // 515
 // a scale that is not finite makes its whole block NaN
 __device__ __forceinline__ __half2 scale2(uint32_t d) {
     if ((d & 0x7c00u) == 0x7c00u) d = 0x7fffu;
@@ -266,6 +283,25 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w, bool& bad) {
     return w;
 }
 
+// Stored value = scale x code, rounded once to half: the type of an f16 cache (2^-11 of the
+// value, where the 8-bit code itself is off by up to 2^-8 of the block's largest).  Scales
+// above 515 could pass the largest half; those products are kept at it (as cache_read does).  In
+// a cut tile what is not finite is dropped and its cell noted.
+template <int N>
+__device__ __forceinline__ void finish(uint32_t (&o)[N], uint32_t scale, bool cut, uint32_t* bad_row, int cell) {
+    if ((scale & 0x7fffu) > 0x6006u) {   // 515
+        const __half2 top = __halves2half2(__ushort_as_half(0x7bffu), __ushort_as_half(0x7bffu));
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(o[i]), top), __hneg2(top)));
+    }
+    if (cut) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = finite2(o[i], bad);
+        if (bad) atomicOr(&bad_row[cell >> 5], 1u << (cell & 31));
+    }
+}
+
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
 // ------------------------------------ work ------------------------------------
@@ -278,144 +314,153 @@ struct Geometry {
 
 // A sequence as the schedulers see it.
 struct Sequence {
-    int64_t q0, n_q, len;
-    int64_t blocks;
+    int32_t q0, n_q, len;
+    uint32_t blocks;
 };
-template <int D>
 __device__ __forceinline__ Sequence read_sequence(const PrefillParams& p, int s) {
     Sequence x = {};
     if (s < 0 || s >= p.n_seq) return x;
-    x.q0 = clamp64(__ldg(p.offsets + s), 0, p.n_tok);
-    x.n_q = clamp64(__ldg(p.offsets + s + 1), x.q0, p.n_tok) - x.q0;
+    const int32_t n_tok = (int32_t)p.n_tok;
+    const int32_t a = __ldg(p.offsets + s), e = __ldg(p.offsets + s + 1);
+    x.q0 = min(max(a, 0), n_tok);
+    x.n_q = min(max(e, x.q0), n_tok) - x.q0;
+    x.len = x.n_q;
     if (p.seq_lens != nullptr) {
         const int64_t cap = p.plan != nullptr ? p.plan_stride : p.n_cells;
-        const int64_t L = clamp64(__ldg(p.seq_lens + s), 0, p.max_len);
-        x.len = L < cap ? L : cap;
-    } else {
-        x.len = x.n_q;
+        x.len = (int32_t)clamp64(__ldg(p.seq_lens + s), 0, cap < p.max_len ? cap : p.max_len);
     }
-    x.blocks = (x.n_q + p.block_tokens - 1) / p.block_tokens;
+    x.blocks = ((uint32_t)x.n_q + (uint32_t)p.block_tokens - 1u) / (uint32_t)p.block_tokens;
     return x;
 }
-// Tiles that the block's first n tokens see.
-__device__ __forceinline__ int64_t tiles_seen(int64_t lim0, int64_t n) {
+// Tiles that the first n tokens of a block see.
+__device__ __forceinline__ int32_t tiles_seen(int64_t lim0, int32_t n) {
     const int64_t lim = n > 0 ? lim0 + n - 1 : 0;
-    return lim > 0 ? (lim + kPrefillTile - 1) / kPrefillTile : 0;
+    return lim > 0 ? (int32_t)((lim + kPrefillTile - 1) / kPrefillTile) : 0;
 }
 
-// The units of all sequences in one line, each as long as its work in cells (rounded to a rule
-// that is linear in the block's number, so that sums have a closed form), plus its fixed cost;
-// CTA c of n takes the part [share(c), share(c + 1)).  Order: sequence, KV head, block.
+// The units of all sequences in one line, in eighths of a tile: each a unit's fixed cost, then
+// its tiles (by a rule that is linear in the block's number, so that sums have a closed form; the
+// last share of a unit takes what is left).  CTA c of n takes [share(c), share(c + 1)) of it.
+// Order: sequence, KV head, block.  The host sees to it that the line fits 32 bits.
 struct Line {
-    int64_t a, step;   // length of block b: a + step b
-    __device__ __forceinline__ int64_t upto(int64_t b) const { return a * b + step * (b * (b - 1) / 2); }
+    uint32_t a, step;   // length of block b: a + step b
+    __device__ __forceinline__ uint32_t upto(uint32_t b) const { return a * b + step * (b * (b - 1u) / 2u); }
 };
 __device__ __forceinline__ Line line_of(const PrefillParams& p, const Sequence& x) {
-    const int64_t lim = x.len - x.n_q + 1;
-    return Line{kPrefillTile * kUnitCost + (lim > 1 ? lim : 1) + p.block_tokens - 1, p.block_tokens};
+    const int32_t lim = max(x.len - x.n_q, 0) + min(x.n_q, p.block_tokens);  // of the first block's last token, or above
+    return Line{8u * (uint32_t)(kUnitCost + (lim + kPrefillTile - 1) / kPrefillTile),
+                (uint32_t)(p.block_tokens + 15) / 16u};
 }
-__device__ __forceinline__ int64_t share_of(int64_t total, int c, int n) {
-    return total / n * c + total % n * c / n;
-}
-__device__ __forceinline__ int64_t shfl64(int64_t v, int l) { return (int64_t)__shfl_sync(0xffffffffu, (long long)v, l); }
-template <int D>
-__device__ __forceinline__ int64_t total_of(const PrefillParams& p) {
-    const int lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    for (int s = lane; s < p.n_seq; s += 32) {
-        const Sequence x = read_sequence<D>(p, s);
-        sum += line_of(p, x).upto(x.blocks) * p.n_head_kv;
+struct Shares {
+    uint32_t total, each, left, n;
+    __device__ __forceinline__ void set(uint32_t total_, uint32_t n_) {
+        total = total_;
+        n = n_;
+        each = total / n;
+        left = total - each * n;
     }
+    __device__ __forceinline__ uint32_t of(uint32_t c) const { return each * c + left * c / n; }
+};
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {  // inclusive, over the lanes
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += (int64_t)__shfl_xor_sync(0xffffffffu, (long long)sum, o);
-    return sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+    }
+    return v;
+}
+__device__ __forceinline__ uint32_t length_of(const PrefillParams& p, const Sequence& x) {
+    return x.blocks != 0u ? line_of(p, x).upto(x.blocks) * (uint32_t)p.n_head_kv : 0u;
+}
+__device__ __forceinline__ uint32_t total_of(const PrefillParams& p) {
+    uint32_t sum = 0;
+    for (int s = threadIdx.x & 31; s < p.n_seq; s += 32) sum += length_of(p, read_sequence(p, s));
+    return __reduce_add_sync(0xffffffffu, sum);
+}
+__device__ __forceinline__ Sequence from_lane(const Sequence& x, int l) {
+    Sequence y;
+    y.q0 = __shfl_sync(0xffffffffu, x.q0, l);
+    y.n_q = __shfl_sync(0xffffffffu, x.n_q, l);
+    y.len = __shfl_sync(0xffffffffu, x.len, l);
+    y.blocks = __shfl_sync(0xffffffffu, x.blocks, l);
+    return y;
 }
 // The unit that holds position `at` of the line (at < total), the same in all lanes.
 struct Place {
     Sequence x;
     Line line;
-    int seq, g;
-    int64_t block, start, end;  // the unit's part of the line
+    int seq;
+    uint32_t g, block, start, end;  // start, end: the unit's part of the line
+    __device__ __forceinline__ int32_t tok0(const PrefillParams& p) const { return (int32_t)block * p.block_tokens; }
+    __device__ __forceinline__ int32_t tiles(const PrefillParams& p) const {
+        const int32_t t = tok0(p);
+        return tiles_seen((int64_t)x.len - x.n_q + 1 + t, min(x.n_q - t, p.block_tokens));
+    }
+    // the tile that position y of the unit (from its start) falls on
+    __device__ __forceinline__ int32_t tile_at(uint32_t y, int32_t n) const {
+        const int32_t t = ((int32_t)y - 8 * (int32_t)kUnitCost) >> 3;
+        return y >= end - start ? n : min(max(t, 0), n);
+    }
 };
-template <int D>
-__device__ __forceinline__ Place place_of(const PrefillParams& p, int64_t at) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ Place place_of(const PrefillParams& p, uint32_t at) {
     Place r = {};
-    int64_t base = 0;
+    uint32_t base = 0;
     for (int s0 = 0; s0 < p.n_seq; s0 += 32) {
-        const Sequence x = read_sequence<D>(p, s0 + lane);
-        const Line line = line_of(p, x);
-        int64_t sum = x.blocks > 0 ? line.upto(x.blocks) * p.n_head_kv : 0;
-        const int64_t own = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = (int64_t)__shfl_up_sync(0xffffffffu, (long long)sum, o);
-            if (lane >= o) sum += v;
-        }
+        const Sequence x = read_sequence(p, s0 + (threadIdx.x & 31));
+        const uint32_t own = length_of(p, x), sum = warp_scan(own);
         const uint32_t hit = __ballot_sync(0xffffffffu, at < base + sum);
         if (hit != 0u) {
             const int l = __ffs(hit) - 1;
             r.seq = s0 + l;
-            r.x.q0 = shfl64(x.q0, l);
-            r.x.n_q = shfl64(x.n_q, l);
-            r.x.len = shfl64(x.len, l);
-            r.x.blocks = shfl64(x.blocks, l);
-            r.line.a = shfl64(line.a, l);
-            r.line.step = shfl64(line.step, l);
-            base += shfl64(sum - own, l);
+            r.x = from_lane(x, l);
+            base += __shfl_sync(0xffffffffu, sum - own, l);
             break;
         }
-        base += shfl64(sum, 31);
+        base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    const int64_t per = r.line.upto(r.x.blocks);
-    int64_t y = at - base;
-    r.g = (int)(y / per);
-    y -= (int64_t)r.g * per;
-    int64_t lo = 0, hi = r.x.blocks - 1;  // the last block that starts at or before y
+    r.line = line_of(p, r.x);
+    const uint32_t per = r.line.upto(r.x.blocks);
+    uint32_t y = at - base;
+    r.g = y / per;
+    y -= r.g * per;
+    uint32_t lo = 0, hi = r.x.blocks - 1u;  // the last block that starts at or before y
     while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
+        const uint32_t mid = (lo + hi + 1u) / 2u;
         if (r.line.upto(mid) <= y)
             lo = mid;
         else
-            hi = mid - 1;
+            hi = mid - 1u;
     }
     r.block = lo;
     r.start = at - (y - r.line.upto(lo));
     r.end = r.start + r.line.a + r.line.step * lo;
     return r;
 }
-// Tiles [first, last) of a unit of `tiles` tiles that the part [a, b) of its line stands for.
-__device__ __forceinline__ void tiles_between(const Place& r, int64_t a, int64_t b, int64_t tiles, int64_t& first, int64_t& last) {
-    const int64_t w = r.end - r.start;
-    first = (a - r.start) * tiles / w;
-    last = (b - r.start) * tiles / w;
-}
 
 // Fills in a piece of work: tiles [first, last) of a block.
 template <int D>
-__device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence& x, int seq, int g, int64_t block, int64_t first,
-                                         int64_t last, int part, Seg& s) {
+__device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence& x, int seq, int g, uint32_t block, int32_t first,
+                                         int32_t last, int part, Seg& s) {
     constexpr int kGroups = Geometry<D>::kGroups;
-    const int64_t tok0 = block * p.block_tokens;
-    const int64_t left = x.n_q - tok0;
+    const int32_t tok0 = (int32_t)block * p.block_tokens;
     s.seq = seq;
     s.g = g;
-    s.n_tok = (int)(left < p.block_tokens ? left : p.block_tokens);
+    s.n_tok = min(x.n_q - tok0, p.block_tokens);
     s.q_tok = x.q0 + tok0;
-    s.cell0 = p.seq_lens != nullptr ? (int64_t)seq * p.n_cells : x.q0;
+    s.cell0 = p.seq_lens != nullptr ? (int64_t)seq * p.n_cells : (int64_t)x.q0;
     s.len = x.len;
-    s.lim0 = x.len - x.n_q + 1 + tok0;
-    s.j0 = (int)first;
+    s.lim0 = (int64_t)x.len - x.n_q + 1 + tok0;
+    s.j0 = first;
     s.part = part;
     int n_max = 0;
     s.n[1] = 0;
 #pragma unroll
     for (int t = 0; t < kGroups; ++t) {
-        const int64_t in = (int64_t)s.n_tok < (int64_t)(t + 1) * p.group_tokens ? s.n_tok : (int64_t)(t + 1) * p.group_tokens;
-        int64_t tiles = in > (int64_t)t * p.group_tokens ? tiles_seen(s.lim0, in) : 0;
-        tiles = tiles < last ? tiles : last;
-        s.n[t] = tiles > first ? (int)(tiles - first) : 0;
-        n_max = s.n[t] > n_max ? s.n[t] : n_max;
+        const int32_t in = min(s.n_tok, (t + 1) * p.group_tokens);
+        const int32_t tiles = min(in > t * p.group_tokens ? tiles_seen(s.lim0, in) : 0, last);
+        s.n[t] = max(tiles - first, 0);
+        n_max = max(n_max, s.n[t]);
     }
     // (one token: all its rows see the same cells)
     const int64_t cut = (s.lim0 > 0 ? s.lim0 : 0) / kPrefillTile - first;
@@ -428,7 +473,7 @@ struct Walk {
     // whole units
     uint32_t round;
     // shares
-    int64_t at, end;
+    uint32_t at, end;
     Place r;
     bool started;
 
@@ -436,9 +481,10 @@ struct Walk {
         round = 0;
         started = false;
         if (p.shares) {
-            const int64_t total = total_of<D>(p);
-            at = share_of(total, blockIdx.x, gridDim.x);
-            end = share_of(total, blockIdx.x + 1, gridDim.x);
+            Shares sh;
+            sh.set(total_of(p), gridDim.x);
+            at = sh.of(blockIdx.x);
+            end = sh.of(blockIdx.x + 1u);
         }
     }
     // The next piece in s; false: none left.
@@ -447,31 +493,21 @@ struct Walk {
     // Unit number i counts from the last sequence's last block (the longest rows of a prompt
     // first), KV heads fastest; round r deals them out forwards or backwards.
     __device__ __forceinline__ bool next_whole(const PrefillParams& p, Seg& s) {
-        const int lane = threadIdx.x & 31;
         const uint32_t n = gridDim.x, c = blockIdx.x;
         const uint32_t i = round * n + ((round & 1u) ? n - 1u - c : c);
         if (i < round * n) return false;  // (beyond 32 bits)
         ++round;
-        const uint32_t g = i % (uint32_t)p.n_head_kv, b = i / (uint32_t)p.n_head_kv;
+        const uint32_t b = i / (uint32_t)p.n_head_kv, g = i - b * (uint32_t)p.n_head_kv;
         uint32_t seen = 0;
         for (int top = p.n_seq; top > 0; top -= 32) {
-            const Sequence x = read_sequence<D>(p, top - 1 - lane);
-            uint32_t sum = (uint32_t)x.blocks;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
-            }
+            const Sequence x = read_sequence(p, top - 1 - (int)(threadIdx.x & 31));
+            const uint32_t sum = warp_scan(x.blocks);
             const uint32_t hit = __ballot_sync(0xffffffffu, b < seen + sum);
             if (hit != 0u) {
                 const int l = __ffs(hit) - 1;
-                Sequence y;
-                y.q0 = shfl64(x.q0, l);
-                y.n_q = shfl64(x.n_q, l);
-                y.len = shfl64(x.len, l);
-                y.blocks = shfl64(x.blocks, l);
-                const uint32_t before = seen + __shfl_sync(0xffffffffu, sum, l) - (uint32_t)y.blocks;
-                make_seg<D>(p, y, top - 1 - l, (int)g, y.blocks - 1 - (int64_t)(b - before), 0, INT_MAX, -1, s);
+                const Sequence y = from_lane(x, l);
+                const uint32_t before = seen + __shfl_sync(0xffffffffu, sum, l) - y.blocks;
+                make_seg<D>(p, y, top - 1 - l, (int)g, y.blocks - 1u - (b - before), 0, INT_MAX, -1, s);
                 return true;
             }
             seen += __shfl_sync(0xffffffffu, sum, 31);
@@ -481,36 +517,100 @@ struct Walk {
 
     __device__ __forceinline__ bool next_share(const PrefillParams& p, Seg& s) {
         while (at < end) {
-            if (!started) {
-                r = place_of<D>(p, at);
+            if (!started || (r.block + 1u == r.x.blocks && r.g + 1u == (uint32_t)p.n_head_kv)) {
+                r = place_of(p, at);
                 started = true;
-            } else {  // the next unit of the line
-                r.start = r.end;
-                ++r.block;
-                if (r.block == r.x.blocks) {
+            } else {  // the next unit of the sequence
+                if (++r.block == r.x.blocks) {
                     r.block = 0;
                     ++r.g;
-                    if (r.g == p.n_head_kv) {
-                        r = place_of<D>(p, at);
-                    }
                 }
+                r.start = r.end;
                 r.end = r.start + r.line.a + r.line.step * r.block;
             }
-            const int64_t a = at, b = r.end < end ? r.end : end;
+            const uint32_t a = at, b = min(r.end, end);
             at = b;
-            const int64_t tok0 = r.block * p.block_tokens;
-            const int64_t left = r.x.n_q - tok0;
-            const int64_t tiles = tiles_seen(r.x.len - r.x.n_q + 1 + tok0, left < p.block_tokens ? left : p.block_tokens);
-            int64_t first, last;
-            tiles_between(r, a, b, tiles, first, last);
+            const int32_t tiles = r.tiles(p);
+            const int32_t first = r.tile_at(a - r.start, tiles), last = r.tile_at(b - r.start, tiles);
             if (tiles == 0 ? a != r.start : first == last) continue;  // (a unit that sees nothing: its first piece)
             const bool whole = first == 0 && last == tiles;
-            make_seg<D>(p, r.x, r.seq, r.g, r.block, first, last, whole ? -1 : 2 * (int)blockIdx.x + (a > r.start ? 0 : 1), s);
+            make_seg<D>(p, r.x, r.seq, (int)r.g, r.block, first, last, whole ? -1 : 2 * (int)blockIdx.x + (a > r.start ? 0 : 1), s);
             return true;
         }
         return false;
     }
 };
+
+// A tile's cells, in a warp: lane l holds cells l, l + 32, l + 64, l + 96.
+struct Tile {
+    int32_t e[4];     // physical cells (no plan: from the tile's first), -1: none
+    int64_t base;     // first physical cell when a run
+    bool run, holes;  // the cells that are there lie at base + their number; some are not
+};
+__device__ __forceinline__ Tile read_tile(const PrefillParams& p, const Seg& s, int j) {
+    Tile t;
+    const int lane = threadIdx.x & 31;
+    const int64_t i0 = (int64_t)(s.j0 + j) * kPrefillTile;
+    const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+    const int left = j < n_max ? (int)clamp64(s.len - i0, 0, kPrefillTile) : 0;
+    t.run = true;
+    t.holes = left < kPrefillTile;
+    t.base = s.cell0 + i0;
+    const int32_t* row = p.plan != nullptr ? p.plan + (int64_t)s.seq * p.plan_stride + i0 : nullptr;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = 32 * k + lane;
+        t.e[k] = -1;
+        if (c < left) t.e[k] = row != nullptr ? __ldg(row + c) : c;
+    }
+    return t;
+}
+// Checks a plan tile's entries and whether they are one run; true: all entries are in range.
+__device__ __forceinline__ bool settle(const PrefillParams& p, Tile& t) {
+    if (p.plan == nullptr) return true;
+    const int lane = threadIdx.x & 31;
+    int lo = INT_MAX, hi = INT_MIN;
+    bool hole = false, good = true;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (t.e[k] < -1 || (int64_t)t.e[k] >= p.n_cells) {
+            good = false;
+            t.e[k] = -1;
+        }
+        if (t.e[k] >= 0) {
+            const int d = t.e[k] - (32 * k + lane);
+            lo = min(lo, d);
+            hi = max(hi, d);
+        } else {
+            hole = true;
+        }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    t.run = lo >= hi;   // (no cell at all: lo > hi)
+    t.base = lo <= hi ? lo : 0;
+    t.holes = __any_sync(0xffffffffu, hole);
+    return good;
+}
+// Writes a plan tile's holes for the softmax (tile number T of the CTA), from one warp.
+__device__ __forceinline__ void write_mask(Header* h, const Tile& t, uint32_t T) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t r = T % kRing;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = t.e[k] < 0 ? -INFINITY : INFINITY;
+    if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
+}
+// Physical cell of the tile's cell c (which may differ from lane to lane), -1: none.
+__device__ __forceinline__ int64_t cell_of(const PrefillParams& p, const Tile& t, int c) {
+    const int32_t v0 = __shfl_sync(0xffffffffu, t.e[0], c & 31);
+    const int32_t v1 = __shfl_sync(0xffffffffu, t.e[1], c & 31);
+    const int32_t v2 = __shfl_sync(0xffffffffu, t.e[2], c & 31);
+    const int32_t v3 = __shfl_sync(0xffffffffu, t.e[3], c & 31);
+    const int32_t v = (c & 64) ? ((c & 32) ? v3 : v2) : ((c & 32) ? v1 : v0);
+    return (p.plan == nullptr && v >= 0) ? t.base + v : v;
+}
 
 // ------------------------------------- the kernel -------------------------------------
 
@@ -539,6 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(smem_addr(&h->empty[i]), 1);  // the MMA lane's commit
             mbar_init(smem_addr(&h->landed[i]), 1);
         }
+        for (int i = 0; i < kRawStages; ++i) {
+            mbar_init(smem_addr(&h->raw_full[i]), 1);
+            mbar_init(smem_addr(&h->raw_empty[i]), 4);
+        }
         mbar_init(smem_addr(&h->q_full), 1);
         mbar_init(smem_addr(&h->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
@@ -551,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(smem_addr(&h->mask_full[i]), 1);
             mbar_init(smem_addr(&h->load_done[i]), 4);
             mbar_init(smem_addr(&h->seg_full[i]), 1);
-            mbar_init(smem_addr(&h->seg_empty[i]), 5 + 4 * kGroups);  // loader, MMA and softmax warps
+            mbar_init(smem_addr(&h->seg_empty[i]), (kQuant ? 2 : 5) + 4 * kGroups);  // loader, MMA and softmax warps
         }
         h->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -584,94 +688,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
 
     if (warp >= 8 && warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        // (the four warpgroups' shares add up to the 4 x 128 registers of the launch)
+        if constexpr (kQuant)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         // ------------------------------------ loader ------------------------------------
         const int lt = tid - 256;       // 0 .. 127
-        const int64_t Hk = p.n_head_kv;
         bool bad_entry = false, ok = true;
-        uint32_t n = 0;                 // slots filled
+        uint32_t filled = 0;            // slots
         uint32_t T = 0;                 // tiles begun
+        uint32_t n = 0;                 // quantised: raw slots turned
         uint32_t landed_use = 0;        // a bit per slot: parity of its landed barrier
         Seg s = {};
-        // plan entries of a tile: lane l holds those of cells l, l + 32, l + 64, l + 96
-        struct Tile {
-            int32_t e[4];     // physical cells, -1: none; no plan: from the sequence's first
-            int64_t base;     // first physical cell when a run
-            bool run, holes;  // the cells that are there lie at base + their number; some are not
-        };
-        auto read_tile = [&](int j) {
-            Tile t;
-            const int64_t i0 = (int64_t)(s.j0 + j) * kPrefillTile;
-            const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
-            const int32_t* prow = p.plan != nullptr ? p.plan + (int64_t)s.seq * p.plan_stride : nullptr;
-            t.run = true;
-            t.holes = i0 + kPrefillTile > s.len;
-            t.base = s.cell0 + i0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t i = i0 + 32 * k + lane;
-                t.e[k] = -1;
-                if (j < n_max && i < s.len) t.e[k] = prow != nullptr ? __ldg(prow + i) : 32 * k + lane;
-            }
-            return t;
-        };
-        // checks a plan tile's entries and whether they are one run; writes its holes
-        auto settle = [&](Tile& t) {
-            if (p.plan == nullptr) return;
-            int lo = INT_MAX, hi = INT_MIN;
-            bool hole = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (t.e[k] < -1 || (int64_t)t.e[k] >= p.n_cells) {
-                    bad_entry = true;
-                    t.e[k] = -1;
-                }
-                if (t.e[k] >= 0) {
-                    const int d = t.e[k] - (32 * k + lane);
-                    lo = min(lo, d);
-                    hi = max(hi, d);
-                } else {
-                    hole = true;
-                }
-            }
-            lo = __reduce_min_sync(0xffffffffu, lo);
-            hi = __reduce_max_sync(0xffffffffu, hi);
-            t.run = lo >= hi;   // (no cell at all: lo > hi)
-            t.base = lo <= hi ? lo : 0;
-            t.holes = __any_sync(0xffffffffu, hole);
-            if (warp == 8) {
-                const uint32_t r = T % kRing;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = t.e[k] < 0 ? -INFINITY : INFINITY;
-                if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
-            }
-        };
-        // physical cell of the tile's cell c (any lane's), -1: none
-        auto cell_of = [&](const Tile& t, int c) -> int64_t {
-            const int32_t v0 = __shfl_sync(0xffffffffu, t.e[0], c & 31);
-            const int32_t v1 = __shfl_sync(0xffffffffu, t.e[1], c & 31);
-            const int32_t v2 = __shfl_sync(0xffffffffu, t.e[2], c & 31);
-            const int32_t v3 = __shfl_sync(0xffffffffu, t.e[3], c & 31);
-            const int32_t v = (c & 64) ? ((c & 32) ? v3 : v2) : ((c & 32) ? v1 : v0);
-            return (p.plan == nullptr && v >= 0) ? t.base + v : v;
+        auto begin_tile = [&](Tile& t) {
+            if (!settle(p, t)) bad_entry = true;
+            if (p.plan != nullptr && warp == 8) write_mask(h, t, T);
+            ++T;
         };
         // Cells with V that is not finite, of a cut tile (unit number i's).
         auto note = [&](uint32_t i, int j, int c, bool bad) {
             if (bad) atomicOr(&h->bad_cells[i % kRing][(j - s.first_cut) % kCutTiles][c >> 5], 1u << (c & 31));
         };
         auto wait_slot_empty = [&]() -> bool {
-            const uint32_t use = n / kSlots;
-            return use == 0 || wait_all(&h->empty[n % kSlots], (use - 1) & 1u);
+            const uint32_t use = filled / kSlots;
+            return use == 0 || wait_all(&h->empty[filled % kSlots], (use - 1) & 1u);
         };
         auto slot_ready = [&](uint64_t* bar) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(bar));
-            ++n;
+            ++filled;
         };
         auto stall_hook = [&](uint64_t* bar) {
-            if (n == 0 && p.stall_tx != 0u && lt == 0) mbar_expect_tx(smem_addr(bar), p.stall_tx);
+            if (filled == 0 && p.stall_tx != 0u && lt == 0) mbar_expect_tx(smem_addr(bar), p.stall_tx);
         };
 
         if constexpr (!kQuant) {
@@ -687,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     uint4 w[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int64_t cell = cell_of(t, (lt >> 4) + 8 * (i0 + k));
+                        const int64_t cell = cell_of(p, t, (lt >> 4) + 8 * (i0 + k));
                         w[k] = make_uint4(0u, 0u, 0u, 0u);
                         if (cell >= 0) w[k] = __ldg(reinterpret_cast<const uint4*>(rows + cell * stride + b / 2));
                     }
@@ -734,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             };
             auto fill = [&](const Tile& t, bool v_side, int half, uint32_t i, int j) {
                 if (!(ok = wait_slot_empty())) return;
-                const int st = (int)(n % kSlots);
+                const int st = (int)(filled % kSlots);
                 unsigned char* slot = slots + st * kSlotBytes;
                 const bool cut = v_side && j >= s.first_cut;
                 uint64_t* bar = &h->full[st];
@@ -766,9 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (warp == 8 && lane < 4 * kCutTiles) h->bad_cells[i % kRing][lane >> 2][lane & 3] = 0u;
                 asm volatile("bar.sync 1, 128;" ::: "memory");   // (before any of them is set)
                 if (n_max > 0) {
-                    Tile tk = read_tile(0), tv = tk, next = read_tile(1);
-                    settle(tk);
-                    ++T;
+                    Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
+                    begin_tile(tk);
                     if (kHalves == 1) {
                         for (int j = 0; j < n_max; ++j) {
                             fill(tk, false, 0, i, j);
@@ -776,9 +824,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             tv = tk;
                             if (j + 1 < n_max) {
                                 tk = next;
-                                settle(tk);
-                                ++T;
-                                next = read_tile(j + 2);
+                                begin_tile(tk);
+                                next = read_tile(p, s, j + 2);
                             }
                             fill(tv, true, 0, i, j);
                             if (!ok) break;
@@ -789,9 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 tv = tk;
                                 if (j + 1 < n_max) {
                                     tk = next;
-                                    settle(tk);
-                                    ++T;
-                                    next = read_tile(j + 2);
+                                    begin_tile(tk);
+                                    next = read_tile(p, s, j + 2);
                                 }
                             }
 #pragma unroll 1
@@ -806,241 +852,100 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 give_back(i);
             }
         } else {
-            // ---- quantised ----
-            constexpr int kStage = Memory<KBITS>::kRawBytes;
-            // A slot to come: its tile's cells (this thread's of the copies), side and half.
-            // Slots are fetched two ahead of the one that is turned into f16, so the walk over
-            // them runs ahead too; what turning needs of a slot is kept in three small words.
-            uint32_t ahead = 0;            // slots fetched
-            uint32_t what[kRawStages];     // v_side | cut << 1 | last of its unit << 2 | (j - first_cut) << 3 | unit << 8
-            auto fetch = [&](const Tile& t, bool v_side, int half, uint32_t word) {
-                const int bits = v_side ? VBITS : KBITS;
-                unsigned char* stage = raws + (ahead % kRawStages) * kStage;
-                const char* rows = static_cast<const char*>(v_side ? p.v : p.k);
-                const char* scales = reinterpret_cast<const char*>(v_side ? p.v_scale : p.k_scale);
-                if (bits == 8) {
-                    const int piece = lt & 7;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int c = (lt >> 3) + 16 * k;
-                        const int64_t cell = cell_of(t, c);
-                        if (cell >= 0)
-                            cp_async_16_cg(smem_addr(stage + c * 128 + piece * 16), rows + (cell * Hk + s.g) * D + half * 128 + 16 * piece);
-                    }
-                } else {
-                    const int piece = lt & 3;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = (lt >> 2) + 32 * k;
-                        const int64_t cell = cell_of(t, c);
-                        if (cell >= 0)
-                            cp_async_16_cg(smem_addr(stage + c * 64 + piece * 16),
-                                           rows + (cell * Hk + s.g) * (D / 2) + half * 64 + 16 * piece);
-                    }
-                }
-                // scales: cell lt's four blocks; zeros where there is no cell, so that whatever
-                // its codes are it stands for zeros
-                const int64_t cell = cell_of(t, lt);
-                const uint32_t dst = smem_addr(stage + kStage - 1024 + 8 * lt);
-                if (cell >= 0)
-                    cp_async_8(dst, scales + ((cell * Hk + s.g) * (D / 32) + half * 4) * 2);
-                else
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                what[kRawStages - 1] = word;
-                ++ahead;
-            };
-            // Turns raw slot number n into f16 (its copies are complete and visible).
-            auto turn = [&](uint32_t word) {
+            // ---- quantised: turns the raw slots that warp 14 brings ----
+            for (;; ++n) {
+                const uint32_t r = n % kRawStages;
+                if (!(ok = wait_all(&h->raw_full[r], (n / kRawStages) & 1u))) break;
+                const uint32_t word = h->raw_word[r];
+                if (word == kNoMore) break;
                 const bool v_side = word & 1u, cut = (word >> 1) & 1u;
-                const int bits = v_side ? VBITS : KBITS;
-                const unsigned char* stage = raws + (n % kRawStages) * kStage;
-                const unsigned short* scales = reinterpret_cast<const unsigned short*>(stage + kStage - 1024);
-                unsigned char* slot = slots + (n % kSlots) * kSlotBytes;
-                uint32_t* bad_row = h->bad_cells[(word >> 8) % kRing][(word >> 3) & 3u];
-                if (bits == 8) {
-                    const int piece = lt & 7;  // halves 16 piece .. of the row: bytes 32 piece ..
-                    unsigned char* plane = slot + (piece >> 2) * kPlaneBytes;
-                    const int b = (piece & 3) * 32;
+                const uint32_t unit = (word >> 8) & 0xffffu;
+                if (!(word & 8u)) {
+                    if (!(ok = wait_slot_empty())) break;
+                    stall_hook(&h->full[filled % kSlots]);
+                    const int bits = v_side ? VBITS : KBITS;
+                    const unsigned char* stage = raws + r * Memory<KBITS>::kRawBytes;
+                    const unsigned short* scales = reinterpret_cast<const unsigned short*>(stage + Memory<KBITS>::kRawBytes - 1024);
+                    unsigned char* slot = slots + (filled % kSlots) * kSlotBytes;
+                    uint32_t* bad_row = h->bad_cells[unit % kRing][(word >> 4) & 3u];
+                    // (all loads first: the stores cannot be seen not to alias them)
+                    if (bits == 8) {
+                        const int piece = lt & 7;  // halves 16 piece .. of the row: bytes 32 piece ..
+                        unsigned char* plane = slot + (piece >> 2) * kPlaneBytes;
+                        const int c0 = lt >> 3;    // cells c0, c0 + 16, ..: the same place in the swizzle
+                        const uint32_t o0 = swz(c0, (piece & 3) * 32), o1 = swz(c0, (piece & 3) * 32 + 16);
+                        uint4 w[8];
+                        uint32_t ds[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int c = (lt >> 3) + 16 * k;
-                        const uint4 w = *reinterpret_cast<const uint4*>(stage + c * 128 + piece * 16);
-                        const uint32_t ds = scales[4 * c + (piece >> 1)];
-                        const __half2 d = scale2(ds);
-                        const uint32_t x[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
-                        uint32_t o[8];
-                        if (!big_scale(ds)) {
+                        for (int k = 0; k < 8; ++k) {
+                            w[k] = *reinterpret_cast<const uint4*>(stage + 16 * lt + 2048 * k);
+                            ds[k] = scales[4 * c0 + (piece >> 1) + 64 * k];
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const __half2 d = scale2(ds[k]);
+                            const uint32_t x[4] = {w[k].x ^ 0x80808080u, w[k].y ^ 0x80808080u, w[k].z ^ 0x80808080u,
+                                                   w[k].w ^ 0x80808080u};
+                            uint32_t o[8];
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                o[2 * q] = dequant(i8x2_lo(x[q]), d, false);
-                                o[2 * q + 1] = dequant(i8x2_hi(x[q]), d, false);
+                                o[2 * q] = hmul2_u32(i8x2_lo(x[q]), as_u32(d));
+                                o[2 * q + 1] = hmul2_u32(i8x2_hi(x[q]), as_u32(d));
                             }
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                o[2 * q] = dequant(i8x2_lo(x[q]), d, true);
-                                o[2 * q + 1] = dequant(i8x2_hi(x[q]), d, true);
-                            }
+                            finish<8>(o, ds[k], cut, bad_row, c0 + 16 * k);
+                            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+                            // (the upper plane's lanes in the other order: eight lanes, eight bank groups)
+                            *reinterpret_cast<uint4*>(plane + (piece < 4 ? o0 : o1) + 2048 * k) = piece < 4 ? a : b;
+                            *reinterpret_cast<uint4*>(plane + (piece < 4 ? o1 : o0) + 2048 * k) = piece < 4 ? b : a;
                         }
-                        if (cut) {
-                            bool bad = false;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) o[q] = finite2(o[q], bad);
-                            if (bad) atomicOr(&bad_row[c >> 5], 1u << (c & 31));
-                        }
-                        *reinterpret_cast<uint4*>(plane + swz(c, b)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(plane + swz(c, b + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                } else {
-                    const int piece = lt & 3;  // block `piece`: halves 32 piece .., bytes 64 piece ..
-                    unsigned char* plane = slot + (piece >> 1) * kPlaneBytes;
-                    const int b = (piece & 1) * 64;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = (lt >> 2) + 32 * k;
-                        const uint4 w = *reinterpret_cast<const uint4*>(stage + c * 64 + piece * 16);
-                        const uint32_t ds = scales[4 * c + piece];
-                        const __half2 d = scale2(ds);
-                        const bool big = big_scale(ds);
-                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t lo[8], hi[8];  // elements 0-15 and 16-31 of the block
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t a = prmt_b32(x[q], 0u, 0x4140u), e = prmt_b32(x[q], 0u, 0x4342u);
-                            lo[2 * q] = dequant(nib2(a & 0x000f000fu), d, big);
-                            lo[2 * q + 1] = dequant(nib2(e & 0x000f000fu), d, big);
-                            hi[2 * q] = dequant(nib2((a >> 4) & 0x000f000fu), d, big);
-                            hi[2 * q + 1] = dequant(nib2((e >> 4) & 0x000f000fu), d, big);
-                        }
-                        if (cut) {
-                            bool bad = false;
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                lo[q] = finite2(lo[q], bad);
-                                hi[q] = finite2(hi[q], bad);
-                            }
-                            if (bad) atomicOr(&bad_row[c >> 5], 1u << (c & 31));
-                        }
-                        *reinterpret_cast<uint4*>(plane + swz(c, b)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        *reinterpret_cast<uint4*>(plane + swz(c, b + 16)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-                        *reinterpret_cast<uint4*>(plane + swz(c, b + 32)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(plane + swz(c, b + 48)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                    }
-                }
-                fence_async();
-            };
-            // The slots in the ring's order, one per call: side, half and tile of the next one.
-            // (At head_dim 128 K0 V0 K1 V1 .., at 256 K0 K1 V0 K2 V1 .., two slots each.)
-            uint32_t unit = 0;             // the unit that is being fetched
-            int step = 0, steps = 0;       // its slots so far and in all
-            Tile tk, tv, next;
-            bool more = true;
-            auto open_unit = [&]() {       // the next unit with tiles; those without are given back
-                for (;;) {
-                    if (!take(unit, s)) {
-                        more = false;
-                        return;
-                    }
-                    // (every warp is here: no bit of the unit four before is set any more)
-                    if (warp == 8 && lane < 4 * kCutTiles) h->bad_cells[unit % kRing][lane >> 2][lane & 3] = 0u;
-                    const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
-                    if (n_max > 0) {
-                        step = 0;
-                        steps = 2 * kHalves * n_max;
-                        tk = read_tile(0);
-                        next = read_tile(1);
-                        settle(tk);
-                        ++T;
-                        tv = tk;
-                        return;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&h->load_done[unit % kRing]));
-                    give_back(unit);
-                    ++unit;
-                }
-            };
-            auto fetch_next = [&]() {      // (a group is committed either way, so that they count)
-                if (more && step == steps) open_unit();
-                if (!more) {
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    what[kRawStages - 1] = 0xffffffffu;
-                    return;
-                }
-                const int n_max = steps / (2 * kHalves);
-                bool v_side;
-                int j, half;
-                if (kHalves == 1) {
-                    v_side = step & 1;
-                    j = step >> 1;
-                    half = 0;
-                } else {   // K0 then, for each j, K of j + 1 (if any) and V of j
-                    const int q = step >> 1;
-                    half = step & 1;
-                    if (q == 0) {
-                        v_side = false;
-                        j = 0;
-                    } else if (q == 2 * n_max - 1) {
-                        v_side = true;
-                        j = n_max - 1;
                     } else {
-                        v_side = !(q & 1);
-                        j = v_side ? (q >> 1) - 1 : (q >> 1) + 1;
+                        const int piece = lt & 3;  // block `piece`: halves 32 piece .., bytes 64 piece ..
+                        unsigned char* plane = slot + (piece >> 1) * kPlaneBytes;
+                        const int c0 = lt >> 2;    // cells c0, c0 + 32, ..
+                        const int b = (piece & 1) * 64;
+                        uint4 w[4];
+                        uint32_t ds[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            w[k] = *reinterpret_cast<const uint4*>(stage + 16 * lt + 2048 * k);
+                            ds[k] = scales[4 * c0 + piece + 128 * k];
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t d = as_u32(scale2(ds[k]));
+                            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                            uint32_t o[16];  // elements 0-15 and 16-31 of the block
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint32_t a = prmt_b32(x[q], 0u, 0x4140u), e = prmt_b32(x[q], 0u, 0x4342u);
+                                o[2 * q] = hmul2_u32(nib2(a & 0x000f000fu), d);
+                                o[2 * q + 1] = hmul2_u32(nib2(e & 0x000f000fu), d);
+                                o[8 + 2 * q] = hmul2_u32(nib2((a >> 4) & 0x000f000fu), d);
+                                o[9 + 2 * q] = hmul2_u32(nib2((e >> 4) & 0x000f000fu), d);
+                            }
+                            finish<16>(o, ds[k], cut, bad_row, c0 + 32 * k);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                *reinterpret_cast<uint4*>(plane + swz(c0, b + 16 * q) + 4096 * k) =
+                                    make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                        }
                     }
+                    fence_async();
+                    slot_ready(&h->full[filled % kSlots]);
                 }
-                if (!v_side && half == 0 && j > 0) {   // a new tile
-                    tv = tk;
-                    tk = next;
-                    settle(tk);
-                    ++T;
-                    next = read_tile(j + 1);
-                }
-                if (kHalves == 2 && v_side && half == 0 && j == n_max - 1) tv = tk;
-                if (kHalves == 1) tv = tk;
-                ++step;
-                const bool cut = v_side && j >= s.first_cut;
-                const uint32_t word = (v_side ? 1u : 0u) | (cut ? 2u : 0u) | (step == steps ? 4u : 0u) |
-                                      ((uint32_t)(cut ? j - s.first_cut : 0) << 3) | ((unit & 0xffffu) << 8);
-                fetch(v_side ? tv : tk, v_side, half, word);
-                if (step == steps) ++unit;
-            };
-            uint32_t handed = 0;           // units given back (16 bits are compared with the words')
-            auto shift = [&]() {
-#pragma unroll
-                for (int k = 0; k + 1 < kRawStages; ++k) what[k] = what[k + 1];
-            };
-            step = steps = 0;
-#pragma unroll
-            for (int k = 0; k < kRawStages - 1; ++k) {
-                shift();
-                fetch_next();
-            }
-            // what[1], what[2]: the two slots in flight
-            for (;;) {
-                shift();                   // what[0]: the slot to turn
-                const uint32_t word = what[0];
-                what[kRawStages - 1] = 0xffffffffu;
-                if (word == 0xffffffffu) break;
-                asm volatile("cp.async.wait_group %0;" ::"n"(kRawStages - 2) : "memory");
-                asm volatile("bar.sync 1, 128;" ::: "memory");   // everyone's copies; the stage before is free
-                fetch_next();
-                if (!(ok = wait_slot_empty())) break;
-                stall_hook(&h->full[n % kSlots]);
-                turn(word);
-                slot_ready(&h->full[(n) % kSlots]);
-                if (word & 4u) {           // the unit's last slot
-                    handed = (word >> 8) & 0xffffu;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&h->load_done[handed % kRing]));
-                    give_back(handed);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&h->raw_empty[r]));
+                    if (word & 4u) mbar_arrive(smem_addr(&h->load_done[unit % kRing]));  // the unit's last slot
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         if (__any_sync(0xffffffffu, bad_entry) && lane == 0 && warp == 8) atomicOr(p.status, KVATTN_DEVICE_BAD_PLAN_ENTRY);
     } else if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if constexpr (kQuant)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 13) {
             // ---------------------------------- scheduler ----------------------------------
             Walk<D> walk;
@@ -1075,6 +980,107 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     __syncwarp();
                 }
             }
+        } else if (kQuant && warp == 14) {
+            // ------------------------------- raw bytes, quantised -------------------------------
+            uint32_t ahead = 0, T = 0;    // slots brought, tiles begun
+            bool bad_entry = false, ok = true;
+            Seg s = {};
+            auto stage_free = [&]() -> bool {
+                return ahead < kRawStages || wait_all(&h->raw_empty[ahead % kRawStages], (ahead / kRawStages - 1u) & 1u);
+            };
+            auto publish = [&](uint32_t word) {
+                const uint32_t r = ahead % kRawStages;
+                if (lane == 0) h->raw_word[r] = word;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&h->raw_full[r]));
+                ++ahead;
+            };
+            auto bring = [&](const Tile& t, bool v_side, int half, uint32_t word) {
+                if (!(ok = stage_free())) return;
+                const int bits = v_side ? VBITS : KBITS;
+                const uint32_t bar = smem_addr(&h->raw_full[ahead % kRawStages]);
+                const uint32_t stage = smem_addr(raws + (ahead % kRawStages) * Memory<KBITS>::kRawBytes);
+                const int64_t Hk = p.n_head_kv;
+                if (t.run && p.use_tma != 0) {
+                    if (lane == 0) {
+                        mbar_expect_tx(bar, 128u * 16u * (uint32_t)bits);
+                        tma_box(stage, v_side ? &p.tmap_v : &p.tmap_k, half * 16 * bits, s.g, (int)t.base, bar);
+                    }
+                } else {   // 16-byte pieces of the cells' 128 dims, `bits` a cell
+                    const char* rows = static_cast<const char*>(v_side ? p.v : p.k);
+#pragma unroll 1
+                    for (int i = lane; i < 128 * bits; i += 32) {
+                        const int c = i / bits, piece = i - c * bits;
+                        const int64_t cell = cell_of(p, t, c);
+                        if (cell >= 0)
+                            cp_async_16_cg(stage + 16 * i, rows + (cell * Hk + s.g) * (D * bits / 8) + half * 16 * bits + 16 * piece);
+                    }
+                }
+                // scales: a cell's four blocks; zeros where there is no cell, so that whatever its
+                // codes are it stands for zeros
+                const __half* scales = (v_side ? p.v_scale : p.k_scale) + half * 4;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t dst = stage + Memory<KBITS>::kRawBytes - 1024 + 8 * (32 * k + lane);
+                    const int64_t cell = p.plan == nullptr ? t.base + t.e[k] : t.e[k];
+                    if (t.e[k] >= 0)
+                        cp_async_8(dst, scales + (cell * Hk + s.g) * (D / 32));
+                    else
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
+                }
+                cp_async_arrive(bar);
+                publish(word);
+            };
+            for (uint32_t i = 0; ok; ++i) {
+                if (!take(i, s)) break;
+                if (lane < 4 * kCutTiles) h->bad_cells[i % kRing][lane >> 2][lane & 3] = 0u;
+                const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+                const uint32_t unit = (i & 0xffffu) << 8;
+                if (n_max == 0) {    // (the turning warps still sign the unit off)
+                    if ((ok = stage_free())) publish(unit | 12u);
+                    give_back(i);
+                    continue;
+                }
+                auto begin_tile = [&](Tile& t) {
+                    if (!settle(p, t)) bad_entry = true;
+                    if (p.plan != nullptr) write_mask(h, t, T);
+                    ++T;
+                };
+                auto word_of = [&](bool v_side, int half, int j) -> uint32_t {
+                    const bool cut = v_side && j >= s.first_cut;
+                    return unit | (v_side ? 1u : 0u) | (cut ? 2u | ((uint32_t)(j - s.first_cut) << 4) : 0u) |
+                           ((v_side && j + 1 == n_max && half + 1 == kHalves) ? 4u : 0u);
+                };
+                Tile tk = read_tile(p, s, 0), next = read_tile(p, s, 1);
+                begin_tile(tk);
+                if (kHalves == 1) {    // K0 V0 K1 V1 ..
+                    for (int j = 0; j < n_max && ok; ++j) {
+                        bring(tk, false, 0, word_of(false, 0, j));
+                        if (ok) bring(tk, true, 0, word_of(true, 0, j));
+                        tk = next;
+                        if (j + 1 < n_max) begin_tile(tk);
+                        next = read_tile(p, s, j + 2);
+                    }
+                } else {               // K0 K1 V0 K2 V1 .., two slots each
+                    Tile tv = tk;
+                    for (int j = -1; j < n_max && ok; ++j) {
+                        if (j >= 0) {
+                            tv = tk;
+                            tk = next;
+                            if (j + 1 < n_max) begin_tile(tk);
+                            next = read_tile(p, s, j + 2);
+                        }
+#pragma unroll 1
+                        for (int half = 0; half < 2 && ok && j + 1 < n_max; ++half) bring(tk, false, half, word_of(false, half, j + 1));
+#pragma unroll 1
+                        for (int half = 0; half < 2 && ok && j >= 0; ++half) bring(tv, true, half, word_of(true, half, j));
+                    }
+                }
+                give_back(i);
+            }
+            if (ok && stage_free()) publish(kNoMore);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (__any_sync(0xffffffffu, bad_entry) && lane == 0) atomicOr(p.status, KVATTN_DEVICE_BAD_PLAN_ENTRY);
         } else if (warp == 12) {
             // ------------------------------------- MMA -------------------------------------
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -1360,6 +1366,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const float inv = none ? 0.f : 1.f / l_run;
                 const int64_t out_row = (s.q_tok + tok) * p.n_head + s.g * G + head_in;
                 const int64_t part_row = ((int64_t)s.part * kGroups + grp) * 128 + row_in;
+                // Rows leave as 128-byte segments: the lane's row is turned among eight lanes, so that
+                // each store of the warp writes four rows' whole segments and not 32 rows' sixteenths
+                // (whose 32 cache lines an access took 9000 cycles a unit; now see DESIGN).
+                const int my_row = !row_ok ? -1 : (s.part >= 0 ? 0 : (int)out_row);
+                int rows[8];   // of the rows 8 (lane / 8) + k of the warp, whose pieces this lane stores
+#pragma unroll
+                for (int k = 0; k < 8; ++k) rows[k] = __shfl_sync(0xffffffffu, my_row, (lane & 24) + k);
+                uint32_t held[16];   // the first 32 columns of a 64-column segment of halves
+#pragma unroll
+                for (int k = 0; k < 16; ++k) held[k] = 0u;   // (or its registers live through the tiles' loop)
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     if (s.part >= 0 && n_tiles == 0) break;      // (its lse says that nothing is there)
@@ -1398,24 +1414,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 }
                             }
                     }
-                    if (row_ok) {
-                        if (s.part >= 0) {
-                            float4* d = reinterpret_cast<float4*>(p.part_o + part_row * D + c0);
+                    if (s.part >= 0) {
+                        turn_rows(ov);
+                        float* d = p.part_o + (part_row - lane + (lane & 24)) * D + c0 + 4 * (lane & 7);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                d[k] = make_float4(__uint_as_float(ov[4 * k]), __uint_as_float(ov[4 * k + 1]),
-                                                   __uint_as_float(ov[4 * k + 2]), __uint_as_float(ov[4 * k + 3]));
-                        } else {
-                            uint4* d = reinterpret_cast<uint4*>(p.out + out_row * D + c0);
+                        for (int k = 0; k < 8; ++k)
+                            if (rows[k] >= 0) *reinterpret_cast<uint4*>(d + k * D) = make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
+                    } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t w[4];
+                        for (int k = 0; k < 16; ++k) ov[k] = pack_half2(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1]));
+                        if ((c0 & 32) == 0) {
 #pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    w[q] = pack_half2(__uint_as_float(ov[8 * k + 2 * q]), __uint_as_float(ov[8 * k + 2 * q + 1]));
-                                d[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            for (int k = 0; k < 16; ++k) held[k] = ov[k];
+                            continue;
                         }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            ov[16 + k] = ov[k];
+                            ov[k] = held[k];
+                        }
+                        turn_rows(ov);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (rows[k] >= 0)
+                                *reinterpret_cast<uint4*>(p.out + (int64_t)rows[k] * D + c0 - 32 + 8 * (lane & 7)) =
+                                    make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
                     }
                 }
                 if (row_ok) {
@@ -1449,69 +1472,82 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 // parts are then known: one of each share that its line meets and that holds tiles of it.
 // blockIdx.y and the warps take its rows, the lanes a row's dims.
 constexpr int kMergeWarps = 4;
+constexpr int kMaxCtas = 1024;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const __grid_constant__ PrefillParams p, int n_ctas) {
     constexpr int kGroups = Geometry<D>::kGroups;
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t total = total_of<D>(p);
+    Shares sh;
+    sh.set(total_of(p), (uint32_t)n_ctas);
     const int c = blockIdx.x + 1;
-    const int64_t at = share_of(total, c, n_ctas);
-    if (at >= total) return;
-    const Place r = place_of<D>(p, at);
-    if (at == r.start || share_of(total, c - 1, n_ctas) > r.start) return;
+    const uint32_t at = sh.of((uint32_t)c);
+    if (at >= sh.total) return;
+    const Place r = place_of(p, at);
+    if (at == r.start || sh.of((uint32_t)c - 1u) > r.start) return;
+    const int32_t tiles = r.tiles(p);
     Seg s;
-    const int64_t tok0 = r.block * p.block_tokens;
-    const int64_t left = r.x.n_q - tok0;
-    const int64_t tiles = tiles_seen(r.x.len - r.x.n_q + 1 + tok0, left < p.block_tokens ? left : p.block_tokens);
-    make_seg<D>(p, r.x, r.seq, r.g, r.block, 0, tiles, -1, s);
-    // the shares that meet the unit: c - 1 .. last
-    int last = c;
-    while (last + 1 < n_ctas && share_of(total, last + 1, n_ctas) < r.end) ++last;
-    const int n_parts = last - c + 2;
-    // part i's slot, -1: it holds no tile; whole: it holds them all and has written the result
-    bool whole = false;
-    auto slot_of = [&](int i) -> int {
+    make_seg<D>(p, r.x, r.seq, (int)r.g, r.block, 0, tiles, -1, s);
+    // the shares that meet the unit, a thread each: share c - 1 + i's partial slot, -1 without a
+    // tile of it; `whole`: one share holds them all and has written the result itself
+    __shared__ int slot[kMaxCtas];
+    __shared__ int n_parts, whole;
+    if (threadIdx.x == 0) {
+        n_parts = 0;
+        whole = 0;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; c - 1 + i < n_ctas; i += 32 * kMergeWarps) {
         const int cta = c - 1 + i;
-        const int64_t x0 = share_of(total, cta, n_ctas), x1 = share_of(total, cta + 1, n_ctas);
-        const int64_t a = x0 > r.start ? x0 : r.start, b = x1 < r.end ? x1 : r.end;
-        int64_t first, end;
-        tiles_between(r, a, b, tiles, first, end);
-        if (first == 0 && end == tiles) whole = true;
-        return first == end ? -1 : 2 * cta + (a > r.start ? 0 : 1);
-    };
-    for (int i = 0; i < n_parts; ++i) slot_of(i);
+        const uint32_t x0 = sh.of((uint32_t)cta), x1 = sh.of((uint32_t)cta + 1u);
+        if (x0 >= r.end) break;
+        const uint32_t a = max(x0, r.start), b = min(x1, r.end);
+        const int32_t first = r.tile_at(a - r.start, tiles), end = r.tile_at(b - r.start, tiles);
+        if (first == 0 && end == tiles) whole = 1;
+        slot[i] = first == end ? -1 : 2 * cta + (a > r.start ? 0 : 1);
+        atomicMax(&n_parts, i + 1);
+    }
+    __syncthreads();
     if (whole) return;
+    const int parts = n_parts;
     const int G = p.group;
     const int step = kMergeWarps * gridDim.y;
     for (int row = (int)blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < 128 * kGroups; row += step) {
         const int grp = row >> 7, in = row & 127;
         const int tok_in = in / G, tok = grp * p.group_tokens + tok_in;
         if (tok_in >= p.group_tokens || tok >= s.n_tok) continue;
+        // maximum over the parts, a lane each
         float m = -INFINITY;
-        for (int i = 0; i < n_parts; ++i) {
-            const int sl = slot_of(i);
-            if (sl < 0) continue;
-            const float v = p.part_lse[(int64_t)sl * kGroups * 128 + row];
+        for (int i = lane; i < parts; i += 32) {
+            if (slot[i] < 0) continue;
+            const float v = p.part_lse[(int64_t)slot[i] * kGroups * 128 + row];
             m = v > m || v != v ? v : m;  // (a NaN stays)
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float v = __shfl_xor_sync(0xffffffffu, m, o);
+            m = v > m || v != v ? v : m;
         }
         float acc[D / 32] = {};
         float sum = 0.f;
-        for (int i = 0; i < n_parts; ++i) {
-            const int sl = slot_of(i);
-            if (sl < 0) continue;
-            const float v = p.part_lse[(int64_t)sl * kGroups * 128 + row];
-            if (v == -INFINITY) continue;
-            const float w = exp2f((v - m) * 1.4426950408889634f);
-            sum += w;
-            const float4* o = reinterpret_cast<const float4*>(p.part_o + ((int64_t)sl * kGroups * 128 + row) * D);
+        if (m != -INFINITY) {
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) {
+                const int sl = slot[i];
+                if (sl < 0) continue;
+                const float v = p.part_lse[(int64_t)sl * kGroups * 128 + row];
+                if (v == -INFINITY) continue;
+                const float w = exp2f((v - m) * 1.4426950408889634f);
+                sum += w;
+                const float4* o = reinterpret_cast<const float4*>(p.part_o + ((int64_t)sl * kGroups * 128 + row) * D);
 #pragma unroll
-            for (int k = 0; k < D / 128; ++k) {
-                const float4 f = o[32 * k + lane];
-                acc[4 * k] += w * f.x;
-                acc[4 * k + 1] += w * f.y;
-                acc[4 * k + 2] += w * f.z;
-                acc[4 * k + 3] += w * f.w;
+                for (int k = 0; k < D / 128; ++k) {
+                    const float4 f = o[32 * k + lane];
+                    acc[4 * k] += w * f.x;
+                    acc[4 * k + 1] += w * f.y;
+                    acc[4 * k + 2] += w * f.z;
+                    acc[4 * k + 3] += w * f.w;
+                }
             }
         }
         const float inv = m == -INFINITY ? 0.f : 1.f / sum;
@@ -1578,6 +1614,7 @@ cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, in
     e = launch(head_dim == 128 ? kernel_of<128>(kv_type) : kernel_of<256>(kv_type), dim3((unsigned)n_ctas), kThreads,
                (size_t)smem_of(kv_type), args, stream, pdl);
     if (e != cudaSuccess || !p.shares || n_ctas < 2) return e;
+    if (n_ctas > kMaxCtas) return cudaErrorInvalidValue;
     // eight CTAs per boundary: 32 or 16 rows each, so that a merge of a few units fills the device
     return launch(head_dim == 128 ? (const void*)prefill_merge_kernel<128> : (const void*)prefill_merge_kernel<256>,
                   dim3((unsigned)n_ctas - 1u, 8), 32 * kMergeWarps, 0, args, stream, pdl);

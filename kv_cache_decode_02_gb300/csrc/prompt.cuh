@@ -38,7 +38,9 @@ cudaError_t launch_cache_read(const CacheIoParams& p, int kv_type, cudaStream_t 
 
 // ---- causal attention of packed query tokens ----
 struct PrefillParams {
-    CUtensorMap tmap_k, tmap_v;  // 3-D {head_dim, KV heads, cells}, boxes {64, 1, 128} (use_tma)
+    // use_tma: f16 {head_dim, KV heads, cells}, boxes {64, 1, 128}; codes {row bytes, KV heads,
+    // cells}, boxes of 128 dims x 128 cells
+    CUtensorMap tmap_k, tmap_v;
     CUtensorMap tmap_q;       // 3-D {head_dim, heads, tokens}, boxes {64, group, group_tokens}
     const void* k;            // f16: rows k_stride elements apart; quantised: dense planes
     const void* v;
@@ -73,6 +75,9 @@ cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, in
 // limit on waits and its test hook.
 bool encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head, int head_dim, int64_t row_stride,
                         int box_heads, int box_rows);
+// The 3-D map {row bytes, KV heads, rows} of a plane of codes, boxes {box_bytes, 1, box_rows}.
+bool encode_codes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int row_bytes, int box_bytes,
+                      int box_rows);
 bool tma_enabled();
 int device_sms();
 bool log_enabled();

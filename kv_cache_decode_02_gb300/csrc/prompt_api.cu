@@ -55,6 +55,8 @@ Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share) {
     const char* env = std::getenv("KVATTN_PREFILL_CTAS");
     const int sms = device_sms();
     c.shares = may_share && tiles > kMinShareTiles && units < 8 * (int64_t)sms;
+    // (the kernel numbers the line of all tiles, in eighths, in 31 bits)
+    const bool fits = units < INT32_MAX && (tiles + 18) * 8 < INT32_MAX / std::max<int64_t>(units, 1);
     int64_t n = units;
     if (c.shares) n = std::max(units, (units * tiles + kMinShareTiles - 1) / kMinShareTiles);
     c.n_ctas = (int)std::max<int64_t>(std::min<int64_t>(n, sms), 1);
@@ -63,7 +65,7 @@ Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share) {
         c.shares = want > 0;
         c.n_ctas = std::max(std::min(want > 0 ? want : c.n_ctas, sms), 1);
     }
-    if (c.n_ctas == 1) c.shares = false;
+    if (c.n_ctas == 1 || !fits) c.shares = false;
     size_t off = kStatusBytes;
     const size_t rows = c.shares ? (size_t)c.n_ctas * 2 * (size_t)prefill_groups(head_dim) * 128 : 0;
     c.lse_off = off;
@@ -90,9 +92,15 @@ int launch_attention(PrefillParams& p, const void* q, int64_t q_stride, int kv_t
     p.shares = c.shares ? 1 : 0;
     debug_waits(&p.wait_limit_ns, &p.stall_tx);
     if (!encode_prefill_map(&p.tmap_q, q, p.n_tok, n_head, head_dim, q_stride, p.group, p.group_tokens)) return KVATTN_ERR_CUDA;
-    p.use_tma = kv_type == KVATTN_KV_F16 && tma_enabled() &&
-                encode_prefill_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim, p.k_stride, 1, kPrefillTile) &&
-                encode_prefill_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim, p.v_stride, 1, kPrefillTile);
+    if (kv_type == KVATTN_KV_F16) {
+        p.use_tma = encode_prefill_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim, p.k_stride, 1, kPrefillTile) &&
+                    encode_prefill_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim, p.v_stride, 1, kPrefillTile);
+    } else {
+        const int kb = kv_type == KVATTN_KV_Q4_0 ? 4 : 8, vb = kv_type == KVATTN_KV_Q8_0 ? 8 : 4;
+        p.use_tma = encode_codes_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim * kb / 8, 16 * kb, kPrefillTile) &&
+                    encode_codes_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim * vb / 8, 16 * vb, kPrefillTile);
+    }
+    if (!tma_enabled()) p.use_tma = 0;
     if (log_enabled()) {
         char buf[256];
         std::snprintf(buf, sizeof(buf), "%s kv_type=%d n_seq=%d n_tok=%lld n_head=%d/%d head_dim=%d plan=%d shares=%d grid=%d tma=%d",

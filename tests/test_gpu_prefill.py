@@ -261,7 +261,9 @@ def test_without_tensor_maps(kvattn):
     code = ("from kv_cache_decode_02_gb300 import kvattn as K\n"
             "from tests import test_gpu_prefill as t\n"
             "t.check_prefill(K, [300, 70], 8, 2, 128)\n"
-            "t.check_chunk(K, t.make_chunk('f16', [60], [400], 4, 1, 256, True, 0.1))\n")
+            "t.check_chunk(K, t.make_chunk('f16', [60], [400], 4, 1, 256, True, 0.1))\n"
+            "t.check_chunk(K, t.make_chunk('q8_0_q4_0', [60], [400], 4, 1, 256, True, 0.1))\n"
+            "t.check_chunk(K, t.make_chunk('q4_0', [60], [400], 4, 1, 128, False))\n")
     import os
     r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, KVATTN_TMA="0"), capture_output=True, text=True,
                        timeout=300)
