@@ -253,12 +253,21 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
+// mbar_wait_bounded in fewer instructions: the kernel has some forty waits, and its sixteen warps'
+// roles together are at the edge of what the instruction caches hold.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    while (!mbar_test(bar, parity)) {
+        if (*abort != 0 || global_ns() - t0 > limit_ns) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
@@ -286,20 +295,21 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w, bool& bad) {
 // Stored value = scale x code, rounded once to half: the type of an f16 cache (2^-11 of the
 // value, where the 8-bit code itself is off by up to 2^-8 of the block's largest).  Scales
 // above 515 could pass the largest half; those products are kept at it (as cache_read does).  In
-// a cut tile what is not finite is dropped and its cell noted.
-template <int N>
-__device__ __forceinline__ void finish(uint32_t (&o)[N], uint32_t scale, bool cut, uint32_t* bad_row, int cell) {
-    if ((scale & 0x7fffu) > 0x6006u) {   // 515
-        const __half2 top = __halves2half2(__ushort_as_half(0x7bffu), __ushort_as_half(0x7bffu));
+// a cut tile what is not finite is dropped and its cell noted.  Both are done to 16 bytes of a
+// slot after they were stored, and rarely.
+constexpr uint32_t kBigScale = 0x6006u;   // 515
+__device__ __forceinline__ void amend(unsigned char* at, bool cut, uint32_t* bad_row, int cell) {
+    const __half2 top = __halves2half2(__ushort_as_half(0x7bffu), __ushort_as_half(0x7bffu));
+    uint4 w = *reinterpret_cast<uint4*>(at);
+    uint32_t o[4] = {w.x, w.y, w.z, w.w};
+    bool bad = false;
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(o[i]), top), __hneg2(top)));
+    for (int i = 0; i < 4; ++i) {
+        o[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(o[i]), top), __hneg2(top)));
+        if (cut) o[i] = finite2(o[i], bad);
     }
-    if (cut) {
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = finite2(o[i], bad);
-        if (bad) atomicOr(&bad_row[cell >> 5], 1u << (cell & 31));
-    }
+    *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (bad) atomicOr(&bad_row[cell >> 5], 1u << (cell & 31));
 }
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : (x > hi ? hi : x); }
@@ -488,11 +498,17 @@ struct Walk {
         }
     }
     // The next piece in s; false: none left.
-    __device__ __forceinline__ bool next(const PrefillParams& p, Seg& s) { return p.shares ? next_share(p, s) : next_whole(p, s); }
+    __device__ __forceinline__ bool next(const PrefillParams& p, Seg& s) {
+        int32_t first = 0, last = INT_MAX;
+        int part = -1;
+        if (!(p.shares ? next_share(p, first, last, part) : next_whole(p))) return false;
+        make_seg<D>(p, r.x, r.seq, (int)r.g, r.block, first, last, part, s);
+        return true;
+    }
 
     // Unit number i counts from the last sequence's last block (the longest rows of a prompt
     // first), KV heads fastest; round r deals them out forwards or backwards.
-    __device__ __forceinline__ bool next_whole(const PrefillParams& p, Seg& s) {
+    __device__ __forceinline__ bool next_whole(const PrefillParams& p) {
         const uint32_t n = gridDim.x, c = blockIdx.x;
         const uint32_t i = round * n + ((round & 1u) ? n - 1u - c : c);
         if (i < round * n) return false;  // (beyond 32 bits)
@@ -505,9 +521,10 @@ struct Walk {
             const uint32_t hit = __ballot_sync(0xffffffffu, b < seen + sum);
             if (hit != 0u) {
                 const int l = __ffs(hit) - 1;
-                const Sequence y = from_lane(x, l);
-                const uint32_t before = seen + __shfl_sync(0xffffffffu, sum, l) - y.blocks;
-                make_seg<D>(p, y, top - 1 - l, (int)g, y.blocks - 1u - (b - before), 0, INT_MAX, -1, s);
+                r.x = from_lane(x, l);
+                r.seq = top - 1 - l;
+                r.g = g;
+                r.block = r.x.blocks - 1u - (b - (seen + __shfl_sync(0xffffffffu, sum, l) - r.x.blocks));
                 return true;
             }
             seen += __shfl_sync(0xffffffffu, sum, 31);
@@ -515,7 +532,7 @@ struct Walk {
         return false;
     }
 
-    __device__ __forceinline__ bool next_share(const PrefillParams& p, Seg& s) {
+    __device__ __forceinline__ bool next_share(const PrefillParams& p, int32_t& first, int32_t& last, int& part) {
         while (at < end) {
             if (!started || (r.block + 1u == r.x.blocks && r.g + 1u == (uint32_t)p.n_head_kv)) {
                 r = place_of(p, at);
@@ -531,15 +548,36 @@ struct Walk {
             const uint32_t a = at, b = min(r.end, end);
             at = b;
             const int32_t tiles = r.tiles(p);
-            const int32_t first = r.tile_at(a - r.start, tiles), last = r.tile_at(b - r.start, tiles);
+            first = r.tile_at(a - r.start, tiles);
+            last = r.tile_at(b - r.start, tiles);
             if (tiles == 0 ? a != r.start : first == last) continue;  // (a unit that sees nothing: its first piece)
-            const bool whole = first == 0 && last == tiles;
-            make_seg<D>(p, r.x, r.seq, (int)r.g, r.block, first, last, whole ? -1 : 2 * (int)blockIdx.x + (a > r.start ? 0 : 1), s);
+            part = first == 0 && last == tiles ? -1 : 2 * (int)blockIdx.x + (a > r.start ? 0 : 1);
             return true;
         }
         return false;
     }
 };
+
+// The order in which the MMA warp takes a piece's slots: at head_dim 128 K0 V0 K1 V1 .., at 256
+// K0 K1 V0 K2 V1 .. with two slots (halves of the dims) each.
+template <int HALVES>
+__device__ __forceinline__ void slot_number(int step, int n_max, bool& v_side, int& j, int& half) {
+    if (HALVES == 1) {
+        v_side = step & 1;
+        j = step >> 1;
+        half = 0;
+        return;
+    }
+    const int q = step >> 1;
+    half = step & 1;
+    if (q == 0 || q == 2 * n_max - 1) {
+        v_side = q != 0;
+        j = q == 0 ? 0 : n_max - 1;
+    } else {
+        v_side = !(q & 1);
+        j = v_side ? (q >> 1) - 1 : (q >> 1) + 1;
+    }
+}
 
 // A tile's cells, in a warp: lane l holds cells l, l + 32, l + 64, l + 96.
 struct Tile {
@@ -674,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     pdl_wait();
     const int G = p.group;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(bar), parity, abort_flag, p.wait_limit_ns));
+        return __all_sync(0xffffffffu, wait_bar(smem_addr(bar), parity, abort_flag, p.wait_limit_ns));
     };
     // piece number i (in the order of the scheduler); false: no more, or a wait that gave up
     auto take = [&](uint32_t i, Seg& s) -> bool {
@@ -701,11 +739,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         uint32_t n = 0;                 // quantised: raw slots turned
         uint32_t landed_use = 0;        // a bit per slot: parity of its landed barrier
         Seg s = {};
-        auto begin_tile = [&](Tile& t) {
-            if (!settle(p, t)) bad_entry = true;
-            if (p.plan != nullptr && warp == 8) write_mask(h, t, T);
-            ++T;
-        };
         // Cells with V that is not finite, of a cut tile (unit number i's).
         auto note = [&](uint32_t i, int j, int c, bool bad) {
             if (bad) atomicOr(&h->bad_cells[i % kRing][(j - s.first_cut) % kCutTiles][c >> 5], 1u << (c & 31));
@@ -732,16 +765,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int b = (lt & 15) * 16;
                 unsigned char* plane = slot + (b >> 7) * kPlaneBytes;
 #pragma unroll 1
-                for (int i0 = 0; i0 < 16; i0 += 8) {
-                    uint4 w[8];
+                for (int i0 = 0; i0 < 16; i0 += 4) {
+                    uint4 w[4];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const int64_t cell = cell_of(p, t, (lt >> 4) + 8 * (i0 + k));
                         w[k] = make_uint4(0u, 0u, 0u, 0u);
                         if (cell >= 0) w[k] = __ldg(reinterpret_cast<const uint4*>(rows + cell * stride + b / 2));
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const int c = (lt >> 4) + 8 * (i0 + k);
                         if (cut) {
                             bool bad = false;
@@ -814,38 +847,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
                 if (warp == 8 && lane < 4 * kCutTiles) h->bad_cells[i % kRing][lane >> 2][lane & 3] = 0u;
                 asm volatile("bar.sync 1, 128;" ::: "memory");   // (before any of them is set)
-                if (n_max > 0) {
-                    Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
-                    begin_tile(tk);
-                    if (kHalves == 1) {
-                        for (int j = 0; j < n_max; ++j) {
-                            fill(tk, false, 0, i, j);
-                            if (!ok) break;
+                Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
+#pragma unroll 1
+                for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
+                    bool v_side;
+                    int j, half;
+                    slot_number<kHalves>(step, n_max, v_side, j, half);
+                    if (!v_side && half == 0) {   // a tile begins (its V comes after the next one's K at 256)
+                        if (j > 0) {
                             tv = tk;
-                            if (j + 1 < n_max) {
-                                tk = next;
-                                begin_tile(tk);
-                                next = read_tile(p, s, j + 2);
-                            }
-                            fill(tv, true, 0, i, j);
-                            if (!ok) break;
+                            tk = next;
+                            next = read_tile(p, s, j + 1);
                         }
-                    } else {   // K of tile j + 1 before V of tile j; each in two halves
-                        for (int j = -1; j < n_max && ok; ++j) {
-                            if (j >= 0) {
-                                tv = tk;
-                                if (j + 1 < n_max) {
-                                    tk = next;
-                                    begin_tile(tk);
-                                    next = read_tile(p, s, j + 2);
-                                }
-                            }
-#pragma unroll 1
-                            for (int half = 0; half < 2 && ok && j + 1 < n_max; ++half) fill(tk, false, half, i, j + 1);
-#pragma unroll 1
-                            for (int half = 0; half < 2 && ok && j >= 0; ++half) fill(tv, true, half, i, j);
-                        }
+                        if (!settle(p, tk)) bad_entry = true;
+                        if (p.plan != nullptr && warp == 8) write_mask(h, tk, T);
+                        ++T;
                     }
+                    if (v_side && (kHalves == 1 || j + 1 == n_max)) tv = tk;
+                    fill(v_side ? tv : tk, v_side, half, i, j);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&h->load_done[i % kRing]));
@@ -868,66 +887,90 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     const unsigned short* scales = reinterpret_cast<const unsigned short*>(stage + Memory<KBITS>::kRawBytes - 1024);
                     unsigned char* slot = slots + (filled % kSlots) * kSlotBytes;
                     uint32_t* bad_row = h->bad_cells[unit % kRing][(word >> 4) & 3u];
-                    // (all loads first: the stores cannot be seen not to alias them)
                     if (bits == 8) {
                         const int piece = lt & 7;  // halves 16 piece .. of the row: bytes 32 piece ..
                         unsigned char* plane = slot + (piece >> 2) * kPlaneBytes;
                         const int c0 = lt >> 3;    // cells c0, c0 + 16, ..: the same place in the swizzle
-                        const uint32_t o0 = swz(c0, (piece & 3) * 32), o1 = swz(c0, (piece & 3) * 32 + 16);
-                        uint4 w[8];
-                        uint32_t ds[8];
+                        const uint32_t oa = swz(c0, (piece & 3) * 32), ob = oa ^ 16u;
+                        // (the upper plane's lanes store in the other order: eight lanes, eight bank groups)
+                        const bool upper = piece >= 4;
+                        unsigned char* d0 = plane + (upper ? ob : oa);
+                        unsigned char* d1 = plane + (upper ? oa : ob);
+                        const unsigned char* src = stage + 16 * lt;
+                        const unsigned short* sc = scales + 4 * c0 + (piece >> 1);
+                        // four cells at a time, loads first: the stores cannot be seen not to alias them
+#pragma unroll 1
+                        for (int k0 = 0; k0 < 8; k0 += 4) {
+                            uint4 w[4];
+                            uint32_t ds[4], big = 0;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            w[k] = *reinterpret_cast<const uint4*>(stage + 16 * lt + 2048 * k);
-                            ds[k] = scales[4 * c0 + (piece >> 1) + 64 * k];
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const __half2 d = scale2(ds[k]);
-                            const uint32_t x[4] = {w[k].x ^ 0x80808080u, w[k].y ^ 0x80808080u, w[k].z ^ 0x80808080u,
-                                                   w[k].w ^ 0x80808080u};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                o[2 * q] = hmul2_u32(i8x2_lo(x[q]), as_u32(d));
-                                o[2 * q + 1] = hmul2_u32(i8x2_hi(x[q]), as_u32(d));
+                            for (int k = 0; k < 4; ++k) {
+                                w[k] = *reinterpret_cast<const uint4*>(src + 2048 * (k0 + k));
+                                ds[k] = sc[64 * (k0 + k)];
+                                big = max(big, ds[k] & 0x7fffu);
                             }
-                            finish<8>(o, ds[k], cut, bad_row, c0 + 16 * k);
-                            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-                            // (the upper plane's lanes in the other order: eight lanes, eight bank groups)
-                            *reinterpret_cast<uint4*>(plane + (piece < 4 ? o0 : o1) + 2048 * k) = piece < 4 ? a : b;
-                            *reinterpret_cast<uint4*>(plane + (piece < 4 ? o1 : o0) + 2048 * k) = piece < 4 ? b : a;
+                            const bool odd = cut || big > kBigScale;   // rare: a loop of its own below
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t d = as_u32(scale2(ds[k]));
+                                const uint32_t x[4] = {w[k].x ^ 0x80808080u, w[k].y ^ 0x80808080u, w[k].z ^ 0x80808080u,
+                                                       w[k].w ^ 0x80808080u};
+                                uint32_t o[8];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    o[2 * q] = hmul2_u32(i8x2_lo(x[q]), d);
+                                    o[2 * q + 1] = hmul2_u32(i8x2_hi(x[q]), d);
+                                }
+                                const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+                                *reinterpret_cast<uint4*>(d0 + 2048 * (k0 + k)) = upper ? b : a;
+                                *reinterpret_cast<uint4*>(d1 + 2048 * (k0 + k)) = upper ? a : b;
+                            }
+                            if (odd)
+#pragma unroll 1
+                                for (int k = 0; k < 4; ++k) {
+                                    amend(d0 + 2048 * (k0 + k), cut, bad_row, c0 + 16 * (k0 + k));
+                                    amend(d1 + 2048 * (k0 + k), cut, bad_row, c0 + 16 * (k0 + k));
+                                }
                         }
                     } else {
                         const int piece = lt & 3;  // block `piece`: halves 32 piece .., bytes 64 piece ..
                         unsigned char* plane = slot + (piece >> 1) * kPlaneBytes;
                         const int c0 = lt >> 2;    // cells c0, c0 + 32, ..
                         const int b = (piece & 1) * 64;
-                        uint4 w[4];
-                        uint32_t ds[4];
+#pragma unroll 1
+                        for (int k0 = 0; k0 < 4; k0 += 2) {
+                            uint4 w[2];
+                            uint32_t ds[2], big = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            w[k] = *reinterpret_cast<const uint4*>(stage + 16 * lt + 2048 * k);
-                            ds[k] = scales[4 * c0 + piece + 128 * k];
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t d = as_u32(scale2(ds[k]));
-                            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                            uint32_t o[16];  // elements 0-15 and 16-31 of the block
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const uint32_t a = prmt_b32(x[q], 0u, 0x4140u), e = prmt_b32(x[q], 0u, 0x4342u);
-                                o[2 * q] = hmul2_u32(nib2(a & 0x000f000fu), d);
-                                o[2 * q + 1] = hmul2_u32(nib2(e & 0x000f000fu), d);
-                                o[8 + 2 * q] = hmul2_u32(nib2((a >> 4) & 0x000f000fu), d);
-                                o[9 + 2 * q] = hmul2_u32(nib2((e >> 4) & 0x000f000fu), d);
+                            for (int k = 0; k < 2; ++k) {
+                                w[k] = *reinterpret_cast<const uint4*>(stage + 16 * lt + 2048 * (k0 + k));
+                                ds[k] = scales[4 * c0 + piece + 128 * (k0 + k)];
+                                big = max(big, ds[k] & 0x7fffu);
                             }
-                            finish<16>(o, ds[k], cut, bad_row, c0 + 32 * k);
+                            const bool odd = cut || big > kBigScale;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                *reinterpret_cast<uint4*>(plane + swz(c0, b + 16 * q) + 4096 * k) =
-                                    make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t d = as_u32(scale2(ds[k]));
+                                const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                                uint32_t o[16];  // elements 0-15 and 16-31 of the block
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const uint32_t a = prmt_b32(x[q], 0u, 0x4140u), e = prmt_b32(x[q], 0u, 0x4342u);
+                                    o[2 * q] = hmul2_u32(nib2(a & 0x000f000fu), d);
+                                    o[2 * q + 1] = hmul2_u32(nib2(e & 0x000f000fu), d);
+                                    o[8 + 2 * q] = hmul2_u32(nib2((a >> 4) & 0x000f000fu), d);
+                                    o[9 + 2 * q] = hmul2_u32(nib2((e >> 4) & 0x000f000fu), d);
+                                }
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    *reinterpret_cast<uint4*>(plane + swz(c0, b + 16 * q) + 4096 * (k0 + k)) =
+                                        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                            }
+                            if (odd)
+#pragma unroll 1
+                                for (int i = 0; i < 8; ++i)
+                                    amend(plane + swz(c0, b + 16 * (i & 3)) + 4096 * (k0 + (i >> 2)), cut, bad_row,
+                                          c0 + 32 * (k0 + (i >> 2)));
                         }
                     }
                     fence_async();
@@ -1041,40 +1084,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     give_back(i);
                     continue;
                 }
-                auto begin_tile = [&](Tile& t) {
-                    if (!settle(p, t)) bad_entry = true;
-                    if (p.plan != nullptr) write_mask(h, t, T);
-                    ++T;
-                };
-                auto word_of = [&](bool v_side, int half, int j) -> uint32_t {
-                    const bool cut = v_side && j >= s.first_cut;
-                    return unit | (v_side ? 1u : 0u) | (cut ? 2u | ((uint32_t)(j - s.first_cut) << 4) : 0u) |
-                           ((v_side && j + 1 == n_max && half + 1 == kHalves) ? 4u : 0u);
-                };
-                Tile tk = read_tile(p, s, 0), next = read_tile(p, s, 1);
-                begin_tile(tk);
-                if (kHalves == 1) {    // K0 V0 K1 V1 ..
-                    for (int j = 0; j < n_max && ok; ++j) {
-                        bring(tk, false, 0, word_of(false, 0, j));
-                        if (ok) bring(tk, true, 0, word_of(true, 0, j));
-                        tk = next;
-                        if (j + 1 < n_max) begin_tile(tk);
-                        next = read_tile(p, s, j + 2);
-                    }
-                } else {               // K0 K1 V0 K2 V1 .., two slots each
-                    Tile tv = tk;
-                    for (int j = -1; j < n_max && ok; ++j) {
-                        if (j >= 0) {
+                Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
+#pragma unroll 1
+                for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
+                    bool v_side;
+                    int j, half;
+                    slot_number<kHalves>(step, n_max, v_side, j, half);
+                    if (!v_side && half == 0) {
+                        if (j > 0) {
                             tv = tk;
                             tk = next;
-                            if (j + 1 < n_max) begin_tile(tk);
-                            next = read_tile(p, s, j + 2);
+                            next = read_tile(p, s, j + 1);
                         }
-#pragma unroll 1
-                        for (int half = 0; half < 2 && ok && j + 1 < n_max; ++half) bring(tk, false, half, word_of(false, half, j + 1));
-#pragma unroll 1
-                        for (int half = 0; half < 2 && ok && j >= 0; ++half) bring(tv, true, half, word_of(true, half, j));
+                        if (!settle(p, tk)) bad_entry = true;
+                        if (p.plan != nullptr) write_mask(h, tk, T);
+                        ++T;
                     }
+                    if (v_side && (kHalves == 1 || j + 1 == n_max)) tv = tk;
+                    const bool cut = v_side && j >= s.first_cut;
+                    bring(v_side ? tv : tk, v_side, half,
+                          unit | (v_side ? 1u : 0u) | (cut ? 2u | ((uint32_t)(j - s.first_cut) << 4) : 0u) |
+                              (step + 1 == 2 * kHalves * n_max ? 4u : 0u));
                 }
                 give_back(i);
             }
@@ -1244,27 +1274,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     const uint32_t t_s = tmem + lane_base + kColS1 * buf;
                     if (!(ok = wait_all(&h->s_full[buf], par))) break;
                     tc_fence_after();
+                    const int rel = rel0 - j * kPrefillTile;
+                    if (pre || !__all_sync(0xffffffffu, rel >= kPrefillTile)) {
+                        // (the rare tiles: scaled, masked and put back by a loop of its own, which keeps
+                        // the code of the others short)
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(t_s + c0, x);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const float f = __uint_as_float(x[c]);
+                                x[c] = c0 + c >= rel ? 0xff800000u : __float_as_uint(pre ? f * p.scale_log2 : f);
+                            }
+                            tmem_st32(t_s + c0, x);
+                        }
+                        tc_wait_st();
+                    }
                     uint32_t sv[128];
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) tmem_ld32(t_s + c, sv + c);
-                    const int rel = rel0 - j * kPrefillTile;
                     tc_wait_ld();
-                    if (pre) {
-                        const uint64_t f = pack2(p.scale_log2, p.scale_log2);
-#pragma unroll
-                        for (int c = 0; c < 128; c += 2) {
-                            float a, b;
-                            unpack2(mul2(pack2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), f), a, b);
-                            sv[c] = __float_as_uint(a);
-                            sv[c + 1] = __float_as_uint(b);
-                        }
-                    }
-                    if (!__all_sync(0xffffffffu, rel >= kPrefillTile)) {
-                        const int lim = rel;
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (c >= lim) sv[c] = 0xff800000u;
-                    }
                     if (p.plan != nullptr) {
                         // (the loader's write, ordered by a barrier of its own; the tile's V slot is
                         // released after this thread's P, and the ring is deeper than the slots reach)
@@ -1369,10 +1400,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // Rows leave as 128-byte segments: the lane's row is turned among eight lanes, so that
                 // each store of the warp writes four rows' whole segments and not 32 rows' sixteenths
                 // (whose 32 cache lines an access took 9000 cycles a unit; now see DESIGN).
-                const int my_row = !row_ok ? -1 : (s.part >= 0 ? 0 : (int)out_row);
+                const int my_row = !row_ok ? -1 : (int)(s.part >= 0 ? part_row : out_row);
                 int rows[8];   // of the rows 8 (lane / 8) + k of the warp, whose pieces this lane stores
 #pragma unroll
                 for (int k = 0; k < 8; ++k) rows[k] = __shfl_sync(0xffffffffu, my_row, (lane & 24) + k);
+                char* to = s.part >= 0 ? reinterpret_cast<char*>(p.part_o) : reinterpret_cast<char*>(p.out);
+                const int64_t row_bytes = s.part >= 0 ? D * 4 : D * 2;
                 uint32_t held[16];   // the first 32 columns of a 64-column segment of halves
 #pragma unroll
                 for (int k = 0; k < 16; ++k) held[k] = 0u;   // (or its registers live through the tiles' loop)
@@ -1414,13 +1447,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 }
                             }
                     }
-                    if (s.part >= 0) {
-                        turn_rows(ov);
-                        float* d = p.part_o + (part_row - lane + (lane & 24)) * D + c0 + 4 * (lane & 7);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (rows[k] >= 0) *reinterpret_cast<uint4*>(d + k * D) = make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
-                    } else {
+                    if (s.part < 0) {   // halves: two 32-column pieces a segment
 #pragma unroll
                         for (int k = 0; k < 16; ++k) ov[k] = pack_half2(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1]));
                         if ((c0 & 32) == 0) {
@@ -1433,13 +1460,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             ov[16 + k] = ov[k];
                             ov[k] = held[k];
                         }
-                        turn_rows(ov);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (rows[k] >= 0)
-                                *reinterpret_cast<uint4*>(p.out + (int64_t)rows[k] * D + c0 - 32 + 8 * (lane & 7)) =
-                                    make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
                     }
+                    turn_rows(ov);
+                    char* d = to + (s.part >= 0 ? c0 * 4 : (c0 - 32) * 2) + 16 * (lane & 7);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (rows[k] >= 0)
+                            *reinterpret_cast<uint4*>(d + rows[k] * row_bytes) =
+                                make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
                 }
                 if (row_ok) {
                     const float v = none ? -INFINITY : (m_run - kLift + fast_log2(l_run)) * kLn2;
