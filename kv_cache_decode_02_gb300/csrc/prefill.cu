@@ -29,9 +29,9 @@
 //    scaled by 2^7 (it cancels in O / l): with the lazily moved maximum below p stays under
 //    2^15, and p of 2^-21 of a row's largest still has all its f16 bits.
 //  * loader (warps 8-11): fills a ring of 32 KB slots, each 128 cells x 128 dims of K or V in
-//    two 128-byte-swizzled planes.  f16: warp 8 issues TMA boxes for tiles whose cells are one
-//    physical run (holes and the end of a sequence included), warps 9-11 mend V tiles that need
-//    it, and all four copy tiles that are no run.  Quantised: warp 14 brings codes (TMA) and
+//    two 128-byte-swizzled planes.  f16: warp 8 issues a TMA box for each slot whose cells are
+//    one physical run (holes and the end of a sequence included); warps 9-11 mend V slots that
+//    need it afterwards, and copy the slots of tiles that are no run.  Quantised: warp 14 brings codes (TMA) and
 //    scales (cp.async) into a ring of raw bytes, and these four turn them into f16.
 //  * MMA (warp 12): one elected lane issues tcgen05.mma.  S of one row group is computed while
 //    the softmax of the other runs (head_dim 128: two S and two O accumulators fill the 512
@@ -100,9 +100,17 @@ struct Seg {
     int part;            // partial slot, or -1: the whole unit
 };
 
+// f16: a slot that warps 9-11 mend or copy, or the end of a unit.
+struct Job {
+    uint32_t n;          // slot number
+    int32_t j;           // tile, from the piece's first
+    uint32_t word;       // type | V << 2 | half << 3 | unit << 8
+};
+constexpr uint32_t kJobMend = 0, kJobCopy = 1, kJobUnit = 2, kJobEnd = 3;
+
 struct Header {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t landed[kMaxSlots];  // the TMA of a V tile that is mended afterwards
+    uint64_t mended[kMaxSlots];  // a V slot that is mended after it landed
     uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // quantised: a slot's raw bytes; they are turned
     uint64_t q_full, q_empty;    // the unit's query rows; its last S is complete
     uint64_t s_full[2];          // S is in TMEM (of row group t, or of buffer b)
@@ -112,12 +120,15 @@ struct Header {
     uint64_t mask_full[kRing];   // through a plan: a tile's bias and holes are written
     uint64_t load_done[kRing];   // every slot of a unit is filled, its bad_cells are complete
     uint64_t seg_full[kRing], seg_empty[kRing];
+    uint64_t job_full[kRing], job_empty[kRing];
     uint32_t tmem;
     int abort_flag;
     uint32_t bad_cells[kRing][kCutTiles][4];  // of a unit: cells of its cut tiles with V that is not finite
     uint32_t holes[kRing];                    // whether the tile has any
+    uint32_t slot_mend[kMaxSlots];            // whether the slot is one
     uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | unit << 8
     Seg seg[kRing];
+    Job job[kRing];
     alignas(16) float bias[kRing][kPrefillTile];  // through a plan: +inf, or -inf for a hole
 };
 static_assert(sizeof(Header) <= kHeaderBytes && offsetof(Header, bias) % 16 == 0, "header");
@@ -203,30 +214,27 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void tma_box4(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
 // arrives on bar when this thread's cp.async so far are complete (adds itself to the phase's
 // pending arrivals first: the phase must be held open by an arrival that comes later)
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// Eight lanes that hold eight 16-byte pieces each of a row of their own: afterwards lane i of
-// them holds piece i of all eight rows (piece k from the k-th lane).
-__device__ __forceinline__ void turn_rows(uint32_t (&r)[32]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int s = 1; s < 8; s <<= 1) {
-        const bool up = lane & s;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (k & s) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t& lo = r[4 * k + i];
-                uint32_t& hi = r[4 * (k | s) + i];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
-                lo = up ? got : lo;
-                hi = up ? hi : got;
-            }
-        }
+// 32 bytes, one sector where the address allows it
+__device__ __forceinline__ void st_sector(void* at, const uint32_t* r, bool whole) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                     "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(at)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        reinterpret_cast<uint4*>(at)[1] = make_uint4(r[4], r[5], r[6], r[7]);
     }
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -278,6 +286,12 @@ __device__ __forceinline__ __half2 scale2(uint32_t d) {
 }
 __device__ __forceinline__ uint32_t nib2(uint32_t n) {
     return as_u32(__hsub2(as_h2(n | 0x64006400u), as_h2(0x64086408u)));
+}
+// Whether eight halves are all finite: adding 1 to an exponent of ones carries into the sign.
+__device__ __forceinline__ bool finite8(const uint4& w) {
+    const uint32_t a = (w.x & 0x7c007c00u) + 0x04000400u, b = (w.y & 0x7c007c00u) + 0x04000400u;
+    const uint32_t c = (w.z & 0x7c007c00u) + 0x04000400u, d = (w.w & 0x7c007c00u) + 0x04000400u;
+    return ((a | b | c | d) & 0x80008000u) == 0u;
 }
 // Zeros in place of the halves that are not finite; `bad` is set when there was one.
 __device__ __forceinline__ uint32_t finite2(uint32_t w, bool& bad) {
@@ -673,9 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     if (tid == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
-            mbar_init(smem_addr(&h->full[i]), 4);   // a lane of each loader warp (and its copies)
-            mbar_init(smem_addr(&h->empty[i]), 1);  // the MMA lane's commit
-            mbar_init(smem_addr(&h->landed[i]), 1);
+            mbar_init(smem_addr(&h->full[i]), kQuant ? 4 : 1);  // the loader's warps, or warp 8
+            mbar_init(smem_addr(&h->empty[i]), 1);              // the MMA lane's commit
+            mbar_init(smem_addr(&h->mended[i]), 3);             // warps 9-11
         }
         for (int i = 0; i < kRawStages; ++i) {
             mbar_init(smem_addr(&h->raw_full[i]), 1);
@@ -691,7 +705,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(smem_addr(&h->pv_done), 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_addr(&h->mask_full[i]), 1);
-            mbar_init(smem_addr(&h->load_done[i]), 4);
+            mbar_init(smem_addr(&h->load_done[i]), kQuant ? 4 : 3);
+            mbar_init(smem_addr(&h->job_full[i]), 1);
+            mbar_init(smem_addr(&h->job_empty[i]), 3);
             mbar_init(smem_addr(&h->seg_full[i]), 1);
             mbar_init(smem_addr(&h->seg_empty[i]), (kQuant ? 2 : 5) + 4 * kGroups);  // loader, MMA and softmax warps
         }
@@ -735,14 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int lt = tid - 256;       // 0 .. 127
         bool bad_entry = false, ok = true;
         uint32_t filled = 0;            // slots
-        uint32_t T = 0;                 // tiles begun
         uint32_t n = 0;                 // quantised: raw slots turned
-        uint32_t landed_use = 0;        // a bit per slot: parity of its landed barrier
         Seg s = {};
-        // Cells with V that is not finite, of a cut tile (unit number i's).
-        auto note = [&](uint32_t i, int j, int c, bool bad) {
-            if (bad) atomicOr(&h->bad_cells[i % kRing][(j - s.first_cut) % kCutTiles][c >> 5], 1u << (c & 31));
-        };
         auto wait_slot_empty = [&]() -> bool {
             const uint32_t use = filled / kSlots;
             return use == 0 || wait_all(&h->empty[filled % kSlots], (use - 1) & 1u);
@@ -757,118 +767,148 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         };
 
         if constexpr (!kQuant) {
-            // ---- f16 ----
-            // f16 rows of a slot by all four warps: 16 lanes a row, 8 rows at a time
-            auto copy_rows = [&](unsigned char* slot, const Tile& t, bool v_side, int half, bool cut, uint32_t i, int j) {
-                const int64_t stride = v_side ? p.v_stride : p.k_stride;
-                const __half* rows = static_cast<const __half*>(v_side ? p.v : p.k) + (int64_t)s.g * D + half * 128;
-                const int b = (lt & 15) * 16;
-                unsigned char* plane = slot + (b >> 7) * kPlaneBytes;
+            if (warp == 8) {
+                // ---- f16: fills the slots by TMA, and leaves jobs to warps 9-11 ----
+                uint32_t jobs = 0, T = 0;     // jobs given, tiles begun
+                auto give_job = [&](uint32_t word, int j) -> bool {
+                    const uint32_t e = jobs % kRing;
+                    if (jobs >= kRing && !wait_all(&h->job_empty[e], (jobs / kRing - 1u) & 1u)) return false;
+                    if (lane == 0) {
+                        h->job[e] = Job{filled, j, word};
+                        mbar_arrive(smem_addr(&h->job_full[e]));
+                    }
+                    __syncwarp();
+                    ++jobs;
+                    return true;
+                };
+                for (uint32_t i = 0; ok; ++i) {
+                    if (!take(i, s)) break;
+                    const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+                    const uint32_t unit = (i & 0xffffu) << 8;
+                    Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
 #pragma unroll 1
-                for (int i0 = 0; i0 < 16; i0 += 4) {
-                    uint4 w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int64_t cell = cell_of(p, t, (lt >> 4) + 8 * (i0 + k));
-                        w[k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (cell >= 0) w[k] = __ldg(reinterpret_cast<const uint4*>(rows + cell * stride + b / 2));
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = (lt >> 4) + 8 * (i0 + k);
-                        if (cut) {
-                            bool bad = false;
-                            w[k].x = finite2(w[k].x, bad);
-                            w[k].y = finite2(w[k].y, bad);
-                            w[k].z = finite2(w[k].z, bad);
-                            w[k].w = finite2(w[k].w, bad);
-                            note(i, j, c, bad);
+                    for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
+                        bool v_side;
+                        int j, half;
+                        slot_number<kHalves>(step, n_max, v_side, j, half);
+                        if (!v_side && half == 0) {   // a tile begins (its V comes after the next one's K at 256)
+                            if (j > 0) {
+                                tv = tk;
+                                tk = next;
+                                next = read_tile(p, s, j + 1);
+                            }
+                            if (!settle(p, tk)) bad_entry = true;
+                            if (p.plan != nullptr) write_mask(h, tk, T);
+                            ++T;
                         }
-                        *reinterpret_cast<uint4*>(plane + swz(c, b & 127)) = w[k];
-                    }
-                }
-                fence_async();
-            };
-            // V rows that landed: zeros for cells that are not there and, in a cut tile, for what
-            // is not finite (warps 9-11, 16 lanes a row)
-            auto mend = [&](unsigned char* slot, const Tile& t, bool cut, uint32_t i, int j) {
-                const int sub = lane >> 4, b = (lane & 15) * 16;
-                unsigned char* plane = slot + (b >> 7) * kPlaneBytes;
-                for (int r = 2 * (warp - 9); r < 128; r += 6) {
-                    const int c = r + sub;   // (r is even: both rows in one word of entries)
-                    const int32_t v = __shfl_sync(0xffffffffu, (r & 64) ? ((r & 32) ? t.e[3] : t.e[2]) : ((r & 32) ? t.e[1] : t.e[0]),
-                                                  c & 31);
-                    uint4* at = reinterpret_cast<uint4*>(plane + swz(c, b & 127));
-                    if (v < 0) {
-                        *at = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (cut) {
-                        uint4 w = *at;
-                        bool bad = false;
-                        w.x = finite2(w.x, bad);
-                        w.y = finite2(w.y, bad);
-                        w.z = finite2(w.z, bad);
-                        w.w = finite2(w.w, bad);
-                        if (bad) *at = w;
-                        note(i, j, c, bad);
-                    }
-                }
-                fence_async();
-            };
-            auto fill = [&](const Tile& t, bool v_side, int half, uint32_t i, int j) {
-                if (!(ok = wait_slot_empty())) return;
-                const int st = (int)(filled % kSlots);
-                unsigned char* slot = slots + st * kSlotBytes;
-                const bool cut = v_side && j >= s.first_cut;
-                uint64_t* bar = &h->full[st];
-                stall_hook(bar);
-                if (t.run && p.use_tma != 0) {
-                    const bool later = v_side && (cut || t.holes);
-                    if (warp == 8) {
+                        if (v_side && (kHalves == 1 || j + 1 == n_max)) tv = tk;
+                        const bool run = (v_side ? tv.run : tk.run) && p.use_tma != 0;
+                        const bool job = !run || (v_side && (j >= s.first_cut || tv.holes));
+                        if (!(ok = wait_slot_empty())) break;
+                        const uint32_t st = filled % kSlots;
                         if (lane == 0) {
-                            const uint32_t b = smem_addr(later ? &h->landed[st] : bar);
-                            mbar_expect_tx(b, (uint32_t)kSlotBytes);
-                            const CUtensorMap* map = v_side ? &p.tmap_v : &p.tmap_k;
-                            tma_box(smem_addr(slot), map, half * 128, s.g, (int)t.base, b);
-                            tma_box(smem_addr(slot) + kPlaneBytes, map, half * 128 + 64, s.g, (int)t.base, b);
-                            if (later) mbar_arrive(b);
+                            const uint32_t bar = smem_addr(&h->full[st]);
+                            h->slot_mend[st] = job ? 1u : 0u;
+                            if (filled == 0 && p.stall_tx != 0u) mbar_expect_tx(bar, p.stall_tx);
+                            if (run) {
+                                mbar_expect_tx(bar, (uint32_t)kSlotBytes);
+                                tma_box4(smem_addr(slots + st * kSlotBytes), v_side ? &p.tmap_v : &p.tmap_k, 0,
+                                         (int)(v_side ? tv.base : tk.base), 2 * half, s.g, bar);
+                            }
+                            mbar_arrive(bar);
                         }
-                    } else if (later) {
-                        if (!(ok = wait_all(&h->landed[st], (landed_use >> st) & 1u))) return;
-                        mend(slot, t, cut, i, j);
+                        __syncwarp();
+                        if (job && !(ok = give_job(unit | (run ? kJobMend : kJobCopy) | (v_side ? 4u : 0u) | (half ? 8u : 0u), j))) break;
+                        ++filled;
                     }
-                    if (later) landed_use ^= 1u << st;
-                } else {
-                    copy_rows(slot, t, v_side, half, cut, i, j);
+                    ok = ok && give_job(unit | kJobUnit, 0);
+                    give_back(i);
                 }
-                slot_ready(bar);
-            };
-            for (uint32_t i = 0; ok; ++i) {
-                if (!take(i, s)) break;
-                const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
-                if (warp == 8 && lane < 4 * kCutTiles) h->bad_cells[i % kRing][lane >> 2][lane & 3] = 0u;
-                asm volatile("bar.sync 1, 128;" ::: "memory");   // (before any of them is set)
-                Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
+                if (ok) give_job(kJobEnd, 0);
+            } else {
+                // ---- warps 9-11: rows that TMA cannot bring, or that are mended after it did ----
+                for (uint32_t k = 0;; ++k) {
+                    const uint32_t e = k % kRing;
+                    if (!wait_all(&h->job_full[e], (k / kRing) & 1u)) break;
+                    const Job job = h->job[e];
+                    const uint32_t type = job.word & 3u;
+                    if (type == kJobEnd) break;
+                    const uint32_t i = (job.word >> 8) & 0xffffu;   // (kRing divides 65536)
+                    if (type == kJobUnit) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&h->load_done[i % kRing]));
+                        give_back(i);
+                    } else {
+                        s = h->seg[i % kRing];                      // (not given back yet)
+                        const bool v_side = job.word & 4u, cut = v_side && job.j >= s.first_cut;
+                        const int half = (job.word >> 3) & 1u;
+                        Tile t = read_tile(p, s, job.j);
+                        settle(p, t);
+                        const uint32_t st = job.n % kSlots;
+                        const int sub = lane >> 4, b = (lane & 15) * 16;      // 16 lanes a row
+                        unsigned char* plane = slots + st * kSlotBytes + (b >> 7) * kPlaneBytes;
+                        uint32_t* bad_row = h->bad_cells[i % kRing][cut ? (job.j - s.first_cut) % kCutTiles : 0];
+                        if (type == kJobMend) {
+                            // (MMA waits for the mended slot, so this use of it is not over)
+                            if (!wait_all(&h->full[st], (job.n / kSlots) & 1u)) break;
 #pragma unroll 1
-                for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
-                    bool v_side;
-                    int j, half;
-                    slot_number<kHalves>(step, n_max, v_side, j, half);
-                    if (!v_side && half == 0) {   // a tile begins (its V comes after the next one's K at 256)
-                        if (j > 0) {
-                            tv = tk;
-                            tk = next;
-                            next = read_tile(p, s, j + 1);
+                            for (int k4 = 0; k4 < 4; ++k4) {                  // 32 cells at a time
+                                const int32_t e = k4 < 2 ? (k4 ? t.e[1] : t.e[0]) : (k4 == 2 ? t.e[2] : t.e[3]);
+                                const uint32_t gone = __ballot_sync(0xffffffffu, e < 0);
+                                if (!cut && gone == 0u) continue;
+                                unsigned char* cells = plane + 4096 * k4;
+#pragma unroll
+                                for (int q = 0; q < 6; ++q) {
+                                    const int c = 2 * (3 * q + warp - 9) + sub;
+                                    if (c >= 32) continue;
+                                    uint4* at = reinterpret_cast<uint4*>(cells + swz(c, b & 127));
+                                    if ((gone >> c) & 1u) {
+                                        *at = make_uint4(0u, 0u, 0u, 0u);
+                                    } else if (cut) {
+                                        uint4 w = *at;
+                                        if (!finite8(w)) {
+                                            bool bad;
+                                            w = make_uint4(finite2(w.x, bad), finite2(w.y, bad), finite2(w.z, bad), finite2(w.w, bad));
+                                            *at = w;
+                                            atomicOr(&bad_row[k4], 1u << c);
+                                        }
+                                    }
+                                }
+                            }
+                        } else {
+                            const char* rows = reinterpret_cast<const char*>(static_cast<const __half*>(v_side ? p.v : p.k) +
+                                                                             (int64_t)s.g * D + half * 128) + b;
+                            const int64_t row_bytes = (v_side ? p.v_stride : p.k_stride) * 2;
+#pragma unroll 1
+                            for (int r0 = 2 * (warp - 9); r0 < 128; r0 += 24) {   // four rows in flight
+                                uint4 w[4];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int64_t cell = cell_of(p, t, min(r0 + 6 * q, 126) + sub);
+                                    w[q] = make_uint4(0u, 0u, 0u, 0u);
+                                    if (cell >= 0) w[q] = __ldg(reinterpret_cast<const uint4*>(rows + cell * row_bytes));
+                                }
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int c = r0 + 6 * q + sub;
+                                    if (c >= 128) continue;
+                                    if (cut && !finite8(w[q])) {
+                                        bool bad;
+                                        w[q] = make_uint4(finite2(w[q].x, bad), finite2(w[q].y, bad), finite2(w[q].z, bad),
+                                                          finite2(w[q].w, bad));
+                                        atomicOr(&bad_row[c >> 5], 1u << (c & 31));
+                                    }
+                                    *reinterpret_cast<uint4*>(plane + swz(c, b & 127)) = w[q];
+                                }
+                            }
                         }
-                        if (!settle(p, tk)) bad_entry = true;
-                        if (p.plan != nullptr && warp == 8) write_mask(h, tk, T);
-                        ++T;
+                        fence_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&h->mended[st]));
                     }
-                    if (v_side && (kHalves == 1 || j + 1 == n_max)) tv = tk;
-                    fill(v_side ? tv : tk, v_side, half, i, j);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&h->job_empty[e]));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&h->load_done[i % kRing]));
-                give_back(i);
             }
         } else {
             // ---- quantised: turns the raw slots that warp 14 brings ----
@@ -998,6 +1038,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 Seg s;
                 if (!walk.next(p, s)) s.n_tok = -1;
                 if (i >= kRing && !wait_all(&h->seg_empty[i % kRing], ((i / kRing) - 1) & 1u)) break;
+                if (lane < 4 * kCutTiles) h->bad_cells[i % kRing][lane >> 2][lane & 3] = 0u;
+                __syncwarp();
                 if (lane == 0) {
                     h->seg[i % kRing] = s;
                     mbar_arrive(smem_addr(&h->seg_full[i % kRing]));
@@ -1076,7 +1118,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             };
             for (uint32_t i = 0; ok; ++i) {
                 if (!take(i, s)) break;
-                if (lane < 4 * kCutTiles) h->bad_cells[i % kRing][lane >> 2][lane & 3] = 0u;
                 const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
                 const uint32_t unit = (i & 0xffffu) << 8;
                 if (n_max == 0) {    // (the turning warps still sign the unit off)
@@ -1113,49 +1154,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (__any_sync(0xffffffffu, bad_entry) && lane == 0) atomicOr(p.status, KVATTN_DEVICE_BAD_PLAN_ENTRY);
         } else if (warp == 12) {
             // ------------------------------------- MMA -------------------------------------
+            // (every operand is the same in all lanes, and known to be: values from shared memory
+            // are broadcast from lane 0)
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            uint32_t n = 0;                   // slots consumed
-            uint32_t done[2] = {0u, 0u};      // head_dim 128: tiles of the row groups so far; 256: [0] tiles
-            uint32_t q_uses = 0;
-            auto wait_slot = [&](uint32_t s) -> bool {
-                if (!wait_all(&h->full[s % kSlots], (s / kSlots) & 1u)) return false;
-                fence_async();  // rows that ordinary stores wrote
+            const uint32_t slot0 = smem_addr(slots), q_addr = smem_addr(q_tiles);
+            uint32_t mends = 0;               // a bit per slot: parity of its mended barrier
+            uint32_t st = 0, use = 0;         // the next slot, and the parity of its use
+            auto wait_slot = [&]() -> bool {
+                if (!wait_all(&h->full[st], use)) return false;
+                if (!kQuant && __shfl_sync(0xffffffffu, h->slot_mend[st], 0) != 0u) {
+                    if (!wait_all(&h->mended[st], (mends >> st) & 1u)) return false;
+                    mends ^= 1u << st;
+                }
                 tc_fence_after();
                 return true;
             };
+            auto next_slot = [&]() {
+                ++st;
+                if (st == kSlots) {
+                    st = 0;
+                    use ^= 1u;
+                }
+            };
             // S (+)= Q K^T over 128 dims: 8 steps of 16, 32 bytes of the swizzled rows each
-            auto issue_s = [&](uint32_t d, uint32_t q_addr, uint32_t slot, bool acc) {
-                const uint64_t qd = smem_desc(q_addr, 16, 1024);
-                const uint64_t kd = smem_desc(smem_addr(slots + (slot % kSlots) * kSlotBytes), 16, 1024);
+            auto issue_s = [&](uint32_t d, uint32_t q_tile, uint32_t slot, bool acc) {
+                const uint64_t qd = smem_desc(q_tile, 16, 1024), kd = smem_desc(slot0 + slot * kSlotBytes, 16, 1024);
+                mma_ss(d, qd, kd, kIdQK, acc ? 1u : 0u);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 1; k < 8; ++k) {
                     const uint64_t off = (uint64_t)(((k >> 2) * kPlaneBytes + 32 * (k & 3)) >> 4);
-                    mma_ss(d, qd + off, kd + off, kIdQK, (acc || k > 0) ? 1u : 0u);
+                    mma_ss(d, qd + off, kd + off, kIdQK, 1u);
                 }
             };
             // O (+)= P V over 128 cells: 8 steps of 16 cells; A = f16 pairs in TMEM
             auto issue_pv = [&](uint32_t d, uint32_t a, uint32_t slot, bool acc) {
-                const uint64_t vd = smem_desc(smem_addr(slots + (slot % kSlots) * kSlotBytes), kPlaneBytes, 1024);
+                const uint64_t vd = smem_desc(slot0 + slot * kSlotBytes, kPlaneBytes, 1024);
+                mma_ts(d, a, vd, kIdPV, acc ? 1u : 0u);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(d, a + 8 * k, vd + (uint64_t)((2048 * k) >> 4), kIdPV, (acc || k > 0) ? 1u : 0u);
+                for (int k = 1; k < 8; ++k) mma_ts(d, a + 8 * k, vd + (uint64_t)((2048 * k) >> 4), kIdPV, 1u);
             };
-            const uint32_t q_addr = smem_addr(q_tiles);
+            uint32_t done[2] = {0u, 0u};      // head_dim 128: tiles of the row groups so far; 256: [0] tiles
+            uint32_t q_uses = 0;
             bool ok = true;
-            Seg s;
             for (uint32_t i = 0; ok; ++i) {
-                if (!take(i, s)) break;
+                if (!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u)) break;
+                const Seg& s = h->seg[i % kRing];
+                const int n_tok = __shfl_sync(0xffffffffu, s.n_tok, 0);
+                const int n0 = __shfl_sync(0xffffffffu, s.n[0], 0), n1 = __shfl_sync(0xffffffffu, s.n[1], 0);
+                if (n_tok < 0) break;
                 give_back(i);
-                const int n0 = s.n[0], n1 = s.n[1], n_max = n0 > n1 ? n0 : n1;
+                const int n_max = n0 > n1 ? n0 : n1;
                 if (n_max == 0) continue;
                 if (!(ok = wait_all(&h->q_full, q_uses & 1u))) break;
                 ++q_uses;
                 tc_fence_after();
                 if (kGroups == 2) {
-                    for (int j = 0; j <= n_max && ok; ++j) {
-                        const uint32_t ks = n, vs = n + 1, v_last = n - 1;
+                    uint32_t vs = 0;          // V of the tile before
+                    for (int j = 0; j <= n_max; ++j) {
+                        const uint32_t ks = st;
                         if (j < n_max) {
-                            if (!(ok = wait_slot(ks))) break;
+                            if (!(ok = wait_slot())) break;
+                            next_slot();
                             if (j < n0 && elect_one()) {
                                 issue_s(tm, q_addr, ks, false);
                                 mma_commit(smem_addr(&h->s_full[0]));
@@ -1167,10 +1226,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             tc_fence_after();
                             if (elect_one()) {
                                 if (j - 1 < n1) {
-                                    issue_pv(tm + kColO + 128, tm + kColS1, v_last, j > 1);
+                                    issue_pv(tm + kColO + 128, tm + kColS1, vs, j > 1);
                                     if (j == n1) mma_commit(smem_addr(&h->o_full[1]));
                                 }
-                                mma_commit(smem_addr(&h->empty[v_last % kSlots]));
+                                mma_commit(smem_addr(&h->empty[vs]));
                             }
                             __syncwarp();
                         }
@@ -1180,11 +1239,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 issue_s(tm + kColS1, q_addr + kQTileBytes, ks, false);
                                 mma_commit(smem_addr(&h->s_full[1]));
                             }
-                            mma_commit(smem_addr(&h->empty[ks % kSlots]));
+                            mma_commit(smem_addr(&h->empty[ks]));
                             if (j + 1 == n_max) mma_commit(smem_addr(&h->q_empty));
                         }
                         __syncwarp();
-                        if (!(ok = wait_slot(vs))) break;
+                        vs = st;
+                        if (!(ok = wait_slot())) break;
+                        next_slot();
                         if (j < n0) {
                             if (!(ok = wait_all(&h->p_full[0], (done[0] + j) & 1u))) break;
                             tc_fence_after();
@@ -1194,47 +1255,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             }
                             __syncwarp();
                         }
-                        n += 2;
                     }
                     done[0] += n0;
                     done[1] += n1;
                 } else {
-                    // S of a tile into buffer T & 1, its two halves of the dims in turn
-                    auto issue_tile_s = [&](int j) -> bool {
-                        const uint32_t buf = (done[0] + j) & 1u;
+                    for (int j = -1; j < n_max && ok; ++j) {
+                        // S of tile j + 1 into its buffer, its two halves of the dims in turn
+                        if (j + 1 < n_max) {
+                            const uint32_t buf = (done[0] + j + 1) & 1u;
 #pragma unroll 1
-                        for (int half = 0; half < 2; ++half, ++n) {
-                            if (!wait_slot(n)) return false;
-                            if (elect_one()) {
-                                issue_s(tm + kColS1 * buf, q_addr + half * kQTileBytes, n, half > 0);
-                                mma_commit(smem_addr(&h->empty[n % kSlots]));
-                                if (half == 1) {
-                                    mma_commit(smem_addr(&h->s_full[buf]));
-                                    if (j + 1 == n_max) mma_commit(smem_addr(&h->q_empty));
+                            for (int half = 0; half < 2; ++half) {
+                                if (!(ok = wait_slot())) break;
+                                if (elect_one()) {
+                                    issue_s(tm + kColS1 * buf, q_addr + half * kQTileBytes, st, half > 0);
+                                    mma_commit(smem_addr(&h->empty[st]));
+                                    if (half == 1) {
+                                        mma_commit(smem_addr(&h->s_full[buf]));
+                                        if (j + 2 == n_max) mma_commit(smem_addr(&h->q_empty));
+                                    }
                                 }
+                                __syncwarp();
+                                next_slot();
                             }
-                            __syncwarp();
                         }
-                        return true;
-                    };
-                    ok = issue_tile_s(0);
-                    for (int j = 0; j < n_max && ok; ++j) {
-                        if (j + 1 < n_max && !(ok = issue_tile_s(j + 1))) break;
-                        const uint32_t t = done[0] + j, buf = t & 1u;
-                        if (!(ok = wait_all(&h->p_full[buf], (t >> 1) & 1u))) break;
+                        if (j < 0 || !ok) continue;
+                        const uint32_t tile = done[0] + j, buf = tile & 1u;
+                        if (!(ok = wait_all(&h->p_full[buf], (tile >> 1) & 1u))) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int half = 0; half < 2; ++half, ++n) {
-                            if (!(ok = wait_slot(n))) break;
+                        for (int half = 0; half < 2; ++half) {
+                            if (!(ok = wait_slot())) break;
                             if (elect_one()) {
-                                issue_pv(tm + kColO + 128 * half, tm + kColS1 * buf, n, j > 0);
-                                mma_commit(smem_addr(&h->empty[n % kSlots]));
+                                issue_pv(tm + kColO + 128 * half, tm + kColS1 * buf, st, j > 0);
+                                mma_commit(smem_addr(&h->empty[st]));
                                 if (half == 1) {
                                     mma_commit(smem_addr(&h->pv_done));
                                     if (j + 1 == n_max) mma_commit(smem_addr(&h->o_full[0]));
                                 }
                             }
                             __syncwarp();
+                            next_slot();
                         }
                     }
                     done[0] += n0;
@@ -1397,18 +1457,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const float inv = none ? 0.f : 1.f / l_run;
                 const int64_t out_row = (s.q_tok + tok) * p.n_head + s.g * G + head_in;
                 const int64_t part_row = ((int64_t)s.part * kGroups + grp) * 128 + row_in;
-                // Rows leave as 128-byte segments: the lane's row is turned among eight lanes, so that
-                // each store of the warp writes four rows' whole segments and not 32 rows' sixteenths
-                // (whose 32 cache lines an access took 9000 cycles a unit; now see DESIGN).
-                const int my_row = !row_ok ? -1 : (int)(s.part >= 0 ? part_row : out_row);
-                int rows[8];   // of the rows 8 (lane / 8) + k of the warp, whose pieces this lane stores
-#pragma unroll
-                for (int k = 0; k < 8; ++k) rows[k] = __shfl_sync(0xffffffffu, my_row, (lane & 24) + k);
-                char* to = s.part >= 0 ? reinterpret_cast<char*>(p.part_o) : reinterpret_cast<char*>(p.out);
-                const int64_t row_bytes = s.part >= 0 ? D * 4 : D * 2;
-                uint32_t held[16];   // the first 32 columns of a 64-column segment of halves
-#pragma unroll
-                for (int k = 0; k < 16; ++k) held[k] = 0u;   // (or its registers live through the tiles' loop)
+                // (a thread stores its own row, in whole 32-byte sectors: a row of halves or floats
+                // lies in lines of its own, and turning rows among lanes first took longer)
+                char* to = s.part >= 0 ? reinterpret_cast<char*>(p.part_o + part_row * D) : reinterpret_cast<char*>(p.out + out_row * D);
+                const bool sectors = p.out_sectors != 0;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     if (s.part >= 0 && n_tiles == 0) break;      // (its lse says that nothing is there)
@@ -1447,27 +1499,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 }
                             }
                     }
-                    if (s.part < 0) {   // halves: two 32-column pieces a segment
+                    if (!row_ok) continue;
+                    if (s.part >= 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) st_sector(to + 4 * c0 + 32 * k, ov + 8 * k, true);
+                    } else {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) ov[k] = pack_half2(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1]));
-                        if ((c0 & 32) == 0) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) held[k] = ov[k];
-                            continue;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            ov[16 + k] = ov[k];
-                            ov[k] = held[k];
-                        }
+                        st_sector(to + 2 * c0, ov, sectors);
+                        st_sector(to + 2 * c0 + 32, ov + 8, sectors);
                     }
-                    turn_rows(ov);
-                    char* d = to + (s.part >= 0 ? c0 * 4 : (c0 - 32) * 2) + 16 * (lane & 7);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (rows[k] >= 0)
-                            *reinterpret_cast<uint4*>(d + rows[k] * row_bytes) =
-                                make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]);
                 }
                 if (row_ok) {
                     const float v = none ? -INFINITY : (m_run - kLift + fast_log2(l_run)) * kLn2;

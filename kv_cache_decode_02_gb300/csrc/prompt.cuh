@@ -38,8 +38,8 @@ cudaError_t launch_cache_read(const CacheIoParams& p, int kv_type, cudaStream_t 
 
 // ---- causal attention of packed query tokens ----
 struct PrefillParams {
-    // use_tma: f16 {head_dim, KV heads, cells}, boxes {64, 1, 128}; codes {row bytes, KV heads,
-    // cells}, boxes of 128 dims x 128 cells
+    // use_tma: f16 rows (encode_planes_map), or codes (encode_codes_map), boxes of 128 dims x 128
+    // cells
     CUtensorMap tmap_k, tmap_v;
     CUtensorMap tmap_q;       // 3-D {head_dim, heads, tokens}, boxes {64, group, group_tokens}
     const void* k;            // f16: rows k_stride elements apart; quantised: dense planes
@@ -63,6 +63,7 @@ struct PrefillParams {
     int block_tokens;         // tokens of a unit: two row groups at head_dim 128, one at 256
     int shares;               // 1: equal shares of all units' tiles, cut anywhere; 0: whole units
     int use_tma;
+    int out_sectors;          // out is 32-byte aligned
     float scale_log2;         // scale * log2(e)
 };
 constexpr int kPrefillTile = 128;  // cells per tile
@@ -75,6 +76,9 @@ cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, in
 // limit on waits and its test hook.
 bool encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head, int head_dim, int64_t row_stride,
                         int box_heads, int box_rows);
+// The 4-D map {64, rows, head_dim / 64 planes, KV heads} of half rows, boxes {64, 128, 2, 1} with
+// the 128-byte swizzle: 128 cells x 128 dims as two planes in one copy.
+bool encode_planes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int head_dim, int64_t row_stride);
 // The 3-D map {row bytes, KV heads, rows} of a plane of codes, boxes {box_bytes, 1, box_rows}.
 bool encode_codes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int row_bytes, int box_bytes,
                       int box_rows);

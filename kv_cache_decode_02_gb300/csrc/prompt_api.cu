@@ -90,11 +90,12 @@ int launch_attention(PrefillParams& p, const void* q, int64_t q_stride, int kv_t
     p.block_tokens = p.group_tokens * prefill_groups(head_dim);
     p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
     p.shares = c.shares ? 1 : 0;
+    p.out_sectors = aligned(p.out, 32) ? 1 : 0;
     debug_waits(&p.wait_limit_ns, &p.stall_tx);
     if (!encode_prefill_map(&p.tmap_q, q, p.n_tok, n_head, head_dim, q_stride, p.group, p.group_tokens)) return KVATTN_ERR_CUDA;
     if (kv_type == KVATTN_KV_F16) {
-        p.use_tma = encode_prefill_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim, p.k_stride, 1, kPrefillTile) &&
-                    encode_prefill_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim, p.v_stride, 1, kPrefillTile);
+        p.use_tma = encode_planes_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim, p.k_stride) &&
+                    encode_planes_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim, p.v_stride);
     } else {
         const int kb = kv_type == KVATTN_KV_Q4_0 ? 4 : 8, vb = kv_type == KVATTN_KV_Q8_0 ? 8 : 4;
         p.use_tma = encode_codes_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim * kb / 8, 16 * kb, kPrefillTile) &&
