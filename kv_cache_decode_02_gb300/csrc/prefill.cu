@@ -25,7 +25,7 @@
 //  * softmax (warps 0-3 and 4-7, 128 threads each): thread t holds row t, which is TMEM lane
 //    t: a row's maximum and sum need no exchange between threads.  At head_dim 128 each group
 //    has its own row group; at 256 the first has the unit's and the second is idle.  The thread
-//    reads its row of S from tensor memory, masks, and writes p over it as f16 pairs.  p is
+//    reads its row of S from tensor memory, masks, and writes p there as f16 pairs.  p is
 //    scaled by 2^7 (it cancels in O / l): with the lazily moved maximum below p stays under
 //    2^15, and p of 2^-21 of a row's largest still has all its f16 bits.
 //  * loader (warps 8-11): fills a ring of 32 KB slots, each 128 cells x 128 dims of K or V in
@@ -33,10 +33,11 @@
 //    one physical run (holes and the end of a sequence included); warps 9-11 mend V slots that
 //    need it afterwards, and copy the slots of tiles that are no run.  Quantised: warp 14 brings codes (TMA) and
 //    scales (cp.async) into a ring of raw bytes, and these four turn them into f16.
-//  * MMA (warp 12): one elected lane issues tcgen05.mma.  S of one row group is computed while
-//    the softmax of the other runs (head_dim 128: two S and two O accumulators fill the 512
-//    TMEM columns), or S of the next tile while the softmax of this one runs (256: two S and
-//    a 256-column O).
+//  * MMA (warp 12): one elected lane issues tcgen05.mma.  The 512 TMEM columns hold two buffers
+//    of S, over which p is written, and O (2 x 128 columns, or 256).  With both row groups at
+//    work each has a buffer, and a group's products run under the other's softmax; with one (256,
+//    or at most 128 rows) its tiles take the buffers in turn, and S of the next tile runs under
+//    the softmax of this one.
 //  * scheduler (warp 13): finds the next unit's sequence, block and tiles while the others work,
 //    and issues the TMA of its query rows once the last S of the unit before is complete.
 //
@@ -68,7 +69,8 @@ constexpr int kSlotBytes = 2 * kPlaneBytes;   // 128 cells x 128 dims of f16
 constexpr int kQTileBytes = 2 * kPlaneBytes;  // 128 rows x 128 dims of f16
 constexpr int kMaxSlots = 5;
 constexpr int kHeaderBytes = 3072;
-constexpr int kRing = 4;                      // tiles whose masks, and units whose plans, are kept
+constexpr int kRing = 4;                      // pieces of work whose plans are kept
+constexpr int kMasks = 3;                     // tiles whose masks are
 constexpr int kRawStages = 3;                 // quantised: slots of raw bytes in flight
 constexpr int kCutTiles = 3;                  // tiles that only some of a unit's (<= 256) tokens see whole
 constexpr float kSlack = 8.f;                 // lazy maximum
@@ -113,23 +115,23 @@ struct Header {
     uint64_t mended[kMaxSlots];  // a V slot that is mended after it landed
     uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // quantised: a slot's raw bytes; they are turned
     uint64_t q_full, q_empty;    // the unit's query rows; its last S is complete
-    uint64_t s_full[2];          // S is in TMEM (of row group t, or of buffer b)
-    uint64_t p_full[2];          // p is
-    uint64_t pv_done;            // head_dim 256: P V of a tile is complete
-    uint64_t o_full[2];          // a row group's last P V is complete
-    uint64_t mask_full[kRing];   // through a plan: a tile's bias and holes are written
+    // an S buffer holds S, or p: [0] the first, [1] the second of group 1, [2] the second of group
+    // 0 (each is waited for in every phase, by one group)
+    uint64_t s_full[3], p_full[3];
+    uint64_t pv_done[3];         // its P V is complete
+    uint64_t mask_full[kMasks], mask_empty[kMasks];  // through a plan: a tile's bias and holes are written, read
     uint64_t load_done[kRing];   // every slot of a unit is filled, its bad_cells are complete
     uint64_t seg_full[kRing], seg_empty[kRing];
     uint64_t job_full[kRing], job_empty[kRing];
     uint32_t tmem;
     int abort_flag;
     uint32_t bad_cells[kRing][kCutTiles][4];  // of a unit: cells of its cut tiles with V that is not finite
-    uint32_t holes[kRing];                    // whether the tile has any
+    uint32_t holes[kMasks];                   // whether the tile has any
     uint32_t slot_mend[kMaxSlots];            // whether the slot is one
     uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | unit << 8
     Seg seg[kRing];
     Job job[kRing];
-    alignas(16) float bias[kRing][kPrefillTile];  // through a plan: +inf, or -inf for a hole
+    alignas(16) float bias[kMasks][kPrefillTile];  // through a plan: +inf, or -inf for a hole
 };
 static_assert(sizeof(Header) <= kHeaderBytes && offsetof(Header, bias) % 16 == 0, "header");
 
@@ -421,12 +423,12 @@ struct Place {
         const int32_t t = tok0(p);
         return tiles_seen((int64_t)x.len - x.n_q + 1 + t, min(x.n_q - t, p.block_tokens));
     }
-    // the tile that position y of the unit (from its start) falls on
-    __device__ __forceinline__ int32_t tile_at(uint32_t y, int32_t n) const {
-        const int32_t t = ((int32_t)y - 8 * (int32_t)kUnitCost) >> 3;
-        return y >= end - start ? n : min(max(t, 0), n);
-    }
 };
+// The tile that position y of a unit of that length and n tiles falls on.
+__device__ __forceinline__ int32_t tile_at(uint32_t y, uint32_t length, int32_t n) {
+    const int32_t t = ((int32_t)y - 8 * (int32_t)kUnitCost) >> 3;
+    return y >= length ? n : min(max(t, 0), n);
+}
 __device__ __forceinline__ Place place_of(const PrefillParams& p, uint32_t at) {
     Place r = {};
     uint32_t base = 0;
@@ -498,6 +500,7 @@ struct Walk {
     uint32_t round;
     // shares
     uint32_t at, end;
+    Shares sh;
     Place r;
     bool started;
 
@@ -505,10 +508,10 @@ struct Walk {
         round = 0;
         started = false;
         if (p.shares) {
-            Shares sh;
             sh.set(total_of(p), gridDim.x);
             at = sh.of(blockIdx.x);
             end = sh.of(blockIdx.x + 1u);
+            if ((threadIdx.x & 31) == 0) p.cuts[blockIdx.x].n_parts = 0;
         }
     }
     // The next piece in s; false: none left.
@@ -562,8 +565,21 @@ struct Walk {
             const uint32_t a = at, b = min(r.end, end);
             at = b;
             const int32_t tiles = r.tiles(p);
-            first = r.tile_at(a - r.start, tiles);
-            last = r.tile_at(b - r.start, tiles);
+            first = tile_at(a - r.start, r.end - r.start, tiles);
+            last = tile_at(b - r.start, r.end - r.start, tiles);
+            // a unit whose first piece is here and whose last is not: the merge joins its parts
+            if (a == r.start && b != r.end && tiles > 0 && (threadIdx.x & 31) == 0) {
+                PrefillCut* cut = p.cuts + blockIdx.x;
+                int parts = 1;
+                while (sh.of(blockIdx.x + (uint32_t)parts) < r.end) ++parts;
+                cut->q_tok = r.x.q0 + r.tok0(p);
+                cut->n_tok = min(r.x.n_q - r.tok0(p), p.block_tokens);
+                cut->g = (int32_t)r.g;
+                cut->tiles = tiles;
+                cut->start = r.start;
+                cut->end = r.end;
+                cut->n_parts = parts;
+            }
             if (tiles == 0 ? a != r.start : first == last) continue;  // (a unit that sees nothing: its first piece)
             part = first == 0 && last == tiles ? -1 : 2 * (int)blockIdx.x + (a > r.start ? 0 : 1);
             return true;
@@ -572,19 +588,16 @@ struct Walk {
     }
 };
 
-// The order in which the MMA warp takes a piece's slots: at head_dim 128 K0 V0 K1 V1 .., at 256
-// K0 K1 V0 K2 V1 .. with two slots (halves of the dims) each.
+// The order in which the MMA warp takes a piece's slots, HALVES (128 of the dims each) per tile of
+// K or V: with both row groups at work K0 V0 K1 V1 .., with one K0 K1 V0 K2 V1 ...
 template <int HALVES>
-__device__ __forceinline__ void slot_number(int step, int n_max, bool& v_side, int& j, int& half) {
-    if (HALVES == 1) {
-        v_side = step & 1;
-        j = step >> 1;
-        half = 0;
-        return;
-    }
-    const int q = step >> 1;
-    half = step & 1;
-    if (q == 0 || q == 2 * n_max - 1) {
+__device__ __forceinline__ void slot_number(int step, int n_max, bool dual, bool& v_side, int& j, int& half) {
+    const int q = step / HALVES;
+    half = step % HALVES;
+    if (dual) {
+        v_side = q & 1;
+        j = q >> 1;
+    } else if (q == 0 || q == 2 * n_max - 1) {
         v_side = q != 0;
         j = q == 0 ? 0 : n_max - 1;
     } else {
@@ -644,16 +657,6 @@ __device__ __forceinline__ bool settle(const PrefillParams& p, Tile& t) {
     t.holes = __any_sync(0xffffffffu, hole);
     return good;
 }
-// Writes a plan tile's holes for the softmax (tile number T of the CTA), from one warp.
-__device__ __forceinline__ void write_mask(Header* h, const Tile& t, uint32_t T) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t r = T % kRing;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = t.e[k] < 0 ? -INFINITY : INFINITY;
-    if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
-}
 // Physical cell of the tile's cell c (which may differ from lane to lane), -1: none.
 __device__ __forceinline__ int64_t cell_of(const PrefillParams& p, const Tile& t, int c) {
     const int32_t v0 = __shfl_sync(0xffffffffu, t.e[0], c & 31);
@@ -671,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr int kGroups = Geometry<D>::kGroups, kHalves = Geometry<D>::kHalves;
     constexpr bool kQuant = KBITS != 16;
     constexpr int kSlots = Memory<KBITS>::kSlots;
+    // TMEM columns: two buffers of S, over which p is written; O of the row groups
     constexpr uint32_t kColS1 = 128, kColO = 256;
     // the swizzled planes want a 1024-byte aligned base; with no static shared memory the window
     // starts on one, and nothing is left to align it with
@@ -691,20 +695,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(smem_addr(&h->empty[i]), 1);              // the MMA lane's commit
             mbar_init(smem_addr(&h->mended[i]), 3);             // warps 9-11
         }
+        for (int i = 0; i < kMasks; ++i) {
+            mbar_init(smem_addr(&h->mask_full[i]), 1);
+            mbar_init(smem_addr(&h->mask_empty[i]), 4 * kGroups);
+        }
         for (int i = 0; i < kRawStages; ++i) {
             mbar_init(smem_addr(&h->raw_full[i]), 1);
             mbar_init(smem_addr(&h->raw_empty[i]), 4);
         }
         mbar_init(smem_addr(&h->q_full), 1);
         mbar_init(smem_addr(&h->q_empty), 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(smem_addr(&h->s_full[i]), 1);
             mbar_init(smem_addr(&h->p_full[i]), 128);
-            mbar_init(smem_addr(&h->o_full[i]), 1);
+            mbar_init(smem_addr(&h->pv_done[i]), 1);
         }
-        mbar_init(smem_addr(&h->pv_done), 1);
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(smem_addr(&h->mask_full[i]), 1);
             mbar_init(smem_addr(&h->load_done[i]), kQuant ? 4 : 3);
             mbar_init(smem_addr(&h->job_full[i]), 1);
             mbar_init(smem_addr(&h->job_empty[i]), 3);
@@ -739,6 +745,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     auto give_back = [&](uint32_t i) {
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&h->seg_empty[i % kRing]));
+    };
+
+    // a plan tile's holes, for the softmax (tile number T of the CTA), from one warp
+    auto put_mask = [&](const Tile& t, uint32_t T) -> bool {
+        const uint32_t r = T % kMasks;
+        if (T >= kMasks && !wait_all(&h->mask_empty[r], (T / kMasks - 1u) & 1u)) return false;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = t.e[k] < 0 ? -INFINITY : INFINITY;
+        if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
+        return true;
     };
 
     if (warp >= 8 && warp < 12) {
@@ -790,18 +808,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
                         bool v_side;
                         int j, half;
-                        slot_number<kHalves>(step, n_max, v_side, j, half);
-                        if (!v_side && half == 0) {   // a tile begins (its V comes after the next one's K at 256)
+                        slot_number<kHalves>(step, n_max, s.n[1] > 0, v_side, j, half);
+                        if (!v_side && half == 0) {   // a tile begins (its V may come after the next one's K)
                             if (j > 0) {
                                 tv = tk;
                                 tk = next;
                                 next = read_tile(p, s, j + 1);
                             }
                             if (!settle(p, tk)) bad_entry = true;
-                            if (p.plan != nullptr) write_mask(h, tk, T);
+                            if (p.plan != nullptr && !(ok = put_mask(tk, T))) break;
                             ++T;
                         }
-                        if (v_side && (kHalves == 1 || j + 1 == n_max)) tv = tk;
+                        if (v_side && (s.n[1] > 0 || j + 1 == n_max)) tv = tk;
                         const bool run = (v_side ? tv.run : tk.run) && p.use_tma != 0;
                         const bool job = !run || (v_side && (j >= s.first_cut || tv.holes));
                         if (!(ok = wait_slot_empty())) break;
@@ -1130,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
                     bool v_side;
                     int j, half;
-                    slot_number<kHalves>(step, n_max, v_side, j, half);
+                    slot_number<kHalves>(step, n_max, s.n[1] > 0, v_side, j, half);
                     if (!v_side && half == 0) {
                         if (j > 0) {
                             tv = tk;
@@ -1138,10 +1156,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             next = read_tile(p, s, j + 1);
                         }
                         if (!settle(p, tk)) bad_entry = true;
-                        if (p.plan != nullptr) write_mask(h, tk, T);
+                        if (p.plan != nullptr && !(ok = put_mask(tk, T))) break;
                         ++T;
                     }
-                    if (v_side && (kHalves == 1 || j + 1 == n_max)) tv = tk;
+                    if (v_side && (s.n[1] > 0 || j + 1 == n_max)) tv = tk;
                     const bool cut = v_side && j >= s.first_cut;
                     bring(v_side ? tv : tk, v_side, half,
                           unit | (v_side ? 1u : 0u) | (cut ? 2u | ((uint32_t)(j - s.first_cut) << 4) : 0u) |
@@ -1193,8 +1211,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                 for (int k = 1; k < 8; ++k) mma_ts(d, a + 8 * k, vd + (uint64_t)((2048 * k) >> 4), kIdPV, 1u);
             };
-            uint32_t done[2] = {0u, 0u};      // head_dim 128: tiles of the row groups so far; 256: [0] tiles
-            uint32_t q_uses = 0;
+            uint32_t uses[3] = {0u, 0u, 0u};  // of s_full and p_full
+            uint32_t q_uses = 0;              // of the query rows
             bool ok = true;
             for (uint32_t i = 0; ok; ++i) {
                 if (!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u)) break;
@@ -1208,7 +1226,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (!(ok = wait_all(&h->q_full, q_uses & 1u))) break;
                 ++q_uses;
                 tc_fence_after();
-                if (kGroups == 2) {
+                if (kGroups == 2 && n1 > 0) {
+                    // both row groups, a buffer each: a group's S and P V run under the other's softmax
                     uint32_t vs = 0;          // V of the tile before
                     for (int j = 0; j <= n_max; ++j) {
                         const uint32_t ks = st;
@@ -1222,12 +1241,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             __syncwarp();
                         }
                         if (j > 0) {
-                            if (j - 1 < n1 && !(ok = wait_all(&h->p_full[1], (done[1] + j - 1) & 1u))) break;
+                            if (j - 1 < n1 && !(ok = wait_all(&h->p_full[1], (uses[1] + j - 1) & 1u))) break;
                             tc_fence_after();
                             if (elect_one()) {
                                 if (j - 1 < n1) {
                                     issue_pv(tm + kColO + 128, tm + kColS1, vs, j > 1);
-                                    if (j == n1) mma_commit(smem_addr(&h->o_full[1]));
+                                    mma_commit(smem_addr(&h->pv_done[1]));
                                 }
                                 mma_commit(smem_addr(&h->empty[vs]));
                             }
@@ -1247,30 +1266,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         if (!(ok = wait_slot())) break;
                         next_slot();
                         if (j < n0) {
-                            if (!(ok = wait_all(&h->p_full[0], (done[0] + j) & 1u))) break;
+                            if (!(ok = wait_all(&h->p_full[0], (uses[0] + j) & 1u))) break;
                             tc_fence_after();
                             if (elect_one()) {
                                 issue_pv(tm + kColO, tm, vs, j > 0);
-                                if (j + 1 == n0) mma_commit(smem_addr(&h->o_full[0]));
+                                mma_commit(smem_addr(&h->pv_done[0]));
                             }
                             __syncwarp();
                         }
                     }
-                    done[0] += n0;
-                    done[1] += n1;
+                    uses[0] += n0;
+                    uses[1] += n1;
                 } else {
+                    // one row group, buffers in turn: S of the next tile runs under this one's softmax
                     for (int j = -1; j < n_max && ok; ++j) {
-                        // S of tile j + 1 into its buffer, its two halves of the dims in turn
                         if (j + 1 < n_max) {
-                            const uint32_t buf = (done[0] + j + 1) & 1u;
+                            const uint32_t buf = (j + 1) & 1;
 #pragma unroll 1
-                            for (int half = 0; half < 2; ++half) {
+                            for (int half = 0; half < kHalves; ++half) {   // of the dims
                                 if (!(ok = wait_slot())) break;
                                 if (elect_one()) {
                                     issue_s(tm + kColS1 * buf, q_addr + half * kQTileBytes, st, half > 0);
                                     mma_commit(smem_addr(&h->empty[st]));
-                                    if (half == 1) {
-                                        mma_commit(smem_addr(&h->s_full[buf]));
+                                    if (half + 1 == kHalves) {
+                                        mma_commit(smem_addr(&h->s_full[2 * buf]));
                                         if (j + 2 == n_max) mma_commit(smem_addr(&h->q_empty));
                                     }
                                 }
@@ -1279,25 +1298,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             }
                         }
                         if (j < 0 || !ok) continue;
-                        const uint32_t tile = done[0] + j, buf = tile & 1u;
-                        if (!(ok = wait_all(&h->p_full[buf], (tile >> 1) & 1u))) break;
+                        const uint32_t buf = j & 1;
+                        if (!(ok = wait_all(&h->p_full[2 * buf], ((buf ? uses[2] : uses[0]) + (j >> 1)) & 1u))) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
+                        for (int half = 0; half < kHalves; ++half) {
                             if (!(ok = wait_slot())) break;
                             if (elect_one()) {
                                 issue_pv(tm + kColO + 128 * half, tm + kColS1 * buf, st, j > 0);
                                 mma_commit(smem_addr(&h->empty[st]));
-                                if (half == 1) {
-                                    mma_commit(smem_addr(&h->pv_done));
-                                    if (j + 1 == n_max) mma_commit(smem_addr(&h->o_full[0]));
-                                }
+                                if (half + 1 == kHalves) mma_commit(smem_addr(&h->pv_done[2 * buf]));
                             }
                             __syncwarp();
                             next_slot();
                         }
                     }
-                    done[0] += n0;
+                    uses[0] += (n_max + 1) >> 1;
+                    uses[2] += n_max >> 1;
                 }
             }
         }
@@ -1311,15 +1328,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // (scale <= 0: scores are scaled before the maximum is taken)
             const bool pre = !(p.scale_log2 > 0.f);
             const float sc = pre ? 1.f : p.scale_log2;
-            uint32_t done = 0;                       // tiles of this group so far
             uint32_t masks = 0;                      // tiles of the CTA so far
-            uint32_t outs = 0;                       // units of this group with tiles so far
+            uint32_t uses01 = 0, uses2 = 0;          // of s_full[grp] and s_full[2] by this group
             bool ok = true;
             for (uint32_t i = 0; ok; ++i) {
                 if (!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u)) break;
                 const Seg& s = h->seg[i % kRing];        // (kept until it is given back)
                 if (s.n_tok < 0) break;
                 const int n_tiles = s.n[grp];
+                const bool dual = kGroups == 2 && s.n[1] > 0;
                 // first cell of the piece that this row does not see, from the piece's first
                 int rel0 = 0;
                 {
@@ -1327,12 +1344,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     if (tok_in < p.group_tokens && tok < s.n_tok)
                         rel0 = (int)clamp64(s.lim0 + tok - (int64_t)s.j0 * kPrefillTile, 0, INT_MAX);
                 }
+                // P V of the piece's tile j is complete (S of tile j came after P V of tile j - 1, or of
+                // j - 2 with buffers in turn: the barrier is in that phase or the one before)
+                auto wait_pv = [&](int j) -> bool {
+                    const int which = dual ? grp : 2 * (j & 1);
+                    const bool got = wait_all(&h->pv_done[which], ((which == 2 ? uses2 : uses01) + (dual ? j : j >> 1)) & 1u);
+                    tc_fence_after();
+                    return got;
+                };
                 float m_run = -INFINITY, l_run = 0.f;
-                for (int j = 0; j < n_tiles; ++j, ++done) {
-                    const int buf = kGroups == 2 ? grp : (int)(done & 1u);
-                    const uint32_t par = kGroups == 2 ? (done & 1u) : ((done >> 1) & 1u);
-                    const uint32_t t_s = tmem + lane_base + kColS1 * buf;
-                    if (!(ok = wait_all(&h->s_full[buf], par))) break;
+                for (int j = 0; j < n_tiles; ++j) {
+                    // its buffer, and the barriers of that use of it
+                    const int which = dual ? grp : 2 * (j & 1);
+                    const uint32_t use = (which == 2 ? uses2 : uses01) + (dual ? j : j >> 1);
+                    const uint32_t t_s = tmem + lane_base + (which ? kColS1 : 0u);
+                    if (!(ok = wait_all(&h->s_full[which], use & 1u))) break;
                     tc_fence_after();
                     const int rel = rel0 - j * kPrefillTile;
                     if (pre || !__all_sync(0xffffffffu, rel >= kPrefillTile)) {
@@ -1357,14 +1383,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     for (int c = 0; c < 128; c += 32) tmem_ld32(t_s + c, sv + c);
                     tc_wait_ld();
                     if (p.plan != nullptr) {
-                        // (the loader's write, ordered by a barrier of its own; the tile's V slot is
-                        // released after this thread's P, and the ring is deeper than the slots reach)
                         const uint32_t t = masks + j;
-                        if (!(ok = wait_all(&h->mask_full[t % kRing], (t / kRing) & 1u))) break;
-                        if (h->holes[t % kRing] != 0u) {
+                        if (!(ok = wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u))) break;
+                        if (h->holes[t % kMasks] != 0u) {
                             // the minimum of the score and -inf for a hole, +inf for a cell: a NaN that
                             // stands in a hole goes too
-                            const float4* bias = reinterpret_cast<const float4*>(h->bias[t % kRing]);
+                            const float4* bias = reinterpret_cast<const float4*>(h->bias[t % kMasks]);
 #pragma unroll
                             for (int c = 0; c < 32; ++c) {
                                 const float4 f = bias[c];
@@ -1374,6 +1398,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 sv[4 * c + 3] = __float_as_uint(fminf(__uint_as_float(sv[4 * c + 3]), f.w));
                             }
                         }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[t % kMasks]));
                     }
                     float mx[4];
 #pragma unroll
@@ -1393,12 +1419,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             l_run *= alpha;
                         }
                         // rows whose maximum moved rescale their O once the last P V is complete
-                        // (head_dim 128: S of this tile came after it)
                         if (j > 0) {
-                            if (kGroups == 1) {
-                                if (!(ok = wait_all(&h->pv_done, (done - 1) & 1u))) break;
-                                tc_fence_after();
-                            }
+                            if (!(ok = wait_pv(j - 1))) break;
 #pragma unroll 1
                             for (int c0 = 0; c0 < D; c0 += 32) {
                                 uint32_t ov[32];
@@ -1433,10 +1455,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     l_run += (s0 + s1) + (s2 + s3);
                     tc_wait_st();
                     tc_fence_before();
-                    mbar_arrive(smem_addr(&h->p_full[buf]));
+                    mbar_arrive(smem_addr(&h->p_full[which]));
                 }
                 if (!ok) break;
-                masks += s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+                const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
+                if (p.plan != nullptr)   // the masks of tiles that only the other group has: in step with them
+                    for (int j = n_tiles; j < n_max && ok; ++j) {
+                        const uint32_t t = masks + j;
+                        ok = wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[t % kMasks]));
+                    }
+                if (!ok) break;
+                masks += n_max;
                 // ---- the piece's result ----
                 const int row_in = tid & 127;
                 const int tok_in = row_in / G, head_in = row_in - tok_in * G;
@@ -1445,9 +1476,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // V that was kept apart: cells that this row sees
                 bool fix = false;
                 if (n_tiles > 0) {
-                    if (!(ok = wait_all(&h->o_full[grp], outs & 1u))) break;
-                    ++outs;
-                    tc_fence_after();
+                    if (!(ok = wait_pv(n_tiles - 1))) break;
+                    uses01 += dual ? n_tiles : (n_tiles + 1) >> 1;
+                    uses2 += dual ? 0 : n_tiles >> 1;
                     if (!(ok = wait_all(&h->load_done[i % kRing], (i / kRing) & 1u))) break;
                     for (int t = 0; t < kCutTiles; ++t)
                         for (int k = 0; k < 4; ++k) fix = fix || h->bad_cells[i % kRing][t][k] != 0u;
@@ -1536,55 +1567,39 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// Joins the partials of the units that were cut: weights exp(lse_p - max lse).  blockIdx.x + 1
-// is the boundary between two shares; the first boundary inside a unit does the unit, whose
-// parts are then known: one of each share that its line meets and that holds tiles of it.
-// blockIdx.y and the warps take its rows, the lanes a row's dims.
+// Joins the partials of the units that were cut: weights exp(lse_p - max lse).  blockIdx.x is the
+// CTA that began the unit (and noted it in cuts); its parts are one of each share that the unit's
+// line meets and that holds tiles of it.  blockIdx.y and the warps take its rows, the lanes a
+// row's dims.
 constexpr int kMergeWarps = 4;
 constexpr int kMaxCtas = 1024;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const __grid_constant__ PrefillParams p, int n_ctas) {
     constexpr int kGroups = Geometry<D>::kGroups;
+    __shared__ int slot[kMaxCtas];   // part i's partial slot, -1: it holds no tile
     pdl_wait();
+    const PrefillCut cut = p.cuts[blockIdx.x];
+    if (cut.n_parts == 0) return;
     const int lane = threadIdx.x & 31;
     Shares sh;
     sh.set(total_of(p), (uint32_t)n_ctas);
-    const int c = blockIdx.x + 1;
-    const uint32_t at = sh.of((uint32_t)c);
-    if (at >= sh.total) return;
-    const Place r = place_of(p, at);
-    if (at == r.start || sh.of((uint32_t)c - 1u) > r.start) return;
-    const int32_t tiles = r.tiles(p);
-    Seg s;
-    make_seg<D>(p, r.x, r.seq, (int)r.g, r.block, 0, tiles, -1, s);
-    // the shares that meet the unit, a thread each: share c - 1 + i's partial slot, -1 without a
-    // tile of it; `whole`: one share holds them all and has written the result itself
-    __shared__ int slot[kMaxCtas];
-    __shared__ int n_parts, whole;
-    if (threadIdx.x == 0) {
-        n_parts = 0;
-        whole = 0;
+    // `whole`: one share holds all its tiles and has written the result itself
+    bool whole = false;
+    for (int i = threadIdx.x; i < cut.n_parts; i += 32 * kMergeWarps) {
+        const uint32_t cta = blockIdx.x + (uint32_t)i;
+        const uint32_t x0 = sh.of(cta), a = max(x0, cut.start), b = min(sh.of(cta + 1u), cut.end);
+        const int32_t first = tile_at(a - cut.start, cut.end - cut.start, cut.tiles);
+        const int32_t last = tile_at(b - cut.start, cut.end - cut.start, cut.tiles);
+        whole = whole || (first == 0 && last == cut.tiles);
+        slot[i] = first == last ? -1 : 2 * (int)cta + (x0 > cut.start ? 0 : 1);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; c - 1 + i < n_ctas; i += 32 * kMergeWarps) {
-        const int cta = c - 1 + i;
-        const uint32_t x0 = sh.of((uint32_t)cta), x1 = sh.of((uint32_t)cta + 1u);
-        if (x0 >= r.end) break;
-        const uint32_t a = max(x0, r.start), b = min(x1, r.end);
-        const int32_t first = r.tile_at(a - r.start, tiles), end = r.tile_at(b - r.start, tiles);
-        if (first == 0 && end == tiles) whole = 1;
-        slot[i] = first == end ? -1 : 2 * cta + (a > r.start ? 0 : 1);
-        atomicMax(&n_parts, i + 1);
-    }
-    __syncthreads();
-    if (whole) return;
-    const int parts = n_parts;
-    const int G = p.group;
+    if (__syncthreads_or(whole)) return;
+    const int parts = cut.n_parts, G = p.group;
     const int step = kMergeWarps * gridDim.y;
     for (int row = (int)blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < 128 * kGroups; row += step) {
         const int grp = row >> 7, in = row & 127;
         const int tok_in = in / G, tok = grp * p.group_tokens + tok_in;
-        if (tok_in >= p.group_tokens || tok >= s.n_tok) continue;
+        if (tok_in >= p.group_tokens || tok >= cut.n_tok) continue;
         // maximum over the parts, a lane each
         float m = -INFINITY;
         for (int i = lane; i < parts; i += 32) {
@@ -1600,11 +1615,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const _
         float acc[D / 32] = {};
         float sum = 0.f;
         if (m != -INFINITY) {
+            // (a part without a cell that the row sees has weight 0 and an O that was not written)
 #pragma unroll 4
             for (int i = 0; i < parts; ++i) {
                 const int sl = slot[i];
-                if (sl < 0) continue;
-                const float v = p.part_lse[(int64_t)sl * kGroups * 128 + row];
+                const float v = sl < 0 ? -INFINITY : p.part_lse[(int64_t)sl * kGroups * 128 + row];
                 if (v == -INFINITY) continue;
                 const float w = exp2f((v - m) * 1.4426950408889634f);
                 sum += w;
@@ -1620,7 +1635,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const _
             }
         }
         const float inv = m == -INFINITY ? 0.f : 1.f / sum;
-        const int64_t out_row = (s.q_tok + tok) * p.n_head + s.g * G + (in - tok_in * G);
+        const int64_t out_row = (cut.q_tok + tok) * p.n_head + cut.g * G + (in - tok_in * G);
         uint2* d = reinterpret_cast<uint2*>(p.out + out_row * D);
 #pragma unroll
         for (int k = 0; k < D / 128; ++k)
@@ -1684,9 +1699,9 @@ cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, in
                (size_t)smem_of(kv_type), args, stream, pdl);
     if (e != cudaSuccess || !p.shares || n_ctas < 2) return e;
     if (n_ctas > kMaxCtas) return cudaErrorInvalidValue;
-    // eight CTAs per boundary: 32 or 16 rows each, so that a merge of a few units fills the device
+    // two rows a warp (one at head_dim 256), so that a merge of a few units fills the device
     return launch(head_dim == 128 ? (const void*)prefill_merge_kernel<128> : (const void*)prefill_merge_kernel<256>,
-                  dim3((unsigned)n_ctas - 1u, 8), 32 * kMergeWarps, 0, args, stream, pdl);
+                  dim3((unsigned)n_ctas, 32), 32 * kMergeWarps, 0, args, stream, pdl);
 }
 
 }  // namespace kvattn

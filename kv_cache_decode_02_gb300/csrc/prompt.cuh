@@ -37,6 +37,11 @@ cudaError_t launch_cache_write(const CacheIoParams& p, int kv_type, cudaStream_t
 cudaError_t launch_cache_read(const CacheIoParams& p, int kv_type, cudaStream_t stream, bool pdl);
 
 // ---- causal attention of packed query tokens ----
+struct PrefillCut {          // a work unit that the shares cut (n_parts > 0), noted by the CTA that began it
+    int64_t q_tok;           // its first token
+    int32_t n_parts, n_tok, g, tiles;
+    uint32_t start, end;     // its part of the line
+};
 struct PrefillParams {
     // use_tma: f16 rows (encode_planes_map), or codes (encode_codes_map), boxes of 128 dims x 128
     // cells
@@ -51,6 +56,7 @@ struct PrefillParams {
     const int32_t* seq_lens;  // null: a sequence's cells are its own tokens
     __half* out;              // [n_tok][n_head][head_dim]
     float* lse;               // nullable: [n_tok][n_head]
+    PrefillCut* cuts;         // [CTAs], when shares
     float* part_o;            // [2 CTAs][row groups][128][head_dim], when shares
     float* part_lse;          // [2 CTAs][row groups][128]
     uint32_t* status;

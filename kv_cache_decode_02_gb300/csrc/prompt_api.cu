@@ -44,7 +44,7 @@ int64_t unit_bound(int64_t n_tok, int n_seq, int n_head_kv, int group, int head_
 struct Cut {
     bool shares;
     int n_ctas;
-    size_t lse_off, o_off, total;
+    size_t cuts_off, lse_off, o_off, total;
 };
 
 constexpr int64_t kMinShareTiles = 4;
@@ -68,6 +68,8 @@ Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share) {
     if (c.n_ctas == 1 || !fits) c.shares = false;
     size_t off = kStatusBytes;
     const size_t rows = c.shares ? (size_t)c.n_ctas * 2 * (size_t)prefill_groups(head_dim) * 128 : 0;
+    c.cuts_off = off;
+    off = align_up(off + (c.shares ? (size_t)c.n_ctas * sizeof(PrefillCut) : 0), kWsAlign);
     c.lse_off = off;
     off = align_up(off + rows * 4, kWsAlign);
     c.o_off = off;
@@ -310,6 +312,7 @@ int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets
     p.lse = lse;
     char* wsb = static_cast<char*>(ws);
     p.status = reinterpret_cast<uint32_t*>(wsb);
+    p.cuts = reinterpret_cast<PrefillCut*>(wsb + c.cuts_off);
     p.part_lse = reinterpret_cast<float*>(wsb + c.lse_off);
     p.part_o = reinterpret_cast<float*>(wsb + c.o_off);
     p.k_stride = p.v_stride = (int64_t)n_head_kv * head_dim;
