@@ -22,12 +22,11 @@
 //
 // Sixteen warps with fixed roles:
 //
-//  * softmax (warps 0-3 and 4-7, 128 threads each): thread t holds row t, which is TMEM lane
-//    t: a row's maximum and sum need no exchange between threads.  At head_dim 128 each group
-//    has its own row group; at 256 the first has the unit's and the second is idle.  The thread
-//    reads its row of S from tensor memory, masks, and writes p there as f16 pairs.  p is
-//    scaled by 2^7 (it cancels in O / l): with the lazily moved maximum below p stays under
-//    2^15, and p of 2^-21 of a row's largest still has all its f16 bits.
+//  * softmax (warps 0-7): threads t and t + 128 hold row t of a row group, which is TMEM lane t,
+//    and half of a tile's columns each; they take the row groups' tiles in turn.  A thread reads
+//    its scores from tensor memory, masks, and writes p over them as f16 pairs.  p is scaled by
+//    2^7 (it cancels in O / l): with the lazily moved maximum below p stays under 2^15, and p of
+//    2^-21 of a row's largest still has all its f16 bits.
 //  * loader (warps 8-11): fills a ring of 32 KB slots, each 128 cells x 128 dims of K or V in
 //    two 128-byte-swizzled planes.  f16: warp 8 issues a TMA box for each slot whose cells are
 //    one physical run (holes and the end of a sequence included); warps 9-11 mend V slots that
@@ -70,7 +69,7 @@ constexpr int kQTileBytes = 2 * kPlaneBytes;  // 128 rows x 128 dims of f16
 constexpr int kMaxSlots = 5;
 constexpr int kHeaderBytes = 3072;
 constexpr int kRing = 4;                      // pieces of work whose plans are kept
-constexpr int kMasks = 3;                     // tiles whose masks are
+constexpr int kMasks = 2;                     // tiles whose masks are
 constexpr int kRawStages = 3;                 // quantised: slots of raw bytes in flight
 constexpr int kCutTiles = 3;                  // tiles that only some of a unit's (<= 256) tokens see whole
 constexpr float kSlack = 8.f;                 // lazy maximum
@@ -115,10 +114,8 @@ struct Header {
     uint64_t mended[kMaxSlots];  // a V slot that is mended after it landed
     uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // quantised: a slot's raw bytes; they are turned
     uint64_t q_full, q_empty;    // the unit's query rows; its last S is complete
-    // an S buffer holds S, or p: [0] the first, [1] the second of group 1, [2] the second of group
-    // 0 (each is waited for in every phase, by one group)
-    uint64_t s_full[3], p_full[3];
-    uint64_t pv_done[3];         // its P V is complete
+    uint64_t s_full[2], p_full[2];  // an S buffer holds S, or p
+    uint64_t pv_done[2];         // its P V is complete
     uint64_t mask_full[kMasks], mask_empty[kMasks];  // through a plan: a tile's bias and holes are written, read
     uint64_t load_done[kRing];   // every slot of a unit is filled, its bad_cells are complete
     uint64_t seg_full[kRing], seg_empty[kRing];
@@ -131,6 +128,7 @@ struct Header {
     uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | unit << 8
     Seg seg[kRing];
     Job job[kRing];
+    float meet[2][128];                       // what two threads of a row tell each other
     alignas(16) float bias[kMasks][kPrefillTile];  // through a plan: +inf, or -inf for a hole
 };
 static_assert(sizeof(Header) <= kHeaderBytes && offsetof(Header, bias) % 16 == 0, "header");
@@ -263,7 +261,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-
 // mbar_wait_bounded in fewer instructions: the kernel has some forty waits, and its sixteen warps'
 // roles together are at the edge of what the instruction caches hold.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
@@ -277,6 +274,16 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         }
     }
     return true;
+}
+// The OR of a predicate over the 64 threads that name this barrier; the barrier orders their
+// shared-memory accesses.
+__device__ __forceinline__ bool bar_or(int id, bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"((uint32_t)x)
+                 : "memory");
+    return r != 0u;
 }
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -697,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         for (int i = 0; i < kMasks; ++i) {
             mbar_init(smem_addr(&h->mask_full[i]), 1);
-            mbar_init(smem_addr(&h->mask_empty[i]), 4 * kGroups);
+            mbar_init(smem_addr(&h->mask_empty[i]), 8);
         }
         for (int i = 0; i < kRawStages; ++i) {
             mbar_init(smem_addr(&h->raw_full[i]), 1);
@@ -705,9 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         mbar_init(smem_addr(&h->q_full), 1);
         mbar_init(smem_addr(&h->q_empty), 1);
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&h->s_full[i]), 1);
-            mbar_init(smem_addr(&h->p_full[i]), 128);
+            mbar_init(smem_addr(&h->p_full[i]), 8);
             mbar_init(smem_addr(&h->pv_done[i]), 1);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -715,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(smem_addr(&h->job_full[i]), 1);
             mbar_init(smem_addr(&h->job_empty[i]), 3);
             mbar_init(smem_addr(&h->seg_full[i]), 1);
-            mbar_init(smem_addr(&h->seg_empty[i]), (kQuant ? 2 : 5) + 4 * kGroups);  // loader, MMA and softmax warps
+            mbar_init(smem_addr(&h->seg_empty[i]), (kQuant ? 2 : 5) + 8);  // loader, MMA and softmax warps
         }
         h->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -761,10 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
     if (warp >= 8 && warp < 12) {
         // (the four warpgroups' shares add up to the 4 x 128 registers of the launch)
-        if constexpr (kQuant)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         // ------------------------------------ loader ------------------------------------
         const int lt = tid - 256;       // 0 .. 127
         bool bad_entry = false, ok = true;
@@ -1043,10 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         if (__any_sync(0xffffffffu, bad_entry) && lane == 0 && warp == 8) atomicOr(p.status, KVATTN_DEVICE_BAD_PLAN_ENTRY);
     } else if (warp >= 12) {
-        if constexpr (kQuant)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         if (warp == 13) {
             // ---------------------------------- scheduler ----------------------------------
             Walk<D> walk;
@@ -1211,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                 for (int k = 1; k < 8; ++k) mma_ts(d, a + 8 * k, vd + (uint64_t)((2048 * k) >> 4), kIdPV, 1u);
             };
-            uint32_t uses[3] = {0u, 0u, 0u};  // of s_full and p_full
+            uint32_t uses[2] = {0u, 0u};      // of the S buffers
             uint32_t q_uses = 0;              // of the query rows
             bool ok = true;
             for (uint32_t i = 0; ok; ++i) {
@@ -1289,7 +1290,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                     issue_s(tm + kColS1 * buf, q_addr + half * kQTileBytes, st, half > 0);
                                     mma_commit(smem_addr(&h->empty[st]));
                                     if (half + 1 == kHalves) {
-                                        mma_commit(smem_addr(&h->s_full[2 * buf]));
+                                        mma_commit(smem_addr(&h->s_full[buf]));
                                         if (j + 2 == n_max) mma_commit(smem_addr(&h->q_empty));
                                     }
                                 }
@@ -1299,7 +1300,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         }
                         if (j < 0 || !ok) continue;
                         const uint32_t buf = j & 1;
-                        if (!(ok = wait_all(&h->p_full[2 * buf], ((buf ? uses[2] : uses[0]) + (j >> 1)) & 1u))) break;
+                        if (!(ok = wait_all(&h->p_full[buf], ((buf ? uses[1] : uses[0]) + (j >> 1)) & 1u))) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int half = 0; half < kHalves; ++half) {
@@ -1307,90 +1308,102 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             if (elect_one()) {
                                 issue_pv(tm + kColO + 128 * half, tm + kColS1 * buf, st, j > 0);
                                 mma_commit(smem_addr(&h->empty[st]));
-                                if (half + 1 == kHalves) mma_commit(smem_addr(&h->pv_done[2 * buf]));
+                                if (half + 1 == kHalves) mma_commit(smem_addr(&h->pv_done[buf]));
                             }
                             __syncwarp();
                             next_slot();
                         }
                     }
                     uses[0] += (n_max + 1) >> 1;
-                    uses[2] += n_max >> 1;
+                    uses[1] += n_max >> 1;
                 }
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         // ------------------------------------ softmax ------------------------------------
-        const int grp = warp >> 2;                   // row group
-        if (grp < kGroups) {
-            const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t t_o = tmem + lane_base + kColO + (kGroups == 2 ? 128u * grp : 0u);
-            // (scale <= 0: scores are scaled before the maximum is taken)
-            const bool pre = !(p.scale_log2 > 0.f);
-            const float sc = pre ? 1.f : p.scale_log2;
-            uint32_t masks = 0;                      // tiles of the CTA so far
-            uint32_t uses01 = 0, uses2 = 0;          // of s_full[grp] and s_full[2] by this group
-            bool ok = true;
-            for (uint32_t i = 0; ok; ++i) {
-                if (!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u)) break;
-                const Seg& s = h->seg[i % kRing];        // (kept until it is given back)
-                if (s.n_tok < 0) break;
-                const int n_tiles = s.n[grp];
-                const bool dual = kGroups == 2 && s.n[1] > 0;
-                // first cell of the piece that this row does not see, from the piece's first
-                int rel0 = 0;
-                {
-                    const int tok_in = (tid & 127) / G, tok = grp * p.group_tokens + tok_in;
-                    if (tok_in < p.group_tokens && tok < s.n_tok)
-                        rel0 = (int)clamp64(s.lim0 + tok - (int64_t)s.j0 * kPrefillTile, 0, INT_MAX);
-                }
-                // P V of the piece's tile j is complete (S of tile j came after P V of tile j - 1, or of
-                // j - 2 with buffers in turn: the barrier is in that phase or the one before)
-                auto wait_pv = [&](int j) -> bool {
-                    const int which = dual ? grp : 2 * (j & 1);
-                    const bool got = wait_all(&h->pv_done[which], ((which == 2 ? uses2 : uses01) + (dual ? j : j >> 1)) & 1u);
+        // Warps w and w + 4 share 32 rows: a thread has one row (its TMEM lane) and half of a
+        // tile's columns, then half of O's.  They meet in a named barrier once per tile, which
+        // also ORs what either saw: a maximum that grew, or a wait that gave up (which both then
+        // leave together: a named barrier has no bound of its own).
+        const int half = warp >> 2;
+        const int row_in = tid & 127;                // TMEM lane
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        auto pair_any = [&](bool x) -> bool { return bar_or(2 + (warp & 3), x); };
+        // (scale <= 0: scores are scaled before the maximum is taken)
+        const bool pre = !(p.scale_log2 > 0.f);
+        const float sc = pre ? 1.f : p.scale_log2;
+        const int tok_in = row_in / G, head_in = row_in - tok_in * G;
+        uint32_t uses0 = 0, uses1 = 0;               // of the S buffers
+        uint32_t masks = 0;                          // tiles of the CTA so far
+        for (uint32_t i = 0;; ++i) {
+            if (pair_any(!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u))) break;
+            const Seg& s = h->seg[i % kRing];        // (kept until it is given back)
+            if (s.n_tok < 0) break;
+            const int n0 = s.n[0], n1 = s.n[1], n_max = n0 > n1 ? n0 : n1;
+            const bool dual = kGroups == 2 && n1 > 0;
+            // first cell of the piece that the thread's row of a group does not see, from its first
+            int rel[2] = {0, 0};
+            {
+                const int64_t r0 = s.lim0 + tok_in - (int64_t)s.j0 * kPrefillTile;
+                if (tok_in < p.group_tokens && tok_in < s.n_tok) rel[0] = (int)clamp64(r0, 0, INT_MAX);
+                if (tok_in < p.group_tokens && tok_in + p.group_tokens < s.n_tok)
+                    rel[1] = (int)clamp64(r0 + p.group_tokens, 0, INT_MAX);
+            }
+            // a row's running maximum (of both halves) and sum (of this one), per group
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            uint32_t use0 = uses0, use1 = uses1;
+            bool lost = false;                       // a wait gave up
+            int masked = -1;                         // the tile whose mask is there,
+            bool holes = false;                      // and whether it has holes
+#pragma unroll 1
+            for (int x = 0; x < (dual ? 2 * n_max : n_max); ++x) {
+                const int g = dual ? x & 1 : 0, j = dual ? x >> 1 : x;
+                const int buf = dual ? g : j & 1;
+                if (j < (g ? n1 : n0)) {
+                    const uint32_t par = (buf ? use1 : use0) & 1u;
+                    if (buf)
+                        ++use1;
+                    else
+                        ++use0;
+                    const uint32_t t_s = tmem + lane_base + (buf ? kColS1 : 0u);
+                    lost = lost || !wait_all(&h->s_full[buf], par);
                     tc_fence_after();
-                    return got;
-                };
-                float m_run = -INFINITY, l_run = 0.f;
-                for (int j = 0; j < n_tiles; ++j) {
-                    // its buffer, and the barriers of that use of it
-                    const int which = dual ? grp : 2 * (j & 1);
-                    const uint32_t use = (which == 2 ? uses2 : uses01) + (dual ? j : j >> 1);
-                    const uint32_t t_s = tmem + lane_base + (which ? kColS1 : 0u);
-                    if (!(ok = wait_all(&h->s_full[which], use & 1u))) break;
-                    tc_fence_after();
-                    const int rel = rel0 - j * kPrefillTile;
-                    if (pre || !__all_sync(0xffffffffu, rel >= kPrefillTile)) {
+                    const int left = (g ? rel[1] : rel[0]) - j * kPrefillTile - 64 * half;
+                    if (pre || !__all_sync(0xffffffffu, left >= 64)) {
                         // (the rare tiles: scaled, masked and put back by a loop of its own, which keeps
                         // the code of the others short)
 #pragma unroll 1
-                        for (int c0 = 0; c0 < 128; c0 += 32) {
-                            uint32_t x[32];
-                            tmem_ld32(t_s + c0, x);
+                        for (int c0 = 0; c0 < 64; c0 += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(t_s + 64 * half + c0, v);
                             tc_wait_ld();
 #pragma unroll
                             for (int c = 0; c < 32; ++c) {
-                                const float f = __uint_as_float(x[c]);
-                                x[c] = c0 + c >= rel ? 0xff800000u : __float_as_uint(pre ? f * p.scale_log2 : f);
+                                const float f = __uint_as_float(v[c]);
+                                v[c] = c0 + c >= left ? 0xff800000u : __float_as_uint(pre ? f * p.scale_log2 : f);
                             }
-                            tmem_st32(t_s + c0, x);
+                            tmem_st32(t_s + 64 * half + c0, v);
                         }
                         tc_wait_st();
                     }
-                    uint32_t sv[128];
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) tmem_ld32(t_s + c, sv + c);
+                    uint32_t sv[64];
+                    tmem_ld32(t_s + 64 * half, sv);
+                    tmem_ld32(t_s + 64 * half + 32, sv + 32);
                     tc_wait_ld();
                     if (p.plan != nullptr) {
                         const uint32_t t = masks + j;
-                        if (!(ok = wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u))) break;
-                        if (h->holes[t % kMasks] != 0u) {
+                        if (j != masked) {   // (once for both groups)
+                            masked = j;
+                            lost = lost || !wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u);
+                            holes = h->holes[t % kMasks] != 0u;
+                        }
+                        if (holes) {
                             // the minimum of the score and -inf for a hole, +inf for a cell: a NaN that
                             // stands in a hole goes too
-                            const float4* bias = reinterpret_cast<const float4*>(h->bias[t % kMasks]);
+                            const float4* bias = reinterpret_cast<const float4*>(h->bias[t % kMasks]) + 16 * half;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
+                            for (int c = 0; c < 16; ++c) {
                                 const float4 f = bias[c];
                                 sv[4 * c] = __float_as_uint(fminf(__uint_as_float(sv[4 * c]), f.x));
                                 sv[4 * c + 1] = __float_as_uint(fminf(__uint_as_float(sv[4 * c + 1]), f.y));
@@ -1398,31 +1411,52 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 sv[4 * c + 3] = __float_as_uint(fminf(__uint_as_float(sv[4 * c + 3]), f.w));
                             }
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[t % kMasks]));
                     }
                     float mx[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
 #pragma unroll
-                    for (int c = 8; c < 128; c += 8)
+                    for (int c = 8; c < 64; c += 8)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mx[k] = max3(mx[k], __uint_as_float(sv[c + 2 * k]), __uint_as_float(sv[c + 2 * k + 1]));
                     const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    const bool grow = tmax > m_run + kSlack;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        float alpha = 1.f;
-                        if (grow) {
-                            alpha = fast_exp2(m_run - tmax);  // (0 from a maximum of -inf)
-                            m_run = tmax;
-                            l_run *= alpha;
+                    float m_run = g ? m[1] : m[0];
+                    // (both have read their scores: p of one is written over the other's)
+                    tc_fence_before();
+                    const bool turn = pair_any(tmax > m_run + kSlack || lost);
+                    tc_fence_after();
+                    if (turn) {
+                        h->meet[half][row_in] = lost ? INFINITY : tmax;
+                        const bool gone = pair_any(lost);          // (and both values are there)
+                        if (gone) {
+                            lost = true;
+                            break;
                         }
-                        // rows whose maximum moved rescale their O once the last P V is complete
+                        const float both = fmaxf(tmax, h->meet[half ^ 1][row_in]);
+                        pair_any(false);                           // (they are read)
+                        float alpha = 1.f;
+                        if (both > m_run + kSlack) {
+                            alpha = fast_exp2(m_run - both);       // (0 from a maximum of -inf)
+                            m_run = both;
+                            if (g) {
+                                m[1] = m_run;
+                                l[1] *= alpha;
+                            } else {
+                                m[0] = m_run;
+                                l[0] *= alpha;
+                            }
+                        }
+                        // rows whose maximum moved rescale their O (each thread its half of it) once the
+                        // last P V is complete: S of this tile came after it, or (buffers in turn) after
+                        // the one before, so the barrier is in that phase or the next
                         if (j > 0) {
-                            if (!(ok = wait_pv(j - 1))) break;
+                            const uint32_t was = dual ? par ^ 1u : ((buf ? use0 : use1) - 1u) & 1u;
+                            lost = !wait_all(&h->pv_done[dual ? g : buf ^ 1], was);
+                            tc_fence_after();
+                            const uint32_t t_o = tmem + lane_base + kColO + (uint32_t)(128 * g + D / 2 * half);
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
+                            for (int c0 = 0; c0 < D / 2; c0 += 32) {
                                 uint32_t ov[32];
                                 tmem_ld32(t_o + c0, ov);
                                 tc_wait_ld();
@@ -1433,10 +1467,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         }
                     }
                     const float nm = (m_run == -INFINITY) ? 0.f : kLift - m_run;
-                    const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(nm, nm);
                     uint64_t sum[2] = {0ull, 0ull};
+                    const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(nm, nm);
 #pragma unroll
-                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                    for (int c0 = 0; c0 < 64; c0 += 32) {
                         uint32_t pw[16];
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
@@ -1447,53 +1481,64 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
                             pw[c >> 1] = pack_half2(a, b);
                         }
-                        tmem_st16(t_s + (c0 >> 1), pw);
+                        tmem_st16(t_s + 32 * half + (c0 >> 1), pw);
                     }
                     float s0, s1, s2, s3;
                     unpack2(sum[0], s0, s1);
                     unpack2(sum[1], s2, s3);
-                    l_run += (s0 + s1) + (s2 + s3);
+                    if (g)
+                        l[1] += (s0 + s1) + (s2 + s3);
+                    else
+                        l[0] += (s0 + s1) + (s2 + s3);
                     tc_wait_st();
                     tc_fence_before();
-                    mbar_arrive(smem_addr(&h->p_full[which]));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&h->p_full[buf]));
                 }
-                if (!ok) break;
-                const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
-                if (p.plan != nullptr)   // the masks of tiles that only the other group has: in step with them
-                    for (int j = n_tiles; j < n_max && ok; ++j) {
-                        const uint32_t t = masks + j;
-                        ok = wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[t % kMasks]));
-                    }
-                if (!ok) break;
-                masks += n_max;
-                // ---- the piece's result ----
-                const int row_in = tid & 127;
-                const int tok_in = row_in / G, head_in = row_in - tok_in * G;
-                const int tok = grp * p.group_tokens + tok_in;
+                if (p.plan != nullptr && g == (dual ? 1 : 0)) {   // every warp, for every tile
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[(masks + j) % kMasks]));
+                }
+            }
+            masks += n_max;
+            if (pair_any(lost)) break;
+            // ---- the piece's result: a thread has its row and half of the columns of each group ----
+#pragma unroll 1
+            for (int g = 0; g < kGroups; ++g) {
+                const int n_tiles = g ? n1 : n0;
+                const int tok = g * p.group_tokens + tok_in;
                 const bool row_ok = tok_in < p.group_tokens && tok < s.n_tok;
-                // V that was kept apart: cells that this row sees
-                bool fix = false;
+                const float m_run = g ? m[1] : m[0];
+                float l_run = g ? l[1] : l[0];
+                bool fix = false;   // V that was kept apart: cells that this row sees
                 if (n_tiles > 0) {
-                    if (!(ok = wait_pv(n_tiles - 1))) break;
-                    uses01 += dual ? n_tiles : (n_tiles + 1) >> 1;
-                    uses2 += dual ? 0 : n_tiles >> 1;
-                    if (!(ok = wait_all(&h->load_done[i % kRing], (i / kRing) & 1u))) break;
+                    const int buf = dual ? g : (n_tiles - 1) & 1;
+                    lost = lost || !wait_all(&h->pv_done[buf], ((buf ? use1 : use0) - 1u) & 1u);
+                    lost = lost || !wait_all(&h->load_done[i % kRing], (i / kRing) & 1u);
+                    tc_fence_after();
                     for (int t = 0; t < kCutTiles; ++t)
                         for (int k = 0; k < 4; ++k) fix = fix || h->bad_cells[i % kRing][t][k] != 0u;
                     fix = fix && row_ok;
                 }
-                const bool none = n_tiles == 0 || l_run == 0.f;  // (a NaN sum stays)
+                h->meet[half][row_in] = l_run;
+                lost = pair_any(lost);
+                if (lost) break;
+                l_run += h->meet[half ^ 1][row_in];
+                pair_any(false);                                   // (they are read)
+                const bool none = n_tiles == 0 || l_run == 0.f;    // (a NaN sum stays)
                 const float inv = none ? 0.f : 1.f / l_run;
                 const int64_t out_row = (s.q_tok + tok) * p.n_head + s.g * G + head_in;
-                const int64_t part_row = ((int64_t)s.part * kGroups + grp) * 128 + row_in;
-                // (a thread stores its own row, in whole 32-byte sectors: a row of halves or floats
-                // lies in lines of its own, and turning rows among lanes first took longer)
-                char* to = s.part >= 0 ? reinterpret_cast<char*>(p.part_o + part_row * D) : reinterpret_cast<char*>(p.out + out_row * D);
+                const int64_t part_row = ((int64_t)s.part * kGroups + g) * 128 + row_in;
+                constexpr int kCols = D / 2;
+                const int d0 = kCols * half;
+                const uint32_t t_o = tmem + lane_base + kColO + (uint32_t)(128 * g + d0);
+                // (a thread stores its part of a row in whole 32-byte sectors: turning rows among lanes
+                // first, to store whole lines, took longer)
+                char* to = s.part >= 0 ? reinterpret_cast<char*>(p.part_o + part_row * D + d0)
+                                       : reinterpret_cast<char*>(p.out + out_row * D + d0);
                 const bool sectors = p.out_sectors != 0;
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = 0; c0 < kCols; c0 += 32) {
                     if (s.part >= 0 && n_tiles == 0) break;      // (its lse says that nothing is there)
                     uint32_t ov[32];
                     if (n_tiles > 0) {
@@ -1518,7 +1563,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                                                        : s.cell0 + at;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
-                                    const int d = c0 + k;
+                                    const int d = d0 + c0 + k;
                                     __half x;
                                     if (VBITS == 16) {
                                         x = static_cast<const __half*>(p.v)[cell * p.v_stride + (int64_t)s.g * D + d];
@@ -1541,16 +1586,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         st_sector(to + 2 * c0 + 32, ov + 8, sectors);
                     }
                 }
-                if (row_ok) {
+                if (row_ok && half == 0) {
                     const float v = none ? -INFINITY : (m_run - kLift + fast_log2(l_run)) * kLn2;
                     if (s.part >= 0)
                         p.part_lse[part_row] = v;
                     else if (p.lse != nullptr)
                         p.lse[out_row] = v;
                 }
-                tc_fence_before();   // (O is read: the next unit's first P, which follows, lets it be written)
-                give_back(i);
             }
+            if (lost) break;
+            uses0 = use0;
+            uses1 = use1;
+            tc_fence_before();   // (O is read: the next piece's first P, which follows, lets it be written)
+            give_back(i);
         }
     }
     tc_fence_before();
