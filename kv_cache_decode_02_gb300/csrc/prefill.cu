@@ -1177,16 +1177,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // are broadcast from lane 0)
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t slot0 = smem_addr(slots), q_addr = smem_addr(q_tiles);
+            const bool leader = elect_one();
             uint32_t mends = 0;               // a bit per slot: parity of its mended barrier
             uint32_t st = 0, use = 0;         // the next slot, and the parity of its use
-            auto wait_slot = [&]() -> bool {
-                if (!wait_all(&h->full[st], use)) return false;
-                if (!kQuant && __shfl_sync(0xffffffffu, h->slot_mend[st], 0) != 0u) {
-                    if (!wait_all(&h->mended[st], (mends >> st) & 1u)) return false;
+            // This warp's own instructions, one after the other, set the pace of everything: a wait
+            // is a test by every lane, without a vote (a lane whose wait gave up is noticed by the
+            // vote at the end of a tile; until then it goes on, over data that nobody will use).
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = wait_bar(smem_addr(bar), parity, abort_flag, p.wait_limit_ns) && ok;
+            };
+            auto wait_slot = [&](bool check) {
+                wait(&h->full[st], use);
+                if (check && h->slot_mend[st] != 0u) {
+                    wait(&h->mended[st], (mends >> st) & 1u);
                     mends ^= 1u << st;
                 }
-                tc_fence_after();
-                return true;
             };
             auto next_slot = [&]() {
                 ++st;
@@ -1212,49 +1218,52 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                 for (int k = 1; k < 8; ++k) mma_ts(d, a + 8 * k, vd + (uint64_t)((2048 * k) >> 4), kIdPV, 1u);
             };
-            uint32_t uses[2] = {0u, 0u};      // of the S buffers
+            uint32_t uses0 = 0, uses1 = 0;    // of the S buffers
             uint32_t q_uses = 0;              // of the query rows
-            bool ok = true;
-            for (uint32_t i = 0; ok; ++i) {
+            for (uint32_t i = 0;; ++i) {
                 if (!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u)) break;
                 const Seg& s = h->seg[i % kRing];
                 const int n_tok = __shfl_sync(0xffffffffu, s.n_tok, 0);
                 const int n0 = __shfl_sync(0xffffffffu, s.n[0], 0), n1 = __shfl_sync(0xffffffffu, s.n[1], 0);
+                // (the tiles whose slots may be mended: cut ones, and a sequence's last; through a plan any)
+                const int whole = (int)clamp64(s.len / kPrefillTile - s.j0, 0, INT_MAX);
+                const int mend_from = p.plan != nullptr || p.use_tma == 0 ? 0 : __shfl_sync(0xffffffffu, min(s.first_cut, whole), 0);
                 if (n_tok < 0) break;
                 give_back(i);
                 const int n_max = n0 > n1 ? n0 : n1;
                 if (n_max == 0) continue;
-                if (!(ok = wait_all(&h->q_full, q_uses & 1u))) break;
+                wait(&h->q_full, q_uses & 1u);
                 ++q_uses;
                 tc_fence_after();
                 if (kGroups == 2 && n1 > 0) {
                     // both row groups, a buffer each: a group's S and P V run under the other's softmax
                     uint32_t vs = 0;          // V of the tile before
+#pragma unroll 1
                     for (int j = 0; j <= n_max; ++j) {
                         const uint32_t ks = st;
+                        const bool check = !kQuant && j >= mend_from;
                         if (j < n_max) {
-                            if (!(ok = wait_slot())) break;
+                            wait_slot(check);
                             next_slot();
-                            if (j < n0 && elect_one()) {
+                            tc_fence_after();
+                            if (leader && j < n0) {
                                 issue_s(tm, q_addr, ks, false);
                                 mma_commit(smem_addr(&h->s_full[0]));
                             }
-                            __syncwarp();
                         }
                         if (j > 0) {
-                            if (j - 1 < n1 && !(ok = wait_all(&h->p_full[1], (uses[1] + j - 1) & 1u))) break;
+                            if (j - 1 < n1) wait(&h->p_full[1], (uses1 + j - 1) & 1u);
                             tc_fence_after();
-                            if (elect_one()) {
+                            if (leader) {
                                 if (j - 1 < n1) {
                                     issue_pv(tm + kColO + 128, tm + kColS1, vs, j > 1);
-                                    mma_commit(smem_addr(&h->pv_done[1]));
+                                    if (j == n1) mma_commit(smem_addr(&h->pv_done[1]));
                                 }
                                 mma_commit(smem_addr(&h->empty[vs]));
                             }
-                            __syncwarp();
                         }
-                        if (j == n_max) break;
-                        if (elect_one()) {
+                        if (!__all_sync(0xffffffffu, ok) || j == n_max) break;
+                        if (leader) {
                             if (j < n1) {
                                 issue_s(tm + kColS1, q_addr + kQTileBytes, ks, false);
                                 mma_commit(smem_addr(&h->s_full[1]));
@@ -1262,31 +1271,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             mma_commit(smem_addr(&h->empty[ks]));
                             if (j + 1 == n_max) mma_commit(smem_addr(&h->q_empty));
                         }
-                        __syncwarp();
                         vs = st;
-                        if (!(ok = wait_slot())) break;
+                        wait_slot(check);
                         next_slot();
                         if (j < n0) {
-                            if (!(ok = wait_all(&h->p_full[0], (uses[0] + j) & 1u))) break;
+                            wait(&h->p_full[0], (uses0 + j) & 1u);
                             tc_fence_after();
-                            if (elect_one()) {
+                            if (leader) {
                                 issue_pv(tm + kColO, tm, vs, j > 0);
-                                mma_commit(smem_addr(&h->pv_done[0]));
+                                if (j + 1 == n0) mma_commit(smem_addr(&h->pv_done[0]));
                             }
-                            __syncwarp();
                         }
                     }
-                    uses[0] += n0;
-                    uses[1] += n1;
+                    uses0 += n0;
+                    uses1 += n1;
                 } else {
                     // one row group, buffers in turn: S of the next tile runs under this one's softmax
-                    for (int j = -1; j < n_max && ok; ++j) {
+#pragma unroll 1
+                    for (int j = -1; j < n_max; ++j) {
                         if (j + 1 < n_max) {
                             const uint32_t buf = (j + 1) & 1;
 #pragma unroll 1
                             for (int half = 0; half < kHalves; ++half) {   // of the dims
-                                if (!(ok = wait_slot())) break;
-                                if (elect_one()) {
+                                wait_slot(!kQuant && j + 1 >= mend_from);
+                                tc_fence_after();
+                                if (leader) {
                                     issue_s(tm + kColS1 * buf, q_addr + half * kQTileBytes, st, half > 0);
                                     mma_commit(smem_addr(&h->empty[st]));
                                     if (half + 1 == kHalves) {
@@ -1294,29 +1303,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                         if (j + 2 == n_max) mma_commit(smem_addr(&h->q_empty));
                                     }
                                 }
-                                __syncwarp();
                                 next_slot();
                             }
                         }
-                        if (j < 0 || !ok) continue;
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        if (j < 0) continue;
                         const uint32_t buf = j & 1;
-                        if (!(ok = wait_all(&h->p_full[buf], ((buf ? uses[1] : uses[0]) + (j >> 1)) & 1u))) break;
-                        tc_fence_after();
+                        wait(&h->p_full[buf], ((buf ? uses1 : uses0) + (j >> 1)) & 1u);
 #pragma unroll 1
                         for (int half = 0; half < kHalves; ++half) {
-                            if (!(ok = wait_slot())) break;
-                            if (elect_one()) {
+                            wait_slot(!kQuant && j >= mend_from);
+                            tc_fence_after();
+                            if (leader) {
                                 issue_pv(tm + kColO + 128 * half, tm + kColS1 * buf, st, j > 0);
                                 mma_commit(smem_addr(&h->empty[st]));
                                 if (half + 1 == kHalves) mma_commit(smem_addr(&h->pv_done[buf]));
                             }
-                            __syncwarp();
                             next_slot();
                         }
                     }
-                    uses[0] += (n_max + 1) >> 1;
-                    uses[1] += n_max >> 1;
+                    uses0 += (n_max + 1) >> 1;
+                    uses1 += n_max >> 1;
                 }
+                if (!__all_sync(0xffffffffu, ok)) break;
             }
         }
     } else {
@@ -1335,6 +1344,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const float sc = pre ? 1.f : p.scale_log2;
         const int tok_in = row_in / G, head_in = row_in - tok_in * G;
         uint32_t uses0 = 0, uses1 = 0;               // of the S buffers
+        uint32_t done0 = 0, done1 = 0;               // of pv_done: once a piece with a buffer each, else per tile
         uint32_t masks = 0;                          // tiles of the CTA so far
         for (uint32_t i = 0;; ++i) {
             if (pair_any(!wait_all(&h->seg_full[i % kRing], (i / kRing) & 1u))) break;
@@ -1448,11 +1458,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             }
                         }
                         // rows whose maximum moved rescale their O (each thread its half of it) once the
-                        // last P V is complete: S of this tile came after it, or (buffers in turn) after
-                        // the one before, so the barrier is in that phase or the next
+                        // last P V is complete.  (With buffers in turn S of this tile came after the P V
+                        // before that, so the barrier is in its phase or the next.)
                         if (j > 0) {
-                            const uint32_t was = dual ? par ^ 1u : ((buf ? use0 : use1) - 1u) & 1u;
-                            lost = !wait_all(&h->pv_done[dual ? g : buf ^ 1], was);
+                            // (with a buffer each, S of this tile came after it)
+                            if (!dual) lost = !wait_all(&h->pv_done[buf ^ 1], ((buf ? done0 : done1) + ((j - 1) >> 1)) & 1u);
                             tc_fence_after();
                             const uint32_t t_o = tmem + lane_base + kColO + (uint32_t)(128 * g + D / 2 * half);
 #pragma unroll 1
@@ -1513,7 +1523,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 bool fix = false;   // V that was kept apart: cells that this row sees
                 if (n_tiles > 0) {
                     const int buf = dual ? g : (n_tiles - 1) & 1;
-                    lost = lost || !wait_all(&h->pv_done[buf], ((buf ? use1 : use0) - 1u) & 1u);
+                    const uint32_t uses = dual ? 0u : (uint32_t)(n_tiles - 1) >> 1;   // before the last in this piece
+                    lost = lost || !wait_all(&h->pv_done[buf], ((buf ? done1 : done0) + uses) & 1u);
                     lost = lost || !wait_all(&h->load_done[i % kRing], (i / kRing) & 1u);
                     tc_fence_after();
                     for (int t = 0; t < kCutTiles; ++t)
@@ -1597,6 +1608,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (lost) break;
             uses0 = use0;
             uses1 = use1;
+            done0 += dual ? (n0 > 0 ? 1 : 0) : (n_max + 1) >> 1;
+            done1 += dual ? 1 : n_max >> 1;
             tc_fence_before();   // (O is read: the next piece's first P, which follows, lets it be written)
             give_back(i);
         }
