@@ -137,6 +137,17 @@ class KvattnError(RuntimeError):
         super().__init__(f"{where}: {kvattn_status_string(status)} ({status})")
 
 
+def _find_raw_stream():
+    try:
+        import torch
+        return torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getDevice") else None
+    except (ImportError, AttributeError):
+        return None
+
+
+_current_raw_stream = _find_raw_stream()
+
+
 def _ptr(x):
     """Address of a torch tensor / numpy array / int / None."""
     if x is None:
@@ -151,6 +162,8 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
+        if _current_raw_stream is not None:  # the same handle without a Stream object (about 4 us)
+            return _current_raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -503,23 +516,31 @@ def build_cell_plan(encoded_per_seq, capacity_cells, plan_stride=None):
     return plan[:n_seq, :plan_stride], lens[:n_seq]
 
 
+# The wrappers below are on the path of single decode steps, where the host's time counts: each
+# reads a tensor's shape and strides once, and calls the library itself with addresses.
+
 def _rows(x, name):
-    """(heads, head_dim, token stride) of half rows [T][heads][D]; the heads of a token must be
-    contiguous, the tokens may be strided (a slice of a fused projection)."""
+    """(tokens, heads, head_dim, token stride) of half rows [T][heads][D]; the heads of a token must
+    be contiguous, the tokens may be strided (a slice of a fused projection)."""
     import torch
-    if x.dim() != 3 or x.dtype != torch.float16:
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or x.dtype is not torch.float16:
         raise ValueError(f"{name}: half rows [tokens][heads][head_dim] are wanted")
-    t, h, d = x.shape
-    if x.numel() and (x.stride(2) != 1 or (h > 1 and x.stride(1) != d)):
+    t, h, d = shape
+    if (stride[2] != 1 or (h > 1 and stride[1] != d)) and x.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return h, d, (x.stride(0) if t > 1 else h * d)
+    return t, h, d, (stride[0] if t > 1 else h * d)
 
 
 def _ints(x, name, n=None):
     import torch
-    if x.dtype != torch.int32 or not x.is_contiguous() or (n is not None and x.numel() != n):
+    if x.dtype is not torch.int32 or not x.is_contiguous() or (n is not None and x.numel() != n):
         raise ValueError(f"{name}: contiguous int32" + ("" if n is None else f" of {n} values") + " is wanted")
-    return x
+    return x.data_ptr()
+
+
+def _raw(x):
+    return None if x is None else x.data_ptr()
 
 
 def _new_out(out, name, shape, like, dtype=None):
@@ -528,37 +549,35 @@ def _new_out(out, name, shape, like, dtype=None):
     dtype = torch.float16 if dtype is None else dtype
     if out is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or not out.is_contiguous():
+    if out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} of shape {tuple(shape)} is wanted")
     return out
 
 
 def _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim):
-    """kv_type from the row widths, as in decode; checks the planes' shapes and layout."""
+    """(kv_type, KV heads, cells) from the planes, the type by the row widths as in decode; checks
+    the planes' shapes, types and layout."""
     import torch
-    widths = k_cache.shape[-1], v_cache.shape[-1]
-    planes = [k_cache, v_cache]
+    ks, vs = k_cache.shape, v_cache.shape
     if k_scales is None and v_scales is None:
-        kv_type, want, kinds = KVATTN_KV_F16, (head_dim, head_dim), (torch.float16, torch.float16)
+        kv_type = KVATTN_KV_F16
+        good = ks == vs and ks[-1] == head_dim and k_cache.dtype is v_cache.dtype is torch.float16
     elif k_scales is None or v_scales is None:
         raise ValueError("k_scales and v_scales go together")
     else:
-        kv_type = {(1, 1): KVATTN_KV_Q8_0, (1, 2): KVATTN_KV_Q8_0_Q4_0, (2, 2): KVATTN_KV_Q4_0}.get(
-            tuple(head_dim // w if w else 0 for w in widths))
-        if kv_type is None:
-            raise ValueError("no cache type has rows of these widths")
-        bits = {KVATTN_KV_Q8_0: (8, 8), KVATTN_KV_Q8_0_Q4_0: (8, 4), KVATTN_KV_Q4_0: (4, 4)}[kv_type]
-        want = tuple(head_dim * b // 8 for b in bits)
-        kinds = tuple(torch.int8 if b == 8 else torch.uint8 for b in bits)
-        for s in (k_scales, v_scales):
-            if s.dtype != torch.float16 or s.shape[:-1] != k_cache.shape[:-1] or s.shape[-1] * 32 != head_dim:
-                raise ValueError("scale planes are half [cells][kv heads][head_dim / 32]")
-        planes += [k_scales, v_scales]
-    if widths != want or k_cache.dtype != kinds[0] or v_cache.dtype != kinds[1] or k_cache.shape[:-1] != v_cache.shape[:-1]:
-        raise ValueError("the cache planes do not agree with each other or with head_dim")
-    if not all(x.is_contiguous() for x in planes):
-        raise ValueError("cache planes are contiguous")
-    return kv_type
+        kb = 8 if ks[-1] == head_dim else 4
+        vb = 8 if vs[-1] == head_dim else 4
+        kv_type = {(8, 8): KVATTN_KV_Q8_0, (8, 4): KVATTN_KV_Q8_0_Q4_0, (4, 4): KVATTN_KV_Q4_0}.get((kb, vb))
+        want = ks[:-1] + (head_dim // 32,)
+        good = (kv_type is not None and ks[:-1] == vs[:-1] and ks[-1] * 8 == head_dim * kb and vs[-1] * 8 == head_dim * vb
+                and k_cache.dtype is (torch.int8 if kb == 8 else torch.uint8)
+                and v_cache.dtype is (torch.int8 if vb == 8 else torch.uint8)
+                and k_scales.dtype is v_scales.dtype is torch.float16 and k_scales.shape == want and v_scales.shape == want
+                and k_scales.is_contiguous() and v_scales.is_contiguous())
+    if len(ks) < 3 or not good or not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("the cache planes are contiguous [cells][kv heads][row] of one type's rows, codes int8 or packed "
+                         "uint8, scales half [cells][kv heads][head_dim / 32]")
+    return kv_type, ks[-2], math.prod(ks[:-2])
 
 
 class RopeTable:
@@ -582,42 +601,42 @@ def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, strea
     """q: half [T][H][D], k: half [T][Hk][D] (either may be None), positions int32 [T].  Rotated rows
     go to new tensors, or to ``q_out`` / ``k_out`` (which may be q and k themselves).  Returns (q, k)."""
     import torch
-    code = {"half": KVATTN_ROPE_HALF, "interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
+    code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
     some = q if q is not None else k
     T, D = some.shape[0], some.shape[-1]
-    args, outs = [], []
-    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            args.append((None, 0, 0, None, 0))
-            outs.append(None)
-            continue
-        h, d, st = _rows(x, name)
-        if y is None:
-            y = torch.empty((T, h, d), dtype=torch.float16, device=x.device)
-        if x.shape[0] != T or d != D or y.shape != x.shape:
-            raise ValueError(f"{name}: shapes do not agree")
-        args.append((x, st, h, y, _rows(y, name + "_out")[2]))
-        outs.append(y)
-    _ints(positions, "positions", T)
-    (q, qs, H, qo, qos), (k, ks, Hk, ko, kos) = args
-    kvattn_rope(q, qs, H, k, ks, Hk, positions, table.turns, table.gain, table.n_rot, code, T, D, qo, qos, ko, kos, stream)
-    return tuple(outs)
+    qa = ka = (None, 0, 0, None, 0)
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        t, h, d, st = _rows(q, "q")
+        if t != T or d != D or q_out.shape != q.shape:
+            raise ValueError("q: shapes do not agree")
+        qa = (q.data_ptr(), st, h, q_out.data_ptr(), _rows(q_out, "q_out")[3])
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.float16, device=k.device)
+        t, h, d, st = _rows(k, "k")
+        if t != T or d != D or k_out.shape != k.shape:
+            raise ValueError("k: shapes do not agree")
+        ka = (k.data_ptr(), st, h, k_out.data_ptr(), _rows(k_out, "k_out")[3])
+    _check(lib.kvattn_rope(qa[0], qa[1], qa[2], ka[0], ka[1], ka[2], _ints(positions, "positions", T), table.turns.data_ptr(),
+                           table.gain, table.n_rot, code, T, D, qa[3], qa[4], ka[3], ka[4], _stream(stream)), "kvattn_rope")
+    return q_out if q is not None else None, k_out if k is not None else None
 
 
 def cache_write(k, v, slots, k_cache, v_cache, *, k_scales=None, v_scales=None, status=None, stream=None):
     """k, v: half [T][Hk][D] into cells ``slots`` (int32 [T], -1: skipped; None: cells 0 .. T - 1) of a
     cache whose type follows from its planes.  ``status``: an int32 tensor whose first word collects
     the KVATTN_DEVICE_* bits."""
-    Hk, D, ks = _rows(k, "k")
-    Hv, Dv, vs = _rows(v, "v")
-    T = k.shape[0]
-    if (Hv, Dv, v.shape[0]) != (Hk, D, T) or k_cache.shape[-2] != Hk:
+    T, Hk, D, ks = _rows(k, "k")
+    vt, vh, vd, vs = _rows(v, "v")
+    kv_type, heads, n_cells = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
+    if (vt, vh, vd) != (T, Hk, D) or heads != Hk:
         raise ValueError("k, v and the cache do not agree")
-    kv_type = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
-    n_cells = k_cache.numel() // max(Hk * k_cache.shape[-1], 1)
-    if slots is not None:
-        _ints(slots, "slots", T)
-    kvattn_cache_write(k, ks, v, vs, slots, T, Hk, D, kv_type, k_cache, v_cache, k_scales, v_scales, n_cells, status, stream)
+    at = None if slots is None else _ints(slots, "slots", T)
+    _check(lib.kvattn_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, at, T, Hk, D, kv_type, k_cache.data_ptr(),
+                                  v_cache.data_ptr(), _raw(k_scales), _raw(v_scales), n_cells, _raw(status), _stream(stream)),
+           "kvattn_cache_write")
 
 
 def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scales=None, k_out=None, v_out=None, status=None,
@@ -625,20 +644,19 @@ def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scale
     """Cells ``slots`` (int32 [T], e.g. a row of a cell plan; -1 gives zeros; None: every cell) as
     half [T][Hk][head_dim] rows.  Returns (k, v)."""
     import torch
-    Hk = k_cache.shape[-2]
-    kv_type = _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim)
-    n_cells = k_cache.numel() // max(Hk * k_cache.shape[-1], 1)
-    T = n_cells if slots is None else _ints(slots, "slots").numel()
+    kv_type, Hk, n_cells = _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim)
+    T, at = (n_cells, None) if slots is None else (slots.numel(), _ints(slots, "slots"))
     if k_out is None:
         k_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
     if v_out is None:
         v_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
-    hk, dk, ks = _rows(k_out, "k_out")
-    hv, dv, vs = _rows(v_out, "v_out")
-    if (hk, dk, k_out.shape[0]) != (Hk, head_dim, T) or (hv, dv, v_out.shape[0]) != (Hk, head_dim, T):
+    kt, kh, kd, ks = _rows(k_out, "k_out")
+    vt, vh, vd, vs = _rows(v_out, "v_out")
+    if (kt, kh, kd) != (T, Hk, head_dim) or (vt, vh, vd) != (T, Hk, head_dim):
         raise ValueError("k_out and v_out are half [slots][kv heads][head_dim]")
-    kvattn_cache_read(k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, slots, T, Hk, head_dim, k_out, ks, v_out, vs,
-                      status, stream)
+    _check(lib.kvattn_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales), _raw(v_scales), kv_type, n_cells, at,
+                                 T, Hk, head_dim, k_out.data_ptr(), ks, v_out.data_ptr(), vs, _raw(status), _stream(stream)),
+           "kvattn_cache_read")
     return k_out, v_out
 
 
@@ -652,19 +670,19 @@ def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream
     """Causal attention of packed prompts: q half [T][H][D], k and v half [T][Hk][D], offsets int32
     [S + 1].  Returns (out half [T][H][D], lse float [T][H])."""
     import torch
-    H, D, qs = _rows(q, "q")
-    Hk, Dk, ks = _rows(k, "k")
-    Hv, Dv, vs = _rows(v, "v")
-    T = q.shape[0]
-    if (Dk, Dv, Hv) != (D, D, Hk) or k.shape[0] != T or v.shape[0] != T:
+    T, H, D, qs = _rows(q, "q")
+    kt, Hk, kd, ks = _rows(k, "k")
+    vt, vh, vd, vs = _rows(v, "v")
+    if (kt, kd) != (T, D) or (vt, vh, vd) != (T, Hk, D):
         raise ValueError("q, k and v do not agree")
-    S = _ints(offsets, "offsets").numel() - 1
+    off, S = _ints(offsets, "offsets"), offsets.numel() - 1
     out = _new_out(out, "out", (T, H, D), q)
     lse = _new_out(lse, "lse", (T, H), q, torch.float32)
     if ws is None:
         ws = prefill_workspace(T, S, H, Hk, D, q.device)
-    kvattn_prefill(q, qs, k, ks, v, vs, offsets, S, T, H, Hk, D, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws,
-                   ws.numel(), stream)
+    _check(lib.kvattn_prefill(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, off, S, T, H, Hk, D,
+                              1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                              ws.numel(), _stream(stream)), "kvattn_prefill")
     return out, lse
 
 
@@ -682,30 +700,29 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     whose ``n_cells`` are each sequence's.  Returns (out half [T][H][D], lse: the given tensor or
     None)."""
     import torch
-    H, D, qs = _rows(q, "q")
-    T, Hk = q.shape[0], k_cache.shape[-2]
-    S = _ints(offsets, "offsets").numel() - 1
-    _ints(seq_lens, "seq_lens", S)
-    kv_type = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
+    T, H, D, qs = _rows(q, "q")
+    off, S = _ints(offsets, "offsets"), offsets.numel() - 1
+    lens = _ints(seq_lens, "seq_lens", S)
+    kv_type, Hk, rows = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
     if n_cells is None:
         n_cells = k_cache.shape[1] if k_cache.dim() == 4 else k_cache.shape[0]
-    stride = 0
+    plan, stride = None, 0
     if cell_plan is not None:
         stride = cell_plan.shape[-1]
-        _ints(cell_plan, "cell_plan", S * stride)
-    rows = k_cache.numel() // max(Hk * k_cache.shape[-1], 1)
-    if (n_cells if cell_plan is not None else n_cells * S) > rows:
+        plan = _ints(cell_plan, "cell_plan", S * stride)
+    if (n_cells if plan is not None else n_cells * S) > rows:
         raise ValueError("the cache has fewer cells than n_cells says")
     if max_len is None:
-        max_len = stride if cell_plan is not None else n_cells
+        max_len = stride if plan is not None else n_cells
     out = _new_out(out, "out", (T, H, D), q)
     if lse is not None:
         _new_out(lse, "lse", (T, H), q, torch.float32)
     if ws is None:
         ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, q.device)
-    kvattn_prefill_chunk(q, qs, offsets, T, k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, cell_plan, stride, seq_lens,
-                         S, max_len, H, Hk, D, 1.0 / math.sqrt(D) if scale is None else scale, out, lse, ws, ws.numel(),
-                         stream)
+    _check(lib.kvattn_prefill_chunk(q.data_ptr(), qs, off, T, k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales),
+                                    _raw(v_scales), kv_type, n_cells, plan, stride, lens, S, max_len, H, Hk, D,
+                                    1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), _raw(lse), ws.data_ptr(),
+                                    ws.numel(), _stream(stream)), "kvattn_prefill_chunk")
     return out, lse
 
 
