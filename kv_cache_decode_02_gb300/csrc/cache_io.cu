@@ -70,10 +70,9 @@ __device__ __forceinline__ int64_t slot_of(const CacheIoParams& p, int64_t tok) 
 // BITS: of this side's rows (16, 8, 4).  One thread: 16 elements of token tok's row.
 template <int BITS>
 __device__ __forceinline__ void write_item(const CacheIoParams& p, int side, int64_t tok, uint32_t item, int64_t cell,
-                                           bool live) {
+                                           const Half16& x) {
     const int64_t row_elems = (int64_t)p.n_head_kv * p.head_dim;
-    Half16 x = {};
-    if (live) x = load16(p.src[side] + tok * p.stride[side] + 16 * (int64_t)item);
+    const bool live = cell >= 0;
     if (BITS == 16) {
         if (live) {
             uint4* d = reinterpret_cast<uint4*>(static_cast<__half*>(p.rows[side]) + cell * row_elems + 16 * item);
@@ -210,13 +209,17 @@ __global__ void __launch_bounds__(kIoThreads) cache_io_kernel(const __grid_const
     const uint32_t tok = in ? i / items : 0u;
     const uint32_t item = in ? i - tok * items : (threadIdx.x & 1u);
     const int side = blockIdx.y;
-    const int64_t cell = in ? slot_of(p, tok) : -1;
     if (WRITE) {  // (all lanes stay: the two halves of a block meet in shuffles)
+        // (the row is on its way while its slot is read; a skipped token's is read for nothing)
+        Half16 x = {};
+        if (in) x = load16(p.src[side] + (int64_t)tok * p.stride[side] + 16 * (int64_t)item);
+        const int64_t cell = in ? slot_of(p, tok) : -1;
         if (side == 0)
-            write_item<KBITS>(p, 0, tok, item, cell, cell >= 0);
+            write_item<KBITS>(p, 0, tok, item, cell, x);
         else
-            write_item<VBITS>(p, 1, tok, item, cell, cell >= 0);
+            write_item<VBITS>(p, 1, tok, item, cell, x);
     } else if (in) {
+        const int64_t cell = slot_of(p, tok);
         if (side == 0)
             read_item<KBITS>(p, 0, tok, item, cell);
         else

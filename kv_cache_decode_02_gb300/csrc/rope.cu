@@ -82,6 +82,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     // element offsets of the lane's two 16-byte pieces
     const int e0 = (INTERLEAVED || !turned) ? 16 * piece : 8 * piece;
     const int e1 = (INTERLEAVED || !turned) ? e0 + 8 : e0 + p.n_rot / 2;
+    const int total = p.n_head[0] + p.n_head[1];
+    auto place = [&](int j, const __half*& src, __half*& dst) {
+        const int which = j >= p.n_head[0] ? 1 : 0;
+        const int h = which ? j - p.n_head[0] : j;
+        src = p.src[which] + tok * p.src_stride[which] + (int64_t)h * D;
+        dst = p.dst[which] + tok * p.dst_stride[which] + (int64_t)h * D;
+    };
+    // two heads in flight per lane, the first two under way before the angles are made (a step of
+    // a few tokens is all latency)
+    uint4 x[2][2];
+    __half* d[2];
+    auto load = [&](int j0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int j = j0 + u * parts * kHeads;
+            const __half* s;
+            place(j < total ? j : j0, s, d[u]);
+            x[u][0] = *reinterpret_cast<const uint4*>(s + e0);
+            x[u][1] = *reinterpret_cast<const uint4*>(s + e1);
+        }
+    };
+    int j0 = part * kHeads + sub;
+    if (j0 >= total) return;
+    load(j0);
     Pairs t;
     if (turned) {
         const uint64_t pos = (uint64_t)(int64_t)__ldg(p.pos + tok);
@@ -95,32 +119,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
             t.s[i] = s * p.gain;
         }
     }
-    const int total = p.n_head[0] + p.n_head[1];
-    auto place = [&](int j, const __half*& src, __half*& dst) {
-        const int which = j >= p.n_head[0] ? 1 : 0;
-        const int h = which ? j - p.n_head[0] : j;
-        src = p.src[which] + tok * p.src_stride[which] + (int64_t)h * D;
-        dst = p.dst[which] + tok * p.dst_stride[which] + (int64_t)h * D;
-    };
-    // two heads in flight per lane
-    for (int j0 = part * kHeads + sub; j0 < total; j0 += 2 * parts * kHeads) {
-        const int j1 = j0 + parts * kHeads;
-        const __half *s0, *s1;
-        __half *d0, *d1;
-        place(j0, s0, d0);
-        place(j1 < total ? j1 : j0, s1, d1);
-        uint4 a0 = *reinterpret_cast<const uint4*>(s0 + e0), b0 = *reinterpret_cast<const uint4*>(s0 + e1);
-        uint4 a1 = *reinterpret_cast<const uint4*>(s1 + e0), b1 = *reinterpret_cast<const uint4*>(s1 + e1);
+    while (true) {
         if (turned) {
-            rotate16<INTERLEAVED>(a0, b0, t);
-            rotate16<INTERLEAVED>(a1, b1, t);
+            rotate16<INTERLEAVED>(x[0][0], x[0][1], t);
+            rotate16<INTERLEAVED>(x[1][0], x[1][1], t);
         }
-        *reinterpret_cast<uint4*>(d0 + e0) = a0;
-        *reinterpret_cast<uint4*>(d0 + e1) = b0;
-        if (j1 < total) {
-            *reinterpret_cast<uint4*>(d1 + e0) = a1;
-            *reinterpret_cast<uint4*>(d1 + e1) = b1;
+        *reinterpret_cast<uint4*>(d[0] + e0) = x[0][0];
+        *reinterpret_cast<uint4*>(d[0] + e1) = x[0][1];
+        if (j0 + parts * kHeads < total) {
+            *reinterpret_cast<uint4*>(d[1] + e0) = x[1][0];
+            *reinterpret_cast<uint4*>(d[1] + e1) = x[1][1];
         }
+        j0 += 2 * parts * kHeads;
+        if (j0 >= total) break;
+        load(j0);
     }
 }
 
