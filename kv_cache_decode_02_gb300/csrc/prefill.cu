@@ -99,6 +99,7 @@ struct Seg {
     int j0, n[2];        // first tile; tiles of the row groups from there
     int first_cut;       // from this tile on (from j0) some row does not see the tile whole
     int part;            // partial slot, or -1: the whole unit
+    int whole, turn;     // the first `whole` tiles, which every row sees whole, are taken from tile `turn` on
 };
 
 // f16: a slot that warps 9-11 mend or copy, or the end of a unit.
@@ -474,7 +475,7 @@ __device__ __forceinline__ Place place_of(const PrefillParams& p, uint32_t at) {
 // Fills in a piece of work: tiles [first, last) of a block.
 template <int D>
 __device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence& x, int seq, int g, uint32_t block, int32_t first,
-                                         int32_t last, int part, Seg& s) {
+                                         int32_t last, int part, int from, Seg& s) {
     constexpr int kGroups = Geometry<D>::kGroups;
     const int32_t tok0 = (int32_t)block * p.block_tokens;
     s.seq = seq;
@@ -498,6 +499,9 @@ __device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence&
     // (one token: all its rows see the same cells)
     const int64_t cut = (s.lim0 > 0 ? s.lim0 : 0) / kPrefillTile - first;
     s.first_cut = (s.n_tok == 1 || cut > n_max) ? n_max : (cut < 0 ? 0 : (int)cut);
+    s.whole = min(s.first_cut, (int)clamp64(x.len / kPrefillTile - first, 0, n_max));
+    if (s.n[1] > 0) s.whole = min(s.whole, min(s.n[0], s.n[1]));
+    s.turn = from < s.whole ? from : 0;
 }
 
 // A warp's walk over its CTA's pieces.
@@ -524,9 +528,9 @@ struct Walk {
     // The next piece in s; false: none left.
     __device__ __forceinline__ bool next(const PrefillParams& p, Seg& s) {
         int32_t first = 0, last = INT_MAX;
-        int part = -1;
-        if (!(p.shares ? next_share(p, first, last, part) : next_whole(p))) return false;
-        make_seg<D>(p, r.x, r.seq, (int)r.g, r.block, first, last, part, s);
+        int part = -1, from = 0;
+        if (!(p.shares ? next_share(p, first, last, part, from) : next_whole(p))) return false;
+        make_seg<D>(p, r.x, r.seq, (int)r.g, r.block, first, last, part, from, s);
         return true;
     }
 
@@ -556,7 +560,11 @@ struct Walk {
         return false;
     }
 
-    __device__ __forceinline__ bool next_share(const PrefillParams& p, int32_t& first, int32_t& last, int& part) {
+    // Blocks of one KV head read the same cells, in pieces that begin anywhere.  So that a tile's
+    // readers come by at about the same time, and find it in L2, every CTA takes tile t of any
+    // unit at about time t modulo the length of a share: a piece's whole tiles begin at the one
+    // whose time it is when the piece begins, and go around (`from`).
+    __device__ __forceinline__ bool next_share(const PrefillParams& p, int32_t& first, int32_t& last, int& part, int& from) {
         while (at < end) {
             if (!started || (r.block + 1u == r.x.blocks && r.g + 1u == (uint32_t)p.n_head_kv)) {
                 r = place_of(p, at);
@@ -589,6 +597,11 @@ struct Walk {
             }
             if (tiles == 0 ? a != r.start : first == last) continue;  // (a unit that sees nothing: its first piece)
             part = first == 0 && last == tiles ? -1 : 2 * (int)blockIdx.x + (a > r.start ? 0 : 1);
+            if (r.x.blocks > 1u) {
+                const int32_t period = max((int32_t)(sh.each >> 3), 1);
+                from = ((int32_t)((a - sh.of(blockIdx.x)) >> 3) - first) % period;
+                if (from < 0) from += period;
+            }
             return true;
         }
         return false;
@@ -622,7 +635,12 @@ struct Tile {
 __device__ __forceinline__ Tile read_tile(const PrefillParams& p, const Seg& s, int j) {
     Tile t;
     const int lane = threadIdx.x & 31;
-    const int64_t i0 = (int64_t)(s.j0 + j) * kPrefillTile;
+    int at = j;
+    if (j < s.whole) {
+        at += s.turn;
+        if (at >= s.whole) at -= s.whole;
+    }
+    const int64_t i0 = (int64_t)(s.j0 + at) * kPrefillTile;
     const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
     const int left = j < n_max ? (int)clamp64(s.len - i0, 0, kPrefillTile) : 0;
     t.run = true;
