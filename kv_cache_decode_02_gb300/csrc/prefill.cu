@@ -123,7 +123,7 @@ struct Header {
     uint64_t job_full[kRing], job_empty[kRing];
     uint32_t tmem;
     int abort_flag;
-    uint32_t bad_cells[kRing][kCutTiles][4];  // of a unit: cells of its cut tiles with V that is not finite
+    alignas(16) uint32_t bad_cells[kRing][kCutTiles][4];  // of a unit: cells of its cut tiles with V that is not finite
     uint32_t holes[kMasks];                   // whether the tile has any
     uint32_t slot_mend[kMaxSlots];            // whether the slot is one
     uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | unit << 8
@@ -132,7 +132,7 @@ struct Header {
     float meet[2][128];                       // what two threads of a row tell each other
     alignas(16) float bias[kMasks][kPrefillTile];  // through a plan: +inf, or -inf for a hole
 };
-static_assert(sizeof(Header) <= kHeaderBytes && offsetof(Header, bias) % 16 == 0, "header");
+static_assert(sizeof(Header) <= kHeaderBytes && offsetof(Header, bias) % 16 == 0 && offsetof(Header, bad_cells) % 16 == 0, "header");
 
 // Shared-memory matrix descriptor: start address, leading and stride byte offsets, the
 // descriptor version of this architecture family, 128-byte swizzle.
@@ -632,6 +632,7 @@ struct Tile {
     int64_t base;     // first physical cell when a run
     bool run, holes;  // the cells that are there lie at base + their number; some are not
 };
+template <bool PLAN>
 __device__ __forceinline__ Tile read_tile(const PrefillParams& p, const Seg& s, int j) {
     Tile t;
     const int lane = threadIdx.x & 31;
@@ -646,7 +647,7 @@ __device__ __forceinline__ Tile read_tile(const PrefillParams& p, const Seg& s, 
     t.run = true;
     t.holes = left < kPrefillTile;
     t.base = s.cell0 + i0;
-    const int32_t* row = p.plan != nullptr ? p.plan + (int64_t)s.seq * p.plan_stride + i0 : nullptr;
+    const int32_t* row = PLAN ? p.plan + (int64_t)s.seq * p.plan_stride + i0 : nullptr;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int c = 32 * k + lane;
@@ -656,8 +657,9 @@ __device__ __forceinline__ Tile read_tile(const PrefillParams& p, const Seg& s, 
     return t;
 }
 // Checks a plan tile's entries and whether they are one run; true: all entries are in range.
+template <bool PLAN>
 __device__ __forceinline__ bool settle(const PrefillParams& p, Tile& t) {
-    if (p.plan == nullptr) return true;
+    if (!PLAN) return true;
     const int lane = threadIdx.x & 31;
     int lo = INT_MAX, hi = INT_MIN;
     bool hole = false, good = true;
@@ -683,18 +685,20 @@ __device__ __forceinline__ bool settle(const PrefillParams& p, Tile& t) {
     return good;
 }
 // Physical cell of the tile's cell c (which may differ from lane to lane), -1: none.
-__device__ __forceinline__ int64_t cell_of(const PrefillParams& p, const Tile& t, int c) {
+template <bool PLAN>
+__device__ __forceinline__ int64_t cell_of(const Tile& t, int c) {
     const int32_t v0 = __shfl_sync(0xffffffffu, t.e[0], c & 31);
     const int32_t v1 = __shfl_sync(0xffffffffu, t.e[1], c & 31);
     const int32_t v2 = __shfl_sync(0xffffffffu, t.e[2], c & 31);
     const int32_t v3 = __shfl_sync(0xffffffffu, t.e[3], c & 31);
     const int32_t v = (c & 64) ? ((c & 32) ? v3 : v2) : ((c & 32) ? v1 : v0);
-    return (p.plan == nullptr && v >= 0) ? t.base + v : v;
+    return (!PLAN && v >= 0) ? t.base + v : v;
 }
 
 // ------------------------------------- the kernel -------------------------------------
 
-template <int D, int KBITS, int VBITS>
+// PLAN: through a cell plan (a kernel of its own: the masks' code slowed the others by 2 %).
+template <int D, int KBITS, int VBITS, bool PLAN>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
     constexpr int kGroups = Geometry<D>::kGroups, kHalves = Geometry<D>::kHalves;
     constexpr bool kQuant = KBITS != 16;
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     if (!take(i, s)) break;
                     const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
                     const uint32_t unit = (i & 0xffffu) << 8;
-                    Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
+                    Tile tk = read_tile<PLAN>(p, s, 0), tv = tk, next = read_tile<PLAN>(p, s, 1);
 #pragma unroll 1
                     for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
                         bool v_side;
@@ -835,10 +839,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             if (j > 0) {
                                 tv = tk;
                                 tk = next;
-                                next = read_tile(p, s, j + 1);
+                                next = read_tile<PLAN>(p, s, j + 1);
                             }
-                            if (!settle(p, tk)) bad_entry = true;
-                            if (p.plan != nullptr && !(ok = put_mask(tk, T))) break;
+                            if (!settle<PLAN>(p, tk)) bad_entry = true;
+                            if (PLAN && !(ok = put_mask(tk, T))) break;
                             ++T;
                         }
                         if (v_side && (s.n[1] > 0 || j + 1 == n_max)) tv = tk;
@@ -882,8 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         s = h->seg[i % kRing];                      // (not given back yet)
                         const bool v_side = job.word & 4u, cut = v_side && job.j >= s.first_cut;
                         const int half = (job.word >> 3) & 1u;
-                        Tile t = read_tile(p, s, job.j);
-                        settle(p, t);
+                        Tile t = read_tile<PLAN>(p, s, job.j);
+                        settle<PLAN>(p, t);
                         const uint32_t st = job.n % kSlots;
                         const int sub = lane >> 4, b = (lane & 15) * 16;      // 16 lanes a row
                         unsigned char* plane = slots + st * kSlotBytes + (b >> 7) * kPlaneBytes;
@@ -924,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 uint4 w[4];
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
-                                    const int64_t cell = cell_of(p, t, min(r0 + 6 * q, 126) + sub);
+                                    const int64_t cell = cell_of<PLAN>(t, min(r0 + 6 * q, 126) + sub);
                                     w[q] = make_uint4(0u, 0u, 0u, 0u);
                                     if (cell >= 0) w[q] = __ldg(reinterpret_cast<const uint4*>(rows + cell * row_bytes));
                                 }
@@ -1133,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll 1
                     for (int i = lane; i < 128 * bits; i += 32) {
                         const int c = i / bits, piece = i - c * bits;
-                        const int64_t cell = cell_of(p, t, c);
+                        const int64_t cell = cell_of<PLAN>(t, c);
                         if (cell >= 0)
                             cp_async_16_cg(stage + 16 * i, rows + (cell * Hk + s.g) * (D * bits / 8) + half * 16 * bits + 16 * piece);
                     }
@@ -1144,7 +1148,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t dst = stage + Memory<KBITS>::kRawBytes - 1024 + 8 * (32 * k + lane);
-                    const int64_t cell = p.plan == nullptr ? t.base + t.e[k] : t.e[k];
+                    const int64_t cell = !PLAN ? t.base + t.e[k] : t.e[k];
                     if (t.e[k] >= 0)
                         cp_async_8(dst, scales + (cell * Hk + s.g) * (D / 32));
                     else
@@ -1162,7 +1166,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     give_back(i);
                     continue;
                 }
-                Tile tk = read_tile(p, s, 0), tv = tk, next = read_tile(p, s, 1);
+                Tile tk = read_tile<PLAN>(p, s, 0), tv = tk, next = read_tile<PLAN>(p, s, 1);
 #pragma unroll 1
                 for (int step = 0; step < 2 * kHalves * n_max && ok; ++step) {
                     bool v_side;
@@ -1172,10 +1176,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         if (j > 0) {
                             tv = tk;
                             tk = next;
-                            next = read_tile(p, s, j + 1);
+                            next = read_tile<PLAN>(p, s, j + 1);
                         }
-                        if (!settle(p, tk)) bad_entry = true;
-                        if (p.plan != nullptr && !(ok = put_mask(tk, T))) break;
+                        if (!settle<PLAN>(p, tk)) bad_entry = true;
+                        if (PLAN && !(ok = put_mask(tk, T))) break;
                         ++T;
                     }
                     if (v_side && (s.n[1] > 0 || j + 1 == n_max)) tv = tk;
@@ -1245,7 +1249,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int n0 = __shfl_sync(0xffffffffu, s.n[0], 0), n1 = __shfl_sync(0xffffffffu, s.n[1], 0);
                 // (the tiles whose slots may be mended: cut ones, and a sequence's last; through a plan any)
                 const int whole = (int)clamp64(s.len / kPrefillTile - s.j0, 0, INT_MAX);
-                const int mend_from = p.plan != nullptr || p.use_tma == 0 ? 0 : __shfl_sync(0xffffffffu, min(s.first_cut, whole), 0);
+                const int mend_from = PLAN || p.use_tma == 0 ? 0 : __shfl_sync(0xffffffffu, min(s.first_cut, whole), 0);
                 if (n_tok < 0) break;
                 give_back(i);
                 const int n_max = n0 > n1 ? n0 : n1;
@@ -1398,6 +1402,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     else
                         ++use0;
                     const uint32_t t_s = tmem + lane_base + (buf ? kColS1 : 0u);
+                    if (PLAN && j != masked) {   // (once for both groups, and while S is on its way)
+                        const uint32_t t = masks + j;
+                        masked = j;
+                        lost = lost || !wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u);
+                        holes = h->holes[t % kMasks] != 0u;
+                    }
                     lost = lost || !wait_all(&h->s_full[buf], par);
                     tc_fence_after();
                     const int left = (g ? rel[1] : rel[0]) - j * kPrefillTile - 64 * half;
@@ -1422,13 +1432,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     tmem_ld32(t_s + 64 * half, sv);
                     tmem_ld32(t_s + 64 * half + 32, sv + 32);
                     tc_wait_ld();
-                    if (p.plan != nullptr) {
+                    if (PLAN) {
                         const uint32_t t = masks + j;
-                        if (j != masked) {   // (once for both groups)
-                            masked = j;
-                            lost = lost || !wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u);
-                            holes = h->holes[t % kMasks] != 0u;
-                        }
                         if (holes) {
                             // the minimum of the score and -inf for a hole, +inf for a cell: a NaN that
                             // stands in a hole goes too
@@ -1526,7 +1531,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&h->p_full[buf]));
                 }
-                if (p.plan != nullptr && g == (dual ? 1 : 0)) {   // every warp, for every tile
+                if (PLAN && g == (dual ? 1 : 0)) {   // every warp, for every tile
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[(masks + j) % kMasks]));
                 }
@@ -1535,7 +1540,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (pair_any(lost)) break;
             // ---- the piece's result: a thread has its row and half of the columns of each group ----
 #pragma unroll 1
-            for (int g = 0; g < kGroups; ++g) {
+            for (int g = 0; g < kGroups && g * p.group_tokens < s.n_tok; ++g) {
                 const int n_tiles = g ? n1 : n0;
                 const int tok = g * p.group_tokens + tok_in;
                 const bool row_ok = tok_in < p.group_tokens && tok < s.n_tok;
@@ -1548,9 +1553,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     lost = lost || !wait_all(&h->pv_done[buf], ((buf ? done1 : done0) + uses) & 1u);
                     lost = lost || !wait_all(&h->load_done[i % kRing], (i / kRing) & 1u);
                     tc_fence_after();
-                    for (int t = 0; t < kCutTiles; ++t)
-                        for (int k = 0; k < 4; ++k) fix = fix || h->bad_cells[i % kRing][t][k] != 0u;
-                    fix = fix && row_ok;
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int t = 0; t < kCutTiles; ++t) {
+                        const uint4 bad = *reinterpret_cast<const uint4*>(h->bad_cells[i % kRing][t]);
+                        any |= bad.x | bad.y | bad.z | bad.w;
+                    }
+                    fix = any != 0u && row_ok;
                 }
                 h->meet[half][row_in] = l_run;
                 lost = pair_any(lost);
@@ -1591,7 +1600,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 if (!((h->bad_cells[i % kRing][t][c >> 5] >> (c & 31)) & 1u)) continue;
                                 const int64_t at = (int64_t)(s.j0 + s.first_cut + t) * kPrefillTile + c;
                                 if (at >= s.lim0 + tok) continue;
-                                const int64_t cell = p.plan != nullptr ? (int64_t)__ldg(p.plan + (int64_t)s.seq * p.plan_stride + at)
+                                const int64_t cell = PLAN ? (int64_t)__ldg(p.plan + (int64_t)s.seq * p.plan_stride + at)
                                                                        : s.cell0 + at;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
@@ -1727,31 +1736,35 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const _
     }
 }
 
-template <int D>
+template <int D, bool PLAN>
 const void* kernel_of(int kv_type) {
     switch (kv_type) {
-    case KVATTN_KV_F16: return (const void*)prefill_kernel<D, 16, 16>;
-    case KVATTN_KV_Q8_0: return (const void*)prefill_kernel<D, 8, 8>;
-    case KVATTN_KV_Q8_0_Q4_0: return (const void*)prefill_kernel<D, 8, 4>;
-    default: return (const void*)prefill_kernel<D, 4, 4>;
+    case KVATTN_KV_F16: return (const void*)prefill_kernel<D, 16, 16, PLAN>;
+    case KVATTN_KV_Q8_0: return (const void*)prefill_kernel<D, 8, 8, PLAN>;
+    case KVATTN_KV_Q8_0_Q4_0: return (const void*)prefill_kernel<D, 8, 4, PLAN>;
+    default: return (const void*)prefill_kernel<D, 4, 4, PLAN>;
     }
+}
+const void* kernel_of(int kv_type, int head_dim, bool plan) {
+    if (head_dim == 128) return plan ? kernel_of<128, true>(kv_type) : kernel_of<128, false>(kv_type);
+    return plan ? kernel_of<256, true>(kv_type) : kernel_of<256, false>(kv_type);
 }
 int smem_of(int kv_type) {
     return kv_type == KVATTN_KV_F16 ? Memory<16>::kBytes : (kv_type == KVATTN_KV_Q4_0 ? Memory<4>::kBytes : Memory<8>::kBytes);
 }
 
 // Per device and kernel, once: its shared memory.
-cudaError_t prefill_setup(int kv_type, int head_dim) {
+cudaError_t prefill_setup(int kv_type, int head_dim, bool plan) {
     static std::mutex mu;
-    static bool done[64][4][2];
+    static bool done[64][4][2][2];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
-    bool& d = done[dev & 63][kv_type][head_dim == 256];
+    bool& d = done[dev & 63][kv_type][head_dim == 256][plan];
     if (!d) {
-        e = cudaFuncSetAttribute(head_dim == 128 ? kernel_of<128>(kv_type) : kernel_of<256>(kv_type),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(kv_type));
+        e = cudaFuncSetAttribute(kernel_of(kv_type, head_dim, plan), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 smem_of(kv_type));
         d = e == cudaSuccess;
     }
     return e;
@@ -1774,11 +1787,11 @@ cudaError_t launch(const void* f, dim3 grid, unsigned threads, size_t smem, void
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl) {
-    cudaError_t e = prefill_setup(kv_type, head_dim);
+    cudaError_t e = prefill_setup(kv_type, head_dim, p.plan != nullptr);
     if (e != cudaSuccess) return e;
     void* args[] = {const_cast<PrefillParams*>(&p), &n_ctas};
-    e = launch(head_dim == 128 ? kernel_of<128>(kv_type) : kernel_of<256>(kv_type), dim3((unsigned)n_ctas), kThreads,
-               (size_t)smem_of(kv_type), args, stream, pdl);
+    e = launch(kernel_of(kv_type, head_dim, p.plan != nullptr), dim3((unsigned)n_ctas), kThreads, (size_t)smem_of(kv_type),
+               args, stream, pdl);
     if (e != cudaSuccess || !p.shares || n_ctas < 2) return e;
     if (n_ctas > kMaxCtas) return cudaErrorInvalidValue;
     // two rows a warp (one at head_dim 256), so that a merge of a few units fills the device
