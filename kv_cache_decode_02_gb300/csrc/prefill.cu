@@ -289,11 +289,6 @@ __device__ __forceinline__ bool bar_or(int id, bool x) {
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// a scale that is not finite makes its whole block NaN
-__device__ __forceinline__ __half2 scale2(uint32_t d) {
-    if ((d & 0x7c00u) == 0x7c00u) d = 0x7fffu;
-    return as_h2(d | (d << 16));
-}
 __device__ __forceinline__ uint32_t nib2(uint32_t n) {
     return as_u32(__hsub2(as_h2(n | 0x64006400u), as_h2(0x64086408u)));
 }
@@ -322,7 +317,7 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w, bool& bad) {
 // a cut tile what is not finite is dropped and its cell noted.  Both are done to 16 bytes of a
 // slot after they were stored, and rarely.
 constexpr uint32_t kBigScale = 0x6006u;   // 515
-__device__ __forceinline__ void amend(unsigned char* at, bool cut, uint32_t* bad_row, int cell) {
+__device__ __forceinline__ void amend(unsigned char* at, uint32_t scale, bool cut, uint32_t* bad_row, int cell) {
     const __half2 top = __halves2half2(__ushort_as_half(0x7bffu), __ushort_as_half(0x7bffu));
     uint4 w = *reinterpret_cast<uint4*>(at);
     uint32_t o[4] = {w.x, w.y, w.z, w.w};
@@ -330,6 +325,7 @@ __device__ __forceinline__ void amend(unsigned char* at, bool cut, uint32_t* bad
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         o[i] = as_u32(__hmax2_nan(__hmin2_nan(as_h2(o[i]), top), __hneg2(top)));
+        if ((scale & 0x7c00u) == 0x7c00u) o[i] = 0x7fff7fffu;   // not finite: the whole block is NaN
         if (cut) o[i] = finite2(o[i], bad);
     }
     *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -991,29 +987,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             for (int k = 0; k < 4; ++k) {
                                 w[k] = *reinterpret_cast<const uint4*>(src + 2048 * (k0 + k));
                                 ds[k] = sc[64 * (k0 + k)];
-                                big = max(big, ds[k] & 0x7fffu);
+                                big = max(big, ds[k]);   // (a negative one, which no write makes, counts as big)
                             }
                             const bool odd = cut || big > kBigScale;   // rare: a loop of its own below
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const uint32_t d = as_u32(scale2(ds[k]));
-                                const uint32_t x[4] = {w[k].x ^ 0x80808080u, w[k].y ^ 0x80808080u, w[k].z ^ 0x80808080u,
-                                                       w[k].w ^ 0x80808080u};
+                                const uint32_t d = prmt_b32(ds[k], 0u, 0x1010u);
+                                const uint32_t x[4] = {(upper ? w[k].z : w[k].x) ^ 0x80808080u, (upper ? w[k].w : w[k].y) ^ 0x80808080u,
+                                                       (upper ? w[k].x : w[k].z) ^ 0x80808080u, (upper ? w[k].y : w[k].w) ^ 0x80808080u};
                                 uint32_t o[8];
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
                                     o[2 * q] = hmul2_u32(i8x2_lo(x[q]), d);
                                     o[2 * q + 1] = hmul2_u32(i8x2_hi(x[q]), d);
                                 }
-                                const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-                                *reinterpret_cast<uint4*>(d0 + 2048 * (k0 + k)) = upper ? b : a;
-                                *reinterpret_cast<uint4*>(d1 + 2048 * (k0 + k)) = upper ? a : b;
+                                *reinterpret_cast<uint4*>(d0 + 2048 * (k0 + k)) = make_uint4(o[0], o[1], o[2], o[3]);
+                                *reinterpret_cast<uint4*>(d1 + 2048 * (k0 + k)) = make_uint4(o[4], o[5], o[6], o[7]);
                             }
                             if (odd)
 #pragma unroll 1
-                                for (int k = 0; k < 4; ++k) {
-                                    amend(d0 + 2048 * (k0 + k), cut, bad_row, c0 + 16 * (k0 + k));
-                                    amend(d1 + 2048 * (k0 + k), cut, bad_row, c0 + 16 * (k0 + k));
+                                for (int k = k0; k < k0 + 4; ++k) {
+                                    amend(d0 + 2048 * k, sc[64 * k], cut, bad_row, c0 + 16 * k);
+                                    amend(d1 + 2048 * k, sc[64 * k], cut, bad_row, c0 + 16 * k);
                                 }
                         }
                     } else {
@@ -1034,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             const bool odd = cut || big > kBigScale;
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const uint32_t d = as_u32(scale2(ds[k]));
+                                const uint32_t d = prmt_b32(ds[k], 0u, 0x1010u);
                                 const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
                                 uint32_t o[16];  // elements 0-15 and 16-31 of the block
 #pragma unroll
@@ -1053,8 +1048,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             if (odd)
 #pragma unroll 1
                                 for (int i = 0; i < 8; ++i)
-                                    amend(plane + swz(c0, b + 16 * (i & 3)) + 4096 * (k0 + (i >> 2)), cut, bad_row,
-                                          c0 + 32 * (k0 + (i >> 2)));
+                                    amend(plane + swz(c0, b + 16 * (i & 3)) + 4096 * (k0 + (i >> 2)),
+                                          scales[4 * c0 + piece + 128 * (k0 + (i >> 2))], cut, bad_row, c0 + 32 * (k0 + (i >> 2)));
                         }
                     }
                     fence_async();
