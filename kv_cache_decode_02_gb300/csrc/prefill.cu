@@ -289,8 +289,13 @@ __device__ __forceinline__ bool bar_or(int id, bool x) {
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-__device__ __forceinline__ uint32_t nib2(uint32_t n) {
-    return as_u32(__hsub2(as_h2(n | 0x64006400u), as_h2(0x64086408u)));
+// Two 4-bit codes - 8 as halves, from bits 0-3 or 4-7 of both 16-bit halves of w: under the
+// exponent of 1024, or of 64, a code stands in the mantissa with weight one.
+__device__ __forceinline__ uint32_t nib_lo(uint32_t w) {
+    return as_u32(__hsub2(as_h2((w & 0x000f000fu) | 0x64006400u), as_h2(0x64086408u)));
+}
+__device__ __forceinline__ uint32_t nib_hi(uint32_t w) {
+    return as_u32(__hsub2(as_h2((w & 0x00f000f0u) | 0x54005400u), as_h2(0x54805480u)));
 }
 // Whether eight halves are all finite: adding 1 to an exponent of ones carries into the sign.
 __device__ __forceinline__ bool finite8(const uint4& w) {
@@ -1035,10 +1040,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
                                     const uint32_t a = prmt_b32(x[q], 0u, 0x4140u), e = prmt_b32(x[q], 0u, 0x4342u);
-                                    o[2 * q] = hmul2_u32(nib2(a & 0x000f000fu), d);
-                                    o[2 * q + 1] = hmul2_u32(nib2(e & 0x000f000fu), d);
-                                    o[8 + 2 * q] = hmul2_u32(nib2((a >> 4) & 0x000f000fu), d);
-                                    o[9 + 2 * q] = hmul2_u32(nib2((e >> 4) & 0x000f000fu), d);
+                                    o[2 * q] = hmul2_u32(nib_lo(a), d);
+                                    o[2 * q + 1] = hmul2_u32(nib_lo(e), d);
+                                    o[8 + 2 * q] = hmul2_u32(nib_hi(a), d);
+                                    o[9 + 2 * q] = hmul2_u32(nib_hi(e), d);
                                 }
 #pragma unroll
                                 for (int q = 0; q < 4; ++q)
