@@ -1408,7 +1408,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         lost = lost || !wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u);
                         holes = h->holes[t % kMasks] != 0u;
                     }
-                    lost = lost || !wait_all(&h->s_full[buf], par);
+                    // (without a vote: the barrier below ORs what a lane lost)
+                    lost = lost || !wait_bar(smem_addr(&h->s_full[buf]), par, abort_flag, p.wait_limit_ns);
+                    __syncwarp();
                     tc_fence_after();
                     const int left = (g ? rel[1] : rel[0]) - j * kPrefillTile - 64 * half;
                     if (pre || !__all_sync(0xffffffffu, left >= 64)) {
