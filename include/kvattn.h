@@ -537,7 +537,7 @@ size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head
  * that follow from the lengths alone (the result does not depend on timing), and merged.
  *  ws        kvattn_prefill_chunk_workspace_bytes(...) bytes, 256-byte aligned, zeroed once after
  *            allocation; work that shares one is ordered by the caller.
- * Errors: INVALID_ARG, UNSUPPORTED (also max_len of 2^31 or more), WORKSPACE (before any launch);
+ * Errors: INVALID_ARG, UNSUPPORTED (also max_len of 2^31 or more, n_seq x n_cells of 2^63), WORKSPACE (before any launch);
  * CUDA.
  */
 int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets, int64_t n_tok, const void* k_cache,

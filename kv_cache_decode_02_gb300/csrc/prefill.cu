@@ -67,7 +67,7 @@ constexpr int kPlaneBytes = 128 * 128;        // 128 cells (or rows) x 128 bytes
 constexpr int kSlotBytes = 2 * kPlaneBytes;   // 128 cells x 128 dims of f16
 constexpr int kQTileBytes = 2 * kPlaneBytes;  // 128 rows x 128 dims of f16
 constexpr int kMaxSlots = 5;
-constexpr int kHeaderBytes = 3072;
+constexpr int kHeaderBytes = 3 * 1024;
 constexpr int kRing = 4;                      // pieces of work whose plans are kept
 constexpr int kMasks = 2;                     // tiles whose masks are
 constexpr int kRawStages = 3;                 // quantised: slots of raw bytes in flight
@@ -454,6 +454,7 @@ __device__ __forceinline__ Place place_of(const PrefillParams& p, uint32_t at) {
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
     }
+    if (r.x.blocks == 0u) return r;   // (no such place: offsets that overlap can pass the line's 32 bits)
     r.line = line_of(p, r.x);
     const uint32_t per = r.line.upto(r.x.blocks);
     uint32_t y = at - base;
@@ -578,6 +579,7 @@ struct Walk {
                 r.start = r.end;
                 r.end = r.start + r.line.a + r.line.step * r.block;
             }
+            if (r.end <= at) break;
             const uint32_t a = at, b = min(r.end, end);
             at = b;
             const int32_t tiles = r.tiles(p);
@@ -587,7 +589,7 @@ struct Walk {
             if (a == r.start && b != r.end && tiles > 0 && (threadIdx.x & 31) == 0) {
                 PrefillCut* cut = p.cuts + blockIdx.x;
                 int parts = 1;
-                while (sh.of(blockIdx.x + (uint32_t)parts) < r.end) ++parts;
+                while (blockIdx.x + (uint32_t)parts < gridDim.x && sh.of(blockIdx.x + (uint32_t)parts) < r.end) ++parts;
                 cut->q_tok = r.x.q0 + r.tok0(p);
                 cut->n_tok = min(r.x.n_q - r.tok0(p), p.block_tokens);
                 cut->g = (int32_t)r.g;
@@ -896,11 +898,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         if (type == kJobMend) {
                             // (MMA waits for the mended slot, so this use of it is not over)
                             if (!wait_all(&h->full[st], (job.n / kSlots) & 1u)) break;
+                            // (cells below the first token's end are seen by all rows: nothing to keep apart)
+                            const int64_t seen = s.lim0 - (int64_t)(s.j0 + job.j) * kPrefillTile;
 #pragma unroll 1
                             for (int k4 = 0; k4 < 4; ++k4) {                  // 32 cells at a time
                                 const int32_t e = k4 < 2 ? (k4 ? t.e[1] : t.e[0]) : (k4 == 2 ? t.e[2] : t.e[3]);
                                 const uint32_t gone = __ballot_sync(0xffffffffu, e < 0);
-                                if (!cut && gone == 0u) continue;
+                                if ((!cut || seen >= 32 * k4 + 32) && gone == 0u) continue;
                                 unsigned char* cells = plane + 4096 * k4;
 #pragma unroll
                                 for (int q = 0; q < 6; ++q) {

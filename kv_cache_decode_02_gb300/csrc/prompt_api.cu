@@ -289,7 +289,8 @@ int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets
     if (st != KVATTN_OK) return st;
     if (max_len < 0 || n_cells < 1 || !std::isfinite(scale) || (cell_plan != nullptr && plan_stride < 1))
         return KVATTN_ERR_INVALID_ARG;
-    if (max_len > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
+    // (cells are numbered in 63 bits over all sequences)
+    if (max_len > INT32_MAX || n_cells > INT64_MAX / std::max(n_seq, 1)) return KVATTN_ERR_UNSUPPORTED;
     st = check_cache(kv_type, k_cache, v_cache, k_scales, v_scales, head_dim);
     if (st != KVATTN_OK) return st;
     if (n_tok == 0 || n_seq == 0) return KVATTN_OK;

@@ -539,6 +539,13 @@ def _ints(x, name, n=None):
     return x.data_ptr()
 
 
+def _here(x, name):
+    """Refuses a host tensor, or one of another device than the current one, whose stream is used."""
+    import torch
+    if not x.is_cuda or x.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: a tensor of the current CUDA device is wanted")
+
+
 def _raw(x):
     return None if x is None else x.data_ptr()
 
@@ -619,6 +626,7 @@ def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, strea
         if t != T or d != D or k_out.shape != k.shape:
             raise ValueError("k: shapes do not agree")
         ka = (k.data_ptr(), st, h, k_out.data_ptr(), _rows(k_out, "k_out")[3])
+    _here(some, "q" if q is not None else "k")
     _check(lib.kvattn_rope(qa[0], qa[1], qa[2], ka[0], ka[1], ka[2], _ints(positions, "positions", T), table.turns.data_ptr(),
                            table.gain, table.n_rot, code, T, D, qa[3], qa[4], ka[3], ka[4], _stream(stream)), "kvattn_rope")
     return q_out if q is not None else None, k_out if k is not None else None
@@ -634,6 +642,8 @@ def cache_write(k, v, slots, k_cache, v_cache, *, k_scales=None, v_scales=None, 
     if (vt, vh, vd) != (T, Hk, D) or heads != Hk:
         raise ValueError("k, v and the cache do not agree")
     at = None if slots is None else _ints(slots, "slots", T)
+    _here(k, "k")
+    _here(k_cache, "k_cache")
     _check(lib.kvattn_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, at, T, Hk, D, kv_type, k_cache.data_ptr(),
                                   v_cache.data_ptr(), _raw(k_scales), _raw(v_scales), n_cells, _raw(status), _stream(stream)),
            "kvattn_cache_write")
@@ -650,6 +660,7 @@ def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scale
         k_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
     if v_out is None:
         v_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
+    _here(k_cache, "k_cache")
     kt, kh, kd, ks = _rows(k_out, "k_out")
     vt, vh, vd, vs = _rows(v_out, "v_out")
     if (kt, kh, kd) != (T, Hk, head_dim) or (vt, vh, vd) != (T, Hk, head_dim):
@@ -676,6 +687,7 @@ def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream
     if (kt, kd) != (T, D) or (vt, vh, vd) != (T, Hk, D):
         raise ValueError("q, k and v do not agree")
     off, S = _ints(offsets, "offsets"), offsets.numel() - 1
+    _here(q, "q")
     out = _new_out(out, "out", (T, H, D), q)
     lse = _new_out(lse, "lse", (T, H), q, torch.float32)
     if ws is None:
@@ -714,6 +726,8 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
         raise ValueError("the cache has fewer cells than n_cells says")
     if max_len is None:
         max_len = stride if plan is not None else n_cells
+    _here(q, "q")
+    _here(k_cache, "k_cache")
     out = _new_out(out, "out", (T, H, D), q)
     if lse is not None:
         _new_out(lse, "lse", (T, H), q, torch.float32)

@@ -106,7 +106,7 @@ def chunk(kvattn, **over):
 
 
 @pytest.mark.parametrize("over,want", [
-    (dict(D=64), UNS), (dict(H=30), INV), (dict(H=129, Hk=1), UNS), 
+    (dict(D=64), UNS), (dict(H=30), INV), (dict(H=129, Hk=1), UNS), (dict(n_cells=1 << 62, n_seq=4), UNS),
     (dict(max_len=-1), INV), (dict(max_len=1 << 31), UNS), (dict(n_cells=0), INV), (dict(plan=A), INV), (dict(plan=A + 2, stride=128), INV),
     (dict(kv_type=5), INV), (dict(kv_type=1), INV), (dict(ksc=A, vsc=A), INV), (dict(kv_type=1, ksc=A, vsc=A + 4), INV),
     (dict(k=None), INV), (dict(v=A + 8), INV), (dict(q=A + 2), INV), (dict(qs=4090), INV), (dict(off=None), INV),
@@ -148,3 +148,17 @@ def test_wrapper_checks(kvattn):
         kvattn.cache_read(torch.zeros(9, 2, 128, dtype=torch.int8), torch.zeros(9, 2, 128, dtype=torch.int8), off, head_dim=128)
     with pytest.raises(ValueError):
         kvattn.rope(h(4, 4, 128), h(5, 2, 128), torch.zeros(4, dtype=torch.int32), kvattn.RopeTable(off, 1.0, 128))
+
+
+def test_wrappers_refuse_host_tensors(kvattn):
+    torch = pytest.importorskip("torch")
+    h = lambda *s: torch.zeros(*s, dtype=torch.float16)  # noqa: E731
+    off, slots = torch.tensor([0, 4], dtype=torch.int32), torch.arange(4, dtype=torch.int32)
+    calls = [lambda: kvattn.prefill(h(4, 4, 128), h(4, 2, 128), h(4, 2, 128), off),
+             lambda: kvattn.prefill_chunk(h(4, 4, 128), off, h(9, 2, 128), h(9, 2, 128), off[1:]),
+             lambda: kvattn.cache_write(h(4, 2, 128), h(4, 2, 128), slots, h(9, 2, 128), h(9, 2, 128)),
+             lambda: kvattn.cache_read(h(9, 2, 128), h(9, 2, 128), slots, head_dim=128),
+             lambda: kvattn.rope(h(4, 4, 128), h(4, 2, 128), slots, kvattn.RopeTable(off, 1.0, 128))]
+    for call in calls:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
