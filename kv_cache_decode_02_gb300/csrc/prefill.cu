@@ -377,14 +377,31 @@ __device__ __forceinline__ int32_t tiles_seen(int64_t lim0, int32_t n) {
 // its tiles (by a rule that is linear in the block's number, so that sums have a closed form; the
 // last share of a unit takes what is left).  CTA c of n takes [share(c), share(c + 1)) of it.
 // Order: sequence, KV head, block.  The host sees to it that the line fits 32 bits.
+// (With f16 rows and no plan a tile for one row group of two takes about 0.55 of one for both,
+// 1900 clocks to 3450: a last block of one group counts 5 / 8 (units of 1 to 256 tokens over 8192
+// to 65536 cells: 243 -> 229 us).  Through a plan, or from quantised rows, it waits for its loader
+// and counts as a whole one: 5 / 8 there took 267 -> 302 us.)
 struct Line {
-    uint32_t a, step;   // length of block b: a + step b
-    __device__ __forceinline__ uint32_t upto(uint32_t b) const { return a * b + step * (b * (b - 1u) / 2u); }
+    uint32_t a, step;       // length of block b: a + step b,
+    uint32_t blocks, less;  // the last one's less this
+    __device__ __forceinline__ uint32_t of(uint32_t b) const { return a + step * b - (b + 1u == blocks ? less : 0u); }
+    __device__ __forceinline__ uint32_t upto(uint32_t b) const {
+        return a * b + step * (b * (b - 1u) / 2u) - (b == blocks ? less : 0u);
+    }
 };
+// Length of a tile of a block of n tokens in the line.
+__device__ __forceinline__ int32_t tile_length(const PrefillParams& p, int32_t n_tok) {
+    return n_tok <= p.group_tokens ? p.single_length : 8;
+}
 __device__ __forceinline__ Line line_of(const PrefillParams& p, const Sequence& x) {
     const int32_t lim = max(x.len - x.n_q, 0) + min(x.n_q, p.block_tokens);  // of the first block's last token, or above
-    return Line{8u * (uint32_t)(kUnitCost + (lim + kPrefillTile - 1) / kPrefillTile),
-                (uint32_t)(p.block_tokens + 15) / 16u};
+    Line l{8u * (uint32_t)(kUnitCost + (lim + kPrefillTile - 1) / kPrefillTile), (uint32_t)(p.block_tokens + 15) / 16u, x.blocks,
+           0u};
+    if (x.blocks != 0u) {
+        const uint32_t whole = l.of(x.blocks - 1u);
+        l.less = whole - (whole * (uint32_t)tile_length(p, x.n_q - (int32_t)(x.blocks - 1u) * p.block_tokens) >> 3);
+    }
+    return l;
 }
 struct Shares {
     uint32_t total, each, left, n;
@@ -428,14 +445,14 @@ struct Place {
     int seq;
     uint32_t g, block, start, end;  // start, end: the unit's part of the line
     __device__ __forceinline__ int32_t tok0(const PrefillParams& p) const { return (int32_t)block * p.block_tokens; }
+    __device__ __forceinline__ int32_t tokens(const PrefillParams& p) const { return min(x.n_q - tok0(p), p.block_tokens); }
     __device__ __forceinline__ int32_t tiles(const PrefillParams& p) const {
-        const int32_t t = tok0(p);
-        return tiles_seen((int64_t)x.len - x.n_q + 1 + t, min(x.n_q - t, p.block_tokens));
+        return tiles_seen((int64_t)x.len - x.n_q + 1 + tok0(p), tokens(p));
     }
 };
-// The tile that position y of a unit of that length and n tiles falls on.
-__device__ __forceinline__ int32_t tile_at(uint32_t y, uint32_t length, int32_t n) {
-    const int32_t t = ((int32_t)y - 8 * (int32_t)kUnitCost) >> 3;
+// The tile that position y of a unit of that length and n tiles of length `each` falls on.
+__device__ __forceinline__ int32_t tile_at(uint32_t y, uint32_t length, int32_t n, int32_t each) {
+    const int32_t t = ((int32_t)y - each * (int32_t)kUnitCost) / each;
     return y >= length ? n : min(max(t, 0), n);
 }
 __device__ __forceinline__ Place place_of(const PrefillParams& p, uint32_t at) {
@@ -470,7 +487,7 @@ __device__ __forceinline__ Place place_of(const PrefillParams& p, uint32_t at) {
     }
     r.block = lo;
     r.start = at - (y - r.line.upto(lo));
-    r.end = r.start + r.line.a + r.line.step * lo;
+    r.end = r.start + r.line.of(lo);
     return r;
 }
 
@@ -577,21 +594,21 @@ struct Walk {
                     ++r.g;
                 }
                 r.start = r.end;
-                r.end = r.start + r.line.a + r.line.step * r.block;
+                r.end = r.start + r.line.of(r.block);
             }
             if (r.end <= at) break;
             const uint32_t a = at, b = min(r.end, end);
             at = b;
-            const int32_t tiles = r.tiles(p);
-            first = tile_at(a - r.start, r.end - r.start, tiles);
-            last = tile_at(b - r.start, r.end - r.start, tiles);
+            const int32_t tiles = r.tiles(p), each = tile_length(p, r.tokens(p));
+            first = tile_at(a - r.start, r.end - r.start, tiles, each);
+            last = tile_at(b - r.start, r.end - r.start, tiles, each);
             // a unit whose first piece is here and whose last is not: the merge joins its parts
             if (a == r.start && b != r.end && tiles > 0 && (threadIdx.x & 31) == 0) {
                 PrefillCut* cut = p.cuts + blockIdx.x;
                 int parts = 1;
                 while (blockIdx.x + (uint32_t)parts < gridDim.x && sh.of(blockIdx.x + (uint32_t)parts) < r.end) ++parts;
                 cut->q_tok = r.x.q0 + r.tok0(p);
-                cut->n_tok = min(r.x.n_q - r.tok0(p), p.block_tokens);
+                cut->n_tok = r.tokens(p);
                 cut->g = (int32_t)r.g;
                 cut->tiles = tiles;
                 cut->start = r.start;
@@ -1442,7 +1459,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         const uint32_t t = masks + j;
                         if (holes) {
                             // the minimum of the score and -inf for a hole, +inf for a cell: a NaN that
-                            // stands in a hole goes too
+                            // stands in a hole goes too (a bit for each cell and a select took longer)
                             const float4* bias = reinterpret_cast<const float4*>(h->bias[t % kMasks]) + 16 * half;
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
@@ -1454,6 +1471,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             }
                         }
                     }
+
                     float mx[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mx[k] = fmaxf(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
@@ -1685,8 +1703,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const _
     for (int i = threadIdx.x; i < cut.n_parts; i += 32 * kMergeWarps) {
         const uint32_t cta = blockIdx.x + (uint32_t)i;
         const uint32_t x0 = sh.of(cta), a = max(x0, cut.start), b = min(sh.of(cta + 1u), cut.end);
-        const int32_t first = tile_at(a - cut.start, cut.end - cut.start, cut.tiles);
-        const int32_t last = tile_at(b - cut.start, cut.end - cut.start, cut.tiles);
+        const int32_t each = tile_length(p, cut.n_tok);
+        const int32_t first = tile_at(a - cut.start, cut.end - cut.start, cut.tiles, each);
+        const int32_t last = tile_at(b - cut.start, cut.end - cut.start, cut.tiles, each);
         whole = whole || (first == 0 && last == cut.tiles);
         slot[i] = first == last ? -1 : 2 * (int)cta + (x0 > cut.start ? 0 : 1);
     }

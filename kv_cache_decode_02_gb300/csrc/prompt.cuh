@@ -67,6 +67,7 @@ struct PrefillParams {
     int n_seq, n_head, n_head_kv, group;
     int group_tokens;         // tokens of a row group: floor(128 / group)
     int block_tokens;         // tokens of a unit: two row groups at head_dim 128, one at 256
+    int single_length;        // of a tile for one row group in the line of shares, in eighths of one for all
     int shares;               // 1: equal shares of all units' tiles, cut anywhere; 0: whole units
     int use_tma;
     int out_sectors;          // out is 32-byte aligned
