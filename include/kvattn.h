@@ -1,6 +1,9 @@
 /*
  * kvattn -- single-query (n_q = 1) split-KV decode attention for GB300 (sm_103a).
  *
+ * At the end of this file, the prompt side of the same caches: rotary positions, cells written
+ * and read, causal attention of whole prompts and of chunks of new tokens.
+ *
  * C ABI: plain pointers and sizes only.  "device" pointers are CUDA device memory of
  * the current device, "host" pointers are ordinary (or pinned, where stated) host
  * memory.  Streams are passed as `void*` holding a cudaStream_t (NULL = the legacy

