@@ -511,6 +511,7 @@ size_t kvattn_prefill_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int 
  *            clamped).  Tokens in front of the first sequence and behind the last are neither read
  *            nor written; sequences may be empty.
  *  out       device half [n_tok][n_head][head_dim];  lse  NULL or device float [n_tok][n_head].
+ *            Neither overlaps an input.
  *  ws        at least kvattn_prefill_workspace_bytes(...) bytes, 256-byte aligned, zeroed once
  *            after allocation; its first word is the sticky status word.  Calls may share it.
  * Values that are not finite reach the rows that see them only.

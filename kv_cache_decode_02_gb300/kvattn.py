@@ -718,7 +718,8 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     lens = _ints(seq_lens, "seq_lens", S)
     kv_type, Hk, rows = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
     if n_cells is None:
-        n_cells = k_cache.shape[1] if k_cache.dim() == 4 else k_cache.shape[0]
+        per_sequence = k_cache.dim() == 4 and cell_plan is None
+        n_cells = k_cache.shape[1] if per_sequence else rows
     plan, stride = None, 0
     if cell_plan is not None:
         stride = cell_plan.shape[-1]

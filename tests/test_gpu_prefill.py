@@ -280,6 +280,43 @@ def test_results_do_not_depend_on_how_the_work_is_cut(kvattn, ctas):
         assert torch.equal(got[-1][0], again[0]) and torch.equal(got[-1][1], again[1])
 
 
+@pytest.mark.parametrize("H", [12, 4])
+@pytest.mark.parametrize("n", [2, 7, 40, 150])
+def test_blocks_of_one_and_two_row_groups_share_the_line(kvattn, ctas, n, H):
+    """Contiguous f16 caches, where a tile for one row group counts less: sequences whose last block
+    has one group, both, and is alone, cut in few and many shares."""
+    ctas(n)
+    check_chunk(kvattn, make_chunk("f16", [130, 1, 45, 22, 64], [2500, 1900, 45, 3100, 1000], H, 2, 128, False))
+
+
+@pytest.mark.parametrize("kind,plan,D", [("f16", False, 128), ("f16", True, 256), ("q8_0", True, 128), ("q4_0", False, 256)])
+@pytest.mark.parametrize("n", [3, 8, 29])
+def test_pieces_that_go_around(kvattn, ctas, kind, plan, D, n):
+    """Several blocks of a KV head: a piece's whole tiles begin somewhere inside it.  A score that
+    rules its row sits in the first tiles, so what is added after them has to be small."""
+    ctas(n)
+    c = make_chunk(kind, [300], [4000], 8, 2, D, plan, 0.1)
+    if kind == "f16":
+        c["k"][(c["plan"][0, 64:72].clamp(min=0).long() if plan else torch.arange(64, 72, device="cuda"))] *= 4
+    check_chunk(kvattn, c)
+
+
+def test_rows_that_a_block_does_not_have(kvattn, ctas):
+    """A call full of queries that are not finite, then calls whose blocks leave rows of a group
+    empty (their rows of shared memory may still hold those): nothing of them shows."""
+    for n in (None, 4):
+        ctas(n)
+        c = make_chunk("f16", [200], [900], 6, 1, 128, False)
+        c["q"][:] = float("nan")
+        out, _ = call_chunk(kvattn, c)
+        assert bool(torch.isnan(out).all())
+        check_chunk(kvattn, make_chunk("f16", [3], [900], 6, 1, 128, False))
+        check_chunk(kvattn, make_chunk("q8_0", [1, 23], [900, 700], 5, 1, 128, True, 0.1))
+        c["q"][:] = float("inf")
+        call_chunk(kvattn, c)
+        check_chunk(kvattn, make_chunk("f16", [3, 30], [900, 30], 3, 1, 256, False))
+
+
 @pytest.mark.parametrize("kind", ["f16", "q8_0", "q4_0"])
 @pytest.mark.parametrize("n", [0, 6])
 def test_chunk_values_that_are_not_finite(kvattn, ctas, kind, n):
