@@ -1702,7 +1702,7 @@ constexpr int kMergeWarps = 4;
 constexpr int kMaxCtas = 1024;
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const __grid_constant__ PrefillParams p, int n_ctas) {
-    constexpr int kGroups = Geometry<D>::kGroups;
+    constexpr int kGroups = Geometry<D>::kGroups, kBatch = 512 / D;
     __shared__ int slot[kMaxCtas];   // part i's partial slot, -1: it holds no tile
     pdl_wait();
     const PrefillCut cut = p.cuts[blockIdx.x];
@@ -1729,10 +1729,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const _
         const int tok_in = in / G, tok = grp * p.group_tokens + tok_in;
         if (tok_in >= p.group_tokens || tok >= cut.n_tok) continue;
         // maximum over the parts, a lane each
+        auto lse_of = [&](int i) -> float {
+            const int sl = i < parts ? slot[i] : -1;
+            return sl < 0 ? -INFINITY : p.part_lse[(int64_t)sl * kGroups * 128 + row];
+        };
         float m = -INFINITY;
         for (int i = lane; i < parts; i += 32) {
-            if (slot[i] < 0) continue;
-            const float v = p.part_lse[(int64_t)slot[i] * kGroups * 128 + row];
+            const float v = lse_of(i);
             m = v > m || v != v ? v : m;  // (a NaN stays)
         }
 #pragma unroll
@@ -1743,24 +1746,42 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const _
         float acc[D / 32] = {};
         float sum = 0.f;
         if (m != -INFINITY) {
-            // (a part without a cell that the row sees has weight 0 and an O that was not written)
-#pragma unroll 4
-            for (int i = 0; i < parts; ++i) {
-                const int sl = slot[i];
-                const float v = sl < 0 ? -INFINITY : p.part_lse[(int64_t)sl * kGroups * 128 + row];
-                if (v == -INFINITY) continue;
-                const float w = exp2f((v - m) * 1.4426950408889634f);
+            for (int i0 = 0; i0 < parts; i0 += 32) {
+                // (a part without a cell that the row sees has weight 0 and an O that was not written)
+                const float v = lse_of(i0 + lane);
+                const float w = v == -INFINITY ? 0.f : exp2f((v - m) * 1.4426950408889634f);
                 sum += w;
-                const float4* o = reinterpret_cast<const float4*>(p.part_o + ((int64_t)sl * kGroups * 128 + row) * D);
+                uint32_t left = __ballot_sync(0xffffffffu, v != -INFINITY);
+                while (left != 0u) {   // the rows of kBatch parts on their way at once
+                    float4 f[kBatch][D / 128];
+                    float wk[kBatch];
+                    int at[kBatch];
 #pragma unroll
-                for (int k = 0; k < D / 128; ++k) {
-                    const float4 f = o[32 * k + lane];
-                    acc[4 * k] += w * f.x;
-                    acc[4 * k + 1] += w * f.y;
-                    acc[4 * k + 2] += w * f.z;
-                    acc[4 * k + 3] += w * f.w;
+                    for (int b = 0; b < kBatch; ++b) {   // (past the last one: weight 0, nothing loaded)
+                        const int i = left != 0u ? __ffs(left) - 1 : 0;
+                        wk[b] = __shfl_sync(0xffffffffu, w, i);
+                        at[b] = left != 0u ? slot[i0 + i] : -1;
+                        left &= left - 1u;
+                    }
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                        for (int k = 0; k < D / 128; ++k)
+                            f[b][k] = at[b] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                : reinterpret_cast<const float4*>(p.part_o + ((int64_t)at[b] * kGroups * 128 + row) * D)[32 * k + lane];
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                        for (int k = 0; k < D / 128; ++k) {
+                            acc[4 * k] += wk[b] * f[b][k].x;
+                            acc[4 * k + 1] += wk[b] * f[b][k].y;
+                            acc[4 * k + 2] += wk[b] * f[b][k].z;
+                            acc[4 * k + 3] += wk[b] * f[b][k].w;
+                        }
                 }
             }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
         const float inv = m == -INFINITY ? 0.f : 1.f / sum;
         const int64_t out_row = (cut.q_tok + tok) * p.n_head + cut.g * G + (in - tok_in * G);
