@@ -138,15 +138,12 @@ class KvattnError(RuntimeError):
         super().__init__(f"{where}: {kvattn_status_string(status)} ({status})")
 
 
-def _find_raw_stream():
-    try:
-        import torch
-        return torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getDevice") else None
-    except (ImportError, AttributeError):
-        return None
-
-
-_current_raw_stream = _find_raw_stream()
+try:  # (looked up once: an import statement and a Stream object cost 0.3 and 4 us in every call)
+    import torch as _torch
+    _F16, _I32 = _torch.float16, _torch.int32
+    _current_raw_stream, _current_device = _torch._C._cuda_getCurrentRawStream, _torch._C._cuda_getDevice
+except (ImportError, AttributeError):
+    _current_raw_stream = None
 
 
 def _ptr(x):
@@ -162,9 +159,9 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(_current_device())
         import torch
-        if _current_raw_stream is not None:  # the same handle without a Stream object (about 4 us)
-            return _current_raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -523,27 +520,24 @@ def build_cell_plan(encoded_per_seq, capacity_cells, plan_stride=None):
 def _rows(x, name):
     """(tokens, heads, head_dim, token stride) of half rows [T][heads][D]; the heads of a token must
     be contiguous, the tokens may be strided (a slice of a fused projection)."""
-    import torch
-    shape, stride = x.shape, x.stride()
-    if len(shape) != 3 or x.dtype is not torch.float16:
+    if x.dtype is not _F16 or x.dim() != 3:
         raise ValueError(f"{name}: half rows [tokens][heads][head_dim] are wanted")
-    t, h, d = shape
-    if (stride[2] != 1 or (h > 1 and stride[1] != d)) and x.numel():
+    t, h, d = x.shape
+    st, sh, sd = x.stride()
+    if (sd != 1 or (h > 1 and sh != d)) and x.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t, h, d, (stride[0] if t > 1 else h * d)
+    return t, h, d, (st if t > 1 else h * d)
 
 
 def _ints(x, name, n=None):
-    import torch
-    if x.dtype is not torch.int32 or not x.is_contiguous() or (n is not None and x.numel() != n):
+    if x.dtype is not _I32 or not x.is_contiguous() or (n is not None and x.numel() != n):
         raise ValueError(f"{name}: contiguous int32" + ("" if n is None else f" of {n} values") + " is wanted")
     return x.data_ptr()
 
 
 def _here(x, name):
     """Refuses a host tensor, or one of another device than the current one, whose stream is used."""
-    import torch
-    if not x.is_cuda or x.get_device() != torch._C._cuda_getDevice():
+    if not x.is_cuda or x.get_device() != _current_device():
         raise ValueError(f"{name}: a tensor of the current CUDA device is wanted")
 
 
@@ -553,34 +547,35 @@ def _raw(x):
 
 def _new_out(out, name, shape, like, dtype=None):
     """A contiguous result tensor: the caller's, checked, or a new one."""
-    import torch
-    dtype = torch.float16 if dtype is None else dtype
+    dtype = _F16 if dtype is None else dtype
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _torch.empty(shape, dtype=dtype, device=like.device)
     if out.shape != shape or out.dtype is not dtype or not out.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} of shape {tuple(shape)} is wanted")
     return out
 
 
+_QUANTISED = {(8, 8): KVATTN_KV_Q8_0, (8, 4): KVATTN_KV_Q8_0_Q4_0, (4, 4): KVATTN_KV_Q4_0}  # by bits of K and V
+
+
 def _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim):
     """(kv_type, KV heads, cells) from the planes, the type by the row widths as in decode; checks
     the planes' shapes, types and layout."""
-    import torch
     ks, vs = k_cache.shape, v_cache.shape
     if k_scales is None and v_scales is None:
         kv_type = KVATTN_KV_F16
-        good = ks == vs and ks[-1] == head_dim and k_cache.dtype is v_cache.dtype is torch.float16
+        good = ks == vs and ks[-1] == head_dim and k_cache.dtype is v_cache.dtype is _F16
     elif k_scales is None or v_scales is None:
         raise ValueError("k_scales and v_scales go together")
     else:
         kb = 8 if ks[-1] == head_dim else 4
         vb = 8 if vs[-1] == head_dim else 4
-        kv_type = {(8, 8): KVATTN_KV_Q8_0, (8, 4): KVATTN_KV_Q8_0_Q4_0, (4, 4): KVATTN_KV_Q4_0}.get((kb, vb))
+        kv_type = _QUANTISED.get((kb, vb))
         want = ks[:-1] + (head_dim // 32,)
         good = (kv_type is not None and ks[:-1] == vs[:-1] and ks[-1] * 8 == head_dim * kb and vs[-1] * 8 == head_dim * vb
-                and k_cache.dtype is (torch.int8 if kb == 8 else torch.uint8)
-                and v_cache.dtype is (torch.int8 if vb == 8 else torch.uint8)
-                and k_scales.dtype is v_scales.dtype is torch.float16 and k_scales.shape == want and v_scales.shape == want
+                and k_cache.dtype is (_torch.int8 if kb == 8 else _torch.uint8)
+                and v_cache.dtype is (_torch.int8 if vb == 8 else _torch.uint8)
+                and k_scales.dtype is v_scales.dtype is _F16 and k_scales.shape == want and v_scales.shape == want
                 and k_scales.is_contiguous() and v_scales.is_contiguous())
     if len(ks) < 3 or not good or not k_cache.is_contiguous() or not v_cache.is_contiguous():
         raise ValueError("the cache planes are contiguous [cells][kv heads][row] of one type's rows, codes int8 or packed "
@@ -608,21 +603,20 @@ def rope_table(n_rot, *, base=10000.0, scaling="none", factor=1.0, original=0, d
 def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, stream=None):
     """q: half [T][H][D], k: half [T][Hk][D] (either may be None), positions int32 [T].  Rotated rows
     go to new tensors, or to ``q_out`` / ``k_out`` (which may be q and k themselves).  Returns (q, k)."""
-    import torch
     code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
     some = q if q is not None else k
     T, D = some.shape[0], some.shape[-1]
     qa = ka = (None, 0, 0, None, 0)
     if q is not None:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+            q_out = _torch.empty(q.shape, dtype=_F16, device=q.device)
         t, h, d, st = _rows(q, "q")
         if t != T or d != D or q_out.shape != q.shape:
             raise ValueError("q: shapes do not agree")
         qa = (q.data_ptr(), st, h, q_out.data_ptr(), _rows(q_out, "q_out")[3])
     if k is not None:
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.float16, device=k.device)
+            k_out = _torch.empty(k.shape, dtype=_F16, device=k.device)
         t, h, d, st = _rows(k, "k")
         if t != T or d != D or k_out.shape != k.shape:
             raise ValueError("k: shapes do not agree")
@@ -654,13 +648,12 @@ def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scale
                stream=None):
     """Cells ``slots`` (int32 [T], e.g. a row of a cell plan; -1 gives zeros; None: every cell) as
     half [T][Hk][head_dim] rows.  Returns (k, v)."""
-    import torch
     kv_type, Hk, n_cells = _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim)
     T, at = (n_cells, None) if slots is None else (slots.numel(), _ints(slots, "slots"))
     if k_out is None:
-        k_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
+        k_out = _torch.empty((T, Hk, head_dim), dtype=_F16, device=k_cache.device)
     if v_out is None:
-        v_out = torch.empty((T, Hk, head_dim), dtype=torch.float16, device=k_cache.device)
+        v_out = _torch.empty((T, Hk, head_dim), dtype=_F16, device=k_cache.device)
     _here(k_cache, "k_cache")
     kt, kh, kd, ks = _rows(k_out, "k_out")
     vt, vh, vd, vs = _rows(v_out, "v_out")
@@ -681,7 +674,6 @@ def prefill_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, device="cuda"):
 def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream=None):
     """Causal attention of packed prompts: q half [T][H][D], k and v half [T][Hk][D], offsets int32
     [S + 1].  Returns (out half [T][H][D], lse float [T][H])."""
-    import torch
     T, H, D, qs = _rows(q, "q")
     kt, Hk, kd, ks = _rows(k, "k")
     vt, vh, vd, vs = _rows(v, "v")
@@ -690,7 +682,7 @@ def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream
     off, S = _ints(offsets, "offsets"), offsets.numel() - 1
     _here(q, "q")
     out = _new_out(out, "out", (T, H, D), q)
-    lse = _new_out(lse, "lse", (T, H), q, torch.float32)
+    lse = _new_out(lse, "lse", (T, H), q, _torch.float32)
     if ws is None:
         ws = prefill_workspace(T, S, H, Hk, D, q.device)
     _check(lib.kvattn_prefill(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, off, S, T, H, Hk, D,
@@ -712,7 +704,6 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     a ``cell_plan`` (int32 [S][stride]), a per-sequence [S][N][Hk][D] cache, or one [cells][Hk][D]
     whose ``n_cells`` are each sequence's.  Returns (out half [T][H][D], lse: the given tensor or
     None)."""
-    import torch
     T, H, D, qs = _rows(q, "q")
     off, S = _ints(offsets, "offsets"), offsets.numel() - 1
     lens = _ints(seq_lens, "seq_lens", S)
@@ -732,7 +723,7 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     _here(k_cache, "k_cache")
     out = _new_out(out, "out", (T, H, D), q)
     if lse is not None:
-        _new_out(lse, "lse", (T, H), q, torch.float32)
+        _new_out(lse, "lse", (T, H), q, _torch.float32)
     if ws is None:
         ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, q.device)
     _check(lib.kvattn_prefill_chunk(q.data_ptr(), qs, off, T, k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales),
