@@ -604,26 +604,31 @@ def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, strea
     """q: half [T][H][D], k: half [T][Hk][D] (either may be None), positions int32 [T].  Rotated rows
     go to new tensors, or to ``q_out`` / ``k_out`` (which may be q and k themselves).  Returns (q, k)."""
     code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
-    some = q if q is not None else k
-    T, D = some.shape[0], some.shape[-1]
+    if q is None and k is None:
+        raise ValueError("q or k is wanted")
+    T = D = None
     qa = ka = (None, 0, 0, None, 0)
     if q is not None:
         if q_out is None:
             q_out = _torch.empty(q.shape, dtype=_F16, device=q.device)
-        t, h, d, st = _rows(q, "q")
-        if t != T or d != D or q_out.shape != q.shape:
-            raise ValueError("q: shapes do not agree")
-        qa = (q.data_ptr(), st, h, q_out.data_ptr(), _rows(q_out, "q_out")[3])
+        T, h, D, st = _rows(q, "q")
+        to, ho, do, so = _rows(q_out, "q_out")
+        if to != T or ho != h or do != D:
+            raise ValueError("q_out: q's shape is wanted")
+        qa = (q.data_ptr(), st, h, q_out.data_ptr(), so)
     if k is not None:
         if k_out is None:
             k_out = _torch.empty(k.shape, dtype=_F16, device=k.device)
         t, h, d, st = _rows(k, "k")
-        if t != T or d != D or k_out.shape != k.shape:
-            raise ValueError("k: shapes do not agree")
-        ka = (k.data_ptr(), st, h, k_out.data_ptr(), _rows(k_out, "k_out")[3])
-    _here(some, "q" if q is not None else "k")
-    _check(lib.kvattn_rope(qa[0], qa[1], qa[2], ka[0], ka[1], ka[2], _ints(positions, "positions", T), table.turns.data_ptr(),
-                           table.gain, table.n_rot, code, T, D, qa[3], qa[4], ka[3], ka[4], _stream(stream)), "kvattn_rope")
+        to, ho, do, so = _rows(k_out, "k_out")
+        if to != t or ho != h or do != d or (q is not None and (t != T or d != D)):
+            raise ValueError("k, k_out: shapes do not agree")
+        T, D = t, d
+        ka = (k.data_ptr(), st, h, k_out.data_ptr(), so)
+    at = _ints(positions, "positions", T)
+    _here(k if q is None else q, "k" if q is None else "q")
+    _check(lib.kvattn_rope(qa[0], qa[1], qa[2], ka[0], ka[1], ka[2], at, table.turns.data_ptr(), table.gain, table.n_rot, code,
+                           T, D, qa[3], qa[4], ka[3], ka[4], _stream(stream)), "kvattn_rope")
     return q_out if q is not None else None, k_out if k is not None else None
 
 

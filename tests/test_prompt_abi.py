@@ -148,6 +148,11 @@ def test_wrapper_checks(kvattn):
         kvattn.cache_read(torch.zeros(9, 2, 128, dtype=torch.int8), torch.zeros(9, 2, 128, dtype=torch.int8), off, head_dim=128)
     with pytest.raises(ValueError):
         kvattn.rope(h(4, 4, 128), h(5, 2, 128), torch.zeros(4, dtype=torch.int32), kvattn.RopeTable(off, 1.0, 128))
+    for kw in (dict(q_out=h(4, 2, 128)), dict(k_out=h(3, 2, 128)), dict(q_out=h(4, 4, 128).float())):
+        with pytest.raises(ValueError):
+            kvattn.rope(h(4, 4, 128), h(4, 2, 128), torch.zeros(4, dtype=torch.int32), kvattn.RopeTable(off, 1.0, 128), **kw)
+    with pytest.raises(ValueError):
+        kvattn.rope(None, None, torch.zeros(4, dtype=torch.int32), kvattn.RopeTable(off, 1.0, 128))
 
 
 def test_wrappers_refuse_host_tensors(kvattn):
