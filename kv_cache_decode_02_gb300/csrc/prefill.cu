@@ -992,13 +992,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // ---- quantised: turns the raw slots that warp 14 brings ----
             for (;; ++n) {
                 const uint32_t r = n % kRawStages;
-                if (!(ok = wait_all(&h->raw_full[r], (n / kRawStages) & 1u))) break;
+                // (both waits with one vote: a word that was read after a lost one is not used)
+                bool got = wait_bar(smem_addr(&h->raw_full[r]), (n / kRawStages) & 1u, abort_flag, p.wait_limit_ns);
                 const uint32_t word = h->raw_word[r];
-                if (word == kNoMore) break;
+                if (!(word & 8u) && filled >= kSlots)
+                    got = wait_bar(smem_addr(&h->empty[filled % kSlots]), (filled / kSlots - 1) & 1u, abort_flag,
+                                   p.wait_limit_ns) && got;
+                if (!(ok = __all_sync(0xffffffffu, got)) || word == kNoMore) break;
                 const bool v_side = word & 1u, cut = (word >> 1) & 1u;
                 const uint32_t unit = (word >> 8) & 0xffffu;
                 if (!(word & 8u)) {
-                    if (!(ok = wait_slot_empty())) break;
                     stall_hook(&h->full[filled % kSlots]);
                     const int bits = v_side ? VBITS : KBITS;
                     const unsigned char* stage = raws + r * Memory<KBITS>::kRawBytes;
