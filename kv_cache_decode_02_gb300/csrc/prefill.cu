@@ -1241,6 +1241,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // This warp's own instructions, one after the other, set the pace of everything: a wait
             // is a test by every lane, without a vote (a lane whose wait gave up is noticed by the
             // vote at the end of a tile; until then it goes on, over data that nobody will use).
+            // The lanes meet once per slot, before the leader gives its products out: without that
+            // one could still test the barrier of a slot (or read its slot_mend) when the products are
+            // done and the loader fills it again, and would wait for a phase that is over.  A barrier
+            // of p, or of the queries, moves on only after products that come after the next meeting.
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = wait_bar(smem_addr(bar), parity, abort_flag, p.wait_limit_ns) && ok;
@@ -1251,6 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     wait(&h->mended[st], (mends >> st) & 1u);
                     mends ^= 1u << st;
                 }
+                __syncwarp();
             };
             auto next_slot = [&]() {
                 ++st;
