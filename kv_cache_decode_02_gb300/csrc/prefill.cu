@@ -527,9 +527,10 @@ __device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence&
         s.n[t] = max(tiles - first, 0);
         n_max = max(n_max, s.n[t]);
     }
-    // (one token: all its rows see the same cells)
+    // (the sequence's last token alone: its rows see all that is there.  With more than 64 heads per
+    // KV head at 256 every token is alone, and the others' last tile holds cells that they do not see)
     const int64_t cut = (s.lim0 > 0 ? s.lim0 : 0) / kPrefillTile - first;
-    s.first_cut = (s.n_tok == 1 || cut > n_max) ? n_max : (cut < 0 ? 0 : (int)cut);
+    s.first_cut = ((s.n_tok == 1 && s.lim0 >= s.len) || cut > n_max) ? n_max : (cut < 0 ? 0 : (int)cut);
     s.whole = min(s.first_cut, (int)clamp64(x.len / kPrefillTile - first, 0, n_max));
     if (s.n[1] > 0) s.whole = min(s.whole, min(s.n[0], s.n[1]));
     s.turn = from < s.whole ? from : 0;
