@@ -5,7 +5,10 @@ tensors are passed by ``data_ptr()``, streams by their ``cuda_stream`` handle, a
 non-OK status raises :class:`KvattnError`.  The convenience wrappers at the end
 (``decode``, ``merge``, ``WindowTail``; ``rope``, ``cache_write``, ``cache_read``, ``prefill``,
 ``prefill_chunk``) only allocate outputs and workspaces with torch and infer sizes from tensor
-shapes; all arithmetic runs in the library's kernels.
+shapes; all arithmetic runs in the library's kernels.  A wrapper's ``stream`` (default: torch's
+current one) is where it launches, and where the tensors that it makes belong, as under
+``torch.cuda.stream(stream)``: work on another stream waits for it before it uses them, and the
+call is ordered behind whatever makes its inputs by the program.
 
 Importing this module loads ``_lib/libkvattn.so`` and raises if it has not been built
 (``python -m kv_cache_decode_02_gb300._build``): there is no fallback path.
@@ -517,6 +520,25 @@ def build_cell_plan(encoded_per_seq, capacity_cells, plan_stride=None):
 # The wrappers below are on the path of single decode steps, where the host's time counts: each
 # reads a tensor's shape and strides once, and calls the library itself with addresses.
 
+def _other_stream(stream):
+    """Whether ``stream`` is another one than torch's current stream."""
+    return stream is not None and _stream(stream) != _stream(None)
+
+
+def _made_on(stream):
+    """A context in which torch allocates, and zeroes, in ``stream``'s order.  What a wrapper makes for
+    a call on another stream than the current one has to be that stream's: a block of the current
+    stream may still be in use there, would be zeroed there at any time, and goes to the next
+    allocation there while the call still runs."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        # (1 is the legacy default stream's other handle)
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    if stream.device_index != torch.cuda.current_device():
+        raise ValueError("stream: a stream of the current device is wanted")
+    return torch.cuda.stream(stream)
+
 def _rows(x, name):
     """(tokens, heads, head_dim, token stride) of half rows [T][heads][D]; the heads of a token must
     be contiguous, the tokens may be strided (a slice of a fused projection)."""
@@ -606,6 +628,9 @@ def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, strea
     code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
     if q is None and k is None:
         raise ValueError("q or k is wanted")
+    if ((q is not None and q_out is None) or (k is not None and k_out is None)) and _other_stream(stream):
+        with _made_on(stream):
+            return rope(q, k, positions, table, layout=layout, q_out=q_out, k_out=k_out)
     T = D = None
     qa = ka = (None, 0, 0, None, 0)
     if q is not None:
@@ -653,6 +678,10 @@ def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scale
                stream=None):
     """Cells ``slots`` (int32 [T], e.g. a row of a cell plan; -1 gives zeros; None: every cell) as
     half [T][Hk][head_dim] rows.  Returns (k, v)."""
+    if (k_out is None or v_out is None) and _other_stream(stream):
+        with _made_on(stream):
+            return cache_read(k_cache, v_cache, slots, head_dim=head_dim, k_scales=k_scales, v_scales=v_scales, k_out=k_out,
+                              v_out=v_out, status=status)
     kv_type, Hk, n_cells = _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim)
     T, at = (n_cells, None) if slots is None else (slots.numel(), _ints(slots, "slots"))
     if k_out is None:
@@ -679,6 +708,9 @@ def prefill_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, device="cuda"):
 def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream=None):
     """Causal attention of packed prompts: q half [T][H][D], k and v half [T][Hk][D], offsets int32
     [S + 1].  Returns (out half [T][H][D], lse float [T][H])."""
+    if (out is None or lse is None or ws is None) and _other_stream(stream):
+        with _made_on(stream):
+            return prefill(q, k, v, offsets, scale=scale, out=out, lse=lse, ws=ws)
     T, H, D, qs = _rows(q, "q")
     kt, Hk, kd, ks = _rows(k, "k")
     vt, vh, vd, vs = _rows(v, "v")
@@ -709,6 +741,10 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     a ``cell_plan`` (int32 [S][stride]), a per-sequence [S][N][Hk][D] cache, or one [cells][Hk][D]
     whose ``n_cells`` are each sequence's.  Returns (out half [T][H][D], lse: the given tensor or
     None)."""
+    if (out is None or ws is None) and _other_stream(stream):
+        with _made_on(stream):
+            return prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, max_len=max_len, n_cells=n_cells, cell_plan=cell_plan,
+                                 k_scales=k_scales, v_scales=v_scales, scale=scale, out=out, lse=lse, ws=ws)
     T, H, D, qs = _rows(q, "q")
     off, S = _ints(offsets, "offsets"), offsets.numel() - 1
     lens = _ints(seq_lens, "seq_lens", S)
