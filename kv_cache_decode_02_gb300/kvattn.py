@@ -409,6 +409,26 @@ def kvattn_prefill_chunk(q, q_stride, offsets, n_tok, k_cache, v_cache, k_scales
 
 # ----------------------------- torch conveniences -----------------------------
 
+def _other_stream(stream):
+    """Whether ``stream`` is another one than torch's current stream."""
+    return stream is not None and _stream(stream) != _stream(None)
+
+
+def _made_on(stream):
+    """A context in which torch allocates, and zeroes, in ``stream``'s order.  What a wrapper makes for
+    a call on another stream than the current one has to be that stream's: a block of the current
+    stream may still be in use there, would be zeroed there at any time, and goes to the next
+    allocation there while the call still runs."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        # (1 is the legacy default stream's other handle)
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    if stream.device_index != torch.cuda.current_device():
+        raise ValueError("stream: a stream of the current device is wanted")
+    return torch.cuda.stream(stream)
+
+
 def decode_workspace(n_seq, n_head, head_dim, max_len, split, device="cuda"):
     import torch
     nbytes = kvattn_decode_workspace_bytes(n_seq, n_head, head_dim, max_len, split)
@@ -425,6 +445,10 @@ def decode(q, k_cache, v_cache, seq_lens, *, split, max_len=None, cell_plan=None
     Returns (out, lse).
     """
     import torch
+    if (out is None or lse is None or ws is None) and _other_stream(stream):
+        with _made_on(stream):
+            return decode(q, k_cache, v_cache, seq_lens, split=split, max_len=max_len, cell_plan=cell_plan, k_scales=k_scales,
+                          v_scales=v_scales, scale=scale, n_cells=n_cells, out=out, lse=lse, ws=ws, kv_type=kv_type)
     S, H, D = q.shape
     if kv_type is None:
         if k_scales is None:
@@ -461,6 +485,10 @@ def decode_multi(q, k_cache, v_cache, seq_lens, *, split, max_len=None, cell_pla
     (the type inferred from the row widths as in decode), as the C ABI describes.  Returns
     (out, lse)."""
     import torch
+    if (out is None or lse is None or ws is None) and _other_stream(stream):
+        with _made_on(stream):
+            return decode_multi(q, k_cache, v_cache, seq_lens, split=split, max_len=max_len, cell_plan=cell_plan, scale=scale,
+                                n_cells=n_cells, out=out, lse=lse, ws=ws, k_scales=k_scales, v_scales=v_scales)
     S, n_q, H, D = q.shape
     Hk = k_cache.shape[-2]
     if n_cells is None:
@@ -491,6 +519,9 @@ def decode_multi(q, k_cache, v_cache, seq_lens, *, split, max_len=None, cell_pla
 def merge(partials, lses, out=None, lse=None, stream=None):
     """partials float [P][R][D], lses float [P][R] (cuda) -> (out [R][D], lse [R])."""
     import torch
+    if (out is None or lse is None) and _other_stream(stream):
+        with _made_on(stream):
+            return merge(partials, lses, out=out, lse=lse)
     P, R, D = partials.shape
     if out is None:
         out = torch.empty((R, D), dtype=torch.float32, device=partials.device)
@@ -519,25 +550,6 @@ def build_cell_plan(encoded_per_seq, capacity_cells, plan_stride=None):
 
 # The wrappers below are on the path of single decode steps, where the host's time counts: each
 # reads a tensor's shape and strides once, and calls the library itself with addresses.
-
-def _other_stream(stream):
-    """Whether ``stream`` is another one than torch's current stream."""
-    return stream is not None and _stream(stream) != _stream(None)
-
-
-def _made_on(stream):
-    """A context in which torch allocates, and zeroes, in ``stream``'s order.  What a wrapper makes for
-    a call on another stream than the current one has to be that stream's: a block of the current
-    stream may still be in use there, would be zeroed there at any time, and goes to the next
-    allocation there while the call still runs."""
-    import torch
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)
-        # (1 is the legacy default stream's other handle)
-        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
-    if stream.device_index != torch.cuda.current_device():
-        raise ValueError("stream: a stream of the current device is wanted")
-    return torch.cuda.stream(stream)
 
 def _rows(x, name):
     """(tokens, heads, head_dim, token stride) of half rows [T][heads][D]; the heads of a token must
@@ -810,6 +822,11 @@ class WindowTail:
     def __call__(self, q, k_win, v_win, k_tail_host, v_tail_host, *, split, tile_cells, tail_split,
                  scale=None, out=None, lse=None, ws=None, compute_stream=None, copy_stream=None):
         import torch
+        if (out is None or lse is None or ws is None) and _other_stream(compute_stream):
+            copy_stream = _stream(copy_stream)   # (None: the current one here)
+            with _made_on(compute_stream):
+                return self(q, k_win, v_win, k_tail_host, v_tail_host, split=split, tile_cells=tile_cells,
+                            tail_split=tail_split, scale=scale, out=out, lse=lse, ws=ws, copy_stream=copy_stream)
         H, D = q.shape[-2], q.shape[-1]
         Hk = k_win.shape[-2] if k_win is not None else k_tail_host.shape[-2]
         n_win = k_win.shape[0] if k_win is not None else 0
