@@ -570,9 +570,32 @@ def _ints(x, name, n=None):
 
 
 def _here(x, name):
-    """Refuses a host tensor, or one of another device than the current one, whose stream is used."""
-    if not x.is_cuda or x.get_device() != _current_device():
+    """The device of x; refuses a host tensor, or one of another device than the current one, whose
+    stream is used."""
+    d = x.get_device()
+    if d < 0 or d != _current_device():
         raise ValueError(f"{name}: a tensor of the current CUDA device is wanted")
+    return d
+
+
+def _elsewhere(dev, **tensors):
+    """Names the tensor that is not on device ``dev`` (or the workspace's or status word's other fault)."""
+    for name, x in tensors.items():
+        if x is not None and x.get_device() != dev:
+            raise ValueError(f"{name}: a tensor of the current CUDA device is wanted")
+    raise ValueError("ws is contiguous; status holds a 32-bit word")
+
+
+def _off(x, dev):
+    return x is not None and x.get_device() != dev
+
+
+def _bad_word(status, dev):
+    return status is not None and (status.get_device() != dev or status.numel() * status.element_size() < 4)
+
+
+def _bad_ws(ws, dev):
+    return ws.get_device() != dev or not ws.is_contiguous()
 
 
 def _raw(x):
@@ -662,9 +685,13 @@ def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, strea
             raise ValueError("k, k_out: shapes do not agree")
         T, D = t, d
         ka = (k.data_ptr(), st, h, k_out.data_ptr(), so)
-    at = _ints(positions, "positions", T)
-    _here(k if q is None else q, "k" if q is None else "q")
-    _check(lib.kvattn_rope(qa[0], qa[1], qa[2], ka[0], ka[1], ka[2], at, table.turns.data_ptr(), table.gain, table.n_rot, code,
+    at, turns = _ints(positions, "positions", T), table.turns
+    d = _here(k if q is None else q, "k" if q is None else "q")
+    if positions.get_device() != d or turns.get_device() != d or _off(k, d) or _off(q_out, d) or _off(k_out, d):
+        _elsewhere(d, k=k, positions=positions, table=turns, q_out=q_out, k_out=k_out)
+    if turns.numel() * 2 < table.n_rot or turns.element_size() != 8 or not turns.is_contiguous():
+        raise ValueError("table: n_rot / 2 contiguous 64-bit angles are wanted")
+    _check(lib.kvattn_rope(qa[0], qa[1], qa[2], ka[0], ka[1], ka[2], at, turns.data_ptr(), table.gain, table.n_rot, code,
                            T, D, qa[3], qa[4], ka[3], ka[4], _stream(stream)), "kvattn_rope")
     return q_out if q is not None else None, k_out if k is not None else None
 
@@ -679,8 +706,10 @@ def cache_write(k, v, slots, k_cache, v_cache, *, k_scales=None, v_scales=None, 
     if (vt, vh, vd) != (T, Hk, D) or heads != Hk:
         raise ValueError("k, v and the cache do not agree")
     at = None if slots is None else _ints(slots, "slots", T)
-    _here(k, "k")
-    _here(k_cache, "k_cache")
+    d = _here(k, "k")
+    if (v.get_device() != d or k_cache.get_device() != d or v_cache.get_device() != d or _off(slots, d) or _off(k_scales, d)
+            or _off(v_scales, d) or _bad_word(status, d)):
+        _elsewhere(d, v=v, k_cache=k_cache, v_cache=v_cache, slots=slots, k_scales=k_scales, v_scales=v_scales, status=status)
     _check(lib.kvattn_cache_write(k.data_ptr(), ks, v.data_ptr(), vs, at, T, Hk, D, kv_type, k_cache.data_ptr(),
                                   v_cache.data_ptr(), _raw(k_scales), _raw(v_scales), n_cells, _raw(status), _stream(stream)),
            "kvattn_cache_write")
@@ -700,7 +729,11 @@ def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scale
         k_out = _torch.empty((T, Hk, head_dim), dtype=_F16, device=k_cache.device)
     if v_out is None:
         v_out = _torch.empty((T, Hk, head_dim), dtype=_F16, device=k_cache.device)
-    _here(k_cache, "k_cache")
+    d = _here(k_cache, "k_cache")
+    if (v_cache.get_device() != d or k_out.get_device() != d or v_out.get_device() != d or _off(slots, d) or _off(k_scales, d)
+            or _off(v_scales, d) or _bad_word(status, d)):
+        _elsewhere(d, v_cache=v_cache, slots=slots, k_scales=k_scales, v_scales=v_scales, k_out=k_out, v_out=v_out,
+                   status=status)
     kt, kh, kd, ks = _rows(k_out, "k_out")
     vt, vh, vd, vs = _rows(v_out, "v_out")
     if (kt, kh, kd) != (T, Hk, head_dim) or (vt, vh, vd) != (T, Hk, head_dim):
@@ -729,11 +762,14 @@ def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream
     if (kt, kd) != (T, D) or (vt, vh, vd) != (T, Hk, D):
         raise ValueError("q, k and v do not agree")
     off, S = _ints(offsets, "offsets"), offsets.numel() - 1
-    _here(q, "q")
+    d = _here(q, "q")
     out = _new_out(out, "out", (T, H, D), q)
     lse = _new_out(lse, "lse", (T, H), q, _torch.float32)
     if ws is None:
         ws = prefill_workspace(T, S, H, Hk, D, q.device)
+    if (k.get_device() != d or v.get_device() != d or offsets.get_device() != d or out.get_device() != d
+            or lse.get_device() != d or _bad_ws(ws, d)):
+        _elsewhere(d, k=k, v=v, offsets=offsets, out=out, lse=lse, ws=ws)
     _check(lib.kvattn_prefill(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, off, S, T, H, Hk, D,
                               1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                               ws.numel(), _stream(stream)), "kvattn_prefill")
@@ -772,13 +808,17 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
         raise ValueError("the cache has fewer cells than n_cells says")
     if max_len is None:
         max_len = stride if plan is not None else n_cells
-    _here(q, "q")
-    _here(k_cache, "k_cache")
+    d = _here(q, "q")
     out = _new_out(out, "out", (T, H, D), q)
     if lse is not None:
         _new_out(lse, "lse", (T, H), q, _torch.float32)
     if ws is None:
         ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, q.device)
+    if (k_cache.get_device() != d or v_cache.get_device() != d or offsets.get_device() != d or seq_lens.get_device() != d
+            or out.get_device() != d or _off(cell_plan, d) or _off(k_scales, d) or _off(v_scales, d) or _off(lse, d)
+            or _bad_ws(ws, d)):
+        _elsewhere(d, k_cache=k_cache, v_cache=v_cache, offsets=offsets, seq_lens=seq_lens, cell_plan=cell_plan,
+                   k_scales=k_scales, v_scales=v_scales, out=out, lse=lse, ws=ws)
     _check(lib.kvattn_prefill_chunk(q.data_ptr(), qs, off, T, k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales),
                                     _raw(v_scales), kv_type, n_cells, plan, stride, lens, S, max_len, H, Hk, D,
                                     1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), _raw(lse), ws.data_ptr(),
