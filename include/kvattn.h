@@ -522,8 +522,10 @@ int kvattn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_str
                    const int32_t* offsets, int n_seq, int64_t n_tok, int n_head, int n_head_kv, int head_dim, float scale,
                    void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace kvattn_prefill_chunk needs on the current device (status word, and partials
- * of at most two work units per SM: about 40 MB whatever the shapes); 0 on invalid arguments. */
+/* Bytes of workspace that kvattn_prefill_chunk needs on the current device for this call and for
+ * every one with the same heads and no more tokens, sequences and max_len: one made for the largest
+ * serves them all.  The status word, and partials of at most two work units per SM (about 40 MB at
+ * most); 0 on invalid arguments. */
 size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim,
                                             int64_t max_len);
 
@@ -539,8 +541,8 @@ size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head
  *            (2^-11 of each value).
  * Few rows over long caches are cut over the cells too, into equal shares for the device's SMs
  * that follow from the lengths alone (the result does not depend on timing), and merged.
- *  ws        kvattn_prefill_chunk_workspace_bytes(...) bytes, 256-byte aligned, zeroed once after
- *            allocation; work that shares one is ordered by the caller.
+ *  ws        at least kvattn_prefill_chunk_workspace_bytes(...) bytes, 256-byte aligned, zeroed once
+ *            after allocation; work that shares one is ordered by the caller.
  * Errors: INVALID_ARG, UNSUPPORTED (also max_len of 2^31 or more, n_seq x n_cells of 2^63), WORKSPACE (before any launch);
  * CUDA.
  */

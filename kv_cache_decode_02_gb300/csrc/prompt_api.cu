@@ -49,14 +49,17 @@ struct Cut {
 
 constexpr int64_t kMinShareTiles = 4;
 
-Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share) {
+// `bound`: of all calls with at most that many units and tiles (one of fewer units may be shared
+// where this one is dealt out whole).
+Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share, bool bound = false) {
     Cut c = {};
     // (KVATTN_PREFILL_CTAS: the CTAs that share the work, for tests; 0: dealt out whole)
     const char* env = std::getenv("KVATTN_PREFILL_CTAS");
     const int sms = device_sms();
+    if (bound) units = std::min(units, 8 * (int64_t)sms - 1);
     c.shares = may_share && tiles > kMinShareTiles && units < 8 * (int64_t)sms;
     // (the kernel numbers the line of all tiles, in eighths, in 31 bits)
-    const bool fits = units < INT32_MAX && (tiles + 18) * 8 < INT32_MAX / std::max<int64_t>(units, 1);
+    const bool fits = bound || (units < INT32_MAX && (tiles + 18) * 8 < INT32_MAX / std::max<int64_t>(units, 1));
     int64_t n = units;
     if (c.shares) n = std::max(units, (units * tiles + kMinShareTiles - 1) / kMinShareTiles);
     c.n_ctas = (int)std::max<int64_t>(std::min<int64_t>(n, sms), 1);
@@ -77,9 +80,9 @@ Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share) {
     return c;
 }
 
-Cut chunk_cut(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim, int64_t max_len) {
+Cut chunk_cut(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim, int64_t max_len, bool bound = false) {
     return cut_of(unit_bound(n_tok, n_seq, n_head_kv, n_head / n_head_kv, head_dim),
-                  (max_len + kPrefillTile - 1) / kPrefillTile, head_dim, true);
+                  (max_len + kPrefillTile - 1) / kPrefillTile, head_dim, true, bound);
 }
 
 // What the two attention entry points have in common.
@@ -278,7 +281,7 @@ int kvattn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_str
 size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim,
                                             int64_t max_len) {
     if (check_heads(n_tok, n_seq, n_head, n_head_kv, head_dim) != KVATTN_OK || max_len < 0 || max_len > INT32_MAX) return 0;
-    return chunk_cut(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len).total;
+    return chunk_cut(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, true).total;
 }
 
 int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets, int64_t n_tok, const void* k_cache,
