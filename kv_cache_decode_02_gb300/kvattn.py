@@ -141,12 +141,21 @@ class KvattnError(RuntimeError):
         super().__init__(f"{where}: {kvattn_status_string(status)} ({status})")
 
 
-try:  # (looked up once: an import statement and a Stream object cost 0.3 and 4 us in every call)
-    import torch as _torch
-    _F16, _I32 = _torch.float16, _torch.int32
-    _current_raw_stream, _current_device = _torch._C._cuda_getCurrentRawStream, _torch._C._cuda_getDevice
-except (ImportError, AttributeError):
-    _current_raw_stream = None
+# What the prompt wrappers use of torch, looked up at the first call (callers of the C binding alone
+# do not wait for torch's import) and once (an import statement and a Stream object cost 0.3 and 4 us
+# in every call).
+_torch = _F16 = _I32 = _current_raw_stream = _current_device = None
+
+
+def _bind_torch():
+    global _torch, _F16, _I32, _current_raw_stream, _current_device
+    import torch
+    if _current_device is None:
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _F16, _I32 = torch.float16, torch.int32
+    _torch = torch
 
 
 def _ptr(x):
@@ -162,10 +171,9 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:
-        if _current_raw_stream is not None:
-            return _current_raw_stream(_current_device())
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _torch is None:
+            _bind_torch()
+        return _current_raw_stream(_current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -660,6 +668,8 @@ def rope_table(n_rot, *, base=10000.0, scaling="none", factor=1.0, original=0, d
 def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, stream=None):
     """q: half [T][H][D], k: half [T][Hk][D] (either may be None), positions int32 [T].  Rotated rows
     go to new tensors, or to ``q_out`` / ``k_out`` (which may be q and k themselves).  Returns (q, k)."""
+    if _torch is None:
+        _bind_torch()
     code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
     if q is None and k is None:
         raise ValueError("q or k is wanted")
@@ -700,6 +710,8 @@ def cache_write(k, v, slots, k_cache, v_cache, *, k_scales=None, v_scales=None, 
     """k, v: half [T][Hk][D] into cells ``slots`` (int32 [T], -1: skipped; None: cells 0 .. T - 1) of a
     cache whose type follows from its planes.  ``status``: an int32 tensor whose first word collects
     the KVATTN_DEVICE_* bits."""
+    if _torch is None:
+        _bind_torch()
     T, Hk, D, ks = _rows(k, "k")
     vt, vh, vd, vs = _rows(v, "v")
     kv_type, heads, n_cells = _cache_type(k_cache, v_cache, k_scales, v_scales, D)
@@ -719,6 +731,8 @@ def cache_read(k_cache, v_cache, slots=None, *, head_dim, k_scales=None, v_scale
                stream=None):
     """Cells ``slots`` (int32 [T], e.g. a row of a cell plan; -1 gives zeros; None: every cell) as
     half [T][Hk][head_dim] rows.  Returns (k, v)."""
+    if _torch is None:
+        _bind_torch()
     if (k_out is None or v_out is None) and _other_stream(stream):
         with _made_on(stream):
             return cache_read(k_cache, v_cache, slots, head_dim=head_dim, k_scales=k_scales, v_scales=v_scales, k_out=k_out,
@@ -753,6 +767,8 @@ def prefill_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, device="cuda"):
 def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream=None):
     """Causal attention of packed prompts: q half [T][H][D], k and v half [T][Hk][D], offsets int32
     [S + 1].  Returns (out half [T][H][D], lse float [T][H])."""
+    if _torch is None:
+        _bind_torch()
     if (out is None or lse is None or ws is None) and _other_stream(stream):
         with _made_on(stream):
             return prefill(q, k, v, offsets, scale=scale, out=out, lse=lse, ws=ws)
@@ -789,6 +805,8 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     a ``cell_plan`` (int32 [S][stride]), a per-sequence [S][N][Hk][D] cache, or one [cells][Hk][D]
     whose ``n_cells`` are each sequence's.  Returns (out half [T][H][D], lse: the given tensor or
     None)."""
+    if _torch is None:
+        _bind_torch()
     if (out is None or ws is None) and _other_stream(stream):
         with _made_on(stream):
             return prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, max_len=max_len, n_cells=n_cells, cell_plan=cell_plan,
