@@ -437,10 +437,16 @@ int kvattn_decode_window_tail_direct(const void* q, const void* k_win, const voi
 
 /*
  * kvattn_rope_table -- host.  The angle per position of each of n_rot / 2 pairs, theta_i =
- * base^(-2i / n_rot), as a 64-bit fixed-point fraction of a turn: turns[i] = 2^64 theta_i / (2 pi).
+ * base^(-2i / n_rot), as a 64-bit fixed-point fraction of a turn: turns[i] = 2^64 theta_i / (2 pi)
+ * (made in doubles: off by up to 2^-54 of a turn per position).
  *  scaling  PLAIN; LINEAR: theta_i / factor; YARN (Peng et al. 2023, "NTK-by-parts"): with r_i =
  *           original_len theta_i / (2 pi) turns over the original context and keep = clamp((r_i - 1)
- *           / 31, 0, 1), theta_i (keep + (1 - keep) / factor), and *gain = 0.1 ln(factor) + 1.
+ *           / 31, 0, 1), theta_i (keep + (1 - keep) / factor), and *gain = 0.1 ln(factor) + 1.  This is
+ *           the paper's ramp, linear in r.  Models trained with a ramp linear in the pair's number
+ *           i between rounded bounds, as many published checkpoints are, or with other bounds or
+ *           another gain, have other frequencies (base 10^6, 128 elements, 32768 x 4: 15 of 64
+ *           differ by more than 5 %, one by 42 %) and need a table of their own: kvattn_rope takes
+ *           any turns and gain.
  *  turns    host uint64 [n_rot / 2];  gain  host float (1 but for YARN), kvattn_rope's gain.
  * Errors: INVALID_ARG (n_rot odd or below 2, base not above 1, factor below 1 where it is used,
  * original_len below 1 with YARN, null outputs).
@@ -452,8 +458,9 @@ int kvattn_rope_table(int n_rot, double base, int scaling, double factor, int64_
  * kvattn_rope -- device.  Rotary positions of q and k in one launch: pair (a, b) number i of a
  * head's first n_rot elements becomes gain (a cos - b sin, a sin + b cos) with the angle
  * positions[t] x theta_i; elements from n_rot on are copied.  The angle is an integer product
- * modulo whole turns, so every int32 position is exact to 2^-32 turns; sums are fp32, rounded to
- * half once.
+ * modulo whole turns, whatever the position; the table's rounding is multiplied by it (2^-54 turns
+ * per position: 2^-34 at 2^20, 2^-23 at 2^31), and cosine and sine take the angle in fp32 (2^-26
+ * turns at most).  Sums are fp32, rounded to half once.
  *  q, k      half rows of n_head / n_head_kv heads (a count of 0: that tensor is not used).
  *  positions device int32 [n_tok], any values.   turns  device uint64 [n_rot / 2].
  *  n_rot     a multiple of 16, at most head_dim (UNSUPPORTED / INVALID_ARG otherwise).
@@ -537,8 +544,11 @@ size_t kvattn_prefill_chunk_workspace_bytes(int64_t n_tok, int n_seq, int n_head
  * the logical positions 0 .. L - n_q + t; a token that sees no cell gets O = 0, LSE = -inf.
  *  q, offsets, out, lse  as kvattn_prefill (n_tok rows of all sequences, packed).
  *  k_cache .. seq_lens, n_seq, max_len, scale  as kvattn_decode; any kv_type, contiguous caches or
- *            a cell plan.  The values of quantised caches enter the matrix products rounded to half
- *            (2^-11 of each value).
+ *            a cell plan.  The values of quantised caches enter the matrix products rounded to half as
+ *            kvattn_cache_read gives them (2^-11 of a value, 2^-25 below 2^-14, kept within
+ *            +-65504), where kvattn_decode and kvattn_decode_multi (up to 128 rows per KV head)
+ *            multiply the exact codes: 4.2e-4 of the result against 2.9e-4 over an f16 cache, of
+ *            which 2.1e-4 is out's own rounding.
  * Few rows over long caches are cut over the cells too, into equal shares for the device's SMs
  * that follow from the lengths alone (the result does not depend on timing), and merged.
  *  ws        at least kvattn_prefill_chunk_workspace_bytes(...) bytes, 256-byte aligned, zeroed once

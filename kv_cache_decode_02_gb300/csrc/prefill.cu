@@ -14,8 +14,9 @@
 // to f16 for the matrix product only, l sums the unrounded p).
 //
 // Work.  The kernel is persistent, one CTA per SM.  Its schedulers cut the work in one of two
-// ways: whole units dealt out longest first, in alternating directions (prompts, where units
-// are many); or (chunks) the concatenation of all units' tiles cut into equal contiguous shares,
+// ways: whole units dealt out in alternating directions, from the last sequence's last block (its
+// longest) to the first's first (prompts, where units are many; with ragged prompts the order of
+// the sequences decides how even that is); or (chunks) the concatenation of all units' tiles cut into equal contiguous shares,
 // one per CTA, wherever the cuts fall.  A unit that is cut leaves partials (O_p, lse_p) in the
 // workspace, two at most per CTA, and the merge kernel joins them.  The shares follow from the
 // lengths alone, so results do not depend on timing.
@@ -53,13 +54,14 @@
 // of that length turn in step, the softmax warps' (per group 550 clocks of exponentials at the
 // special-function rate, the rest scores from and p to tensor memory, maxima, packing, a barrier)
 // and each group's p -> P V -> S -> p; the four products alone take 2123.  A prompt of 8192 tokens
-// (32 / 8 heads) takes 386 us, 1424 TFLOP/s (75 % of cuBLAS bf16); 16 / 8 heads of 256, where one
-// group's tiles follow each other, 420 us.  Two row groups and halves of the columns for two warps
+// (32 / 8 heads) takes 390 us, 1409 TFLOP/s (74 % of cuBLAS bf16) with pauses between the calls and
+// 407 one after the other; 16 / 8 heads of 256, where one group's tiles follow each other, 428 with
+// pauses.  Two row groups and halves of the columns for two warps
 // are there for this: one warp per 32 rows and all columns took 3 % more over an 8-bit cache at
 // 128, 28 % at 256.
-// Chunks: 512 tokens over 16384 f16 cells 118 us (60 %).  Quantised caches: the turning of codes
+// Chunks: 512 tokens over 16384 f16 cells 114 us (62 %).  Quantised caches: the turning of codes
 // into f16, about 1500 clocks a slot, shares the issue slots with the softmax: 100 tokens over
-// 131072 8-bit cells 236 us (48 %).
+// 131072 8-bit cells 240 us (47 %).
 //
 // Every wait is bounded, as in the decode kernels; a wait that gives up sets a flag that the
 // others see, and KVATTN_DEVICE_WAIT_TIMEOUT in the workspace.

@@ -4,9 +4,10 @@
 // Angles: theta_i is kept as a fixed-point fraction of a turn (2^-64 turns, 64 bits), and
 // pos x theta_i is a 64-bit integer product whose overflow drops whole turns, exactly what a
 // periodic function may drop.  The top 32 bits, as a signed number of half turns, feed
-// sincospif: no 64-bit floating-point arithmetic on the device and no range reduction, and a
-// position of 2^31 is as exact (2^-33 turns) as position 1, where a product in fp32 is off by
-// 0.06 rad at position 10^6 already.
+// sincospif: no 64-bit floating-point arithmetic on the device and no range reduction.  The angle
+// is off by the position times the table's rounding (made in doubles: 2^-54 turns), 2^-32 turns
+// for the bits dropped, and 2^-25 of itself for the conversion to fp32 (at most 2^-26 turns): 2e-7
+// rad at position 10^6, where a product in fp32 is off by 0.06 rad.
 //
 // Bound: bytes.  Every element is read and written once, 16 bytes per access; a warp keeps one
 // token's cosines and sines (8 pairs per lane) in registers and walks the heads of q and k, so

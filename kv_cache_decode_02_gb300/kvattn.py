@@ -649,15 +649,17 @@ def _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim):
 
 
 class RopeTable:
-    """Angles per position of a model's rotary pairs (``turns``, device uint64 kept as int64) and
-    the gain on cosine and sine; made by :func:`rope_table`."""
+    """Angles per position of a model's rotary pairs (``turns``, device uint64 kept as int64: 2^64
+    theta / (2 pi)) and the gain on cosine and sine; made by :func:`rope_table`, or by a program from
+    frequencies of its own."""
 
     def __init__(self, turns, gain, n_rot):
         self.turns, self.gain, self.n_rot = turns, gain, n_rot
 
 
 def rope_table(n_rot, *, base=10000.0, scaling="none", factor=1.0, original=0, device="cuda"):
-    """``scaling``: "none", "linear" or "yarn" (``factor`` times the ``original`` context)."""
+    """``scaling``: "none", "linear" or "yarn" (``factor`` times the ``original`` context; the paper's
+    ramp, see kvattn_rope_table: a model trained with another one needs a RopeTable of its own)."""
     import torch
     kind = {"none": KVATTN_ROPE_PLAIN, "linear": KVATTN_ROPE_LINEAR, "yarn": KVATTN_ROPE_YARN}[scaling]
     host = np.zeros(n_rot // 2, dtype=np.uint64)
