@@ -409,8 +409,8 @@ __device__ __forceinline__ int32_t tile_length(const PrefillParams& p, int32_t n
 }
 __device__ __forceinline__ Line line_of(const PrefillParams& p, const Sequence& x) {
     const int32_t lim = max(x.len - x.n_q, 0) + min(x.n_q, p.block_tokens);  // of the first block's last token, or above
-    Line l{8u * (uint32_t)(kUnitCost + (lim + kPrefillTile - 1) / kPrefillTile), (uint32_t)(p.block_tokens + 15) / 16u, x.blocks,
-           0u};
+    const int32_t tiles = lim / kPrefillTile + (lim % kPrefillTile != 0 ? 1 : 0);   // (lim can be 2^31 - 1)
+    Line l{8u * (uint32_t)(kUnitCost + tiles), (uint32_t)(p.block_tokens + 15) / 16u, x.blocks, 0u};
     if (x.blocks != 0u) {
         const uint32_t whole = l.of(x.blocks - 1u);
         l.less = whole - (whole * (uint32_t)tile_length(p, x.n_q - (int32_t)(x.blocks - 1u) * p.block_tokens) >> 3);
