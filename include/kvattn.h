@@ -82,6 +82,7 @@ typedef enum {
 /* Sticky device-side status bits, read with kvattn_workspace_status. */
 #define KVATTN_DEVICE_WAIT_TIMEOUT 1u   /* a bounded pipeline wait gave up; results invalid */
 #define KVATTN_DEVICE_BAD_PLAN_ENTRY 2u /* a plan entry outside [-1, n_cells) was masked */
+#define KVATTN_DEVICE_NO_ROOM 4u        /* kvattn_step_maps had no blocks, rows or entries for a sequence */
 
 /* Human-readable name of a kvattn_status (static storage, never NULL). */
 const char* kvattn_status_string(int status);
@@ -430,6 +431,9 @@ int kvattn_decode_window_tail_direct(const void* q, const void* k_win, const voi
 /* Pair layouts of the rotated part of a head: (i, i + n_rot / 2), or (2i, 2i + 1). */
 #define KVATTN_ROPE_HALF 0
 #define KVATTN_ROPE_INTERLEAVED 1
+/* Orders in which kvattn_rope_axes gives pairs to the axes of positions. */
+#define KVATTN_AXES_BLOCKS 0
+#define KVATTN_AXES_CYCLE 1
 /* Context scalings of kvattn_rope_table. */
 #define KVATTN_ROPE_PLAIN 0
 #define KVATTN_ROPE_LINEAR 1
@@ -471,6 +475,75 @@ int kvattn_rope_table(int n_rot, double base, int scaling, double factor, int64_
 int kvattn_rope(const void* q, int64_t q_stride, int n_head, const void* k, int64_t k_stride, int n_head_kv,
                 const int32_t* positions, const uint64_t* turns, float gain, int n_rot, int layout, int64_t n_tok,
                 int head_dim, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * kvattn_rope_axes -- host.  Which axis of positions (time, height, width, ...) turns each pair:
+ * sections[a] pairs for axis a, in consecutive blocks (BLOCKS), or dealt out one at a time in turn,
+ * an axis that has all of its pairs left out (CYCLE).
+ *  axis     host uint8 [n_rot / 2] output, for kvattn_norm_rope.
+ * Errors: INVALID_ARG (n_rot odd or below 2, sections that do not sum to n_rot / 2, unknown order, null
+ * pointers); UNSUPPORTED (more than four axes).
+ */
+int kvattn_rope_axes(int n_rot, const int32_t* sections, int n_axes, int order, uint8_t* axis);
+
+/*
+ * kvattn_norm_rope -- device.  Norms of the heads of q and k and the rotation in one pass: a head x of
+ * a side that has weights w becomes x w / sqrt(mean(x^2) + eps) over its head_dim elements, then its
+ * pairs are turned as in kvattn_rope, pair i by positions[axis[i]][t] x theta_i.  Sums and products are
+ * fp32, rounded to half once.  Without weights for either side it is the rotation by positions of
+ * several axes alone.
+ *  q_weight, k_weight  device half [head_dim], 16-byte aligned; NULL: that side is not normed.
+ *  eps       finite, >= 0 (0: a head of zeros becomes NaN).
+ *  positions device int32 [n_axes] rows of n_tok, pos_stride apart (not read when n_rot is 0).
+ *  n_axes    1 to 4 (UNSUPPORTED beyond).  axis  device uint8 [n_rot / 2], 8-byte aligned; a value of
+ *            n_axes or above turns its pair by position 0.  Not used with one axis.
+ *  Other arguments, in-place calls and errors: as kvattn_rope.
+ */
+int kvattn_norm_rope(const void* q, int64_t q_stride, int n_head, const void* q_weight, const void* k, int64_t k_stride,
+                     int n_head_kv, const void* k_weight, float eps, const int32_t* positions, int64_t pos_stride, int n_axes,
+                     const uint8_t* axis, const uint64_t* turns, float gain, int n_rot, int layout, int64_t n_tok, int head_dim,
+                     void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * kvattn_step_maps -- device.  What the other entry points want of a step, made on the device from how
+ * many cells each sequence holds and how many new tokens it gets: blocks from a free list, offsets,
+ * lengths, positions, slots and cell plan.  A block is block_cells cells of the unified cache, block b
+ * the cells from b x block_cells on; a sequence's cells lie in the blocks of its table's row in order.
+ *
+ * Sequence s needs ceil((lens[s] + n_new[s]) / block_cells) - ceil(lens[s] / block_cells) blocks more.
+ * They are taken from the end of the free list (its first *n_free entries are free) in the order of
+ * the sequences: block number i that is asked for is free_blocks[*n_free - 1 - i].  A sequence is
+ * served when it needs none, or when the list holds what is asked for up to and with it; a sequence
+ * whose table or plan row is too short, or whose tokens have no rows left below n_tok, asks for none and
+ * is not served (so is one behind it that the list would still serve).  One that is not served keeps its
+ * length and table, its rows get slot -1, and KVATTN_DEVICE_NO_ROOM is or-ed into *status.
+ *
+ *  lens, n_new  device int32 [n_seq]: before the step; the step's (values below 0 count as 0, lengths
+ *           above the rows' room as that).
+ *  tables   device int32 [n_seq][table_stride], in place: new blocks are entered behind those held.
+ *  block_cells  a power of two, 4 to 65536 (UNSUPPORTED otherwise).  128 or more lets attention load
+ *           whole tiles.
+ *  free_blocks, n_list, n_free  device int32 [n_list] and int32 [1]; or NULL, 0, NULL: the tables hold
+ *           every block that is needed, and none is taken.
+ *  n_cells  of the cache, below 2^31.  A block outside it (a table's -1 too) gives slots and plan entries
+ *           -1, and KVATTN_DEVICE_BAD_PLAN_ENTRY in *status.
+ *  n_tok    rows of the step's packed tokens, at least the sum of n_new.
+ *  offsets  device int32 [n_seq + 1] output, at most n_tok.   seq_lens  device int32 [n_seq] output: with
+ *           the step's tokens.
+ *  positions (or NULL), slots  device int32 [n_tok] outputs for kvattn_rope and kvattn_cache_write; rows
+ *           behind the last token get position 0 and slot -1.
+ *  n_free_out  device int32 [1] output: what is left (NULL when nothing is taken).
+ *  cell_plan  NULL or device int32 [n_seq][plan_stride] (plan_stride a multiple of four and 16-byte rows
+ *           are written fastest).  whole_plan 0: the new tokens' entries are written, the others stay
+ *           as the step before left them; else whole rows, -1 behind the sequence's end.
+ *  status   NULL or a device uint32.
+ * No output overlaps an input or another output.  n_seq at most 16384.
+ * Errors: INVALID_ARG, UNSUPPORTED (before the launch); CUDA.
+ */
+int kvattn_step_maps(const int32_t* lens, const int32_t* n_new, int n_seq, int32_t* tables, int64_t table_stride, int block_cells,
+                     const int32_t* free_blocks, int64_t n_list, const int32_t* n_free, int64_t n_cells, int64_t n_tok,
+                     int32_t* offsets, int32_t* seq_lens, int32_t* positions, int32_t* slots, int32_t* n_free_out,
+                     int32_t* cell_plan, int64_t plan_stride, int whole_plan, uint32_t* status, void* stream);
 
 /*
  * kvattn_cache_write -- device.  New K and V rows into cells of a cache of any kv_type: token t's
@@ -529,6 +602,15 @@ int kvattn_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_str
                    const int32_t* offsets, int n_seq, int64_t n_tok, int n_head, int n_head_kv, int head_dim, float scale,
                    void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * kvattn_prefill_window -- device.  kvattn_prefill with a sliding window: a token sees its sequence's
+ * last `window` tokens (its own is one of them) and the first `sinks`.
+ *  window >= 1, sinks >= 0 (INVALID_ARG otherwise).  Other arguments and errors: as kvattn_prefill.
+ */
+int kvattn_prefill_window(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const int32_t* offsets, int n_seq, int64_t n_tok, int n_head, int n_head_kv, int head_dim, float scale,
+                          int64_t window, int64_t sinks, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Bytes of workspace that kvattn_prefill_chunk needs on the current device for this call and for
  * every one with the same heads and no more tokens, sequences and max_len: one made for the largest
  * serves them all.  The status word, and partials of at most two work units per SM (about 40 MB at
@@ -561,6 +643,44 @@ int kvattn_prefill_chunk(const void* q, int64_t q_stride, const int32_t* offsets
                          const int32_t* cell_plan, int64_t plan_stride, const int32_t* seq_lens, int n_seq,
                          int64_t max_len, int n_head, int n_head_kv, int head_dim, float scale, void* out, float* lse,
                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * kvattn_prefill_chunk_window -- device.  kvattn_prefill_chunk with a sliding window: a token with limit
+ * lim = L - n_q + 1 + t sees the logical positions c < lim with c < sinks or c >= lim - window (plan
+ * entries or cells, holes masked).  Cells outside are not read, so that the time goes by the window and
+ * not by the length; single tokens (one for each sequence) are a decode step.
+ *  window >= 1, sinks >= 0 (INVALID_ARG otherwise).  ws: as kvattn_prefill_chunk, the same size.
+ *  Other arguments and errors: as kvattn_prefill_chunk.
+ */
+int kvattn_prefill_chunk_window(const void* q, int64_t q_stride, const int32_t* offsets, int64_t n_tok, const void* k_cache,
+                                const void* v_cache, const void* k_scales, const void* v_scales, int kv_type, int64_t n_cells,
+                                const int32_t* cell_plan, int64_t plan_stride, const int32_t* seq_lens, int n_seq,
+                                int64_t max_len, int n_head, int n_head_kv, int head_dim, float scale, int64_t window,
+                                int64_t sinks, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace that kvattn_prefill_chunk_shared needs on the current device for this call and for
+ * every one with the same heads and no more tokens, sequences and max_len: status word, two results in
+ * 32 bits for each (token, head), and about 40 MB of partials; 0 on invalid arguments. */
+size_t kvattn_prefill_chunk_shared_workspace_bytes(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim,
+                                                   int64_t max_len);
+
+/*
+ * kvattn_prefill_chunk_shared -- device.  kvattn_prefill_chunk of sequences that begin with the same
+ * cells: the first prefix_cells logical positions of every sequence hold the same K and V (the same
+ * entries in every row of a cell plan, or copies in the sequences' own caches).  They are read once, for
+ * the new tokens of all sequences together, and each sequence's other cells for its own tokens; the
+ * result is kvattn_prefill_chunk's.
+ *  prefix_cells  any value >= 0 (INVALID_ARG otherwise).  It counts in whole tiles of 128 cells, as far
+ *           as every sequence that has new tokens holds them in front of those; what is left is read as
+ *           the sequences' own.  The shared cells are read through the first sequence that has tokens.
+ *  ws       at least kvattn_prefill_chunk_shared_workspace_bytes(...) bytes, otherwise as there.
+ *  Other arguments and errors: as kvattn_prefill_chunk.  offsets must not decrease.
+ */
+int kvattn_prefill_chunk_shared(const void* q, int64_t q_stride, const int32_t* offsets, int64_t n_tok, const void* k_cache,
+                                const void* v_cache, const void* k_scales, const void* v_scales, int kv_type, int64_t n_cells,
+                                const int32_t* cell_plan, int64_t plan_stride, const int32_t* seq_lens, int n_seq,
+                                int64_t max_len, int n_head, int n_head_kv, int head_dim, float scale, int64_t prefix_cells,
+                                void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* Wait (host, bounded) until everything the last kvattn_decode_window_tail on this ctx
  * enqueued has finished.  Polls an event; returns TIMEOUT after timeout_ms, CUDA if the

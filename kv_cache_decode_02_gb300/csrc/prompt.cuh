@@ -1,6 +1,7 @@
-// Prompt-side operators: rotary positions (rope.cu), the cache written in its stored type and
-// read back (cache_io.cu), and causal attention of many query tokens per sequence (prefill.cu).
-// prompt_api.cu holds their C entry points.
+// Prompt-side operators: rotary positions (rope.cu), with norms and several axes (norm_rope.cu), a
+// step's maps (step_maps.cu), the cache written in its stored type and read back (cache_io.cu), and
+// causal attention of many query tokens per sequence (prefill.cu, prefill_window.cu,
+// prefill_shared.cu).  prompt_api.cu holds their C entry points.
 #pragma once
 
 #include "kvattn_internal.cuh"
@@ -20,6 +21,38 @@ struct RopeParams {
     float gain;               // multiplies cosine and sine
 };
 cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t stream, bool pdl);
+
+// ---- norms of the heads with the rotation, positions of several axes ----
+constexpr int kMaxAxes = 4;
+struct NormRopeParams {
+    RopeParams r;             // pos: [n_axes] rows, pos_stride apart
+    const __half* weight[2];  // [head_dim], null: that side is not normed
+    const uint8_t* axis;      // [n_rot / 2]: each pair's row of positions (one axis: not read)
+    int64_t pos_stride;
+    int n_axes;
+    float eps;
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, int sms, cudaStream_t stream, bool pdl);
+
+// ---- a step's maps ----
+constexpr int kMaxMapSequences = 16384;   // (every block of threads reads all of their lengths)
+struct StepMapsParams {
+    const int32_t* lens;      // [n_seq] before the step
+    const int32_t* n_new;     // [n_seq]
+    int32_t* tables;          // [n_seq][table_stride]
+    const int32_t* free_list; // nullable: nothing is taken
+    const int32_t* n_free;
+    int32_t* offsets;         // [n_seq + 1]
+    int32_t* seq_lens;        // [n_seq]
+    int32_t* positions;       // nullable: [n_tok]
+    int32_t* slots;           // [n_tok]
+    int32_t* n_free_out;
+    int32_t* plan;            // nullable: [n_seq][plan_stride]
+    uint32_t* status;         // nullable
+    int64_t table_stride, plan_stride, n_list, n_cells, n_tok, max_len;
+    int n_seq, block_shift, whole, pieces;
+};
+cudaError_t launch_step_maps(const StepMapsParams& p, cudaStream_t stream, bool pdl);
 
 // ---- cache rows in their stored type ----
 struct CacheIoParams {
@@ -42,6 +75,10 @@ struct PrefillCut {          // a work unit that the shares cut (n_parts > 0), n
     int32_t n_parts, n_tok, g, tiles;
     uint32_t start, end;     // its part of the line
 };
+struct PrefillNote {         // shared prefix: a work unit, noted for each of its tokens by the CTA that began it
+    int32_t cta, tiles, tok0, n_tok;
+    uint32_t start, end;     // its part of the line
+};
 struct PrefillParams {
     // use_tma: f16 rows (encode_planes_map), or codes (encode_codes_map), boxes of 128 dims x 128
     // cells
@@ -60,6 +97,12 @@ struct PrefillParams {
     float* part_o;            // [2 CTAs][row groups][128][head_dim], when shares
     float* part_lse;          // [2 CTAs][row groups][128]
     uint32_t* status;
+    int64_t window, sinks;    // with a window: a token sees its last `window` cells and the first `sinks`
+    int64_t prefix_cells;     // shared prefix: the first cells of all sequences that are the same
+    PrefillNote* notes;       // [2][n_tok][n_head_kv]: units of the sequences' own cells, of the prefix
+    uint2* join;              // the prefix's tiles, the line's length when shares
+    float* whole_o;           // [2][n_tok][n_head][head_dim]: results of units that are not cut
+    float* whole_lse;         // [2][n_tok][n_head]
     int64_t k_stride, v_stride;
     int64_t n_tok, n_cells, plan_stride, max_len;
     uint64_t wait_limit_ns;
@@ -71,12 +114,16 @@ struct PrefillParams {
     int shares;               // 1: equal shares of all units' tiles, cut anywhere; 0: whole units
     int use_tma;
     int out_sectors;          // out is 32-byte aligned
+    int window_tiles;         // tiles that a unit's windows and first tokens meet, at most
     float scale_log2;         // scale * log2(e)
 };
 constexpr int kPrefillTile = 128;  // cells per tile
 inline int prefill_groups(int head_dim) { return head_dim == 128 ? 2 : 1; }
 // The attention kernel on n_ctas CTAs (at most one per SM) and, with shares, the merge.
 cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl);
+cudaError_t launch_prefill_window(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl);
+// (always with its merge)
+cudaError_t launch_prefill_shared(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl);
 
 // From api.cu: a 3-D map {head_dim, heads, rows} of half rows with boxes {64, box_heads, box_rows}
 // and the 128-byte swizzle, SM count, log switch and line, the programmatic-launch switch, the

@@ -3,8 +3,8 @@
 Every function with a ``kvattn_`` name calls the C entry point of the same name; torch
 tensors are passed by ``data_ptr()``, streams by their ``cuda_stream`` handle, and a
 non-OK status raises :class:`KvattnError`.  The convenience wrappers at the end
-(``decode``, ``merge``, ``WindowTail``; ``rope``, ``cache_write``, ``cache_read``, ``prefill``,
-``prefill_chunk``) only allocate outputs and workspaces with torch and infer sizes from tensor
+(``decode``, ``merge``, ``WindowTail``; ``rope``, ``norm_rope``, ``step_maps``, ``cache_write``,
+``cache_read``, ``prefill``, ``prefill_chunk``) only allocate outputs and workspaces with torch and infer sizes from tensor
 shapes; all arithmetic runs in the library's kernels.  A wrapper's ``stream`` (default: torch's
 current one) is where it launches, and where the tensors that it makes belong, as under
 ``torch.cuda.stream(stream)``: work on another stream waits for it before it uses them, and the
@@ -40,12 +40,15 @@ KVATTN_KV_Q8_0_Q4_0 = 2
 KVATTN_KV_Q4_0 = 3
 KVATTN_DEVICE_WAIT_TIMEOUT = 1
 KVATTN_DEVICE_BAD_PLAN_ENTRY = 2
+KVATTN_DEVICE_NO_ROOM = 4
 KVATTN_TAIL_PREFETCH = 1
 KVATTN_ROPE_HALF = 0
 KVATTN_ROPE_INTERLEAVED = 1
 KVATTN_ROPE_PLAIN = 0
 KVATTN_ROPE_LINEAR = 1
 KVATTN_ROPE_YARN = 2
+KVATTN_AXES_BLOCKS = 0
+KVATTN_AXES_CYCLE = 1
 
 EXPORTED = (
     "kvattn_status_string", "kvattn_version", "kvattn_build_cell_plan", "kvattn_build_descriptors",
@@ -57,7 +60,8 @@ EXPORTED = (
     "kvattn_select_split_for", "kvattn_select_split", "kvattn_decode_multi_workspace_bytes",
     "kvattn_decode_multi", "kvattn_tail_ctx_set_flags", "kvattn_rope_table", "kvattn_rope", "kvattn_cache_write",
     "kvattn_cache_read", "kvattn_prefill_workspace_bytes", "kvattn_prefill", "kvattn_prefill_chunk_workspace_bytes",
-    "kvattn_prefill_chunk",
+    "kvattn_prefill_chunk", "kvattn_rope_axes", "kvattn_norm_rope", "kvattn_step_maps", "kvattn_prefill_window",
+    "kvattn_prefill_chunk_window", "kvattn_prefill_chunk_shared_workspace_bytes", "kvattn_prefill_chunk_shared",
 )
 
 _P = ctypes.c_void_p
@@ -133,6 +137,23 @@ lib.kvattn_prefill_chunk_workspace_bytes.restype = _SZ
 lib.kvattn_prefill_chunk.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _F,
                                      _P, _P, _P, _SZ, _P]
 lib.kvattn_prefill_chunk.restype = _I
+lib.kvattn_prefill_window.argtypes = [_P, _I64, _P, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _F, _I64, _I64, _P, _P, _P, _SZ, _P]
+lib.kvattn_prefill_window.restype = _I
+lib.kvattn_prefill_chunk_window.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _F,
+                                            _I64, _I64, _P, _P, _P, _SZ, _P]
+lib.kvattn_prefill_chunk_window.restype = _I
+lib.kvattn_prefill_chunk_shared_workspace_bytes.argtypes = [_I64, _I, _I, _I, _I, _I64]
+lib.kvattn_prefill_chunk_shared_workspace_bytes.restype = _SZ
+lib.kvattn_prefill_chunk_shared.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I, _I64, _P, _I64, _P, _I, _I64, _I, _I, _I, _F,
+                                            _I64, _P, _P, _P, _SZ, _P]
+lib.kvattn_prefill_chunk_shared.restype = _I
+lib.kvattn_rope_axes.argtypes = [_I, _P, _I, _I, _P]
+lib.kvattn_rope_axes.restype = _I
+lib.kvattn_norm_rope.argtypes = [_P, _I64, _I, _P, _P, _I64, _I, _P, _F, _P, _I64, _I, _P, _P, _F, _I, _I, _I64, _I,
+                                 _P, _I64, _P, _I64, _P]
+lib.kvattn_norm_rope.restype = _I
+lib.kvattn_step_maps.argtypes = [_P, _P, _I, _P, _I64, _I, _P, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _I, _P, _P]
+lib.kvattn_step_maps.restype = _I
 
 
 class KvattnError(RuntimeError):
@@ -415,6 +436,59 @@ def kvattn_prefill_chunk(q, q_stride, offsets, n_tok, k_cache, v_cache, k_scales
     _check(rc, "kvattn_prefill_chunk")
 
 
+def kvattn_prefill_window(q, q_stride, k, k_stride, v, v_stride, offsets, n_seq, n_tok, n_head, n_head_kv, head_dim, scale,
+                          window, sinks, out, lse, ws, ws_bytes, stream=None):
+    rc = lib.kvattn_prefill_window(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(offsets), n_seq, n_tok, n_head,
+                                   n_head_kv, head_dim, scale, window, sinks, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes,
+                                   _stream(stream))
+    _check(rc, "kvattn_prefill_window")
+
+
+def kvattn_prefill_chunk_window(q, q_stride, offsets, n_tok, k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, cell_plan,
+                                plan_stride, seq_lens, n_seq, max_len, n_head, n_head_kv, head_dim, scale, window, sinks, out,
+                                lse, ws, ws_bytes, stream=None):
+    rc = lib.kvattn_prefill_chunk_window(_ptr(q), q_stride, _ptr(offsets), n_tok, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                                         _ptr(v_scales), kv_type, n_cells, _ptr(cell_plan), plan_stride, _ptr(seq_lens), n_seq,
+                                         max_len, n_head, n_head_kv, head_dim, scale, window, sinks, _ptr(out), _ptr(lse),
+                                         _ptr(ws), ws_bytes, _stream(stream))
+    _check(rc, "kvattn_prefill_chunk_window")
+
+
+def kvattn_prefill_chunk_shared_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len) -> int:
+    return lib.kvattn_prefill_chunk_shared_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len)
+
+
+def kvattn_prefill_chunk_shared(q, q_stride, offsets, n_tok, k_cache, v_cache, k_scales, v_scales, kv_type, n_cells, cell_plan,
+                                plan_stride, seq_lens, n_seq, max_len, n_head, n_head_kv, head_dim, scale, prefix_cells, out,
+                                lse, ws, ws_bytes, stream=None):
+    rc = lib.kvattn_prefill_chunk_shared(_ptr(q), q_stride, _ptr(offsets), n_tok, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                                         _ptr(v_scales), kv_type, n_cells, _ptr(cell_plan), plan_stride, _ptr(seq_lens), n_seq,
+                                         max_len, n_head, n_head_kv, head_dim, scale, prefix_cells, _ptr(out), _ptr(lse),
+                                         _ptr(ws), ws_bytes, _stream(stream))
+    _check(rc, "kvattn_prefill_chunk_shared")
+
+
+def kvattn_rope_axes(n_rot, sections, n_axes, order, axis) -> None:
+    """``sections``: host int32 [n_axes], ``axis``: host uint8 [n_rot // 2] (numpy)."""
+    _check(lib.kvattn_rope_axes(n_rot, _ptr(sections), n_axes, order, _ptr(axis)), "kvattn_rope_axes")
+
+
+def kvattn_norm_rope(q, q_stride, n_head, q_weight, k, k_stride, n_head_kv, k_weight, eps, positions, pos_stride, n_axes, axis,
+                     turns, gain, n_rot, layout, n_tok, head_dim, q_out, q_out_stride, k_out, k_out_stride, stream=None):
+    rc = lib.kvattn_norm_rope(_ptr(q), q_stride, n_head, _ptr(q_weight), _ptr(k), k_stride, n_head_kv, _ptr(k_weight), eps,
+                              _ptr(positions), pos_stride, n_axes, _ptr(axis), _ptr(turns), gain, n_rot, layout, n_tok, head_dim,
+                              _ptr(q_out), q_out_stride, _ptr(k_out), k_out_stride, _stream(stream))
+    _check(rc, "kvattn_norm_rope")
+
+
+def kvattn_step_maps(lens, n_new, n_seq, tables, table_stride, block_cells, free_blocks, n_list, n_free, n_cells, n_tok, offsets,
+                     seq_lens, positions, slots, n_free_out, cell_plan, plan_stride, whole_plan, status, stream=None):
+    rc = lib.kvattn_step_maps(_ptr(lens), _ptr(n_new), n_seq, _ptr(tables), table_stride, block_cells, _ptr(free_blocks), n_list,
+                              _ptr(n_free), n_cells, n_tok, _ptr(offsets), _ptr(seq_lens), _ptr(positions), _ptr(slots),
+                              _ptr(n_free_out), _ptr(cell_plan), plan_stride, int(whole_plan), _ptr(status), _stream(stream))
+    _check(rc, "kvattn_step_maps")
+
+
 # ----------------------------- torch conveniences -----------------------------
 
 def _other_stream(stream):
@@ -650,26 +724,44 @@ def _cache_type(k_cache, v_cache, k_scales, v_scales, head_dim):
 
 class RopeTable:
     """Angles per position of a model's rotary pairs (``turns``, device uint64 kept as int64: 2^64
-    theta / (2 pi)) and the gain on cosine and sine; made by :func:`rope_table`, or by a program from
-    frequencies of its own."""
+    theta / (2 pi)) and the gain on cosine and sine; with several axes of positions also each pair's
+    ``axis`` (device uint8).  Made by :func:`rope_table`, or by a program from frequencies of its own."""
 
-    def __init__(self, turns, gain, n_rot):
-        self.turns, self.gain, self.n_rot = turns, gain, n_rot
+    def __init__(self, turns, gain, n_rot, axis=None, n_axes=1):
+        self.turns, self.gain, self.n_rot, self.axis, self.n_axes = turns, gain, n_rot, axis, n_axes
 
 
-def rope_table(n_rot, *, base=10000.0, scaling="none", factor=1.0, original=0, device="cuda"):
+def rope_table(n_rot, *, base=10000.0, scaling="none", factor=1.0, original=0, sections=None, order="blocks", restart=False,
+               device="cuda"):
     """``scaling``: "none", "linear" or "yarn" (``factor`` times the ``original`` context; the paper's
-    ramp, see kvattn_rope_table: a model trained with another one needs a RopeTable of its own)."""
+    ramp, see kvattn_rope_table: a model trained with another one needs a RopeTable of its own).
+    ``sections``: pairs of each axis of positions (one to four axes, n_rot / 2 pairs in all), in
+    consecutive blocks or dealt out in turn (``order`` "blocks" or "cycle"); ``restart``: each axis has
+    the frequencies of a head of its own pairs alone, instead of the pairs' own."""
     import torch
     kind = {"none": KVATTN_ROPE_PLAIN, "linear": KVATTN_ROPE_LINEAR, "yarn": KVATTN_ROPE_YARN}[scaling]
     host = np.zeros(n_rot // 2, dtype=np.uint64)
     gain = kvattn_rope_table(n_rot, base, kind, factor, original, host)
-    return RopeTable(torch.from_numpy(host.view(np.int64)).to(device), gain, n_rot)
+    axis, n_axes = None, 1
+    if sections is not None:
+        n_axes, counts, of = len(sections), np.array(sections, dtype=np.int32), np.zeros(n_rot // 2, dtype=np.uint8)
+        kvattn_rope_axes(n_rot, counts, n_axes, {"blocks": KVATTN_AXES_BLOCKS, "cycle": KVATTN_AXES_CYCLE}[order], of)
+        if restart:
+            for a, count in enumerate(sections):
+                own = np.zeros(count, dtype=np.uint64)
+                if count:
+                    kvattn_rope_table(2 * count, base, kind, factor, original, own)
+                host[of == a] = own
+        axis = torch.from_numpy(of).to(device)
+    return RopeTable(torch.from_numpy(host.view(np.int64)).to(device), gain, n_rot, axis, n_axes)
 
 
 def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, stream=None):
-    """q: half [T][H][D], k: half [T][Hk][D] (either may be None), positions int32 [T].  Rotated rows
-    go to new tensors, or to ``q_out`` / ``k_out`` (which may be q and k themselves).  Returns (q, k)."""
+    """q: half [T][H][D], k: half [T][Hk][D] (either may be None), positions int32 [T], or [axes][T] with
+    a table of several axes.  Rotated rows go to new tensors, or to ``q_out`` / ``k_out`` (which may be q
+    and k themselves).  Returns (q, k)."""
+    if table.axis is not None:
+        return norm_rope(q, k, positions, table, layout=layout, q_out=q_out, k_out=k_out, stream=stream)
     if _torch is None:
         _bind_torch()
     code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
@@ -706,6 +798,116 @@ def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, strea
     _check(lib.kvattn_rope(qa[0], qa[1], qa[2], ka[0], ka[1], ka[2], at, turns.data_ptr(), table.gain, table.n_rot, code,
                            T, D, qa[3], qa[4], ka[3], ka[4], _stream(stream)), "kvattn_rope")
     return q_out if q is not None else None, k_out if k is not None else None
+
+
+def norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, layout="half", q_out=None, k_out=None,
+              stream=None):
+    """:func:`rope` of heads that are normed first, in the same pass: ``q_weight`` / ``k_weight`` half
+    [D] (None: that side is not normed), ``eps`` beside the mean square."""
+    if _torch is None:
+        _bind_torch()
+    code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
+    if q is None and k is None:
+        raise ValueError("q or k is wanted")
+    if ((q is not None and q_out is None) or (k is not None and k_out is None)) and _other_stream(stream):
+        with _made_on(stream):
+            return norm_rope(q, k, positions, table, q_weight=q_weight, k_weight=k_weight, eps=eps, layout=layout, q_out=q_out,
+                             k_out=k_out)
+    T = D = None
+    qa = ka = (None, 0, 0, None, 0)
+    if q is not None:
+        if q_out is None:
+            q_out = _torch.empty(q.shape, dtype=_F16, device=q.device)
+        T, h, D, st = _rows(q, "q")
+        to, ho, do, so = _rows(q_out, "q_out")
+        if to != T or ho != h or do != D:
+            raise ValueError("q_out: q's shape is wanted")
+        qa = (q.data_ptr(), st, h, q_out.data_ptr(), so)
+    if k is not None:
+        if k_out is None:
+            k_out = _torch.empty(k.shape, dtype=_F16, device=k.device)
+        t, h, d, st = _rows(k, "k")
+        to, ho, do, so = _rows(k_out, "k_out")
+        if to != t or ho != h or do != d or (q is not None and (t != T or d != D)):
+            raise ValueError("k, k_out: shapes do not agree")
+        T, D = t, d
+        ka = (k.data_ptr(), st, h, k_out.data_ptr(), so)
+    at, turns, axis, n_axes = _ints(positions, "positions", T * table.n_axes), table.turns, table.axis, table.n_axes
+    d = _here(k if q is None else q, "k" if q is None else "q")
+    if (positions.get_device() != d or turns.get_device() != d or _off(k, d) or _off(q_out, d) or _off(k_out, d)
+            or _off(q_weight, d) or _off(k_weight, d) or _off(axis, d)):
+        _elsewhere(d, k=k, positions=positions, table=turns, axis=axis, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
+                   k_out=k_out)
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not _F16 or w.numel() != D or not w.is_contiguous()):
+            raise ValueError("q_weight, k_weight: contiguous half of head_dim values is wanted")
+    if turns.numel() * 2 < table.n_rot or turns.element_size() != 8 or not turns.is_contiguous():
+        raise ValueError("table: n_rot / 2 contiguous 64-bit angles are wanted")
+    if n_axes > 1 and (axis is None or axis.numel() * 2 < table.n_rot or axis.element_size() != 1 or not axis.is_contiguous()):
+        raise ValueError("table: n_rot / 2 contiguous 8-bit axes are wanted")
+    _check(lib.kvattn_norm_rope(qa[0], qa[1], qa[2], _raw(q_weight), ka[0], ka[1], ka[2], _raw(k_weight), eps, at, T, n_axes,
+                                _raw(axis), turns.data_ptr(), table.gain, table.n_rot, code, T, D, qa[3], qa[4], ka[3], ka[4],
+                                _stream(stream)), "kvattn_norm_rope")
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+class StepMaps:
+    """What :func:`step_maps` makes: int32 ``offsets`` [S + 1], ``seq_lens`` [S], ``positions`` [T],
+    ``slots`` [T] and ``n_free`` [1]."""
+    __slots__ = ("offsets", "seq_lens", "positions", "slots", "n_free")
+
+    def __init__(self, offsets, seq_lens, positions, slots, n_free):
+        self.offsets, self.seq_lens, self.positions, self.slots, self.n_free = offsets, seq_lens, positions, slots, n_free
+
+
+def step_maps_buffers(n_seq, n_tok, device="cuda"):
+    """A StepMaps for steps of at most ``n_tok`` tokens."""
+    import torch
+    return StepMaps(*(torch.empty(n, dtype=torch.int32, device=device) for n in (n_seq + 1, n_seq, n_tok, n_tok, 1)))
+
+
+def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells, n_cells, n_tok=None, plan=None,
+              whole_plan=True, status=None, out=None, stream=None):
+    """A step's maps from the sequences' lengths and new tokens (int32 [S]): blocks of ``block_cells``
+    cells are taken from the end of ``free_blocks`` (int32, the first ``n_free`` [1] of them free; None:
+    nothing is taken) into ``tables`` (int32 [S][stride], in place), and the offsets, lengths, positions
+    and slots of ``n_tok`` packed rows follow (rows behind the last token: slot -1).  ``plan`` (int32
+    [S][stride]): the cell plan, whole rows or the new tokens' entries.  ``out``: a StepMaps to write.
+    Returns a StepMaps."""
+    if _torch is None:
+        _bind_torch()
+    if out is None and _other_stream(stream):
+        with _made_on(stream):
+            return step_maps(lens, n_new, tables, free_blocks, n_free, block_cells=block_cells, n_cells=n_cells, n_tok=n_tok,
+                             plan=plan, whole_plan=whole_plan, status=status)
+    S = lens.numel()
+    a, b = _ints(lens, "lens", S), _ints(n_new, "n_new", S)
+    d = _here(lens, "lens")
+    if tables.dim() != 2 or tables.shape[0] != S or (plan is not None and (plan.dim() != 2 or plan.shape[0] != S)):
+        raise ValueError("tables, plan: a row for each sequence is wanted")
+    if (free_blocks is None) != (n_free is None):
+        raise ValueError("free_blocks and n_free go together")
+    if out is None:
+        if n_tok is None:
+            raise ValueError("n_tok or out is wanted")
+        out = step_maps_buffers(S, n_tok, lens.device)
+    T = out.slots.numel()
+    if n_tok is not None and n_tok != T:
+        raise ValueError("n_tok: out has other rows")
+    if (n_new.get_device() != d or tables.get_device() != d or _off(free_blocks, d) or _off(n_free, d) or _off(plan, d)
+            or _bad_word(status, d) or out.offsets.get_device() != d or out.seq_lens.get_device() != d
+            or out.positions.get_device() != d or out.slots.get_device() != d or out.n_free.get_device() != d):
+        _elsewhere(d, n_new=n_new, tables=tables, free_blocks=free_blocks, n_free=n_free, plan=plan, status=status,
+                   offsets=out.offsets, seq_lens=out.seq_lens, positions=out.positions, slots=out.slots, out_n_free=out.n_free)
+    take = free_blocks is not None
+    _check(lib.kvattn_step_maps(a, b, S, _ints(tables, "tables"), tables.shape[1], block_cells,
+                                _ints(free_blocks, "free_blocks") if take else None, free_blocks.numel() if take else 0,
+                                _ints(n_free, "n_free", 1) if take else None, n_cells, T, _ints(out.offsets, "offsets", S + 1),
+                                _ints(out.seq_lens, "seq_lens", S), _ints(out.positions, "positions", T),
+                                _ints(out.slots, "slots", T), _ints(out.n_free, "n_free", 1) if take else None,
+                                None if plan is None else _ints(plan, "plan"), 0 if plan is None else plan.shape[1],
+                                1 if whole_plan else 0, _raw(status), _stream(stream)), "kvattn_step_maps")
+    return out
 
 
 def cache_write(k, v, slots, k_cache, v_cache, *, k_scales=None, v_scales=None, status=None, stream=None):
@@ -766,14 +968,15 @@ def prefill_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, device="cuda"):
     return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
-def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream=None):
+def prefill(q, k, v, offsets, *, scale=None, window=None, sinks=0, out=None, lse=None, ws=None, stream=None):
     """Causal attention of packed prompts: q half [T][H][D], k and v half [T][Hk][D], offsets int32
-    [S + 1].  Returns (out half [T][H][D], lse float [T][H])."""
+    [S + 1].  With a ``window`` a token sees its sequence's last ``window`` tokens (its own among them)
+    and the first ``sinks``.  Returns (out half [T][H][D], lse float [T][H])."""
     if _torch is None:
         _bind_torch()
     if (out is None or lse is None or ws is None) and _other_stream(stream):
         with _made_on(stream):
-            return prefill(q, k, v, offsets, scale=scale, out=out, lse=lse, ws=ws)
+            return prefill(q, k, v, offsets, scale=scale, window=window, sinks=sinks, out=out, lse=lse, ws=ws)
     T, H, D, qs = _rows(q, "q")
     kt, Hk, kd, ks = _rows(k, "k")
     vt, vh, vd, vs = _rows(v, "v")
@@ -788,31 +991,44 @@ def prefill(q, k, v, offsets, *, scale=None, out=None, lse=None, ws=None, stream
     if (k.get_device() != d or v.get_device() != d or offsets.get_device() != d or out.get_device() != d
             or lse.get_device() != d or _bad_ws(ws, d)):
         _elsewhere(d, k=k, v=v, offsets=offsets, out=out, lse=lse, ws=ws)
-    _check(lib.kvattn_prefill(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, off, S, T, H, Hk, D,
-                              1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                              ws.numel(), _stream(stream)), "kvattn_prefill")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if window is not None:
+        _check(lib.kvattn_prefill_window(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, off, S, T, H, Hk, D, scale, window,
+                                         sinks, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
+               "kvattn_prefill_window")
+        return out, lse
+    if sinks:
+        raise ValueError("sinks: with a window only")
+    _check(lib.kvattn_prefill(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, off, S, T, H, Hk, D, scale, out.data_ptr(),
+                              lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), "kvattn_prefill")
     return out, lse
 
 
-def prefill_chunk_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, device="cuda"):
+def prefill_chunk_workspace(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, device="cuda", shared=0):
+    """For calls with ``shared`` cells, whatever their number, when ``shared`` is not 0."""
     import torch
-    nbytes = kvattn_prefill_chunk_workspace_bytes(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len)
+    query = kvattn_prefill_chunk_shared_workspace_bytes if shared else kvattn_prefill_chunk_workspace_bytes
+    nbytes = query(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len)
     return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cells=None, cell_plan=None, k_scales=None,
-                  v_scales=None, scale=None, out=None, lse=None, ws=None, stream=None):
+                  v_scales=None, scale=None, window=None, sinks=0, shared=0, out=None, lse=None, ws=None, stream=None):
     """Causal attention of new tokens over caches that hold their cells: q half [T][H][D] (the
     sequences' tokens packed, offsets int32 [S + 1]), the cache as in decode: one unified cache with
     a ``cell_plan`` (int32 [S][stride]), a per-sequence [S][N][Hk][D] cache, or one [cells][Hk][D]
-    whose ``n_cells`` are each sequence's.  Returns (out half [T][H][D], lse: the given tensor or
-    None)."""
+    whose ``n_cells`` are each sequence's.  With a ``window`` a token sees its sequence's last ``window``
+    cells (its own among them) and the first ``sinks``; with ``shared`` the sequences' first ``shared``
+    cells hold the same and are read once for all of them (one or the other).  Returns (out half
+    [T][H][D], lse: the given tensor or None)."""
     if _torch is None:
         _bind_torch()
     if (out is None or ws is None) and _other_stream(stream):
         with _made_on(stream):
             return prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, max_len=max_len, n_cells=n_cells, cell_plan=cell_plan,
-                                 k_scales=k_scales, v_scales=v_scales, scale=scale, out=out, lse=lse, ws=ws)
+                                 k_scales=k_scales, v_scales=v_scales, scale=scale, window=window, sinks=sinks, shared=shared,
+                                 out=out, lse=lse, ws=ws)
     T, H, D, qs = _rows(q, "q")
     off, S = _ints(offsets, "offsets"), offsets.numel() - 1
     lens = _ints(seq_lens, "seq_lens", S)
@@ -833,16 +1049,35 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     if lse is not None:
         _new_out(lse, "lse", (T, H), q, _torch.float32)
     if ws is None:
-        ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, q.device)
+        ws = prefill_chunk_workspace(T, S, H, Hk, D, max_len, q.device, shared)
     if (k_cache.get_device() != d or v_cache.get_device() != d or offsets.get_device() != d or seq_lens.get_device() != d
             or out.get_device() != d or _off(cell_plan, d) or _off(k_scales, d) or _off(v_scales, d) or _off(lse, d)
             or _bad_ws(ws, d)):
         _elsewhere(d, k_cache=k_cache, v_cache=v_cache, offsets=offsets, seq_lens=seq_lens, cell_plan=cell_plan,
                    k_scales=k_scales, v_scales=v_scales, out=out, lse=lse, ws=ws)
-    _check(lib.kvattn_prefill_chunk(q.data_ptr(), qs, off, T, k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales),
-                                    _raw(v_scales), kv_type, n_cells, plan, stride, lens, S, max_len, H, Hk, D,
-                                    1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), _raw(lse), ws.data_ptr(),
-                                    ws.numel(), _stream(stream)), "kvattn_prefill_chunk")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if window is None and not shared:
+        if sinks:
+            raise ValueError("sinks: with a window only")
+        _check(lib.kvattn_prefill_chunk(q.data_ptr(), qs, off, T, k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales),
+                                        _raw(v_scales), kv_type, n_cells, plan, stride, lens, S, max_len, H, Hk, D, scale,
+                                        out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _stream(stream)),
+               "kvattn_prefill_chunk")
+    elif window is not None:
+        if shared:
+            raise ValueError("window or shared, not both")
+        _check(lib.kvattn_prefill_chunk_window(q.data_ptr(), qs, off, T, k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales),
+                                               _raw(v_scales), kv_type, n_cells, plan, stride, lens, S, max_len, H, Hk, D, scale,
+                                               window, sinks, out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(),
+                                               _stream(stream)), "kvattn_prefill_chunk_window")
+    else:
+        if sinks:
+            raise ValueError("sinks: with a window only")
+        _check(lib.kvattn_prefill_chunk_shared(q.data_ptr(), qs, off, T, k_cache.data_ptr(), v_cache.data_ptr(), _raw(k_scales),
+                                               _raw(v_scales), kv_type, n_cells, plan, stride, lens, S, max_len, H, Hk, D, scale,
+                                               shared, out.data_ptr(), _raw(lse), ws.data_ptr(), ws.numel(), _stream(stream)),
+               "kvattn_prefill_chunk_shared")
     return out, lse
 
 
