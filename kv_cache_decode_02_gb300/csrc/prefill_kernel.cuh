@@ -1127,23 +1127,36 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                     const int64_t c0 = (int64_t)tile_of<MODE>(s, job.j) * kPrefillTile + 32 * k4;
                                     all = all && (c0 >= s.low_last || c0 + 32 <= p.sinks);
                                 }
-                                if ((!cut || all) && gone == 0u) continue;
+                                const bool look = cut && !all;
+                                if (!look && gone == 0u) continue;
                                 unsigned char* cells = plane + 4096 * k4;
+                                // (all loads first, and one test: stores in between would make each wait for the
+                                // one before, 4000 clocks a slot)
+                                uint4 w[6];
+                                uint32_t wild = 0;
 #pragma unroll
                                 for (int q = 0; q < 6; ++q) {
-                                    const int c = 2 * (3 * q + warp - 9) + sub;
-                                    if (c >= 32) continue;
-                                    uint4* at = reinterpret_cast<uint4*>(cells + swz(c, b & 127));
-                                    if ((gone >> c) & 1u) {
-                                        *at = make_uint4(0u, 0u, 0u, 0u);
-                                    } else if (cut) {
-                                        uint4 w = *at;
-                                        if (!finite8(w)) {
-                                            bool bad;
-                                            w = make_uint4(finite2(w.x, bad), finite2(w.y, bad), finite2(w.z, bad), finite2(w.w, bad));
-                                            *at = w;
-                                            atomicOr(&bad_row[k4], 1u << c);
-                                        }
+                                    const int c = min(2 * (3 * q + warp - 9), 30) + sub;   // (the last one twice)
+                                    w[q] = make_uint4(0u, 0u, 0u, 0u);
+                                    if (look && !((gone >> c) & 1u)) w[q] = *reinterpret_cast<const uint4*>(cells + swz(c, b & 127));
+                                    wild |= (uint32_t)!finite8(w[q]) << q;
+                                }
+                                if (__any_sync(0xffffffffu, wild != 0u)) {
+#pragma unroll
+                                    for (int q = 0; q < 6; ++q) {
+                                        const int c = min(2 * (3 * q + warp - 9), 30) + sub;
+                                        if (!((wild >> q) & 1u)) continue;
+                                        bool bad;
+                                        *reinterpret_cast<uint4*>(cells + swz(c, b & 127)) =
+                                            make_uint4(finite2(w[q].x, bad), finite2(w[q].y, bad), finite2(w[q].z, bad), finite2(w[q].w, bad));
+                                        atomicOr(&bad_row[k4], 1u << c);
+                                    }
+                                }
+                                if (gone != 0u) {
+#pragma unroll
+                                    for (int q = 0; q < 6; ++q) {
+                                        const int c = min(2 * (3 * q + warp - 9), 30) + sub;
+                                        if ((gone >> c) & 1u) *reinterpret_cast<uint4*>(cells + swz(c, b & 127)) = make_uint4(0u, 0u, 0u, 0u);
                                     }
                                 }
                             }
@@ -1224,7 +1237,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 ds[k] = sc[64 * (k0 + k)];
                                 big = max(big, ds[k]);   // (a negative one, which no write makes, counts as big)
                             }
-                            const bool odd = cut || big > kBigScale;   // rare: a loop of its own below
+                            // (a code is finite, and so is its product with a scale that is not big)
+                            const bool odd = big > kBigScale;   // rare: a loop of its own below
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const uint32_t d = prmt_b32(ds[k], 0u, 0x1010u);
@@ -1261,7 +1275,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 ds[k] = scales[4 * c0 + piece + 128 * (k0 + k)];
                                 big = max(big, ds[k] & 0x7fffu);
                             }
-                            const bool odd = cut || big > kBigScale;
+                            const bool odd = big > kBigScale;
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const uint32_t d = prmt_b32(ds[k], 0u, 0x1010u);
@@ -1666,7 +1680,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         hide1 = min((g ? low[1] : low[0]) - off, 64);
                         seen = seen && hide0 >= hide1;
                     }
-                    if (pre || !__all_sync(0xffffffffu, seen)) {
+                    // (kWindow: a third of the tiles are masked, in registers below)
+                    if (pre || (MODE != kWindow && !__all_sync(0xffffffffu, seen))) {
                         // (the rare tiles: scaled, masked and put back by a loop of its own, which keeps
                         // the code of the others short)
 #pragma unroll 1
@@ -1688,6 +1703,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     tmem_ld32(t_s + 64 * half, sv);
                     tmem_ld32(t_s + 64 * half + 32, sv + 32);
                     tc_wait_ld();
+                    if constexpr (MODE == kWindow) {
+                        if (!pre && !__all_sync(0xffffffffu, seen)) {
+                            auto below = [](int n) -> uint64_t { return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1ull); };
+                            const uint64_t in = below(left) & ~(hide1 > hide0 ? below(hide1) & ~below(hide0) : 0ull);
+                            const uint32_t in0 = (uint32_t)in, in1 = (uint32_t)(in >> 32);
+#pragma unroll
+                            for (int c = 0; c < 64; ++c)
+                                sv[c] = ((c < 32 ? in0 : in1) >> (c & 31)) & 1u ? sv[c] : 0xff800000u;
+                        }
+                    }
                     if (PLAN) {
                         const uint32_t t = masks + j;
                         if (holes) {
