@@ -537,7 +537,7 @@ int kvattn_norm_rope(const void* q, int64_t q_stride, int n_head, const void* q_
  *           are written fastest).  whole_plan 0: the new tokens' entries are written, the others stay
  *           as the step before left them; else whole rows, -1 behind the sequence's end.
  *  status   NULL or a device uint32.
- * No output overlaps an input or another output.  n_seq at most 16384.
+ * No output overlaps an input or another output.  n_seq at most 16384, plan_stride below 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED (before the launch); CUDA.
  */
 int kvattn_step_maps(const int32_t* lens, const int32_t* n_new, int n_seq, int32_t* tables, int64_t table_stride, int block_cells,

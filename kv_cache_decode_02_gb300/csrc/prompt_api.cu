@@ -323,7 +323,7 @@ int kvattn_step_maps(const int32_t* lens, const int32_t* n_new, int n_seq, int32
         (cell_plan != nullptr && plan_stride < 0))
         return KVATTN_ERR_INVALID_ARG;
     if ((block_cells & (block_cells - 1)) != 0 || block_cells < 4 || block_cells > 65536 || n_seq > kMaxMapSequences ||
-        n_cells > INT32_MAX || n_tok > INT32_MAX || n_list > INT32_MAX)
+        n_cells > INT32_MAX || n_tok > INT32_MAX || n_list > INT32_MAX || (cell_plan != nullptr && plan_stride > INT32_MAX))
         return KVATTN_ERR_UNSUPPORTED;
     if (offsets == nullptr || !aligned(offsets, 4) || !aligned(positions, 4) || (n_tok > 0 && slots == nullptr) ||
         !aligned(slots, 4) || !aligned(cell_plan, 4) || !aligned(status, 4))

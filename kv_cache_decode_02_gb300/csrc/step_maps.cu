@@ -10,8 +10,10 @@
 //
 // One launch, whatever the sizes: blocks of threads do not wait for one another, each makes the two
 // running sums over the sequences itself (new tokens, then needed blocks) and finds new blocks in the
-// free list, not in the tables that another one may be writing.  A few sequences and tokens are all
-// latency; a whole plan is bytes (4 an entry, written in 16-byte pieces).
+// free list, not in the tables that another one may be writing.  One warp makes the sums, 128 sequences
+// at a time, while the others write what does not depend on them: plan entries of cells held before.
+// 64 rows of 131584 entries over blocks of 16 cells: 11.0 us (a fill of the same bytes takes 6.2; 15.6 with
+// sums by all warps in front of everything); 64 single tokens 4.1 us, all latency.
 #include <cstdint>
 
 #include "prompt.cuh"
@@ -20,103 +22,180 @@ namespace kvattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kPieceEntries = 8192;   // of a plan row, for one block of threads
+constexpr int kQuads = 8;                                // of plan entries, for one thread at a time
+constexpr int kPieceEntries = 4 * kQuads * kThreads;     // of a plan row, for one block of threads
 constexpr int kPieceTokens = 1024;
+constexpr int64_t kMaxPieces = 1024;
+constexpr int kLaneSequences = 4;
 
-// Inclusive sum over the block's threads, added to `base`, which moves on by the whole sum.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t& base, int64_t* part) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int64_t lane_sum(int64_t v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t w = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += w;
     }
-    if (lane == 31) part[warp] = v;
-    __syncthreads();
-    int64_t before = base;
-    for (int i = 0; i < kWarps; ++i) {
-        const int64_t w = part[i];
-        if (i < warp) before += w;
-        base += w;
-    }
-    __syncthreads();
-    return before + v;
+    return v;
 }
 
+struct Mine {       // of the block's sequence
+    int64_t len, n, row0, before, need;   // length, new tokens, first row, blocks taken before its own
+    bool served;
+};
+
 __global__ void __launch_bounds__(kThreads) step_maps_kernel(const __grid_constant__ StepMapsParams p) {
-    __shared__ int64_t part[kWarps];
-    __shared__ int64_t mine[5];   // of this block's sequence: length, new tokens, first row, blocks taken before, needed
-    __shared__ int mine_served;
-    __shared__ unsigned long long most;   // blocks taken in all
+    __shared__ Mine mine;
+    __shared__ int64_t all_rows, all_taken;   // new tokens, blocks taken
+    __shared__ int64_t free_count;
     pdl_wait();
     const int tid = threadIdx.x;
     const int seq = (int)(blockIdx.x / (unsigned)p.pieces), piece = (int)(blockIdx.x % (unsigned)p.pieces);
     const int shift = p.block_shift;
     const int64_t B = (int64_t)1 << shift;
-    int64_t n_free = 0;
-    if (p.free_list != nullptr) {
-        n_free = __ldg(p.n_free);
-        n_free = n_free < 0 ? 0 : (n_free > p.n_list ? p.n_list : n_free);
-    }
-    if (tid == 0) most = 0ull;
-    __syncthreads();
-    int64_t rows = 0, taken_all = 0;
-    bool unserved = false;
-    for (int s0 = 0; s0 < p.n_seq; s0 += kThreads) {
-        const int s = s0 + tid;
-        int64_t len = 0, n = 0;
-        if (s < p.n_seq) {
-            len = __ldg(p.lens + s);
-            n = __ldg(p.n_new + s);
-            len = len < 0 ? 0 : (len > p.max_len ? p.max_len : len);
-            n = n < 0 ? 0 : n;
-        }
-        const int64_t end_row = block_sum(n, rows, part);
-        const bool fits = n == 0 || (len + n <= p.max_len && end_row <= p.n_tok);
-        const int64_t need = fits && p.free_list != nullptr ? ((len + n + B - 1) >> shift) - ((len + B - 1) >> shift) : 0;
-        const int64_t taken = block_sum(need, taken_all, part);
-        const bool served = fits && (need == 0 || taken <= n_free);
-        unserved = unserved || !served;
-        if (need > 0 && served) atomicMax(&most, (unsigned long long)taken);
-        if (s == seq) {
-            mine[0] = len;
-            mine[1] = n;
-            mine[2] = end_row - n;
-            mine[3] = taken - need;
-            mine[4] = need;
-            mine_served = served ? 1 : 0;
-        }
-    }
-    __syncthreads();
-    if (blockIdx.x == 0 && tid == 0) p.offsets[0] = 0;
-    // rows behind the last token: no cell
-    for (int64_t r = rows + (int64_t)blockIdx.x * kThreads + tid; r < p.n_tok; r += (int64_t)gridDim.x * kThreads) {
-        if (p.positions != nullptr) p.positions[r] = 0;
-        p.slots[r] = -1;
-    }
-    if (blockIdx.x == 0) {
-        if (tid == 0 && p.n_free_out != nullptr) *p.n_free_out = (int32_t)(n_free - (int64_t)most);
-        if (unserved && p.status != nullptr) atomicOr(p.status, KVATTN_DEVICE_NO_ROOM);
-    }
-    if (seq >= p.n_seq) return;
-
-    const int64_t len = mine[0], n = mine[1], row0 = mine[2], before = mine[3], need = mine[4];
-    const bool served = mine_served != 0;
-    const int64_t after = served ? len + n : len;
-    const int64_t held = (len + B - 1) >> shift;
+    const bool whole = p.plan != nullptr && p.whole && seq < p.n_seq;
     int32_t* table = p.tables + (int64_t)seq * p.table_stride;
+    int32_t* row = p.plan == nullptr ? nullptr : p.plan + (int64_t)seq * p.plan_stride;
+    // (a row that does not lie on 16 bytes is written entry by entry)
+    const bool wide = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
+    const uint32_t stride = (uint32_t)p.plan_stride, in_block = (1u << shift) - 1u;
     bool bad = false;
-    // first cell of the sequence's block e, -1: none
-    auto block_cell = [&](int64_t e) -> int32_t {
-        const int32_t id = served && e >= held && e < held + need ? __ldg(p.free_list + (n_free - 1 - (before + e - held))) : table[e];
+    auto first_of = [&](int32_t id) -> int32_t {   // cell of block `id`, -1: outside the cache
         if (id >= 0 && (((int64_t)id + 1) << shift) <= p.n_cells) return (int32_t)((int64_t)id << shift);
         bad = true;
         return -1;
     };
-    auto cell_at = [&](int64_t i) -> int32_t {
-        const int32_t c = block_cell(i >> shift);
-        return c < 0 ? -1 : c + (int32_t)(i & (B - 1));
+    auto quad = [&](uint32_t i0, int k) -> uint32_t { return i0 + 4u * (uint32_t)(tid + k * kThreads); };
+    auto put4 = [&](uint32_t i, const int4& e) {
+        if (wide && i + 4 <= stride) {
+            *reinterpret_cast<int4*>(row + i) = e;
+        } else {
+            if (i < stride) row[i] = e.x;
+            if (i + 1 < stride) row[i + 1] = e.y;
+            if (i + 2 < stride) row[i + 2] = e.z;
+            if (i + 3 < stride) row[i + 3] = e.w;
+        }
+    };
+    // What a thread writes of a plan row is quads, four entries of one block (a block holds a multiple of
+    // four cells).  Those below the sequence's length, and those that the step's tokens cannot reach, do
+    // not depend on the sums.
+    uint32_t held_cells = 0, most = 0;
+    auto put_known = [&](uint32_t i0) {
+        int32_t id[kQuads];
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const uint32_t i = quad(i0, k);
+            id[k] = i < held_cells ? table[i >> shift] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const uint32_t i = quad(i0, k);
+            if (i >= most) {
+                put4(i, make_int4(-1, -1, -1, -1));
+            } else if (i + 4 <= held_cells) {
+                const int32_t first = first_of(id[k]), c = first + (int32_t)(i & in_block);
+                put4(i, first < 0 ? make_int4(-1, -1, -1, -1) : make_int4(c, c + 1, c + 2, c + 3));
+            }
+        }
+    };
+    if (whole) {
+        const int64_t l = __ldg(p.lens + seq), n = __ldg(p.n_new + seq);
+        const int64_t held = l < 0 ? 0 : (l > p.max_len ? p.max_len : l), end = held + (n < 0 ? 0 : n);
+        held_cells = (uint32_t)held;
+        most = (uint32_t)(end > p.max_len ? held : end);   // (one that does not fit is not served)
+        if (tid >= 32) put_known((uint32_t)piece * kPieceEntries);
+    }
+
+    if (tid < 32) {
+        int64_t n_free = 0;
+        if (p.free_list != nullptr) {
+            n_free = __ldg(p.n_free);
+            n_free = n_free < 0 ? 0 : (n_free > p.n_list ? p.n_list : n_free);
+        }
+        int64_t rows = 0, asked = 0, taken_all = 0;
+        bool unserved = false;
+        for (int s0 = 0; s0 < p.n_seq; s0 += 32 * kLaneSequences) {
+            const int first = s0 + kLaneSequences * tid;
+            int64_t len[kLaneSequences], n[kLaneSequences], need[kLaneSequences];
+            int64_t sum = 0;
+#pragma unroll
+            for (int k = 0; k < kLaneSequences; ++k) {
+                len[k] = n[k] = 0;
+                if (first + k < p.n_seq) {
+                    len[k] = __ldg(p.lens + first + k);
+                    n[k] = __ldg(p.n_new + first + k);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kLaneSequences; ++k) {
+                len[k] = len[k] < 0 ? 0 : (len[k] > p.max_len ? p.max_len : len[k]);
+                n[k] = n[k] < 0 ? 0 : n[k];
+                sum += n[k];
+            }
+            const int64_t row_end = rows + lane_sum(sum);
+            int64_t row = row_end - sum;
+            bool fits[kLaneSequences];
+            sum = 0;
+#pragma unroll
+            for (int k = 0; k < kLaneSequences; ++k) {
+                row += n[k];
+                fits[k] = n[k] == 0 || (len[k] + n[k] <= p.max_len && row <= p.n_tok);
+                need[k] = fits[k] && p.free_list != nullptr ? ((len[k] + n[k] + B - 1) >> shift) - ((len[k] + B - 1) >> shift) : 0;
+                sum += need[k];
+            }
+            const int64_t asked_end = asked + lane_sum(sum);
+            int64_t taken = asked_end - sum;
+            row = row_end;
+#pragma unroll
+            for (int k = kLaneSequences - 1; k >= 0; --k) row -= n[k];
+#pragma unroll
+            for (int k = 0; k < kLaneSequences; ++k) {
+                taken += need[k];
+                const bool served = fits[k] && (need[k] == 0 || taken <= n_free);
+                if (need[k] > 0 && served) taken_all = taken;
+                unserved = unserved || !served;
+                if (first + k == seq && first + k < p.n_seq) mine = Mine{len[k], n[k], row, taken - need[k], need[k], served};
+                row += n[k];
+            }
+            rows = __shfl_sync(0xffffffffu, row_end, 31);
+            asked = __shfl_sync(0xffffffffu, asked_end, 31);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const int64_t w = __shfl_xor_sync(0xffffffffu, taken_all, o);
+            taken_all = w > taken_all ? w : taken_all;
+        }
+        unserved = __any_sync(0xffffffffu, unserved);
+        if (tid == 0) {
+            all_rows = rows;
+            all_taken = taken_all;
+            free_count = n_free;
+            if (blockIdx.x == 0) {
+                p.offsets[0] = 0;
+                if (unserved && p.status != nullptr) atomicOr(p.status, KVATTN_DEVICE_NO_ROOM);
+            }
+        }
+    }
+    if (whole && tid < 32) put_known((uint32_t)piece * kPieceEntries);
+    __syncthreads();
+    const int64_t n_free = free_count;
+    if (blockIdx.x == 0 && tid == 0 && p.n_free_out != nullptr) *p.n_free_out = (int32_t)(n_free - all_taken);
+    // rows behind the last token: no cell
+    for (int64_t r = all_rows + (int64_t)blockIdx.x * kThreads + tid; r < p.n_tok; r += (int64_t)gridDim.x * kThreads) {
+        if (p.positions != nullptr) p.positions[r] = 0;
+        p.slots[r] = -1;
+    }
+    if (seq >= p.n_seq) return;
+
+    const int64_t len = mine.len, n = mine.n, row0 = mine.row0;
+    const bool served = mine.served;
+    const int64_t after = served ? len + n : len;
+    const int64_t held = (len + B - 1) >> shift, fresh = served ? held + mine.need : held;
+    // new block e is entry `from_end - e` of the free list
+    const int64_t from_end = n_free - 1 - mine.before + held;
+    // first cell of the sequence's block e, whose entry in the table is (or was) `id`; -1: none
+    auto block_cell = [&](int64_t e, int32_t id) -> int32_t {
+        return first_of(e >= held && e < fresh ? __ldg(p.free_list + (from_end - e)) : id);
     };
     if (piece == 0) {
         if (tid == 0) {
@@ -124,37 +203,35 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const __grid_consta
             p.offsets[seq + 1] = (int32_t)(end < p.n_tok ? end : p.n_tok);
             p.seq_lens[seq] = (int32_t)after;
         }
-        if (served)
-            for (int64_t j = tid; j < need; j += kThreads) table[held + j] = __ldg(p.free_list + (n_free - 1 - (before + j)));
+        for (int64_t e = held + tid; e < fresh; e += kThreads) table[e] = __ldg(p.free_list + (from_end - e));
     }
-    int32_t* row = p.plan == nullptr ? nullptr : p.plan + (int64_t)seq * p.plan_stride;
     // (the tokens of a sequence that is served all have rows)
     const int64_t there = row0 + n <= p.n_tok ? n : (row0 < p.n_tok ? p.n_tok - row0 : 0);
     for (int64_t t = (int64_t)piece * kThreads + tid; t < there; t += (int64_t)p.pieces * kThreads) {
-        const int32_t cell = served ? cell_at(len + t) : -1;
+        int32_t cell = -1;
+        if (served) {
+            const int64_t e = (len + t) >> shift;
+            cell = block_cell(e, e < held || e >= fresh ? table[e] : -1);   // (not one that is being written)
+            if (cell >= 0) cell += (int32_t)((len + t) & (B - 1));
+        }
         if (p.positions != nullptr) p.positions[row0 + t] = len + t < INT32_MAX ? (int32_t)(len + t) : INT32_MAX;
         p.slots[row0 + t] = cell;
         if (row != nullptr && !p.whole && served) row[len + t] = cell;
     }
-    if (row != nullptr && p.whole) {
-        // (blocks hold a multiple of four cells: four entries that begin at a multiple of four have one
-        // block; a row that does not lie on 16 bytes is written one by one)
-        const bool wide = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
-        for (int64_t i = 4 * ((int64_t)piece * kThreads + tid); i < p.plan_stride; i += 4 * (int64_t)p.pieces * kThreads) {
-            const int32_t first = i < after ? block_cell(i >> shift) : -1;
-            const int32_t c = first < 0 ? -1 : first + (int32_t)(i & (B - 1));
-            int4 e;
-            e.x = c;
-            e.y = c < 0 || i + 1 >= after ? -1 : c + 1;
-            e.z = c < 0 || i + 2 >= after ? -1 : c + 2;
-            e.w = c < 0 || i + 3 >= after ? -1 : c + 3;
-            if (wide && i + 4 <= p.plan_stride) {
-                *reinterpret_cast<int4*>(row + i) = e;
-            } else {
-                row[i] = e.x;
-                if (i + 1 < p.plan_stride) row[i + 1] = e.y;
-                if (i + 2 < p.plan_stride) row[i + 2] = e.z;
-                if (i + 3 < p.plan_stride) row[i + 3] = e.w;
+    if (whole) {
+        const uint32_t last = (uint32_t)after;
+        for (uint32_t i0 = (uint32_t)piece * kPieceEntries; i0 < stride; i0 += (uint32_t)p.pieces * kPieceEntries) {
+            if (i0 != (uint32_t)piece * kPieceEntries) put_known(i0);
+            if (i0 + kPieceEntries <= held_cells || i0 >= most) continue;
+            for (int k = 0; k < kQuads; ++k) {
+                const uint32_t i = quad(i0, k);
+                if (i >= most || i + 4 <= held_cells) continue;
+                const int64_t e = (int64_t)(i >> shift);
+                const int32_t first = i < last ? block_cell(e, e < held || e >= fresh ? table[e] : -1) : -1;
+                const int32_t c = first + (int32_t)(i & in_block);
+                const bool none = first < 0;
+                put4(i, make_int4(none ? -1 : c, none || i + 1 >= last ? -1 : c + 1, none || i + 2 >= last ? -1 : c + 2,
+                                  none || i + 3 >= last ? -1 : c + 3));
             }
         }
     }
@@ -172,7 +249,7 @@ cudaError_t launch_step_maps(const StepMapsParams& p0, cudaStream_t stream, bool
         const int64_t of_plan = (p.plan_stride + kPieceEntries - 1) / kPieceEntries;
         pieces = pieces > of_plan ? pieces : of_plan;
     }
-    pieces = pieces < 1 ? 1 : (pieces > 64 ? 64 : pieces);
+    pieces = pieces < 1 ? 1 : (pieces > kMaxPieces ? kMaxPieces : pieces);
     p.pieces = (int)pieces;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(seqs * pieces), 1, 1);

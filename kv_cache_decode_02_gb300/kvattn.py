@@ -853,17 +853,32 @@ def norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6,
 
 class StepMaps:
     """What :func:`step_maps` makes: int32 ``offsets`` [S + 1], ``seq_lens`` [S], ``positions`` [T],
-    ``slots`` [T] and ``n_free`` [1]."""
-    __slots__ = ("offsets", "seq_lens", "positions", "slots", "n_free")
+    ``slots`` [T] and ``n_free`` [1]; made by :func:`step_maps_buffers`, and written by any number of
+    steps."""
+    __slots__ = ("_all", "_at")
 
-    def __init__(self, offsets, seq_lens, positions, slots, n_free):
-        self.offsets, self.seq_lens, self.positions, self.slots, self.n_free = offsets, seq_lens, positions, slots, n_free
+    def __init__(self, n_seq, n_tok, device):
+        import torch
+        # one allocation; each tensor on 16 bytes
+        counts = (n_seq + 1, n_seq, n_tok, n_tok, 1)
+        room = torch.empty(sum(-(-n // 4) * 4 for n in counts), dtype=torch.int32, device=device)
+        views, at = [], 0
+        for n in counts:
+            views.append(room[at:at + n])
+            at += -(-n // 4) * 4
+        self._all = tuple(views)
+        self._at = (n_seq, n_tok, room.get_device()) + tuple(room.data_ptr() + 4 * x.storage_offset() for x in views)
+
+    offsets = property(lambda self: self._all[0])
+    seq_lens = property(lambda self: self._all[1])
+    positions = property(lambda self: self._all[2])
+    slots = property(lambda self: self._all[3])
+    n_free = property(lambda self: self._all[4])
 
 
 def step_maps_buffers(n_seq, n_tok, device="cuda"):
-    """A StepMaps for steps of at most ``n_tok`` tokens."""
-    import torch
-    return StepMaps(*(torch.empty(n, dtype=torch.int32, device=device) for n in (n_seq + 1, n_seq, n_tok, n_tok, 1)))
+    """A StepMaps for steps of ``n_seq`` sequences and at most ``n_tok`` tokens."""
+    return StepMaps(n_seq, n_tok, device)
 
 
 def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells, n_cells, n_tok=None, plan=None,
@@ -872,41 +887,44 @@ def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells
     cells are taken from the end of ``free_blocks`` (int32, the first ``n_free`` [1] of them free; None:
     nothing is taken) into ``tables`` (int32 [S][stride], in place), and the offsets, lengths, positions
     and slots of ``n_tok`` packed rows follow (rows behind the last token: slot -1).  ``plan`` (int32
-    [S][stride]): the cell plan, whole rows or the new tokens' entries.  ``out``: a StepMaps to write.
-    Returns a StepMaps."""
+    [S][stride]): the cell plan, whole rows or the new tokens' entries.  ``out``: a StepMaps to write
+    (of a step before: its ``seq_lens`` must not be this one's ``lens``, nor its ``n_free``).  Returns a
+    StepMaps."""
     if _torch is None:
         _bind_torch()
-    if out is None and _other_stream(stream):
-        with _made_on(stream):
-            return step_maps(lens, n_new, tables, free_blocks, n_free, block_cells=block_cells, n_cells=n_cells, n_tok=n_tok,
-                             plan=plan, whole_plan=whole_plan, status=status)
-    S = lens.numel()
-    a, b = _ints(lens, "lens", S), _ints(n_new, "n_new", S)
-    d = _here(lens, "lens")
-    if tables.dim() != 2 or tables.shape[0] != S or (plan is not None and (plan.dim() != 2 or plan.shape[0] != S)):
-        raise ValueError("tables, plan: a row for each sequence is wanted")
-    if (free_blocks is None) != (n_free is None):
-        raise ValueError("free_blocks and n_free go together")
     if out is None:
         if n_tok is None:
             raise ValueError("n_tok or out is wanted")
-        out = step_maps_buffers(S, n_tok, lens.device)
-    T = out.slots.numel()
+        if _other_stream(stream):
+            with _made_on(stream):
+                out = StepMaps(lens.numel(), n_tok, lens.device)
+        else:
+            out = StepMaps(lens.numel(), n_tok, lens.device)
+    S, T, d, offsets, seq_lens, positions, slots, left = out._at
     if n_tok is not None and n_tok != T:
         raise ValueError("n_tok: out has other rows")
-    if (n_new.get_device() != d or tables.get_device() != d or _off(free_blocks, d) or _off(n_free, d) or _off(plan, d)
-            or _bad_word(status, d) or out.offsets.get_device() != d or out.seq_lens.get_device() != d
-            or out.positions.get_device() != d or out.slots.get_device() != d or out.n_free.get_device() != d):
-        _elsewhere(d, n_new=n_new, tables=tables, free_blocks=free_blocks, n_free=n_free, plan=plan, status=status,
-                   offsets=out.offsets, seq_lens=out.seq_lens, positions=out.positions, slots=out.slots, out_n_free=out.n_free)
-    take = free_blocks is not None
-    _check(lib.kvattn_step_maps(a, b, S, _ints(tables, "tables"), tables.shape[1], block_cells,
-                                _ints(free_blocks, "free_blocks") if take else None, free_blocks.numel() if take else 0,
-                                _ints(n_free, "n_free", 1) if take else None, n_cells, T, _ints(out.offsets, "offsets", S + 1),
-                                _ints(out.seq_lens, "seq_lens", S), _ints(out.positions, "positions", T),
-                                _ints(out.slots, "slots", T), _ints(out.n_free, "n_free", 1) if take else None,
-                                None if plan is None else _ints(plan, "plan"), 0 if plan is None else plan.shape[1],
-                                1 if whole_plan else 0, _raw(status), _stream(stream)), "kvattn_step_maps")
+    _here(lens, "lens")
+    a, b, tab = _ints(lens, "lens", S), _ints(n_new, "n_new", S), _ints(tables, "tables")
+    shape = tables.shape
+    if len(shape) != 2 or shape[0] != S:
+        raise ValueError("tables: a row for each sequence is wanted")
+    pl, stride, free, count, n_list = None, 0, None, None, 0
+    if plan is not None:
+        pl = _ints(plan, "plan")
+        rows, stride = plan.shape if plan.dim() == 2 else (-1, 0)
+        if rows != S:
+            raise ValueError("plan: a row for each sequence is wanted")
+    if free_blocks is not None and n_free is not None:
+        free, count, n_list = _ints(free_blocks, "free_blocks"), _ints(n_free, "n_free", 1), free_blocks.numel()
+    elif free_blocks is not None or n_free is not None:
+        raise ValueError("free_blocks and n_free go together")
+    else:
+        left = None
+    if (lens.get_device() != d or n_new.get_device() != d or tables.get_device() != d or _off(free_blocks, d)
+            or _off(n_free, d) or _off(plan, d) or (status is not None and _bad_word(status, d))):
+        _elsewhere(d, lens=lens, n_new=n_new, tables=tables, free_blocks=free_blocks, n_free=n_free, plan=plan, status=status)
+    _check(lib.kvattn_step_maps(a, b, S, tab, shape[1], block_cells, free, n_list, count, n_cells, T, offsets, seq_lens, positions,
+                                slots, left, pl, stride, 1 if whole_plan else 0, _raw(status), _stream(stream)), "kvattn_step_maps")
     return out
 
 
