@@ -88,9 +88,11 @@ constexpr int kPlaneBytes = 128 * 128;        // 128 cells (or rows) x 128 bytes
 constexpr int kSlotBytes = 2 * kPlaneBytes;   // 128 cells x 128 dims of f16
 constexpr int kQTileBytes = 2 * kPlaneBytes;  // 128 rows x 128 dims of f16
 constexpr int kMaxSlots = 5;
-constexpr int kHeaderBytes = 3 * 1024;
 constexpr int kRing = 4;                      // pieces of work whose plans are kept
-constexpr int kMasks = 2;                     // tiles whose masks are
+// Tiles whose masks are kept: how far a loader runs ahead of the softmax through a plan.  Quantised rows
+// take longer to come (TMA, then turned), and their header has room.
+template <int MODE, int KBITS>
+constexpr int kMasks = KBITS != 16 ? 4 : (MODE == kShared ? 3 : 2);
 constexpr int kRawStages = 3;                 // quantised: slots of raw bytes in flight
 // Tiles that only some of a unit's (<= 256) tokens see whole: three at their ends; with a window three
 // at its beginnings too, and the one that the first tokens end in.
@@ -108,6 +110,7 @@ template <int KBITS>
 struct Memory {
     static constexpr int kSlots = KBITS == 16 ? 5 : (KBITS == 8 ? 3 : 4);
     static constexpr int kRawBytes = KBITS == 16 ? 0 : 128 * 8 * KBITS * 2 + 1024;  // codes, then scales
+    static constexpr int kHeaderBytes = KBITS == 16 ? 3 * 1024 : 5 * 1024;
     static constexpr int kBytes = 2 * kQTileBytes + kSlots * kSlotBytes + kRawStages * kRawBytes + kHeaderBytes;
     static_assert(kBytes <= 232448, "227 KB");
 };
@@ -141,18 +144,21 @@ template <>
 struct SegOf<kWindow> {
     using type = WindowSeg;
 };
-// Through a plan: what a score's minimum is taken with, +inf, or -inf for a hole.  kWindow, whose
-// header has no room for it in 32 bits: the upper halves of those.
+// Through a plan: what a score's minimum is taken with, +inf, or -inf for a hole.  kWindow and kShared,
+// whose f16 header has no room for it in 32 bits: the upper halves of those.
 template <int MODE>
 struct BiasOf {
     using type = float;
     static __device__ __forceinline__ float of(bool hole) { return hole ? -INFINITY : INFINITY; }
 };
-template <>
-struct BiasOf<kWindow> {
+struct HalfBias {
     using type = uint16_t;
     static __device__ __forceinline__ uint16_t of(bool hole) { return hole ? 0xff80u : 0x7f80u; }
 };
+template <>
+struct BiasOf<kWindow> : HalfBias {};
+template <>
+struct BiasOf<kShared> : HalfBias {};
 
 // f16: a slot that warps 9-11 mend or copy, or the end of a unit.
 struct Job {
@@ -162,7 +168,7 @@ struct Job {
 };
 constexpr uint32_t kJobMend = 0, kJobCopy = 1, kJobUnit = 2, kJobEnd = 3;
 
-template <int MODE>
+template <int MODE, int MASKS>
 struct Header {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t mended[kMaxSlots];  // a V slot that is mended after it landed
@@ -170,20 +176,20 @@ struct Header {
     uint64_t q_full, q_empty;    // the unit's query rows; its last S is complete
     uint64_t s_full[2], p_full[2];  // an S buffer holds S, or p
     uint64_t pv_done[2];         // its P V is complete
-    uint64_t mask_full[kMasks], mask_empty[kMasks];  // through a plan: a tile's bias and holes are written, read
+    uint64_t mask_full[MASKS], mask_empty[MASKS];  // through a plan: a tile's bias and holes are written, read
     uint64_t load_done[kRing];   // every slot of a unit is filled, its bad_cells are complete
     uint64_t seg_full[kRing], seg_empty[kRing];
     uint64_t job_full[kRing], job_empty[kRing];
     uint32_t tmem;
     int abort_flag;
     alignas(16) uint32_t bad_cells[kRing][kCutTiles<MODE>][4];  // of a unit: cells of its cut tiles with V that is not finite
-    uint32_t holes[kMasks];                   // whether the tile has any
+    uint32_t holes[MASKS];                    // whether the tile has any
     uint32_t slot_mend[kMaxSlots];            // whether the slot is one
     uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | unit << 8
     typename SegOf<MODE>::type seg[kRing];
     Job job[kRing];
     float meet[2][128];                       // what two threads of a row tell each other
-    alignas(16) typename BiasOf<MODE>::type bias[kMasks][kPrefillTile];
+    alignas(16) typename BiasOf<MODE>::type bias[MASKS][kPrefillTile];
 };
 
 // Shared-memory matrix descriptor: start address, leading and stride byte offsets, the
@@ -768,6 +774,9 @@ struct Walk {
                     note.n_tok = r.tokens(p);
                     note.start = r.start;
                     note.end = r.end;
+                    note.parts = 1;
+                    while (blockIdx.x + (uint32_t)note.parts < gridDim.x && sh.of(blockIdx.x + (uint32_t)note.parts) < r.end) ++note.parts;
+                    note.unused = 0;
                     const int64_t side = is_prefix<MODE>(p, r.seq) ? p.n_tok : 0;
                     for (int t = threadIdx.x & 31; t < note.n_tok; t += 32)
                         p.notes[(side + note.tok0 + t) * p.n_head_kv + (int)r.g] = note;
@@ -927,10 +936,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     extern __shared__ __align__(1024) unsigned char q_tiles[];
     unsigned char* slots = q_tiles + 2 * kQTileBytes;
     unsigned char* raws = slots + kSlots * kSlotBytes;
-    using Head = Header<MODE>;
+    constexpr int kMaskRing = kMasks<MODE, KBITS>;
+    using Head = Header<MODE, kMaskRing>;
     using Piece = typename SegOf<MODE>::type;
     constexpr int kCut = kCutTiles<MODE>;
-    static_assert(sizeof(Head) <= kHeaderBytes && alignof(Head) == 16, "header");
+    static_assert(sizeof(Head) <= Memory<KBITS>::kHeaderBytes && alignof(Head) == 16, "header");
     Head* h = reinterpret_cast<Head*>(raws + kRawStages * Memory<KBITS>::kRawBytes);
     volatile int* abort_flag = &h->abort_flag;
 
@@ -945,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(smem_addr(&h->empty[i]), 1);              // the MMA lane's commit
             mbar_init(smem_addr(&h->mended[i]), 3);             // warps 9-11
         }
-        for (int i = 0; i < kMasks; ++i) {
+        for (int i = 0; i < kMaskRing; ++i) {
             mbar_init(smem_addr(&h->mask_full[i]), 1);
             mbar_init(smem_addr(&h->mask_empty[i]), 8);
         }
@@ -999,8 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
     // a plan tile's holes, for the softmax (tile number T of the CTA), from one warp
     auto put_mask = [&](const Tile& t, uint32_t T) -> bool {
-        const uint32_t r = T % kMasks;
-        if (T >= kMasks && !wait_all(&h->mask_empty[r], (T / kMasks - 1u) & 1u)) return false;
+        const uint32_t r = T % kMaskRing;
+        if (T >= kMaskRing && !wait_all(&h->mask_empty[r], (T / kMaskRing - 1u) & 1u)) return false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = BiasOf<MODE>::of(t.e[k] < 0);
         if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
@@ -1663,8 +1673,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     if (PLAN && j != masked) {   // (once for both groups, and while S is on its way)
                         const uint32_t t = masks + j;
                         masked = j;
-                        lost = lost || !wait_all(&h->mask_full[t % kMasks], (t / kMasks) & 1u);
-                        holes = h->holes[t % kMasks] != 0u;
+                        lost = lost || !wait_all(&h->mask_full[t % kMaskRing], (t / kMaskRing) & 1u);
+                        holes = h->holes[t % kMaskRing] != 0u;
                     }
                     // (without a vote: the barrier below ORs what a lane lost)
                     lost = lost || !wait_bar(smem_addr(&h->s_full[buf]), par, abort_flag, p.wait_limit_ns);
@@ -1718,11 +1728,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         if (holes) {
                             // the minimum of the score and -inf for a hole, +inf for a cell: a NaN that
                             // stands in a hole goes too (a bit for each cell and a select took longer)
-                            const auto* bias = h->bias[t % kMasks] + 64 * half;
+                            const auto* bias = h->bias[t % kMaskRing] + 64 * half;
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
                                 float4 f;
-                                if constexpr (MODE == kWindow) {
+                                if constexpr (MODE != kPlain) {
                                     const uint2 u = reinterpret_cast<const uint2*>(bias)[c];
                                     f = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
                                                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
@@ -1822,7 +1832,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 }
                 if (PLAN && g == (dual ? 1 : 0)) {   // every warp, for every tile
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[(masks + j) % kMasks]));
+                    if (lane == 0) mbar_arrive(smem_addr(&h->mask_empty[(masks + j) % kMaskRing]));
                 }
             }
             masks += n_max;

@@ -16,11 +16,12 @@ namespace kvattn {
 
 namespace {
 
-// A warp joins a row's parts: lane i of a batch holds part i's weight, the lanes a row's dims.  The
-// maximum runs along from batch to batch.
+// A warp joins a row's parts: lane i of a batch holds the weights of part i over the row's own cells and of
+// part i over the prefix, then the lanes hold the row's dims, with the rows of kBatch parts on their way
+// at once.  The maximum runs along from batch to batch.
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefill_join_kernel(const __grid_constant__ PrefillParams p, int n_ctas) {
-    constexpr int kGroups = Geometry<D>::kGroups, kBatch = 512 / D;
+    constexpr int kGroups = Geometry<D>::kGroups, kBatch = 1536 / D;
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
@@ -29,104 +30,119 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefill_join_kernel(const __
     const int head = (int)(row - tok * p.n_head), G = p.group, g = head / G;
     const int32_t most = (int32_t)p.n_tok;
     const int32_t first = min(max(__ldg(p.offsets), 0), most), last = min(max(__ldg(p.offsets + p.n_seq), 0), most);
-    if (tok < first || tok >= last) return;
     const uint2 join = *p.join;   // the prefix's tiles, the length of the line (0: all units are whole)
+    PrefillNote note[2];          // of the sequence's own cells, of the prefix
+#pragma unroll
+    for (int side = 0; side < 2; ++side) note[side] = p.notes[((int64_t)side * p.n_tok + tok) * p.n_head_kv + g];
+    if (tok < first || tok >= last) return;
     Shares sh;
     sh.set(join.y, (uint32_t)n_ctas);
-    const int sides = join.x != 0u ? 2 : 1;   // the sequence's own cells, the prefix
+    const bool line = join.y != 0u;
+
+    int parts[2], part_row[2];
+    bool whole[2];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        PrefillNote& x = note[side];
+        const bool there = side == 0 || join.x != 0u;
+        // (offsets that decrease leave tokens without a note: what stands there must not lead outside)
+        x.cta = min(max(x.cta, 0), n_ctas - 1);
+        const int t = (int)tok - x.tok0, grp = t / p.group_tokens;
+        part_row[side] = min(max(128 * grp + (t - grp * p.group_tokens) * G + (head - g * G), 0), 128 * kGroups - 1);
+        whole[side] = !line || x.tiles == 0;
+        parts[side] = !there ? 0 : (whole[side] ? 1 : min(max(x.parts, 1), n_ctas - x.cta));
+    }
+    // part i's place: 2 x CTA + (0: what it began with, 1: what it ended with); -1: it holds no tile
+    auto slot_of = [&](int side, int i, bool& all) -> int {
+        if (i >= parts[side]) return -1;
+        const PrefillNote& x = note[side];
+        const uint32_t cta = (uint32_t)(x.cta + i), x0 = sh.of(cta);
+        const uint32_t a = max(x0, x.start), b = min(sh.of(cta + 1u), x.end);
+        const int32_t each = tile_length(p, x.n_tok);
+        const int32_t t0 = tile_at(a - x.start, x.end - x.start, x.tiles, each);
+        const int32_t t1 = tile_at(b - x.start, x.end - x.start, x.tiles, each);
+        all = t0 == 0 && t1 == x.tiles;
+        return t0 == t1 ? -1 : 2 * (int)cta + (x0 > x.start ? 0 : 1);
+    };
 
     float m = -INFINITY, sum = 0.f;
     float acc[D / 32] = {};
-    for (int side = 0; side < sides; ++side) {
-        const int64_t whole_row = (int64_t)side * p.n_tok * p.n_head + row;
-        PrefillNote note = {};
-        int parts = 1, part_row = 0;
-        bool whole = join.y == 0u;
-        if (!whole) {
-            note = p.notes[((int64_t)side * p.n_tok + tok) * p.n_head_kv + g];
-            // (offsets that decrease leave tokens without a note: what stands there must not lead outside)
-            note.cta = min(max(note.cta, 0), n_ctas - 1);
-            while (note.cta + parts < n_ctas && sh.of((uint32_t)(note.cta + parts)) < note.end) ++parts;
-            const int t = (int)tok - note.tok0, grp = t / p.group_tokens;
-            part_row = min(max(128 * grp + (t - grp * p.group_tokens) * G + (head - g * G), 0), 128 * kGroups - 1);
-            whole = note.tiles == 0;
+    for (int i0 = 0; i0 < max(parts[0], parts[1]); i0 += 32) {
+        const float* from[2];
+        float v[2];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            bool all = false;
+            int slot = -1;
+            if (!whole[side]) slot = slot_of(side, i0 + lane, all);
+            if (line && __any_sync(0xffffffffu, all)) {   // one part holds all tiles, and wrote them as a whole unit
+                whole[side] = true;
+                parts[side] = i0 + 1;
+            }
+            v[side] = -INFINITY;
+            from[side] = nullptr;
+            if (whole[side]) {
+                if (lane == 0 && i0 < parts[side]) {
+                    const int64_t at = (int64_t)side * p.n_tok * p.n_head + row;
+                    v[side] = p.whole_lse[at];
+                    from[side] = p.whole_o + at * D;
+                }
+            } else if (slot >= 0) {
+                const int64_t at = (int64_t)slot * kGroups * 128 + part_row[side];
+                v[side] = p.part_lse[at];
+                from[side] = p.part_o + at * D;
+            }
         }
-        // part i's place: 2 x CTA + (0: what it began with, 1: what it ended with); -1: it holds no tile
-        auto slot_of = [&](int i, bool& all) -> int {
-            if (i >= parts) return -1;
-            const uint32_t cta = (uint32_t)(note.cta + i), x0 = sh.of(cta);
-            const uint32_t a = max(x0, note.start), b = min(sh.of(cta + 1u), note.end);
-            const int32_t each = tile_length(p, note.n_tok);
-            const int32_t t0 = tile_at(a - note.start, note.end - note.start, note.tiles, each);
-            const int32_t t1 = tile_at(b - note.start, note.end - note.start, note.tiles, each);
-            all = t0 == 0 && t1 == note.tiles;
-            return t0 == t1 ? -1 : 2 * (int)cta + (x0 > note.start ? 0 : 1);
-        };
-        if (!whole)   // (one part may hold all tiles, and wrote them as a whole unit)
-            for (int i0 = 0; i0 < parts; i0 += 32) {
-                bool all = false;
-                slot_of(i0 + lane, all);
-                whole = whole || __any_sync(0xffffffffu, all);
+        float top = v[1] > v[0] || v[1] != v[1] ? v[1] : v[0];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float w = __shfl_xor_sync(0xffffffffu, top, o);
+            top = w > top || w != w ? w : top;   // (a NaN stays)
+        }
+        if (top == -INFINITY) continue;          // (no part with a cell: its O was not written)
+        if (!(m >= top)) {                       // (a NaN too)
+            const float old = m == -INFINITY ? 0.f : exp2f((m - top) * 1.4426950408889634f);
+            sum *= old;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) acc[k] *= old;
+            m = top;
+        }
+        float w[2];
+        uint32_t left[2];
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            w[side] = v[side] == -INFINITY ? 0.f : exp2f((v[side] - m) * 1.4426950408889634f);
+            sum += w[side];                      // (this lane's parts)
+            left[side] = __ballot_sync(0xffffffffu, v[side] != -INFINITY);
+        }
+        while ((left[0] | left[1]) != 0u) {
+            float4 f[kBatch][D / 128];
+            float wk[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const bool second = left[0] == 0u, in = (left[0] | left[1]) != 0u;
+                const uint32_t bits = second ? left[1] : left[0];
+                const int i = in ? __ffs(bits) - 1 : 0;
+                if (second)
+                    left[1] &= left[1] - 1u;
+                else
+                    left[0] &= left[0] - 1u;
+                wk[b] = __shfl_sync(0xffffffffu, second ? w[1] : w[0], i);
+                const float4* o = reinterpret_cast<const float4*>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(second ? from[1] : from[0]), i));
+#pragma unroll
+                for (int k = 0; k < D / 128; ++k) f[b][k] = in ? o[32 * k + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!in) wk[b] = 0.f;
             }
-        if (whole) parts = 1;
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            float v = -INFINITY;
-            const float* from = nullptr;
-            if (whole) {
-                if (lane == 0) {
-                    v = p.whole_lse[whole_row];
-                    from = p.whole_o + whole_row * D;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                for (int k = 0; k < D / 128; ++k) {
+                    acc[4 * k] += wk[b] * f[b][k].x;
+                    acc[4 * k + 1] += wk[b] * f[b][k].y;
+                    acc[4 * k + 2] += wk[b] * f[b][k].z;
+                    acc[4 * k + 3] += wk[b] * f[b][k].w;
                 }
-            } else {
-                bool all;
-                const int slot = slot_of(i0 + lane, all);
-                if (slot >= 0) {
-                    const int64_t at = (int64_t)slot * kGroups * 128 + part_row;
-                    v = p.part_lse[at];
-                    from = p.part_o + at * D;
-                }
-            }
-            float top = v;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float w = __shfl_xor_sync(0xffffffffu, top, o);
-                top = w > top || w != w ? w : top;   // (a NaN stays)
-            }
-            if (top == -INFINITY) continue;          // (no part with a cell: its O was not written)
-            if (!(m >= top)) {                       // (a NaN too)
-                const float old = m == -INFINITY ? 0.f : exp2f((m - top) * 1.4426950408889634f);
-                sum *= old;
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) acc[k] *= old;
-                m = top;
-            }
-            const float w = v == -INFINITY ? 0.f : exp2f((v - m) * 1.4426950408889634f);
-            sum += w;                                // (this lane's parts)
-            uint32_t left = __ballot_sync(0xffffffffu, v != -INFINITY);
-            while (left != 0u) {
-                float4 f[kBatch][D / 128];
-                float wk[kBatch];
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const bool in = left != 0u;
-                    const int i = in ? __ffs(left) - 1 : 0;
-                    wk[b] = __shfl_sync(0xffffffffu, w, i);
-                    const float4* o = reinterpret_cast<const float4*>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), i));
-                    left &= left - 1u;
-#pragma unroll
-                    for (int k = 0; k < D / 128; ++k) f[b][k] = in ? o[32 * k + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-                    for (int k = 0; k < D / 128; ++k) {
-                        acc[4 * k] += wk[b] * f[b][k].x;
-                        acc[4 * k + 1] += wk[b] * f[b][k].y;
-                        acc[4 * k + 2] += wk[b] * f[b][k].z;
-                        acc[4 * k + 3] += wk[b] * f[b][k].w;
-                    }
-            }
         }
     }
 #pragma unroll

@@ -78,6 +78,7 @@ struct PrefillCut {          // a work unit that the shares cut (n_parts > 0), n
 struct PrefillNote {         // shared prefix: a work unit, noted for each of its tokens by the CTA that began it
     int32_t cta, tiles, tok0, n_tok;
     uint32_t start, end;     // its part of the line
+    int32_t parts, unused;   // CTAs whose shares it meets
 };
 struct PrefillParams {
     // use_tma: f16 rows (encode_planes_map), or codes (encode_codes_map), boxes of 128 dims x 128

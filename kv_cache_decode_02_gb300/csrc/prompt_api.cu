@@ -145,7 +145,7 @@ int launch_attention(Form form, PrefillParams& p, const void* q, int64_t q_strid
     p.group_tokens = 128 / p.group;
     p.block_tokens = p.group_tokens * prefill_groups(head_dim);
     p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-    p.single_length = kv_type == KVATTN_KV_F16 && head_dim == 128 && p.plan == nullptr ? 5 : 8;
+    p.single_length = kv_type == KVATTN_KV_F16 && head_dim == 128 && (p.plan == nullptr || form == Form::shared) ? 5 : 8;
     p.shares = shares ? 1 : 0;
     p.out_sectors = aligned(p.out, 32) ? 1 : 0;
     debug_waits(&p.wait_limit_ns, &p.stall_tx);
