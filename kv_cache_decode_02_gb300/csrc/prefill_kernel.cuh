@@ -31,8 +31,8 @@
 //  * loader (warps 8-11): fills a ring of 32 KB slots, each 128 cells x 128 dims of K or V in
 //    two 128-byte-swizzled planes.  f16: warp 8 issues a TMA box for each slot whose cells are
 //    one physical run (holes and the end of a sequence included); warps 9-11 mend V slots that
-//    need it afterwards, and copy the slots of tiles that are no run.  Quantised: warp 14 brings codes (TMA) and
-//    scales (cp.async) into a ring of raw bytes, and these four turn them into f16.
+//    need it afterwards, and copy the slots of tiles that are no run.  Quantised: warps 14 and 15 bring the codes (TMA)
+//    and scales (cp.async) of K and of V into a ring of raw bytes, and these four turn them into f16.
 //  * MMA (warp 12): one elected lane issues tcgen05.mma.  The 512 TMEM columns hold two buffers
 //    of S, over which p is written, and O (2 x 128 columns, or 256).  With both row groups at
 //    work each has a buffer, and a group's products run under the other's softmax; with one (256,
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(smem_addr(&h->job_full[i]), 1);
             mbar_init(smem_addr(&h->job_empty[i]), 3);
             mbar_init(smem_addr(&h->seg_full[i]), 1);
-            mbar_init(smem_addr(&h->seg_empty[i]), (kQuant ? 2 : 5) + 8);  // loader, MMA and softmax warps
+            mbar_init(smem_addr(&h->seg_empty[i]), (kQuant ? 3 : 5) + 8);  // loader, MMA and softmax warps
         }
         h->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1142,24 +1142,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 unsigned char* cells = plane + 4096 * k4;
                                 // (all loads first, and one test: stores in between would make each wait for the
                                 // one before, 4000 clocks a slot)
-                                uint4 w[6];
-                                uint32_t wild = 0;
-#pragma unroll
-                                for (int q = 0; q < 6; ++q) {
-                                    const int c = min(2 * (3 * q + warp - 9), 30) + sub;   // (the last one twice)
-                                    w[q] = make_uint4(0u, 0u, 0u, 0u);
-                                    if (look && !((gone >> c) & 1u)) w[q] = *reinterpret_cast<const uint4*>(cells + swz(c, b & 127));
-                                    wild |= (uint32_t)!finite8(w[q]) << q;
-                                }
-                                if (__any_sync(0xffffffffu, wild != 0u)) {
+                                if (look) {
+                                    uint4 w[6];
+                                    uint32_t wild = 0;
 #pragma unroll
                                     for (int q = 0; q < 6; ++q) {
-                                        const int c = min(2 * (3 * q + warp - 9), 30) + sub;
-                                        if (!((wild >> q) & 1u)) continue;
-                                        bool bad;
-                                        *reinterpret_cast<uint4*>(cells + swz(c, b & 127)) =
-                                            make_uint4(finite2(w[q].x, bad), finite2(w[q].y, bad), finite2(w[q].z, bad), finite2(w[q].w, bad));
-                                        atomicOr(&bad_row[k4], 1u << c);
+                                        const int c = min(2 * (3 * q + warp - 9), 30) + sub;   // (the last one twice)
+                                        w[q] = *reinterpret_cast<const uint4*>(cells + swz(c, b & 127));
+                                    }
+#pragma unroll
+                                    for (int q = 0; q < 6; ++q) wild |= (uint32_t)!finite8(w[q]) << q;
+                                    if (__any_sync(0xffffffffu, wild != 0u)) {
+#pragma unroll
+                                        for (int q = 0; q < 6; ++q) {
+                                            const int c = min(2 * (3 * q + warp - 9), 30) + sub;
+                                            if (!((wild >> q) & 1u) || ((gone >> c) & 1u)) continue;
+                                            bool bad;
+                                            *reinterpret_cast<uint4*>(cells + swz(c, b & 127)) =
+                                                make_uint4(finite2(w[q].x, bad), finite2(w[q].y, bad), finite2(w[q].z, bad), finite2(w[q].w, bad));
+                                            atomicOr(&bad_row[k4], 1u << c);
+                                        }
                                     }
                                 }
                                 if (gone != 0u) {
@@ -1206,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 }
             }
         } else {
-            // ---- quantised: turns the raw slots that warp 14 brings ----
+            // ---- quantised: turns the raw slots that warps 14 and 15 bring ----
             for (;; ++n) {
                 const uint32_t r = n % kRawStages;
                 // (both waits with one vote: a word that was read after a lost one is not used)
@@ -1360,8 +1362,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     __syncwarp();
                 }
             }
-        } else if (kQuant && warp == 14) {
+        } else if (kQuant && warp >= 14) {
             // ------------------------------- raw bytes, quantised -------------------------------
+            // Warp 14 brings K, warp 15 V: one for both took 1900 clocks a slot of its own
+            // instructions, more than the slot's turning.  Both count, and wait for the stage of, every
+            // slot: a warp that left the other's out could meet a stage's barrier a phase behind.
+            const bool v_warp = warp == 15;
             uint32_t ahead = 0, T = 0;    // slots brought, tiles begun
             bool bad_entry = false, ok = true;
             Piece s = {};
@@ -1377,6 +1383,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             };
             auto bring = [&](const Tile& t, bool v_side, int half, uint32_t word) {
                 if (!(ok = stage_free())) return;
+                if (v_side != v_warp) {
+                    ++ahead;
+                    return;
+                }
                 const int bits = v_side ? VBITS : KBITS;
                 const uint32_t bar = smem_addr(&h->raw_full[ahead % kRawStages]);
                 const uint32_t stage = smem_addr(raws + (ahead % kRawStages) * Memory<KBITS>::kRawBytes);
@@ -1398,13 +1408,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 }
                 // scales: a cell's four blocks; zeros where there is no cell, so that whatever its
                 // codes are it stands for zeros
-                const __half* scales = (v_side ? p.v_scale : p.k_scale) + half * 4;
+                const int row = p.n_head_kv * (D / 32);
+                const __half* scales = (v_side ? p.v_scale : p.k_scale) + half * 4 + s.g * (D / 32) + (PLAN ? 0 : t.base * row);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t dst = stage + Memory<KBITS>::kRawBytes - 1024 + 8 * (32 * k + lane);
-                    const int64_t cell = !PLAN ? t.base + t.e[k] : t.e[k];
                     if (t.e[k] >= 0)
-                        cp_async_8(dst, scales + (cell * Hk + s.g) * (D / 32));
+                        cp_async_8(dst, scales + (int64_t)t.e[k] * row);
                     else
                         asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
                 }
@@ -1416,7 +1426,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
                 const uint32_t unit = (i & 0xffffu) << 8;
                 if (n_max == 0) {    // (the turning warps still sign the unit off)
-                    if ((ok = stage_free())) publish(unit | 12u);
+                    if ((ok = stage_free())) {
+                        if (v_warp)
+                            ++ahead;
+                        else
+                            publish(unit | 12u);
+                    }
                     give_back(i);
                     continue;
                 }
@@ -1433,7 +1448,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             next = read_tile<MODE, PLAN>(p, s, j + 1);
                         }
                         if (!settle<PLAN>(p, tk)) bad_entry = true;
-                        if (PLAN && !(ok = put_mask(tk, T))) break;
+                        if (PLAN && !v_warp && !(ok = put_mask(tk, T))) break;
                         ++T;
                     }
                     if (v_side && (s.n[1] > 0 || j + 1 == n_max)) tv = tk;
@@ -1444,7 +1459,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 }
                 give_back(i);
             }
-            if (ok && stage_free()) publish(kNoMore);
+            if (ok && !v_warp && stage_free()) publish(kNoMore);
             asm volatile("cp.async.wait_all;" ::: "memory");
             if (__any_sync(0xffffffffu, bad_entry) && lane == 0) atomicOr(p.status, KVATTN_DEVICE_BAD_PLAN_ENTRY);
         } else if (warp == 12) {
