@@ -105,11 +105,11 @@ constexpr uint32_t kNoMore = 0xffffffffu;
 constexpr int kUnitCost = 2;                  // a unit's fixed cost in tiles, for the equal shares
 
 // f16 slots in the ring: what the 227 KB hold beside the queries (64 KB) and, for quantised
-// caches, the raw ring (17 KB a stage with 8-bit rows, 9 KB with 4-bit ones)
+// caches, the raw ring (18 KB a stage with 8-bit rows, 10 KB with 4-bit ones)
 template <int KBITS>
 struct Memory {
     static constexpr int kSlots = KBITS == 16 ? 5 : (KBITS == 8 ? 3 : 4);
-    static constexpr int kRawBytes = KBITS == 16 ? 0 : 128 * 8 * KBITS * 2 + 1024;  // codes, then scales
+    static constexpr int kRawBytes = KBITS == 16 ? 0 : 128 * 8 * KBITS * 2 + 2048;  // codes, then scales (eight a cell)
     static constexpr int kHeaderBytes = KBITS == 16 ? 3 * 1024 : 5 * 1024;
     static constexpr int kBytes = 2 * kQTileBytes + kSlots * kSlotBytes + kRawStages * kRawBytes + kHeaderBytes;
     static_assert(kBytes <= 232448, "227 KB");
@@ -185,7 +185,7 @@ struct Header {
     alignas(16) uint32_t bad_cells[kRing][kCutTiles<MODE>][4];  // of a unit: cells of its cut tiles with V that is not finite
     uint32_t holes[MASKS];                    // whether the tile has any
     uint32_t slot_mend[kMaxSlots];            // whether the slot is one
-    uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | unit << 8
+    uint32_t raw_word[kRawStages];  // of a raw slot: V, cut, its unit's last, no slot at all | cut tile << 4 | upper scales << 7 | unit << 8
     typename SegOf<MODE>::type seg[kRing];
     Job job[kRing];
     float meet[2][128];                       // what two threads of a row tell each other
@@ -271,6 +271,13 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
         "{%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_box2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_box4(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
@@ -1011,8 +1018,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     auto put_mask = [&](const Tile& t, uint32_t T) -> bool {
         const uint32_t r = T % kMaskRing;
         if (T >= kMaskRing && !wait_all(&h->mask_empty[r], (T / kMaskRing - 1u) & 1u)) return false;
+        if (t.holes)   // (else nobody looks)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = BiasOf<MODE>::of(t.e[k] < 0);
+            for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = BiasOf<MODE>::of(t.e[k] < 0);
         if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
@@ -1224,7 +1232,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     stall_hook(&h->full[filled % kSlots]);
                     const int bits = v_side ? VBITS : KBITS;
                     const unsigned char* stage = raws + r * Memory<KBITS>::kRawBytes;
-                    const unsigned short* scales = reinterpret_cast<const unsigned short*>(stage + Memory<KBITS>::kRawBytes - 1024);
+                    const unsigned short* scales = reinterpret_cast<const unsigned short*>(stage + Memory<KBITS>::kRawBytes - 2048) +
+                                                   ((word >> 7) & 1u) * 4u;
                     unsigned char* slot = slots + (filled % kSlots) * kSlotBytes;
                     uint32_t* bad_row = h->bad_cells[unit % kRing][(word >> 4) & 7u];
                     if (bits == 8) {
@@ -1237,7 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         unsigned char* d0 = plane + (upper ? ob : oa);
                         unsigned char* d1 = plane + (upper ? oa : ob);
                         const unsigned char* src = stage + 16 * lt;
-                        const unsigned short* sc = scales + 4 * c0 + (piece >> 1);
+                        const unsigned short* sc = scales + 8 * c0 + (piece >> 1);
                         // four cells at a time, loads first: the stores cannot be seen not to alias them
 #pragma unroll 1
                         for (int k0 = 0; k0 < 8; k0 += 4) {
@@ -1246,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 w[k] = *reinterpret_cast<const uint4*>(src + 2048 * (k0 + k));
-                                ds[k] = sc[64 * (k0 + k)];
+                                ds[k] = sc[128 * (k0 + k)];
                                 big = max(big, ds[k]);   // (a negative one, which no write makes, counts as big)
                             }
                             // (a code is finite, and so is its product with a scale that is not big)
@@ -1268,8 +1277,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             if (odd)
 #pragma unroll 1
                                 for (int k = k0; k < k0 + 4; ++k) {
-                                    amend(d0 + 2048 * k, sc[64 * k], cut, bad_row, c0 + 16 * k);
-                                    amend(d1 + 2048 * k, sc[64 * k], cut, bad_row, c0 + 16 * k);
+                                    amend(d0 + 2048 * k, sc[128 * k], cut, bad_row, c0 + 16 * k);
+                                    amend(d1 + 2048 * k, sc[128 * k], cut, bad_row, c0 + 16 * k);
                                 }
                         }
                     } else {
@@ -1284,7 +1293,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 w[k] = *reinterpret_cast<const uint4*>(stage + 16 * lt + 2048 * (k0 + k));
-                                ds[k] = scales[4 * c0 + piece + 128 * (k0 + k)];
+                                ds[k] = scales[8 * c0 + piece + 256 * (k0 + k)];
                                 big = max(big, ds[k] & 0x7fffu);
                             }
                             const bool odd = big > kBigScale;
@@ -1310,7 +1319,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll 1
                                 for (int i = 0; i < 8; ++i)
                                     amend(plane + swz(c0, b + 16 * (i & 3)) + 4096 * (k0 + (i >> 2)),
-                                          scales[4 * c0 + piece + 128 * (k0 + (i >> 2))], cut, bad_row, c0 + 32 * (k0 + (i >> 2)));
+                                          scales[8 * c0 + piece + 256 * (k0 + (i >> 2))], cut, bad_row, c0 + 32 * (k0 + (i >> 2)));
                         }
                     }
                     fence_async();
@@ -1391,9 +1400,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const uint32_t bar = smem_addr(&h->raw_full[ahead % kRawStages]);
                 const uint32_t stage = smem_addr(raws + (ahead % kRawStages) * Memory<KBITS>::kRawBytes);
                 const int64_t Hk = p.n_head_kv;
+                // A cell's four scales are 8 bytes, half of what TMA moves at least: a box brings eight,
+                // of two KV heads at head_dim 128, and the slot's word says which four.  (A cp.async for
+                // each cell took 600 of the warp's clocks.)  Tiles with holes keep to those.
+                const int scale0 = s.g * (D / 32) + half * 4;
+                const bool scale_box = t.run && !t.holes && p.scl_tma != 0;
                 if (t.run && p.use_tma != 0) {
                     if (lane == 0) {
-                        mbar_expect_tx(bar, 128u * 16u * (uint32_t)bits);
+                        mbar_expect_tx(bar, 128u * 16u * (uint32_t)bits + (scale_box ? 2048u : 0u));
+                        if (scale_box)
+                            tma_box2(stage + Memory<KBITS>::kRawBytes - 2048, v_side ? &p.tmap_vs : &p.tmap_ks, scale0 & ~7,
+                                     (int)t.base, bar);
                         tma_box(stage, v_side ? &p.tmap_v : &p.tmap_k, half * 16 * bits, s.g, (int)t.base, bar);
                     }
                 } else {   // 16-byte pieces of the cells' 128 dims, `bits` a cell
@@ -1406,19 +1423,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             cp_async_16_cg(stage + 16 * i, rows + (cell * Hk + s.g) * (D * bits / 8) + half * 16 * bits + 16 * piece);
                     }
                 }
-                // scales: a cell's four blocks; zeros where there is no cell, so that whatever its
-                // codes are it stands for zeros
-                const int row = p.n_head_kv * (D / 32);
-                const __half* scales = (v_side ? p.v_scale : p.k_scale) + half * 4 + s.g * (D / 32) + (PLAN ? 0 : t.base * row);
+                if (!scale_box) {
+                    // a cell's four blocks; zeros where there is no cell, so that whatever its codes are
+                    // it stands for zeros
+                    const int row = p.n_head_kv * (D / 32);
+                    const __half* scales = (v_side ? p.v_scale : p.k_scale) + scale0 + (PLAN ? 0 : t.base * row);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t dst = stage + Memory<KBITS>::kRawBytes - 1024 + 8 * (32 * k + lane);
-                    if (t.e[k] >= 0)
-                        cp_async_8(dst, scales + (int64_t)t.e[k] * row);
-                    else
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t dst = stage + Memory<KBITS>::kRawBytes - 2048 + 16 * (32 * k + lane) + 2 * (scale0 & 4);
+                        if (t.e[k] >= 0)
+                            cp_async_8(dst, scales + (int64_t)t.e[k] * row);
+                        else
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
+                    }
+                    fence_async();   // (a box may bring the next slot's)
+                    cp_async_arrive(bar);
                 }
-                cp_async_arrive(bar);
+                word |= (scale0 & 4) ? 128u : 0u;
                 publish(word);
             };
             for (uint32_t i = 0; ok; ++i) {

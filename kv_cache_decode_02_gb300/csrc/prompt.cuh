@@ -84,6 +84,7 @@ struct PrefillParams {
     // use_tma: f16 rows (encode_planes_map), or codes (encode_codes_map), boxes of 128 dims x 128
     // cells
     CUtensorMap tmap_k, tmap_v;
+    CUtensorMap tmap_ks, tmap_vs;   // scl_tma: quantised caches' scales (encode_scale_tensor_map), boxes of 8 x 128 cells
     CUtensorMap tmap_q;       // 3-D {head_dim, heads, tokens}, boxes {64, group, group_tokens}
     const void* k;            // f16: rows k_stride elements apart; quantised: dense planes
     const void* v;
@@ -114,6 +115,7 @@ struct PrefillParams {
     int single_length;        // of a tile for one row group in the line of shares, in eighths of one for all
     int shares;               // 1: equal shares of all units' tiles, cut anywhere; 0: whole units
     int use_tma;
+    int scl_tma;
     int out_sectors;          // out is 32-byte aligned
     int window_tiles;         // tiles that a unit's windows and first tokens meet, at most
     float scale_log2;         // scale * log2(e)

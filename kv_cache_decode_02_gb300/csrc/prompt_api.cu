@@ -157,8 +157,11 @@ int launch_attention(Form form, PrefillParams& p, const void* q, int64_t q_strid
         const int kb = kv_type == KVATTN_KV_Q4_0 ? 4 : 8, vb = kv_type == KVATTN_KV_Q8_0 ? 8 : 4;
         p.use_tma = encode_codes_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim * kb / 8, 16 * kb, kPrefillTile) &&
                     encode_codes_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim * vb / 8, 16 * vb, kPrefillTile);
+        p.scl_tma = p.use_tma != 0 && rows <= (int64_t)INT32_MAX &&
+                    encode_scale_tensor_map(&p.tmap_ks, p.k_scale, rows, n_head_kv, head_dim, kPrefillTile) &&
+                    encode_scale_tensor_map(&p.tmap_vs, p.v_scale, rows, n_head_kv, head_dim, kPrefillTile);
     }
-    if (!tma_enabled()) p.use_tma = 0;
+    if (!tma_enabled()) p.use_tma = p.scl_tma = 0;
     if (log_enabled()) {
         char buf[256];
         std::snprintf(buf, sizeof(buf), "%s kv_type=%d n_seq=%d n_tok=%lld n_head=%d/%d head_dim=%d plan=%d shares=%d grid=%d tma=%d",
