@@ -11,7 +11,9 @@
 //
 // Bound: bytes.  A lane holds 16 elements of a head (its 8 pairs, or 16 elements that are not
 // turned), 8 or 16 lanes a head, which sum their squares in three or four shuffles; a warp keeps one
-// token's cosines and sines and both sides' weights in registers and walks the heads of q and k.
+// token's cosines and sines and a side's weights in registers and walks the heads of q and k.  16384
+// tokens of 16 / 8 heads of 256, 64 turned (403 MB): 67 us, 90 % of the measured copy rate; 8192 tokens
+// of 32 / 8 heads of 128 by three axes, not normed (168 MB): 27.5 us, 91 %; 64 tokens 3.4 us in a graph.
 #include <cstdint>
 
 #include "prompt.cuh"
@@ -20,6 +22,10 @@ namespace kvattn {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kBlocksPerSm = 8;    // 64 registers: 67 us for the prompt below, 72 without the bound, 92 at ten
+// A token is split among warps until there are this many for an SM: 8192 tokens of 32 / 8 heads of 128
+// 28.0 us at 16, 27.5 at 64, 31.5 at 128 (every warp makes the token's angles).
+constexpr int kWarpsPerSm = 64;
 
 __device__ __forceinline__ void unpack8(const uint4& w, float* x) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -33,15 +39,12 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* x) {
 __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
 }
-__device__ __forceinline__ uint4 pick(bool second, const uint4& a, const uint4& b) {
-    return make_uint4(second ? b.x : a.x, second ? b.y : a.y, second ? b.z : a.z, second ? b.w : a.w);
-}
 
 // A warp serves one token and the groups of 512 / D heads [part, +parts, ...): lane l holds the
 // elements of piece l % (D / 16) of head l / (D / 16) of a group.  Every lane stays to the end (heads
 // meet in shuffles); a lane whose group ends before it repeats the last head and stores nothing.
 template <int D, bool INTERLEAVED, bool NORM>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int parts) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int parts) {
     constexpr int kPieces = D / 16, kHeads = 32 / kPieces;
     pdl_wait();
     const int lane = threadIdx.x & 31;
@@ -75,15 +78,19 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     int base = part * kHeads;
     if (base >= total) return;
     load(base);
-    uint4 wt[2][2] = {};
-    if (NORM) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-            if (p.weight[s] != nullptr) {
-                wt[s][0] = __ldg(reinterpret_cast<const uint4*>(p.weight[s] + e0));
-                wt[s][1] = __ldg(reinterpret_cast<const uint4*>(p.weight[s] + e1));
-            }
-    }
+    // the weights of the side that the lane is at (a head's side changes once, from q to k)
+    uint4 w0 = {}, w1 = {};
+    bool normed = false, second = false;
+    auto weights = [&](bool k) {
+        second = k;
+        const __half* at = p.weight[k ? 1 : 0];
+        normed = at != nullptr;
+        if (normed) {
+            w0 = __ldg(reinterpret_cast<const uint4*>(at + e0));
+            w1 = __ldg(reinterpret_cast<const uint4*>(at + e1));
+        }
+    };
+    if (NORM) weights(side[0]);
     float cs[8], sn[8];
     if (turned) {
         int32_t pos[kMaxAxes];
@@ -121,13 +128,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
                 float all = sum[0] + sum[1];
 #pragma unroll
                 for (int o = 1; o < kPieces; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-                if (p.weight[side[u] ? 1 : 0] != nullptr) {
+                if (side[u] != second) weights(side[u]);
+                if (normed) {
                     const float r = rsqrtf(fmaf(all, 1.f / D, p.eps));
-                    float g[16];
-                    unpack8(pick(side[u], wt[0][0], wt[1][0]), g);
-                    unpack8(pick(side[u], wt[0][1], wt[1][1]), g + 8);
+                    float g[8];
+                    unpack8(w0, g);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] *= r * g[i];
+                    for (int i = 0; i < 8; ++i) f[i] *= r * g[i];
+                    unpack8(w1, g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[8 + i] *= r * g[i];
                 }
             }
             if (turned) {
@@ -166,9 +176,8 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int sms, cudaStream_t stre
     const RopeParams& r = p.r;
     const int heads_per_warp = 512 / r.head_dim;
     const int groups = (r.n_head[0] + r.n_head[1] + heads_per_warp - 1) / heads_per_warp;
-    // Warps per token: as rope.cu (one walks all heads when the tokens alone fill the device).
     int parts = 1;
-    while (2 * parts < groups && r.n_tok * parts < (int64_t)sms * 16) parts *= 2;
+    while (2 * parts < groups && r.n_tok * parts < (int64_t)sms * kWarpsPerSm) parts *= 2;
     const int64_t warps = r.n_tok * parts;
     const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;

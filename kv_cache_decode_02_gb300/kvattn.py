@@ -800,6 +800,12 @@ def rope(q, k, positions, table, *, layout="half", q_out=None, k_out=None, strea
     return q_out if q is not None else None, k_out if k is not None else None
 
 
+def _weight(w, name, n):
+    if w.dtype is not _F16 or w.numel() != n or not w.is_contiguous():
+        raise ValueError(f"{name}: contiguous half of head_dim values is wanted")
+    return w.data_ptr()
+
+
 def norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, layout="half", q_out=None, k_out=None,
               stream=None):
     """:func:`rope` of heads that are normed first, in the same pass: ``q_weight`` / ``k_weight`` half
@@ -832,21 +838,24 @@ def norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6,
             raise ValueError("k, k_out: shapes do not agree")
         T, D = t, d
         ka = (k.data_ptr(), st, h, k_out.data_ptr(), so)
-    at, turns, axis, n_axes = _ints(positions, "positions", T * table.n_axes), table.turns, table.axis, table.n_axes
+    turns, axis, n_axes, n_rot = table.turns, table.axis, table.n_axes, table.n_rot
+    at = _ints(positions, "positions", T * n_axes)
     d = _here(k if q is None else q, "k" if q is None else "q")
     if (positions.get_device() != d or turns.get_device() != d or _off(k, d) or _off(q_out, d) or _off(k_out, d)
             or _off(q_weight, d) or _off(k_weight, d) or _off(axis, d)):
         _elsewhere(d, k=k, positions=positions, table=turns, axis=axis, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
                    k_out=k_out)
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype is not _F16 or w.numel() != D or not w.is_contiguous()):
-            raise ValueError("q_weight, k_weight: contiguous half of head_dim values is wanted")
-    if turns.numel() * 2 < table.n_rot or turns.element_size() != 8 or not turns.is_contiguous():
+    qw = kw = None
+    if q_weight is not None:
+        qw = _weight(q_weight, "q_weight", D)
+    if k_weight is not None:
+        kw = _weight(k_weight, "k_weight", D)
+    if turns.numel() * 2 < n_rot or turns.element_size() != 8 or not turns.is_contiguous():
         raise ValueError("table: n_rot / 2 contiguous 64-bit angles are wanted")
-    if n_axes > 1 and (axis is None or axis.numel() * 2 < table.n_rot or axis.element_size() != 1 or not axis.is_contiguous()):
+    if n_axes > 1 and (axis is None or axis.numel() * 2 < n_rot or axis.element_size() != 1 or not axis.is_contiguous()):
         raise ValueError("table: n_rot / 2 contiguous 8-bit axes are wanted")
-    _check(lib.kvattn_norm_rope(qa[0], qa[1], qa[2], _raw(q_weight), ka[0], ka[1], ka[2], _raw(k_weight), eps, at, T, n_axes,
-                                _raw(axis), turns.data_ptr(), table.gain, table.n_rot, code, T, D, qa[3], qa[4], ka[3], ka[4],
+    _check(lib.kvattn_norm_rope(qa[0], qa[1], qa[2], qw, ka[0], ka[1], ka[2], kw, eps, at, T, n_axes,
+                                _raw(axis), turns.data_ptr(), table.gain, n_rot, code, T, D, qa[3], qa[4], ka[3], ka[4],
                                 _stream(stream)), "kvattn_norm_rope")
     return q_out if q is not None else None, k_out if k is not None else None
 
