@@ -289,12 +289,12 @@ bool kvattn::encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows
 }
 
 bool kvattn::encode_planes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int head_dim,
-                               int64_t row_stride) {
+                               int64_t row_stride, int box_rows, int box_planes) {
     EncodeTiledFn enc = tensor_map_encoder();
     if (enc == nullptr || rows < 1 || rows > (int64_t)INT32_MAX || !aligned(base, 16)) return false;
     const cuuint64_t dims[4] = {64u, (cuuint64_t)rows, (cuuint64_t)head_dim / 64, (cuuint64_t)n_head_kv};
     const cuuint64_t strides[3] = {(cuuint64_t)row_stride * 2, 128u, (cuuint64_t)head_dim * 2};
-    const cuuint32_t box[4] = {64u, (cuuint32_t)kPrefillTile, 2u, 1u};
+    const cuuint32_t box[4] = {64u, (cuuint32_t)box_rows, (cuuint32_t)box_planes, 1u};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

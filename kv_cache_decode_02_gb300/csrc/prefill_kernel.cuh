@@ -128,11 +128,12 @@ struct Seg {
     int part;            // partial slot, or -1: the whole unit
     int whole, turn;     // the first `whole` tiles, which every row sees whole, are taken from tile `turn` on
 };
-// With a window: tile number x of a unit is tile x of the sequence up to `front`, x + gap behind it.
+// With a window: places [0, front) of a unit are the sequence's first cells, the ones behind them lie
+// `gap` cells further on (len, lim0 and what follows count places).
 struct WindowSeg : Seg {
     int front, gap;
-    int cut0, cut1;      // tiles (from j0) at the beginnings of the rows' windows, some of whose cells some row does not see
-    long long low_last;  // first cell of the last token's window
+    int cut0, cut1;      // tiles (from j0) at the beginnings of the rows' windows, some of whose places some row does not see
+    long long low_last;  // first place of the last token's window
 };
 // With a shared prefix a piece of the prefix, all of whose cells all rows see, has this lim0.
 constexpr long long kNoLimit = 1ll << 40;
@@ -475,16 +476,22 @@ __device__ __forceinline__ int32_t tiles_seen(int64_t lim0, int32_t n) {
     return lim > 0 ? (int32_t)((lim + kPrefillTile - 1) / kPrefillTile) : 0;
 }
 
-// kWindow: tiles [0, front) hold the first tokens, the next one that the block's tokens (the first
-// with limit lim0, `tiles` up to the last one's) see lies `gap` tiles behind them.
+// kWindow: a unit's places are the sequence's cells without those that no row of it sees between the
+// first ones and its first token's window (the token with limit lim0).  Without a plan the first cells
+// take a multiple of 32 places (boxes of 32 bring the tile where both meet) and the window follows at
+// once; through a plan both stay where the tiles are, whose cells are runs there.
 struct Gap {
     int32_t front, gap;
 };
-__device__ __forceinline__ Gap window_gap(const PrefillParams& p, int64_t lim0, int32_t tiles) {
-    Gap r;
-    r.front = (int32_t)clamp64((p.sinks + kPrefillTile - 1) / kPrefillTile, 0, tiles);
-    const int64_t low = lim0 > p.window ? lim0 - p.window : 0;
-    r.gap = (int32_t)clamp64(low / kPrefillTile, r.front, tiles) - r.front;
+__device__ __forceinline__ Gap window_gap(const PrefillParams& p, int64_t lim0) {
+    Gap r = {0, 0};
+    const int64_t low = lim0 - p.window;
+    const int64_t front = p.plan != nullptr ? (p.sinks + kPrefillTile - 1) / kPrefillTile * kPrefillTile : (p.sinks + 31) / 32 * 32;
+    if (low > front) {
+        r.front = (int32_t)front;
+        r.gap = (int32_t)(low - front);
+        if (p.plan != nullptr) r.gap = r.gap / kPrefillTile * kPrefillTile;
+    }
     return r;
 }
 // Tiles of a unit whose first token is number tok0 of the sequence's, n tokens long.
@@ -493,9 +500,8 @@ __device__ __forceinline__ int32_t unit_tiles(const PrefillParams& p, const Sequ
                                               const Prefix& pre) {
     if (is_prefix<MODE>(p, seq)) return pre.tiles;
     const int64_t lim0 = (int64_t)x.len - x.n_q + 1 + tok0;
-    const int32_t tiles = tiles_seen(lim0, n);
-    if (MODE == kWindow) return tiles - window_gap(p, lim0, tiles).gap;
-    return tiles - (MODE == kShared ? pre.tiles : 0);
+    if (MODE == kWindow) return tiles_seen(lim0 - window_gap(p, lim0).gap, n);
+    return tiles_seen(lim0, n) - (MODE == kShared ? pre.tiles : 0);
 }
 
 // The units of all sequences in one line, in eighths of a tile: each a unit's fixed cost, then
@@ -646,15 +652,16 @@ __device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence&
     s.cell0 = p.seq_lens != nullptr ? (int64_t)s.seq * p.n_cells : (int64_t)x.q0;
     s.len = x.len;
     s.lim0 = prefix ? kNoLimit : (int64_t)x.len - x.n_q + 1 + tok0;
-    // tiles of the sequence that are not this unit's, in front of its first one, or of its window
-    int32_t skip = 0;
-    if (MODE == kShared && !prefix) skip = pre.tiles;
-    Gap gap = {};
-    if (MODE == kWindow) {
-        gap = window_gap(p, s.lim0, tiles_seen(s.lim0, s.n_tok));
-        skip = gap.gap;
+    // tiles of the sequence in front of the unit's first one
+    const int32_t skip = MODE == kShared && !prefix ? pre.tiles : 0;
+    if constexpr (MODE == kWindow) {
+        const Gap gap = window_gap(p, s.lim0);
+        s.front = gap.front;
+        s.gap = gap.gap;
+        s.lim0 -= gap.gap;
+        s.len -= gap.gap;
     }
-    s.j0 = MODE == kShared ? first + skip : first;
+    s.j0 = first + skip;
     s.part = part;
     int n_max = 0;
     s.n[1] = 0;
@@ -670,12 +677,10 @@ __device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence&
     // KV head at 256 every token is alone, and the others' last tile holds cells that they do not see)
     const int64_t cut = (s.lim0 > 0 ? s.lim0 : 0) / kPrefillTile - skip - first;
     s.first_cut = (prefix || (s.n_tok == 1 && s.lim0 >= s.len) || cut > n_max) ? n_max : (cut < 0 ? 0 : (int)cut);
-    s.whole = min(s.first_cut, (int)clamp64(x.len / kPrefillTile - skip - first, 0, n_max));
+    s.whole = min(s.first_cut, (int)clamp64(s.len / kPrefillTile - skip - first, 0, n_max));
     if (s.n[1] > 0) s.whole = min(s.whole, min(s.n[0], s.n[1]));
     s.turn = from < s.whole ? from : 0;
     if constexpr (MODE == kWindow) {
-        s.front = gap.front;
-        s.gap = gap.gap;
         s.whole = s.turn = 0;
         // from the tile that the first tokens end in, or that follows them, to the one from which on
         // every row's window has begun
@@ -683,7 +688,7 @@ __device__ __forceinline__ void make_seg(const PrefillParams& p, const Sequence&
         s.cut0 = s.cut1 = 0;
         if (s.low_last > p.sinks) {
             s.cut0 = (int)(p.sinks / kPrefillTile) - first;
-            s.cut1 = (int)((s.low_last + kPrefillTile - 1) / kPrefillTile) - gap.gap - first;
+            s.cut1 = (int)((s.low_last + kPrefillTile - 1) / kPrefillTile) - first;
         }
         if (s.cut0 > s.first_cut) s.cut0 = s.cut1 = s.first_cut;   // (all of those tiles are cut at the rows' ends too)
     }
@@ -833,14 +838,7 @@ __device__ __forceinline__ void slot_number(int step, int n_max, bool dual, bool
     }
 }
 
-// The sequence's tile that is number j of a piece (the turn of its whole tiles aside), whether some
-// row does not see it whole, and its number among those tiles of the unit.
-template <int MODE>
-__device__ __forceinline__ int32_t tile_of(const typename SegOf<MODE>::type& s, int j) {
-    const int32_t x = s.j0 + j;
-    if constexpr (MODE == kWindow) return x < s.front ? x : x + s.gap;
-    return x;
-}
+// Whether some row does not see tile j of a piece whole, and its number among those tiles of the unit.
 template <int MODE>
 __device__ __forceinline__ bool is_cut(const typename SegOf<MODE>::type& s, int j) {
     if constexpr (MODE == kWindow) return j >= s.first_cut || (j >= s.cut0 && j < s.cut1);
@@ -864,6 +862,7 @@ struct Tile {
     int32_t e[4];     // physical cells (no plan: from the tile's first), -1: none
     int64_t base;     // first physical cell when a run
     bool run, holes;  // the cells that are there lie at base + their number; some are not
+    int32_t split, gap;   // kWindow, no plan: those from `split` on (a multiple of 32) lie `gap` further
 };
 template <int MODE, bool PLAN>
 __device__ __forceinline__ Tile read_tile(const PrefillParams& p, const typename SegOf<MODE>::type& s, int j) {
@@ -874,18 +873,29 @@ __device__ __forceinline__ Tile read_tile(const PrefillParams& p, const typename
         at += s.turn;
         if (at >= s.whole) at -= s.whole;
     }
-    const int64_t i0 = (int64_t)tile_of<MODE>(s, at) * kPrefillTile;
+    const int64_t i0 = (int64_t)(s.j0 + at) * kPrefillTile;
+    // (kWindow) how far on the tile's cells lie from its places, or those of them from `split` on
+    int32_t on = 0, split = kPrefillTile, gap = 0;
+    if constexpr (MODE == kWindow) {
+        gap = s.gap;
+        on = i0 >= s.front ? gap : 0;
+        if (!PLAN) {   // (through one the first cells end with a tile)
+            if (i0 < s.front && s.front - i0 < kPrefillTile && gap != 0) split = s.front - (int32_t)i0;
+            t.gap = gap;
+            t.split = split;
+        }
+    }
     const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
     const int left = j < n_max ? (int)clamp64(s.len - i0, 0, kPrefillTile) : 0;
     t.run = true;
     t.holes = left < kPrefillTile;
-    t.base = s.cell0 + i0;
-    const int32_t* row = PLAN ? p.plan + (int64_t)s.seq * p.plan_stride + i0 : nullptr;
+    t.base = s.cell0 + i0 + on;
+    const int32_t* row = PLAN ? p.plan + (int64_t)s.seq * p.plan_stride + i0 + on : nullptr;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int c = 32 * k + lane;
         t.e[k] = -1;
-        if (c < left) t.e[k] = row != nullptr ? __ldg(row + c) : c;
+        if (c < left) t.e[k] = row != nullptr ? __ldg(row + c) : (MODE == kWindow && c >= split ? c + gap : c);
     }
     return t;
 }
@@ -1093,7 +1103,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             const uint32_t bar = smem_addr(&h->full[st]);
                             h->slot_mend[st] = job ? 1u : 0u;
                             if (filled == 0 && p.stall_tx != 0u) mbar_expect_tx(bar, p.stall_tx);
-                            if (run) {
+                            if (MODE == kWindow && !PLAN && run && (v_side ? tv.split : tk.split) < kPrefillTile) {
+                                const int32_t split = v_side ? tv.split : tk.split, gap = v_side ? tv.gap : tk.gap;
+                                mbar_expect_tx(bar, (uint32_t)kSlotBytes);
+#pragma unroll 1
+                                for (int k = 0; k < 8; ++k) {   // 32 cells x 64 dims at a time
+                                    const int c = 32 * (k >> 1);
+                                    tma_box4(smem_addr(slots + st * kSlotBytes) + (k & 1) * kPlaneBytes + c * 128,
+                                             v_side ? &p.tmap_v32 : &p.tmap_k32, 0,
+                                             (int)(v_side ? tv.base : tk.base) + c + (c >= split ? gap : 0), 2 * half + (k & 1), s.g, bar);
+                                }
+                            } else if (run) {
                                 mbar_expect_tx(bar, (uint32_t)kSlotBytes);
                                 tma_box4(smem_addr(slots + st * kSlotBytes), v_side ? &p.tmap_v : &p.tmap_k, 0,
                                          (int)(v_side ? tv.base : tk.base), 2 * half, s.g, bar);
@@ -1135,14 +1155,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             // (MMA waits for the mended slot, so this use of it is not over)
                             if (!wait_all(&h->full[st], (job.n / kSlots) & 1u)) break;
                             // (cells below the first token's end are seen by all rows: nothing to keep apart)
-                            const int64_t seen = s.lim0 - (int64_t)tile_of<MODE>(s, job.j) * kPrefillTile;
+                            const int64_t seen = s.lim0 - (int64_t)(s.j0 + job.j) * kPrefillTile;
 #pragma unroll 1
                             for (int k4 = 0; k4 < 4; ++k4) {                  // 32 cells at a time
                                 const int32_t e = k4 < 2 ? (k4 ? t.e[1] : t.e[0]) : (k4 == 2 ? t.e[2] : t.e[3]);
                                 const uint32_t gone = __ballot_sync(0xffffffffu, e < 0);
                                 bool all = seen >= 32 * k4 + 32;
                                 if constexpr (MODE == kWindow) {   // (nor those that every window or the first tokens hold)
-                                    const int64_t c0 = (int64_t)tile_of<MODE>(s, job.j) * kPrefillTile + 32 * k4;
+                                    const int64_t c0 = (int64_t)(s.j0 + job.j) * kPrefillTile + 32 * k4;
                                     all = all && (c0 >= s.low_last || c0 + 32 <= p.sinks);
                                 }
                                 const bool look = cut && !all;
@@ -1404,14 +1424,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // of two KV heads at head_dim 128, and the slot's word says which four.  (A cp.async for
                 // each cell took 600 of the warp's clocks.)  Tiles with holes keep to those.
                 const int scale0 = s.g * (D / 32) + half * 4;
-                const bool scale_box = t.run && !t.holes && p.scl_tma != 0;
+                const bool split = MODE == kWindow && !PLAN && t.split < kPrefillTile;
+                const bool scale_box = t.run && !t.holes && p.scl_tma != 0 && !split;
                 if (t.run && p.use_tma != 0) {
                     if (lane == 0) {
                         mbar_expect_tx(bar, 128u * 16u * (uint32_t)bits + (scale_box ? 2048u : 0u));
                         if (scale_box)
                             tma_box2(stage + Memory<KBITS>::kRawBytes - 2048, v_side ? &p.tmap_vs : &p.tmap_ks, scale0 & ~7,
                                      (int)t.base, bar);
-                        tma_box(stage, v_side ? &p.tmap_v : &p.tmap_k, half * 16 * bits, s.g, (int)t.base, bar);
+                        if (split) {
+#pragma unroll 1
+                            for (int c = 0; c < kPrefillTile; c += 32)
+                                tma_box(stage + 16 * bits * c, v_side ? &p.tmap_v32 : &p.tmap_k32, half * 16 * bits, s.g,
+                                        (int)t.base + c + (c >= t.split ? t.gap : 0), bar);
+                        } else {
+                            tma_box(stage, v_side ? &p.tmap_v : &p.tmap_k, half * 16 * bits, s.g, (int)t.base, bar);
+                        }
                     }
                 } else {   // 16-byte pieces of the cells' 128 dims, `bits` a cell
                     const char* rows = static_cast<const char*>(v_side ? p.v : p.k);
@@ -1716,8 +1744,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     lost = lost || !wait_bar(smem_addr(&h->s_full[buf]), par, abort_flag, p.wait_limit_ns);
                     __syncwarp();
                     tc_fence_after();
-                    int off = j * kPrefillTile + 64 * half;
-                    if constexpr (MODE == kWindow) off += s.j0 + j >= s.front ? s.gap * kPrefillTile : 0;
+                    const int off = j * kPrefillTile + 64 * half;
                     const int left = (g ? rel[1] : rel[0]) - off;
                     bool seen = left >= 64;
                     int hide0 = 0, hide1 = 0;    // kWindow: columns [hide0, hide1) are hidden
@@ -1939,11 +1966,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll 1
                             for (int c = 0; c < 128; ++c) {
                                 if (!((h->bad_cells[i % kRing][t][c >> 5] >> (c & 31)) & 1u)) continue;
-                                const int64_t at = (int64_t)tile_of<MODE>(s, cut_tile<MODE>(s, t)) * kPrefillTile + c;
+                                const int64_t at = (int64_t)(s.j0 + cut_tile<MODE>(s, t)) * kPrefillTile + c;
                                 if (at >= s.lim0 + tok) continue;
                                 if (MODE == kWindow && at >= p.sinks && at < s.lim0 + tok - p.window) continue;
-                                const int64_t cell = PLAN ? (int64_t)__ldg(p.plan + (int64_t)s.seq * p.plan_stride + at)
-                                                                       : s.cell0 + at;
+                                int64_t place = at;
+                                if constexpr (MODE == kWindow) place += at >= s.front ? s.gap : 0;
+                                const int64_t cell = PLAN ? (int64_t)__ldg(p.plan + (int64_t)s.seq * p.plan_stride + place)
+                                                                       : s.cell0 + place;
 #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
                                     const int d = d0 + c0 + k;

@@ -1,12 +1,12 @@
 // Attention with a sliding window and first tokens that stay visible: a token with limit lim sees the
 // cells c < lim with c < sinks or c >= lim - window.
 //
-// A block's tiles are those of the first tokens, then, behind a gap that no row of it sees, those from
-// its first token's window to its last token's end: sinks / 128 + (window + block) / 128 + 2 at most,
-// however long the sequence.  What differs from the plain form: where a unit's tiles lie; a second
-// bound in the rare path that masks a tile; up to four more tiles at the front that only some rows
-// see whole, whose values that are not finite are kept apart like those at the end; and shares of
-// equal length for all units, which a window makes about equal.
+// A block's places are the first cells and, without the gap that no row of it sees, those from its first
+// token's window to its last token's end: (sinks + 31 + window + block) / 128 tiles, however long the
+// sequence.  What differs from the plain form: where a unit's places lie; a second bound in the masks,
+// which are applied in registers (a third of the tiles have one); up to four more tiles at the front
+// that only some rows see whole, whose values that are not finite are kept apart like those at the end;
+// and shares of equal length for all units, which a window makes about equal.
 #include "prefill_kernel.cuh"
 
 namespace kvattn {

@@ -84,6 +84,7 @@ struct PrefillParams {
     // use_tma: f16 rows (encode_planes_map), or codes (encode_codes_map), boxes of 128 dims x 128
     // cells
     CUtensorMap tmap_k, tmap_v;
+    CUtensorMap tmap_k32, tmap_v32;   // with a window: the same with boxes of 32 cells (f16: of 64 dims)
     CUtensorMap tmap_ks, tmap_vs;   // scl_tma: quantised caches' scales (encode_scale_tensor_map), boxes of 8 x 128 cells
     CUtensorMap tmap_q;       // 3-D {head_dim, heads, tokens}, boxes {64, group, group_tokens}
     const void* k;            // f16: rows k_stride elements apart; quantised: dense planes
@@ -133,9 +134,10 @@ cudaError_t launch_prefill_shared(const PrefillParams& p, int kv_type, int head_
 // limit on waits and its test hook.
 bool encode_prefill_map(CUtensorMap* map, const void* base, int64_t rows, int n_head, int head_dim, int64_t row_stride,
                         int box_heads, int box_rows);
-// The 4-D map {64, rows, head_dim / 64 planes, KV heads} of half rows, boxes {64, 128, 2, 1} with
-// the 128-byte swizzle: 128 cells x 128 dims as two planes in one copy.
-bool encode_planes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int head_dim, int64_t row_stride);
+// The 4-D map {64, rows, head_dim / 64 planes, KV heads} of half rows, boxes {64, box_rows, box_planes,
+// 1} with the 128-byte swizzle: two planes bring 128 dims in one copy.
+bool encode_planes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int head_dim, int64_t row_stride,
+                       int box_rows, int box_planes);
 // The 3-D map {row bytes, KV heads, rows} of a plane of codes, boxes {box_bytes, 1, box_rows}.
 bool encode_codes_map(CUtensorMap* map, const void* base, int64_t rows, int n_head_kv, int row_bytes, int box_bytes,
                       int box_rows);

@@ -87,11 +87,11 @@ Cut chunk_cut(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim,
 
 int block_tokens_of(int group, int head_dim) { return 128 / group * prefill_groups(head_dim); }
 
-// With a window: tiles that the first tokens and the windows of a block meet, at most (a stretch of n
-// cells meets (n + 254) / 128 tiles).
-int64_t window_tiles_of(int64_t window, int64_t sinks, int group, int head_dim) {
-    return (sinks + kPrefillTile - 1) / kPrefillTile +
-           (window + block_tokens_of(group, head_dim) - 1 + 2 * (kPrefillTile - 1)) / kPrefillTile;
+// With a window: tiles that the first tokens and the windows of a block meet, at most (window_gap in
+// prefill_kernel.cuh; through a plan the window begins anywhere in a tile).
+int64_t window_tiles_of(int64_t window, int64_t sinks, int group, int head_dim, bool plan) {
+    const int64_t front = plan ? (sinks + kPrefillTile - 1) / kPrefillTile * kPrefillTile + kPrefillTile - 1 : (sinks + 31) / 32 * 32;
+    return (front + window + block_tokens_of(group, head_dim) - 1 + kPrefillTile - 1) / kPrefillTile;
 }
 
 // With a shared prefix: the line holds the sequences' units and the prefix's, and is always cut into
@@ -150,13 +150,21 @@ int launch_attention(Form form, PrefillParams& p, const void* q, int64_t q_strid
     p.out_sectors = aligned(p.out, 32) ? 1 : 0;
     debug_waits(&p.wait_limit_ns, &p.stall_tx);
     if (!encode_prefill_map(&p.tmap_q, q, p.n_tok, n_head, head_dim, q_stride, p.group, p.group_tokens)) return KVATTN_ERR_CUDA;
+    // (a window's first tile is brought in parts, by maps with smaller boxes)
+    const bool parts = form == Form::window && p.plan == nullptr;
     if (kv_type == KVATTN_KV_F16) {
-        p.use_tma = encode_planes_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim, p.k_stride) &&
-                    encode_planes_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim, p.v_stride);
+        auto planes = [&](CUtensorMap* m, const void* x, int64_t stride, int box_rows, int box_planes) {
+            return encode_planes_map(m, x, rows, n_head_kv, head_dim, stride, box_rows, box_planes);
+        };
+        p.use_tma = planes(&p.tmap_k, p.k, p.k_stride, kPrefillTile, 2) && planes(&p.tmap_v, p.v, p.v_stride, kPrefillTile, 2) &&
+                    (!parts || (planes(&p.tmap_k32, p.k, p.k_stride, 32, 1) && planes(&p.tmap_v32, p.v, p.v_stride, 32, 1)));
     } else {
         const int kb = kv_type == KVATTN_KV_Q4_0 ? 4 : 8, vb = kv_type == KVATTN_KV_Q8_0 ? 8 : 4;
-        p.use_tma = encode_codes_map(&p.tmap_k, p.k, rows, n_head_kv, head_dim * kb / 8, 16 * kb, kPrefillTile) &&
-                    encode_codes_map(&p.tmap_v, p.v, rows, n_head_kv, head_dim * vb / 8, 16 * vb, kPrefillTile);
+        auto codes = [&](CUtensorMap* m, const void* x, int bits, int box_rows) {
+            return encode_codes_map(m, x, rows, n_head_kv, head_dim * bits / 8, 16 * bits, box_rows);
+        };
+        p.use_tma = codes(&p.tmap_k, p.k, kb, kPrefillTile) && codes(&p.tmap_v, p.v, vb, kPrefillTile) &&
+                    (!parts || (codes(&p.tmap_k32, p.k, kb, 32) && codes(&p.tmap_v32, p.v, vb, 32)));
         p.scl_tma = p.use_tma != 0 && rows <= (int64_t)INT32_MAX &&
                     encode_scale_tensor_map(&p.tmap_ks, p.k_scale, rows, n_head_kv, head_dim, kPrefillTile) &&
                     encode_scale_tensor_map(&p.tmap_vs, p.v_scale, rows, n_head_kv, head_dim, kPrefillTile);
@@ -457,7 +465,7 @@ static int prompt_attention(const void* q, int64_t q_stride, const void* k, int6
     if (windowed) {
         p.window = window;
         p.sinks = std::min(sinks, n_tok);
-        p.window_tiles = (int)window_tiles_of(p.window, p.sinks, n_head / n_head_kv, head_dim);
+        p.window_tiles = (int)window_tiles_of(p.window, p.sinks, n_head / n_head_kv, head_dim, false);
     }
     return launch_attention(windowed ? Form::window : Form::plain, p, q, q_stride, KVATTN_KV_F16, n_head, n_head_kv, head_dim, n_tok,
                             scale, c.shares, c.n_ctas, windowed ? "prefill_window" : "prefill", stream);
@@ -537,7 +545,7 @@ static int chunk_attention(Form form, const void* q, int64_t q_stride, const int
         if (form == Form::window) {
             p.window = window;
             p.sinks = std::min(sinks, max_len);
-            p.window_tiles = (int)window_tiles_of(p.window, p.sinks, group, head_dim);
+            p.window_tiles = (int)window_tiles_of(p.window, p.sinks, group, head_dim, cell_plan != nullptr);
             tiles = std::min<int64_t>(tiles, p.window_tiles);
         }
         const Cut c = cut_of(units, tiles, head_dim, true);
