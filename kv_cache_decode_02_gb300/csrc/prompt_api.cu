@@ -152,7 +152,14 @@ int launch_attention(Form form, PrefillParams& p, const void* q, int64_t q_strid
     p.group_tokens = 128 / p.group;
     p.block_tokens = p.group_tokens * prefill_groups(head_dim);
     p.scale_log2 = (float)((double)scale * 1.4426950408889634074);
-    p.single_length = kv_type == KVATTN_KV_F16 && head_dim == 128 && (p.plan == nullptr || form == Form::shared) ? 5 : 8;
+    p.single_length = 8;
+    if (kv_type == KVATTN_KV_F16 && head_dim == 128) {
+        // (64 single tokens behind 8192 shared cells: 52 us at 5, 48 at 4; through a plan 55, 55, 58 at 6)
+        if (form == Form::shared)
+            p.single_length = p.plan == nullptr ? 4 : 5;
+        else if (p.plan == nullptr)
+            p.single_length = 5;
+    }
     p.shares = shares ? 1 : 0;
     p.out_sectors = aligned(p.out, 32) ? 1 : 0;
     debug_waits(&p.wait_limit_ns, &p.stall_tx);
