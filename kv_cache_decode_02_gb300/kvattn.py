@@ -925,6 +925,8 @@ def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells
             raise ValueError("plan: a row for each sequence is wanted")
     if free_blocks is not None and n_free is not None:
         free, count, n_list = _ints(free_blocks, "free_blocks"), _ints(n_free, "n_free", 1), free_blocks.numel()
+        if n_list == 0:
+            free = count   # (torch gives an empty list no address; nothing is read of it)
     elif free_blocks is not None or n_free is not None:
         raise ValueError("free_blocks and n_free go together")
     else:

@@ -98,6 +98,10 @@ def test_tables_that_are_complete(kvattn):
     check(kvattn, [20, 16, 0], [20, 40, 33], tables, None, 0, 16, 9 * 16, 93, status=False)
 
 
+def test_an_empty_free_list(kvattn):
+    check(kvattn, [16, 3], [1, 4], [[0, -1], [1, -1]], [], 0, 16, 64, 5, [[9] * 32] * 2, True)
+
+
 def test_no_sequences(kvattn):
     out = kvattn.step_maps_buffers(0, 5)
     empty = torch.zeros(0, dtype=torch.int32, device="cuda")
