@@ -145,21 +145,20 @@ template <>
 struct SegOf<kWindow> {
     using type = WindowSeg;
 };
-// Through a plan: what a score's minimum is taken with, +inf, or -inf for a hole.  kWindow and kShared,
-// whose f16 header has no room for it in 32 bits: the upper halves of those.
-template <int MODE>
-struct BiasOf {
+// Through a plan: what a score's minimum is taken with, +inf, or -inf for a hole.  HALF: the upper halves
+// of those, where the header has no room for more (f16, kWindow and kShared).
+template <bool HALF>
+struct Bias {
     using type = float;
     static __device__ __forceinline__ float of(bool hole) { return hole ? -INFINITY : INFINITY; }
 };
-struct HalfBias {
+template <>
+struct Bias<true> {
     using type = uint16_t;
     static __device__ __forceinline__ uint16_t of(bool hole) { return hole ? 0xff80u : 0x7f80u; }
 };
-template <>
-struct BiasOf<kWindow> : HalfBias {};
-template <>
-struct BiasOf<kShared> : HalfBias {};
+template <int MODE, int KBITS>
+constexpr bool kHalfBias = MODE != kPlain && KBITS == 16;
 
 // f16: a slot that warps 9-11 mend or copy, or the end of a unit.
 struct Job {
@@ -169,7 +168,7 @@ struct Job {
 };
 constexpr uint32_t kJobMend = 0, kJobCopy = 1, kJobUnit = 2, kJobEnd = 3;
 
-template <int MODE, int MASKS>
+template <int MODE, int KBITS, int MASKS>
 struct Header {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t mended[kMaxSlots];  // a V slot that is mended after it landed
@@ -190,7 +189,7 @@ struct Header {
     typename SegOf<MODE>::type seg[kRing];
     Job job[kRing];
     float meet[2][128];                       // what two threads of a row tell each other
-    alignas(16) typename BiasOf<MODE>::type bias[MASKS][kPrefillTile];
+    alignas(16) typename Bias<kHalfBias<MODE, KBITS>>::type bias[MASKS][kPrefillTile];
 };
 
 // Shared-memory matrix descriptor: start address, leading and stride byte offsets, the
@@ -954,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     unsigned char* slots = q_tiles + 2 * kQTileBytes;
     unsigned char* raws = slots + kSlots * kSlotBytes;
     constexpr int kMaskRing = kMasks<MODE, KBITS>;
-    using Head = Header<MODE, kMaskRing>;
+    using Head = Header<MODE, KBITS, kMaskRing>;
     using Piece = typename SegOf<MODE>::type;
     constexpr int kCut = kCutTiles<MODE>;
     static_assert(sizeof(Head) <= Memory<KBITS>::kHeaderBytes && alignof(Head) == 16, "header");
@@ -1030,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (T >= kMaskRing && !wait_all(&h->mask_empty[r], (T / kMaskRing - 1u) & 1u)) return false;
         if (t.holes)   // (else nobody looks)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = BiasOf<MODE>::of(t.e[k] < 0);
+            for (int k = 0; k < 4; ++k) h->bias[r][32 * k + lane] = Bias<kHalfBias<MODE, KBITS>>::of(t.e[k] < 0);
         if (lane == 0) h->holes[r] = t.holes ? 1u : 0u;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&h->mask_full[r]));
@@ -1795,7 +1794,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
                                 float4 f;
-                                if constexpr (MODE != kPlain) {
+                                if constexpr (kHalfBias<MODE, KBITS>) {
                                     const uint2 u = reinterpret_cast<const uint2*>(bias)[c];
                                     f = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
                                                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));

@@ -913,16 +913,19 @@ def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells
     if n_tok is not None and n_tok != T:
         raise ValueError("n_tok: out has other rows")
     _here(lens, "lens")
-    a, b, tab = _ints(lens, "lens", S), _ints(n_new, "n_new", S), _ints(tables, "tables")
     shape = tables.shape
     if len(shape) != 2 or shape[0] != S:
         raise ValueError("tables: a row for each sequence is wanted")
+    if (lens.get_device() != d or n_new.get_device() != d or tables.get_device() != d or _off(free_blocks, d)
+            or _off(n_free, d) or _off(plan, d) or (status is not None and _bad_word(status, d))):
+        _elsewhere(d, lens=lens, n_new=n_new, tables=tables, free_blocks=free_blocks, n_free=n_free, plan=plan, status=status)
+    a, b, tab = _ints(lens, "lens", S), _ints(n_new, "n_new", S), _ints(tables, "tables")
     pl, stride, free, count, n_list = None, 0, None, None, 0
     if plan is not None:
-        pl = _ints(plan, "plan")
-        rows, stride = plan.shape if plan.dim() == 2 else (-1, 0)
-        if rows != S:
+        pl, rows = _ints(plan, "plan"), plan.shape
+        if len(rows) != 2 or rows[0] != S:
             raise ValueError("plan: a row for each sequence is wanted")
+        stride = rows[1]
     if free_blocks is not None and n_free is not None:
         free, count, n_list = _ints(free_blocks, "free_blocks"), _ints(n_free, "n_free", 1), free_blocks.numel()
         if n_list == 0:
@@ -931,9 +934,6 @@ def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells
         raise ValueError("free_blocks and n_free go together")
     else:
         left = None
-    if (lens.get_device() != d or n_new.get_device() != d or tables.get_device() != d or _off(free_blocks, d)
-            or _off(n_free, d) or _off(plan, d) or (status is not None and _bad_word(status, d))):
-        _elsewhere(d, lens=lens, n_new=n_new, tables=tables, free_blocks=free_blocks, n_free=n_free, plan=plan, status=status)
     _check(lib.kvattn_step_maps(a, b, S, tab, shape[1], block_cells, free, n_list, count, n_cells, T, offsets, seq_lens, positions,
                                 slots, left, pl, stride, 1 if whole_plan else 0, _raw(status), _stream(stream)), "kvattn_step_maps")
     return out
