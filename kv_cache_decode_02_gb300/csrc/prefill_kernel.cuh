@@ -61,7 +61,7 @@
 // 128, 28 % at 256.
 // Chunks: 512 tokens over 16384 f16 cells 114 us (62 %).  Quantised caches: the turning of codes
 // into f16, about 1500 clocks a slot, shares the issue slots with the softmax: 100 tokens over
-// 131072 8-bit cells 240 us (47 %).
+// 131072 8-bit cells 236 us (48 %).
 //
 // Every wait is bounded, as in the decode kernels; a wait that gives up sets a flag that the
 // others see, and KVATTN_DEVICE_WAIT_TIMEOUT in the workspace.
