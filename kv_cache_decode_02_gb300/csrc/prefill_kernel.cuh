@@ -383,10 +383,10 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w, bool& bad) {
 
 // Stored value = scale x code, rounded once to half: the type of an f16 cache (2^-11 of the
 // value, where the 8-bit code itself is off by up to 2^-8 of the block's largest).  Scales
-// above 515 could pass the largest half; those products are kept at it (as cache_read does).  In
+// above 511 could pass the largest half; those products are kept at it (as cache_read does).  In
 // a cut tile what is not finite is dropped and its cell noted.  Both are done to 16 bytes of a
 // slot after they were stored, and rarely.
-constexpr uint32_t kBigScale = 0x6006u;   // 515
+constexpr uint32_t kBigScale = 0x5fffu;   // 511.75 (a code of -128, which no write makes, is finite up to it)
 __device__ __forceinline__ void amend(unsigned char* at, uint32_t scale, bool cut, uint32_t* bad_row, int cell) {
     const __half2 top = __halves2half2(__ushort_as_half(0x7bffu), __ushort_as_half(0x7bffu));
     uint4 w = *reinterpret_cast<uint4*>(at);
@@ -1516,7 +1516,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // are broadcast from lane 0)
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t slot0 = smem_addr(slots), q_addr = smem_addr(q_tiles);
-            const bool leader = elect_one();
+            bool leader = elect_one();        // (until one of its own waits gives up)
             uint32_t mends = 0;               // a bit per slot: parity of its mended barrier
             uint32_t st = 0, use = 0;         // the next slot, and the parity of its use
             // This warp's own instructions, one after the other, set the pace of everything: a wait
@@ -1527,8 +1527,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // done and the loader fills it again, and would wait for a phase that is over.  A barrier
             // of p, or of the queries, moves on only after products that come after the next meeting.
             bool ok = true;
+            // The leader gives nothing out after a wait of its own that gave up: a commit on a slot that
+            // never became full would let the loader, woken by it, fill the slot once more and arrive on a
+            // barrier whose phase has had all of its arrivals.
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                ok = wait_bar(smem_addr(bar), parity, abort_flag, p.wait_limit_ns) && ok;
+                const bool got = wait_bar(smem_addr(bar), parity, abort_flag, p.wait_limit_ns);
+                ok = got && ok;
+                leader = got && leader;
             };
             auto wait_slot = [&](bool check) {
                 wait(&h->full[st], use);
