@@ -1045,9 +1045,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         uint32_t filled = 0;            // slots
         uint32_t n = 0;                 // quantised: raw slots turned
         Piece s = {};
+        // (The MMA warp goes on for a tile after a wait that gave up, and may release a slot that never
+        // became full: to fill that once more would arrive on a barrier whose phase has had all of its
+        // arrivals, which faults.  It raises the flag first.)
         auto wait_slot_empty = [&]() -> bool {
             const uint32_t use = filled / kSlots;
-            return use == 0 || wait_all(&h->empty[filled % kSlots], (use - 1) & 1u);
+            return use == 0 || __all_sync(0xffffffffu, wait_bar(smem_addr(&h->empty[filled % kSlots]), (use - 1) & 1u, abort_flag,
+                                                                 p.wait_limit_ns) && *abort_flag == 0);
         };
         auto slot_ready = [&](uint64_t* bar) {
             __syncwarp();
@@ -1243,7 +1247,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const uint32_t word = h->raw_word[r];
                 if (!(word & 8u) && filled >= kSlots)
                     got = wait_bar(smem_addr(&h->empty[filled % kSlots]), (filled / kSlots - 1) & 1u, abort_flag,
-                                   p.wait_limit_ns) && got;
+                                   p.wait_limit_ns) && *abort_flag == 0 && got;   // (as in wait_slot_empty)
                 if (!(ok = __all_sync(0xffffffffu, got)) || word == kNoMore) break;
                 const bool v_side = word & 1u, cut = (word >> 1) & 1u;
                 const uint32_t unit = (word >> 8) & 0xffffu;
@@ -1516,7 +1520,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // are broadcast from lane 0)
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t slot0 = smem_addr(slots), q_addr = smem_addr(q_tiles);
-            bool leader = elect_one();        // (until one of its own waits gives up)
+            const bool leader = elect_one();
             uint32_t mends = 0;               // a bit per slot: parity of its mended barrier
             uint32_t st = 0, use = 0;         // the next slot, and the parity of its use
             // This warp's own instructions, one after the other, set the pace of everything: a wait
@@ -1527,13 +1531,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // done and the loader fills it again, and would wait for a phase that is over.  A barrier
             // of p, or of the queries, moves on only after products that come after the next meeting.
             bool ok = true;
-            // The leader gives nothing out after a wait of its own that gave up: a commit on a slot that
-            // never became full would let the loader, woken by it, fill the slot once more and arrive on a
-            // barrier whose phase has had all of its arrivals.
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = wait_bar(smem_addr(bar), parity, abort_flag, p.wait_limit_ns);
-                ok = got && ok;
-                leader = got && leader;
+                ok = wait_bar(smem_addr(bar), parity, abort_flag, p.wait_limit_ns) && ok;
             };
             auto wait_slot = [&](bool check) {
                 wait(&h->full[st], use);
