@@ -94,6 +94,7 @@ constexpr int kRing = 4;                      // pieces of work whose plans are 
 template <int MODE, int KBITS>
 constexpr int kMasks = KBITS != 16 ? 4 : (MODE == kShared ? 3 : 2);
 constexpr int kRawStages = 3;                 // quantised: slots of raw bytes in flight
+constexpr int kVGo = 4;                       // more than there are stages, so that none is passed twice unseen
 // Tiles that only some of a unit's (<= 256) tokens see whole: three at their ends; with a window three
 // at its beginnings too, and the one that the first tokens end in.
 template <int MODE>
@@ -173,6 +174,7 @@ struct Header {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t mended[kMaxSlots];  // a V slot that is mended after it landed
     uint64_t raw_full[kRawStages], raw_empty[kRawStages];  // quantised: a slot's raw bytes; they are turned
+    uint64_t v_go[KBITS == 16 ? 1 : kVGo];                 // the stage of a raw slot of V is free
     uint64_t q_full, q_empty;    // the unit's query rows; its last S is complete
     uint64_t s_full[2], p_full[2];  // an S buffer holds S, or p
     uint64_t pv_done[2];         // its P V is complete
@@ -979,6 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(smem_addr(&h->raw_full[i]), 1);
             mbar_init(smem_addr(&h->raw_empty[i]), 4);
         }
+        if (kQuant)
+            for (int i = 0; i < kVGo; ++i) mbar_init(smem_addr(&h->v_go[kQuant ? i : 0]), 1);
         mbar_init(smem_addr(&h->q_full), 1);
         mbar_init(smem_addr(&h->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
@@ -1397,9 +1401,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         } else if (kQuant && warp >= 14) {
             // ------------------------------- raw bytes, quantised -------------------------------
             // Warp 14 brings K, warp 15 V: one for both took 1900 clocks a slot of its own
-            // instructions, more than the slot's turning.  Both count, and wait for the stage of, every
-            // slot: a warp that left the other's out could meet a stage's barrier a phase behind.
+            // instructions, more than the slot's turning.  Both count every slot, but only warp 14 waits
+            // for the stages, and tells the other of V's: each passes through the barriers of all slots,
+            // and one that looked late at a slot that is not its own could find the phase over and the
+            // next one too.
             const bool v_warp = warp == 15;
+            uint32_t v_slots = 0;
             uint32_t ahead = 0, T = 0;    // slots brought, tiles begun
             bool bad_entry = false, ok = true;
             Piece s = {};
@@ -1414,7 +1421,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 ++ahead;
             };
             auto bring = [&](const Tile& t, bool v_side, int half, uint32_t word) {
-                if (!(ok = stage_free())) return;
+                if (v_side && v_warp)
+                    ok = wait_all(&h->v_go[v_slots % kVGo], (v_slots / kVGo) & 1u);
+                else if (!v_warp)
+                    ok = stage_free();
+                if (!ok) return;
+                if (v_side && !v_warp && lane == 0) mbar_arrive(smem_addr(&h->v_go[v_slots % kVGo]));
+                if (v_side) ++v_slots;
                 if (v_side != v_warp) {
                     ++ahead;
                     return;
@@ -1478,12 +1491,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int n_max = s.n[0] > s.n[1] ? s.n[0] : s.n[1];
                 const uint32_t unit = (i & 0xffffu) << 8;
                 if (n_max == 0) {    // (the turning warps still sign the unit off)
-                    if ((ok = stage_free())) {
-                        if (v_warp)
-                            ++ahead;
-                        else
-                            publish(unit | 12u);
-                    }
+                    if (v_warp)
+                        ++ahead;
+                    else if ((ok = stage_free()))
+                        publish(unit | 12u);
                     give_back(i);
                     continue;
                 }
