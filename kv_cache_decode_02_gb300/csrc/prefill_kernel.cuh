@@ -1049,17 +1049,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         uint32_t filled = 0;            // slots
         uint32_t n = 0;                 // quantised: raw slots turned
         Piece s = {};
-        // (The MMA warp goes on for a tile after a wait that gave up, and may release a slot that never
-        // became full: to fill that once more would arrive on a barrier whose phase has had all of its
-        // arrivals, which faults.  It raises the flag first.)
         auto wait_slot_empty = [&]() -> bool {
             const uint32_t use = filled / kSlots;
-            return use == 0 || __all_sync(0xffffffffu, wait_bar(smem_addr(&h->empty[filled % kSlots]), (use - 1) & 1u, abort_flag,
-                                                                 p.wait_limit_ns) && *abort_flag == 0);
+            return use == 0 || wait_all(&h->empty[filled % kSlots], (use - 1) & 1u);
         };
-        auto slot_ready = [&](uint64_t* bar) {
+        // `gone`: the abort flag, read after the wait for the slot.  The MMA warp goes on for a tile after a
+        // wait that gave up, and may release a slot that never became full: to arrive for it once more, on
+        // a barrier whose phase has had all of its arrivals, faults.  (It raises the flag first.)
+        auto slot_ready = [&](uint64_t* bar, int gone) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(bar));
+            if (lane == 0 && gone == 0) mbar_arrive(smem_addr(bar));
             ++filled;
         };
         auto stall_hook = [&](uint64_t* bar) {
@@ -1125,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                                 tma_box4(smem_addr(slots + st * kSlotBytes), v_side ? &p.tmap_v : &p.tmap_k, 0,
                                          (int)(v_side ? tv.base : tk.base), 2 * half, s.g, bar);
                             }
-                            mbar_arrive(bar);
+                            if (*abort_flag == 0) mbar_arrive(bar);   // (as in slot_ready)
                         }
                         __syncwarp();
                         if (job && !(ok = give_job(unit | (run ? kJobMend : kJobCopy) | (v_side ? 4u : 0u) | (half ? 8u : 0u), j))) break;
@@ -1251,7 +1250,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const uint32_t word = h->raw_word[r];
                 if (!(word & 8u) && filled >= kSlots)
                     got = wait_bar(smem_addr(&h->empty[filled % kSlots]), (filled / kSlots - 1) & 1u, abort_flag,
-                                   p.wait_limit_ns) && *abort_flag == 0 && got;   // (as in wait_slot_empty)
+                                   p.wait_limit_ns) && got;
+                const int gone = *abort_flag;
                 if (!(ok = __all_sync(0xffffffffu, got)) || word == kNoMore) break;
                 const bool v_side = word & 1u, cut = (word >> 1) & 1u;
                 const uint32_t unit = (word >> 8) & 0xffffu;
@@ -1350,7 +1350,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         }
                     }
                     fence_async();
-                    slot_ready(&h->full[filled % kSlots]);
+                    slot_ready(&h->full[filled % kSlots], gone);
                 }
                 __syncwarp();
                 if (lane == 0) {
