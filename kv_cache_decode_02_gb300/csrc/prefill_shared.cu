@@ -12,8 +12,8 @@
 // launches each leave a tail.
 //
 // What it measured: 64 single tokens behind 8192 f16 cells with 30 to 1038 of their own, through a plan,
-// 32 / 8 heads of 128: 53 us (49 % of the copy rate; about 4000 clocks for each of 512 units beside its
-// tiles); 16 behind 131072 8-bit cells 111 us (40 %; turning codes into halves); 8 x 4 tokens behind 4096
+// 32 / 8 heads of 128: 54 us (49 % of the copy rate; about 4000 clocks for each of 512 units beside its
+// tiles); 16 behind 131072 8-bit cells 117 us (38 %; turning codes into halves); 8 x 4 tokens behind 4096
 // cells at head_dim 256 22 us.  The join takes 3 to 5 us of each.
 #include "prefill_kernel.cuh"
 

@@ -9,10 +9,10 @@
 // and shares of equal length for all units, which a window makes about equal.
 //
 // What bounds it: single tokens the bytes of whole tiles and the rounds of units (64 tokens, window 1024
-// and 4 first tokens, 32 / 8 heads of 128: 52 us, 73 % of the copy rate for the cells that they see);
+// and 4 first tokens, 32 / 8 heads of 128: 51 us, 74 % of the copy rate for the cells that they see);
 // prompts the ends of their short units, about 8000 clocks beside 3300 a tile (8192 tokens through that
-// window 139 us, 49 % of cuBLAS bf16; ragged prompts of 16 / 8 heads of 256, window 500 and 130 first
-// tokens, 88 us, 33 %).  Bringing only the blocks of 32 cells that a row of the unit sees gained 1 us for
+// window 138 us, 49 % of cuBLAS bf16; ragged prompts of 16 / 8 heads of 256, window 500 and 130 first
+// tokens, 92 us, 31 %).  Bringing only the blocks of 32 cells that a row of the unit sees gained 1 us for
 // the single tokens and cost prompts 3 to 10 %.
 #include "prefill_kernel.cuh"
 
