@@ -138,7 +138,9 @@ SharedCut shared_cut(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int he
     c.lse_off = off;
     off = align_up(off + rows * 4, kWsAlign);
     c.o_off = off;
-    c.total = align_up(off + rows * (size_t)head_dim * 4, kWsAlign);
+    // (a call that shares no tile is the plain form's, whose notes of cuts can be more than few rows' results)
+    c.total = std::max(align_up(off + rows * (size_t)head_dim * 4, kWsAlign),
+                       chunk_cut(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, true).total);
     return c;
 }
 

@@ -77,3 +77,18 @@ def test_a_prompt_window_whose_wait_runs_out_is_reported(kvattn, monkeypatch):
     monkeypatch.delenv("KVATTN_DEBUG_STALL_TX")
     kvattn.prefill(q, k, v, U.ints([0, 256]), window=50, sinks=3, ws=ws)
     assert kvattn.kvattn_workspace_status(ws) == 0
+
+
+def test_a_shared_workspace_serves_calls_that_share_nothing(kvattn):
+    """Few rows behind long caches: the plain form's notes need more room than the shared form's results."""
+    for D in (128, 256):
+        for T, S, H, Hk in ((1, 1, 1, 1), (1, 1, 4, 1), (2, 1, 1, 1), (3, 2, 2, 2), (64, 8, 8, 2)):
+            for n in (0, 128, 5000, 100000, 2 ** 31 - 1):
+                assert (kvattn.kvattn_prefill_chunk_shared_workspace_bytes(T, S, H, Hk, D, n) >=
+                        kvattn.kvattn_prefill_chunk_workspace_bytes(T, S, H, Hk, D, n))
+    c = X.make("f16", 100, [1], [200], 1, 1, 128, False)
+    ws = kvattn.prefill_chunk_workspace(1, 1, 1, 1, 128, 100000, shared=1)
+    for shared in (100, 128, 256):
+        out, lse = P.call_chunk(kvattn, c, shared=shared, ws=ws, max_len=100000)
+        assert kvattn.kvattn_workspace_status(ws) == 0
+        W.check_chunk(c, out, lse)
