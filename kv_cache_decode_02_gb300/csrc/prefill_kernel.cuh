@@ -103,7 +103,6 @@ constexpr float kSlack = 8.f;                 // lazy maximum
 constexpr float kLift = 7.f;                  // p is scaled by 2^kLift
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint32_t kNoMore = 0xffffffffu;
-constexpr int kUnitCost = 2;                  // a unit's fixed cost in tiles, for the equal shares
 
 // f16 slots in the ring: what the 227 KB hold beside the queries (64 KB) and, for quantised
 // caches, the raw ring (18 KB a stage with 8-bit rows, 10 KB with 4-bit ones)
@@ -505,22 +504,13 @@ __device__ __forceinline__ int32_t unit_tiles(const PrefillParams& p, const Sequ
     return tiles_seen(lim0, n) - (MODE == kShared ? pre.tiles : 0);
 }
 
-// The units of all sequences in one line, in eighths of a tile: each a unit's fixed cost, then
-// its tiles (by a rule that is linear in the block's number, so that sums have a closed form; the
-// last share of a unit takes what is left).  CTA c of n takes [share(c), share(c + 1)) of it.
-// Order: sequence, KV head, block.  The host sees to it that the line fits 32 bits.
+// The units of all sequences in one line (line.cuh).  CTA c of n takes [share(c), share(c + 1)) of it.
+// Order: sequence, KV head, block.  The host sees to it that the line fits 32 bits (shared_line_fits; the
+// other forms share fewer units than eight a CTA).
 // (With f16 rows and no plan a tile for one row group of two takes about 0.55 of one for both,
 // 1900 clocks to 3450: a last block of one group counts 5 / 8 (units of 1 to 256 tokens over 8192
 // to 65536 cells: 243 -> 229 us).  Through a plan, or from quantised rows, it waits for its loader
 // and counts as a whole one: 5 / 8 there took 267 -> 302 us.)
-struct Line {
-    uint32_t a, step;       // length of block b: a + step b,
-    uint32_t blocks, less;  // the last one's less this
-    __device__ __forceinline__ uint32_t of(uint32_t b) const { return a + step * b - (b + 1u == blocks ? less : 0u); }
-    __device__ __forceinline__ uint32_t upto(uint32_t b) const {
-        return a * b + step * (b * (b - 1u) / 2u) - (b == blocks ? less : 0u);
-    }
-};
 // Length of a tile of a block of n tokens in the line.
 __device__ __forceinline__ int32_t tile_length(const PrefillParams& p, int32_t n_tok) {
     return n_tok <= p.group_tokens ? p.single_length : 8;
@@ -538,7 +528,7 @@ __device__ __forceinline__ Line line_of(const PrefillParams& p, const Sequence& 
     int32_t tiles = lim / kPrefillTile + (lim % kPrefillTile != 0 ? 1 : 0);   // (lim can be 2^31 - 1)
     if (MODE == kWindow) tiles = min((int32_t)(((uint32_t)x.len + (uint32_t)kPrefillTile - 1u) / (uint32_t)kPrefillTile), p.window_tiles);
     if (MODE == kShared) tiles -= pre.tiles;
-    Line l{8u * (uint32_t)(kUnitCost + tiles), MODE == kWindow ? 0u : (uint32_t)(p.block_tokens + 15) / 16u, x.blocks, 0u};
+    Line l{8u * (uint32_t)(kUnitCost + tiles), MODE == kWindow ? 0u : line_step(p.block_tokens), x.blocks, 0u};
     if (x.blocks != 0u) {
         const uint32_t whole = l.of(x.blocks - 1u);
         l.less = whole - (whole * (uint32_t)tile_length(p, x.n_q - (int32_t)(x.blocks - 1u) * p.block_tokens) >> 3);

@@ -5,6 +5,7 @@
 #pragma once
 
 #include "kvattn_internal.cuh"
+#include "line.cuh"
 
 namespace kvattn {
 
@@ -121,8 +122,6 @@ struct PrefillParams {
     int window_tiles;         // tiles that a unit's windows and first tokens meet, at most
     float scale_log2;         // scale * log2(e)
 };
-constexpr int kPrefillTile = 128;  // cells per tile
-inline int prefill_groups(int head_dim) { return head_dim == 128 ? 2 : 1; }
 // The attention kernel on n_ctas CTAs (at most one per SM) and, with shares, the merge.
 cudaError_t launch_prefill(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl);
 cudaError_t launch_prefill_window(const PrefillParams& p, int kv_type, int head_dim, int n_ctas, cudaStream_t stream, bool pdl);

@@ -31,12 +31,6 @@ int check_cache(int kv_type, const void* k, const void* v, const void* ks, const
     return ks != nullptr && vs != nullptr && aligned(ks, sa) && aligned(vs, sa) ? KVATTN_OK : KVATTN_ERR_INVALID_ARG;
 }
 
-// Units of all sequences together: at most one part-filled block per sequence.
-int64_t unit_bound(int64_t n_tok, int n_seq, int n_head_kv, int group, int head_dim) {
-    const int64_t per = (int64_t)(128 / group) * prefill_groups(head_dim);
-    return std::min((n_tok + per - 1) / per + std::max(n_seq - 1, 0), n_tok) * n_head_kv;
-}
-
 // How a call's work is cut.  Units that are many and short are dealt out whole; few or long ones
 // (chunks over long caches) are cut into equal shares, one per CTA: 16 units of 1024 tiles would
 // otherwise keep 16 of 152 SMs busy.  A share costs its CTA a partial (written and read once
@@ -88,11 +82,9 @@ Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share, bool boun
 }
 
 Cut chunk_cut(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim, int64_t max_len, bool bound = false) {
-    return cut_of(unit_bound(n_tok, n_seq, n_head_kv, n_head / n_head_kv, head_dim),
+    return cut_of(unit_bound(n_tok, n_seq, n_head_kv, block_tokens_of(n_head / n_head_kv, head_dim)),
                   (max_len + kPrefillTile - 1) / kPrefillTile, head_dim, true, bound);
 }
-
-int block_tokens_of(int group, int head_dim) { return 128 / group * prefill_groups(head_dim); }
 
 // With a window: tiles that the first tokens and the windows of a block meet, at most (window_gap in
 // prefill_kernel.cuh; through a plan the window begins anywhere in a tile).
@@ -101,8 +93,9 @@ int64_t window_tiles_of(int64_t window, int64_t sinks, int group, int head_dim, 
     return (front + window + block_tokens_of(group, head_dim) - 1 + kPrefillTile - 1) / kPrefillTile;
 }
 
-// With a shared prefix: the line holds the sequences' units and the prefix's, and is always cut into
-// shares (a prefix's units are few and long beside the others), but where it would pass 31 bits.
+// With a shared prefix: the line holds the sequences' units and the prefix's, however many, and is always
+// cut into shares (a prefix's units are few and long beside the others), but where it would pass 31 bits
+// (units are whole then: 65600 tokens, each a block of 128 heads that share one, make 2.15e9 eighths).
 struct SharedCut {
     bool shares;
     int n_ctas;
@@ -111,18 +104,17 @@ struct SharedCut {
 
 SharedCut shared_cut(int64_t n_tok, int n_seq, int n_head, int n_head_kv, int head_dim, int64_t max_len, int64_t prefix_cells) {
     SharedCut c = {};
-    const int group = n_head / n_head_kv, sms = device_sms();
-    const int64_t units = unit_bound(n_tok, n_seq, n_head_kv, group, head_dim);
-    const int64_t prefix_units = unit_bound(n_tok, 1, n_head_kv, group, head_dim);
-    const int64_t tiles = (max_len + kPrefillTile - 1) / kPrefillTile;
+    const int group = n_head / n_head_kv, block_tokens = block_tokens_of(group, head_dim), sms = device_sms();
+    const int64_t units = unit_bound(n_tok, n_seq, n_head_kv, block_tokens);
+    const int64_t prefix_units = unit_bound(n_tok, 1, n_head_kv, block_tokens);
     const int64_t prefix_tiles = std::min(prefix_cells, max_len) / kPrefillTile;
-    const int64_t work = units * (tiles + 18) + prefix_units * (prefix_tiles + 18);   // (each below 2^31 x 2^25)
+    const bool fits = shared_line_fits(n_tok, n_seq, n_head_kv, group, head_dim, max_len, prefix_cells);
     const char* env = std::getenv("KVATTN_PREFILL_CTAS");
     int64_t n = units + prefix_units * (prefix_tiles / kMinShareTiles + 1);
     n = std::max<int64_t>(std::min<int64_t>(n, sms), 1);
     if (env != nullptr && *env != 0 && std::atoi(env) > 0) n = std::min(std::atoi(env), sms);
     c.n_ctas = (int)n;
-    c.shares = n > 1 && work < INT32_MAX / 8 && !(env != nullptr && *env != 0 && std::atoi(env) <= 0);
+    c.shares = n > 1 && fits && !(env != nullptr && *env != 0 && std::atoi(env) <= 0);
     // (the parts' room does not go by the lengths, so that a size serves every smaller call)
     const size_t rows = (size_t)sms * 2 * (size_t)prefill_groups(head_dim) * 128;
     const size_t out_rows = 2 * (size_t)n_tok * (size_t)n_head;
@@ -460,7 +452,7 @@ static int prompt_attention(const void* q, int64_t q_stride, const void* k, int6
         !aligned(out, 16) || !aligned(lse, 4) || ws == nullptr || !aligned(ws, kWsAlign))
         return KVATTN_ERR_INVALID_ARG;
     if (ws_bytes < kStatusBytes) return KVATTN_ERR_WORKSPACE;
-    const int64_t units = unit_bound(n_tok, n_seq, n_head_kv, n_head / n_head_kv, head_dim);
+    const int64_t units = unit_bound(n_tok, n_seq, n_head_kv, block_tokens_of(n_head / n_head_kv, head_dim));
     if (units > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
     PrefillParams p = {};
     p.k = k;
@@ -534,7 +526,7 @@ static int chunk_attention(Form form, const void* q, int64_t q_stride, const int
         ws == nullptr || !aligned(ws, kWsAlign))
         return KVATTN_ERR_INVALID_ARG;
     const int group = n_head / n_head_kv;
-    const int64_t units = unit_bound(n_tok, n_seq, n_head_kv, group, head_dim);
+    const int64_t units = unit_bound(n_tok, n_seq, n_head_kv, block_tokens_of(group, head_dim));
     if (units > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
     if (form == Form::window && window >= max_len) form = Form::plain;   // (it holds all that there is)
     const SharedCut sc = form == Form::shared ? shared_cut(n_tok, n_seq, n_head, n_head_kv, head_dim, max_len, prefix_cells) : SharedCut{};
@@ -546,7 +538,7 @@ static int chunk_attention(Form form, const void* q, int64_t q_stride, const int
     int n_ctas;
     if (form == Form::shared) {
         const SharedCut& c = sc;
-        if (units + unit_bound(n_tok, 1, n_head_kv, group, head_dim) > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
+        if (units + unit_bound(n_tok, 1, n_head_kv, block_tokens_of(group, head_dim)) > INT32_MAX) return KVATTN_ERR_UNSUPPORTED;
         shares = c.shares;
         n_ctas = c.n_ctas;
         p.prefix_cells = prefix_cells;
