@@ -46,19 +46,16 @@ constexpr int64_t kMinShareTiles = 4;
 // `bound`: of all calls with at most that many units and tiles (one of fewer units may be shared
 // where this one is dealt out whole).
 //
-// With a window units are about equal, and whole ones are dealt out where the last round's idle CTAs
-// cost less than cut units' partials and merge, in tiles (`cut_cost`; 0: any length).  Single tokens:
-// 64 sequences of 9 tiles (5.7 tiles lost) 57 us whole and 64 shared, 32 of 33 (10.4) 90 and 100, 48 of
-// 35 through a plan (16.6) 173 and 162, 20 of 33 (31) 87 and 67.  A tile of many rows takes twice as long.
-constexpr int64_t kCutCostSingle = 10, kCutCost = 5;
-Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share, bool bound = false, int64_t cut_cost = 0) {
+// `cost`: with a window units are about equal, and are dealt out whole where that takes no longer
+// (whole_units); 0: any length.
+Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share, bool bound = false, uint32_t cost = 0) {
     Cut c = {};
     // (KVATTN_PREFILL_CTAS: the CTAs that share the work, for tests; 0: dealt out whole)
     const char* env = std::getenv("KVATTN_PREFILL_CTAS");
     const int sms = device_sms();
     if (bound) units = std::min(units, 8 * (int64_t)sms - 1);
     c.shares = may_share && tiles > kMinShareTiles && units < 8 * (int64_t)sms;
-    if (cut_cost > 0 && (units + sms - 1) / sms * tiles <= units * tiles / sms + cut_cost) c.shares = false;
+    if (cost > 0 && c.shares && whole_units((uint32_t)units, (uint64_t)(units * tiles), (uint32_t)tiles, (uint32_t)sms, cost)) c.shares = false;
     // (the kernel numbers the line of all tiles, in eighths, in 31 bits)
     const bool fits = bound || (units < INT32_MAX && (tiles + 18) * 8 < INT32_MAX / std::max<int64_t>(units, 1));
     int64_t n = units;
@@ -556,8 +553,8 @@ static int chunk_attention(Form form, const void* q, int64_t q_stride, const int
             p.window_tiles = (int)window_tiles_of(p.window, p.sinks, group, head_dim, cell_plan != nullptr);
             tiles = std::min<int64_t>(tiles, p.window_tiles);
         }
-        const int64_t cut_cost = form == Form::plain ? 0 : (n_tok <= n_seq ? kCutCostSingle : kCutCost);
-        const Cut c = cut_of(units, tiles, head_dim, true, false, cut_cost);
+        const bool fast_single = kv_type == KVATTN_KV_F16 && head_dim == 128 && cell_plan == nullptr;
+        const Cut c = cut_of(units, tiles, head_dim, true, false, form == Form::plain ? 0u : cut_cost(n_tok, n_seq, fast_single));
         if (ws_bytes < c.total) return KVATTN_ERR_WORKSPACE;
         shares = c.shares;
         n_ctas = c.n_ctas;

@@ -1,5 +1,6 @@
 """The line that equal shares of attention are cut from (csrc/line.cuh, compiled for the host): where the
-host says that it fits, 32 bits hold it, whatever the sequences' lengths (no GPU needed)."""
+host says that it fits, 32 bits hold it, whatever the sequences' lengths; and the rule by which units of a
+window are dealt out whole (no GPU needed)."""
 import ctypes
 import os
 import random
@@ -18,6 +19,8 @@ uint32_t step(int block_tokens) { return line_step(block_tokens); }
 int fits(int64_t n_tok, int n_seq, int n_head_kv, int group, int head_dim, int64_t max_len, int64_t prefix) {
     return shared_line_fits(n_tok, n_seq, n_head_kv, group, head_dim, max_len, prefix);
 }
+int whole(uint32_t units, uint64_t tiles, uint32_t longest, uint32_t n, uint32_t cost) { return whole_units(units, tiles, longest, n, cost); }
+uint32_t cost(int64_t n_tok, int n_seq, int fast) { return cut_cost(n_tok, n_seq, fast != 0); }
 }
 """
 
@@ -32,6 +35,8 @@ def line(tmp_path_factory):
     lib.upto.restype = lib.of.restype = ctypes.c_uint32
     lib.step.argtypes, lib.step.restype = [ctypes.c_int], ctypes.c_uint32
     lib.fits.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int64]
+    lib.whole.argtypes = [ctypes.c_uint32, ctypes.c_uint64] + [ctypes.c_uint32] * 3
+    lib.cost.argtypes, lib.cost.restype = [ctypes.c_int64, ctypes.c_int, ctypes.c_int], ctypes.c_uint32
     return lib
 
 
@@ -111,3 +116,35 @@ def test_a_line_of_its_largest_number_of_blocks(line, blocks):
         bt = block(group, D)
         fits = check(line, [blocks * bt], [blocks * bt], 1, group, D, 128, blocks * bt)
         assert fits == (8 * blocks * (2 + -(-blocks * bt // 128)) + -(-bt // 16) * (blocks * (blocks - 1) // 2) + 8 * blocks * 3 < 2 ** 31)
+
+
+# (single tokens, fast tiles of one row group, units, tiles of each, us whole, us in shares) of equal sequences
+# on 152 SMs.  Points at which both took the same within 3 % say nothing and are not asked.
+MEASURED = [
+    (1, 1, 512, 9, 57.3, 62.6), (1, 1, 256, 33, 91.7, 100.3), (1, 1, 160, 33, 88.9, 66.4),
+    (1, 0, 272, 19, 69.2, 72.5), (1, 0, 240, 19, 68.5, 64.1), (1, 0, 352, 19, 98.7, 87.7), (1, 0, 384, 35, 177.2, 164.7),
+    (1, 0, 320, 11, 59.8, 56.1), (1, 0, 160, 11, 41.2, 35.8),
+    (1, 0, 240, 9, 40.6, 43.5), (1, 0, 272, 17, 67.9, 72.6), (1, 0, 240, 17, 67.6, 64.3), (1, 0, 256, 33, 122.3, 113.5),
+    (1, 0, 256, 17, 91.7, 99.1), (1, 0, 320, 9, 78.5, 74.2), (1, 0, 160, 17, 88.8, 68.1),
+    (0, 1, 512, 9, 88.3, 99.9), (0, 1, 256, 9, 48.9, 65.1), (0, 1, 160, 9, 46.5, 51.6), (0, 1, 160, 17, 72.3, 67.6),
+    (0, 1, 480, 33, 247.6, 229.7), (0, 1, 800, 5, 87.6, 106.2),
+    (0, 0, 256, 11, 62.8, 80.5), (0, 0, 240, 19, 92.8, 102.2), (0, 0, 160, 19, 91.9, 79.2), (0, 0, 320, 19, 134.3, 126.3),
+    (0, 0, 160, 9, 50.6, 52.8), (0, 0, 320, 9, 73.2, 79.2), (0, 0, 120, 17, 44.9, 60.3), (0, 0, 160, 17, 80.3, 70.9),
+    (0, 0, 320, 17, 119.0, 113.2), (0, 0, 240, 17, 82.7, 92.0), (0, 0, 160, 11, 68.4, 63.5), (0, 0, 320, 11, 96.4, 102.0),
+    (0, 0, 240, 17, 95.9, 113.0), (0, 0, 128, 33, 88.6, 115.6), (0, 0, 160, 19, 112.7, 94.3),
+]
+
+
+@pytest.mark.parametrize("single,fast,units,tiles,whole,shares", MEASURED)
+def test_whole_units_where_they_were_measured_to_take_less(line, single, fast, units, tiles, whole, shares):
+    assert abs(whole / shares - 1) > 0.03
+    n_tok, n_seq = (8, 8) if single else (64, 8)
+    assert line.whole(units, units * tiles, tiles, 152, line.cost(n_tok, n_seq, fast)) == (whole < shares)
+
+
+def test_whole_units_are_compared_in_whole_numbers(line):
+    """No part of a tile is rounded away: 256 units of 33 tiles on 152 SMs lose 10.42."""
+    assert not line.whole(256, 256 * 33, 33, 152, 10) and line.whole(256, 256 * 33, 33, 152, 11)
+    assert line.whole(304, 304 * 10 ** 6, 10 ** 6, 152, 1)        # full rounds lose nothing
+    assert line.whole(0, 0, 0, 152, 10)
+    assert line.whole(2 ** 31, 2 ** 31 * 5, 5, 2 ** 10, 1)
