@@ -36,24 +36,35 @@ struct Line {
 // A causal block of n tokens ends n / 128 tiles behind the one before it: n / 16 eighths, rounded up.
 KVATTN_HD uint32_t line_step(int block_tokens) { return (uint32_t)(block_tokens + 15) / 16u; }
 
-// With a window: whether `units` units of `tiles` tiles together, the longest of them `longest`, are dealt
-// out whole to n CTAs.  They take a round of the longest and the others of the mean, where shares would
-// take tiles / n; what is lost is weighed against what cut units cost with their partials and the merge, in
-// tiles (cost; the other side in us, whole units and shares, by tiles lost):
-//   single tokens, f16 rows of 128 without a plan: 5.7 57 62, 10.4 92 100, 15.2 73 71, 31 89 66;
-//   single tokens else: f16 plan 4.0 69 73, 6.9 79 80, 8.0 69 64, 13 99 88; 8-bit rows 3.6 68 73, 5.4 67 67,
-//     7.2 68 64, 10.4 122 113; head_dim 256 5.4 92 99, 7.2 92 94, 8.1 79 74, 16 89 68;
-//   several tokens: f16 2.8 49 65, 8.5 47 52, 15.2 106 105, 28 248 230, through a plan 8.0 93 102, 9.8 88 92, 18
-//     92 79; 8-bit rows 3.6 45 60, 8.1 73 79, 15.2 119 113, through a plan 8.0 105 114, 9.8 96 102, 10.4 68 63;
-//     head_dim 256 5.2 89 116, 8.1 85 91, 16 92 84, through a plan 8.0 119 128, 9.8 108 106.
-KVATTN_HD bool whole_units(uint32_t units, uint64_t tiles, uint32_t longest, uint32_t n, uint32_t cost) {
+// With a window: when units are dealt out whole.  They take a round of the longest and the others of the
+// mean, where shares would take tiles / n; what is lost is weighed against what cut units cost with their
+// partials and the merge: base tiles, and up to `more` the more units there are to cut.  Measured, in us
+// whole and in shares, of equal units on 152 SMs (units x tiles, tiles lost):
+//   single tokens, f16 rows of 128 without a plan (whose tiles are short): 16 x 12 (8.0) 21 17, 64 x 9 (5.2) 17 19,
+//     96 x 17 (6.3) 27 30, 512 x 9 (5.7) 57 63, 256 x 33 (10.4) 92 100, 320 x 17 (15) 73 71, 160 x 33 (31) 89 66;
+//   single tokens else: 64 x 6 (3.5) 18 20, 128 x 17 (2.7) 38 42, 272 x 17 (3.6) 68 73, 256 x 17 (5.4) 68 67, 240 x
+//     17 (7.2) 68 64, through a plan 272 x 19 (4.0) 69 73, 240 x 19 (8.0) 69 64, 352 x 19 (13) 99 88;
+//   several tokens: 64 x 9 (5.2) 25 34, 64 x 17 (9.8) 38 41, 256 x 9 (2.8) 49 65, 160 x 17 (16) 72 68, through a plan
+//     320 x 11 (9.8) 88 92; 8-bit rows 112 x 33 (8.7) 75 81, 160 x 11 (10.4) 68 63; head_dim 256 8 x 12 (8.0) 34 25,
+//     128 x 33 (5.2) 89 116, 240 x 17 (7.2) 96 113, 160 x 17 (16) 92 84.
+struct WholeRule {
+    uint32_t base, more;   // tiles; base 0: shares
+    uint32_t sms;
+};
+// `units` units of `tiles` tiles together, the longest of them `longest`, and n CTAs for them.
+KVATTN_HD bool whole_units(uint32_t units, uint64_t tiles, uint32_t longest, uint32_t n, const WholeRule& r) {
     if (units == 0u) return true;
     const uint32_t before_last = (units - 1u) / n * n;   // units of all rounds but the last
-    return (uint64_t)longest * units * n <= (uint64_t)cost * units * n + (uint64_t)(units - before_last) * tiles;
+    const uint64_t cost = (uint64_t)r.base * r.sms + (uint64_t)r.more * (units < r.sms ? units : r.sms);
+    return (uint64_t)longest * r.sms * units * n <= cost * units * n + (uint64_t)(units - before_last) * tiles * r.sms;
 }
-// `cost`; fast_single: a tile of one row group takes about half the time of one of both (f16 rows of 128
-// without a plan).
-inline uint32_t cut_cost(int64_t n_tok, int n_seq, bool fast_single) { return n_tok > n_seq ? 10u : (fast_single ? 13u : 7u); }
+// fast_single: f16 rows of 128 without a plan; merged: the merge is launched all the same (2 us for single
+// tokens, 4 for several).
+inline WholeRule whole_rule(int64_t n_tok, int n_seq, bool fast_single, bool merged, int sms) {
+    const uint32_t less = merged ? 1u : 0u;
+    if (n_tok > n_seq) return WholeRule{4u - less, 8u, (uint32_t)sms};
+    return fast_single ? WholeRule{5u - less, 7u, (uint32_t)sms} : WholeRule{4u - less, 3u, (uint32_t)sms};
+}
 
 // Whether the line of a call with a shared prefix stays below 2^31, whatever its sequences' lengths.  Then
 // Line's 32 bits hold every part of it, b (b - 1) among them: that is below 2^32 where its half is below

@@ -516,6 +516,9 @@ __device__ __forceinline__ int32_t tile_length(const PrefillParams& p, int32_t n
     return n_tok <= p.group_tokens ? p.single_length : 8;
 }
 // kWindow: every unit counts as the longest that its window allows.
+__device__ __forceinline__ uint32_t window_line_tiles(const PrefillParams& p, const Sequence& x) {
+    return min(((uint32_t)x.len + (uint32_t)kPrefillTile - 1u) / (uint32_t)kPrefillTile, (uint32_t)p.window_tiles);
+}
 template <int MODE>
 __device__ __forceinline__ Line line_of(const PrefillParams& p, const Sequence& x, int seq, const Prefix& pre) {
     if (is_prefix<MODE>(p, seq)) {
@@ -526,7 +529,7 @@ __device__ __forceinline__ Line line_of(const PrefillParams& p, const Sequence& 
     }
     const int32_t lim = max(x.len - x.n_q, 0) + min(x.n_q, p.block_tokens);  // of the first block's last token, or above
     int32_t tiles = lim / kPrefillTile + (lim % kPrefillTile != 0 ? 1 : 0);   // (lim can be 2^31 - 1)
-    if (MODE == kWindow) tiles = min((int32_t)(((uint32_t)x.len + (uint32_t)kPrefillTile - 1u) / (uint32_t)kPrefillTile), p.window_tiles);
+    if (MODE == kWindow) tiles = (int32_t)window_line_tiles(p, x);
     if (MODE == kShared) tiles -= pre.tiles;
     Line l{8u * (uint32_t)(kUnitCost + tiles), MODE == kWindow ? 0u : line_step(p.block_tokens), x.blocks, 0u};
     if (x.blocks != 0u) {
@@ -564,6 +567,24 @@ __device__ __forceinline__ uint32_t total_of(const PrefillParams& p, const Prefi
     for (int s = threadIdx.x & 31; s < lines<MODE>(p); s += 32)
         sum += length_of<MODE>(p, read_sequence<MODE>(p, s, pre), s, pre);
     return __reduce_add_sync(0xffffffffu, sum);
+}
+// kWindow: the same, and whether the units are dealt out whole all the same.
+__device__ __forceinline__ uint32_t window_total(const PrefillParams& p, bool& whole) {
+    const Prefix none = {0, 0};
+    uint32_t total = 0, units = 0, tiles = 0, longest = 0;
+    for (int s = threadIdx.x & 31; s < p.n_seq; s += 32) {
+        const Sequence x = read_sequence<kWindow>(p, s, none);
+        const uint32_t n = x.blocks * (uint32_t)p.n_head_kv, each = window_line_tiles(p, x);
+        total += length_of<kWindow>(p, x, s, none);
+        units += n;
+        tiles += n * each;   // (the line's eighths of them fit 31 bits)
+        longest = max(longest, n != 0u ? each : 0u);
+    }
+    units = __reduce_add_sync(0xffffffffu, units);
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    whole = p.whole.base != 0u && whole_units(units, tiles, longest, gridDim.x, p.whole);
+    return __reduce_add_sync(0xffffffffu, total);
 }
 __device__ __forceinline__ Sequence from_lane(const Sequence& x, int l) {
     Sequence y;
@@ -696,13 +717,21 @@ struct Walk {
     Shares sh;
     Place r;
     bool started;
+    bool cut;   // kWindow: shares
 
+    __device__ __forceinline__ bool shares(const PrefillParams& p) const { return MODE == kWindow ? cut : p.shares != 0; }
     __device__ __forceinline__ void begin(const PrefillParams& p) {
         round = 0;
         started = false;
         pre = prefix_of<MODE>(p);
+        cut = false;
         if (p.shares) {
-            sh.set(total_of<MODE>(p, pre), gridDim.x);
+            bool whole = false;
+            if constexpr (MODE == kWindow)
+                sh.set(window_total(p, whole), gridDim.x);
+            else
+                sh.set(total_of<MODE>(p, pre), gridDim.x);
+            cut = !whole;
             at = sh.of(blockIdx.x);
             end = sh.of(blockIdx.x + 1u);
             if (MODE != kShared && (threadIdx.x & 31) == 0) p.cuts[blockIdx.x].n_parts = 0;
@@ -714,7 +743,7 @@ struct Walk {
     __device__ __forceinline__ bool next(const PrefillParams& p, typename SegOf<MODE>::type& s) {
         int32_t first = 0, last = INT_MAX;
         int part = -1, from = 0;
-        if (!(p.shares ? next_share(p, first, last, part, from) : next_whole(p))) return false;
+        if (!(shares(p) ? next_share(p, first, last, part, from) : next_whole(p))) return false;
         make_seg<MODE, D>(p, r.x, r.seq, (int)r.g, r.block, first, last, part, from, pre, s);
         return true;
     }
@@ -2199,9 +2228,12 @@ cudaError_t run_prefill(const PrefillParams& p, int kv_type, int head_dim, int n
         return e;
     } else {
         if (e != cudaSuccess || !p.shares || n_ctas < 2) return e;
-        // two rows a warp (one at head_dim 256), so that a merge of a few units fills the device
+        // two rows a warp (one at head_dim 256), so that a merge of a few units fills the device; single tokens
+        // through a window have few rows, and more blocks would only take longer to find nothing (2 us in place
+        // of 4 where the units turned out to be whole)
+        const unsigned rows = MODE == kWindow && p.n_tok <= p.n_seq ? 8u : 32u;
         return launch(head_dim == 128 ? (const void*)prefill_merge_kernel<MODE, 128> : (const void*)prefill_merge_kernel<MODE, 256>,
-                      dim3((unsigned)n_ctas, 32), 32 * kMergeWarps, 0, args, stream, pdl);
+                      dim3((unsigned)n_ctas, rows), 32 * kMergeWarps, 0, args, stream, pdl);
     }
 }
 

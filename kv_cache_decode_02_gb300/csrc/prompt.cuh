@@ -116,6 +116,7 @@ struct PrefillParams {
     int block_tokens;         // tokens of a unit: two row groups at head_dim 128, one at 256
     int single_length;        // of a tile for one row group in the line of shares, in eighths of one for all
     int shares;               // 1: equal shares of all units' tiles, cut anywhere; 0: whole units
+    WholeRule whole;          // with a window and shares: whole units all the same where whole_units says so
     int use_tma;
     int scl_tma;
     int out_sectors;          // out is 32-byte aligned

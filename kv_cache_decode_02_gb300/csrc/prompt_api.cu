@@ -36,32 +36,39 @@ int check_cache(int kv_type, const void* k, const void* v, const void* ks, const
 // otherwise keep 16 of 152 SMs busy.  A share costs its CTA a partial (written and read once
 // more) and the call a merge, so a CTA gets at least four tiles' worth of the bound below.
 struct Cut {
-    bool shares;
+    bool shares, forced;   // forced: by the environment
     int n_ctas;
     size_t cuts_off, lse_off, o_off, total;
 };
 
-constexpr int64_t kMinShareTiles = 4;
+constexpr int64_t kMinShareTiles = 4, kFewTiles = 13;
 
 // `bound`: of all calls with at most that many units and tiles (one of fewer units may be shared
 // where this one is dealt out whole).
 //
-// `cost`: with a window units are about equal, and are dealt out whole where that takes no longer
-// (whole_units); 0: any length.
-Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share, bool bound = false, uint32_t cost = 0) {
+// `whole`: with a window units are often about equal, and are dealt out whole where that takes no longer
+// (whole_units).  The schedulers decide, who know how many blocks and cells the sequences have: one of 60000
+// cells and 18 of 100 behind a window of 8192 take 78 us whole, on 8 SMs, and 23 in shares.  Units of few
+// tiles lose little whatever their lengths: they are whole, without a merge to launch, where equal ones
+// would be.
+Cut cut_of(int64_t units, int64_t tiles, int head_dim, bool may_share, bool bound = false, WholeRule whole = {}) {
     Cut c = {};
     // (KVATTN_PREFILL_CTAS: the CTAs that share the work, for tests; 0: dealt out whole)
     const char* env = std::getenv("KVATTN_PREFILL_CTAS");
     const int sms = device_sms();
     if (bound) units = std::min(units, 8 * (int64_t)sms - 1);
     c.shares = may_share && tiles > kMinShareTiles && units < 8 * (int64_t)sms;
-    if (cost > 0 && c.shares && whole_units((uint32_t)units, (uint64_t)(units * tiles), (uint32_t)tiles, (uint32_t)sms, cost)) c.shares = false;
+    c.forced = may_share && env != nullptr && *env != 0;
     // (the kernel numbers the line of all tiles, in eighths, in 31 bits)
     const bool fits = bound || (units < INT32_MAX && (tiles + 18) * 8 < INT32_MAX / std::max<int64_t>(units, 1));
-    int64_t n = units;
-    if (c.shares) n = std::max(units, (units * tiles + kMinShareTiles - 1) / kMinShareTiles);
-    c.n_ctas = (int)std::max<int64_t>(std::min<int64_t>(n, sms), 1);
-    if (may_share && env != nullptr && *env != 0) {
+    auto ctas = [&](int64_t n) { return (int)std::max<int64_t>(std::min<int64_t>(n, sms), 1); };
+    c.n_ctas = ctas(c.shares ? std::max(units, (units * tiles + kMinShareTiles - 1) / kMinShareTiles) : units);
+    if (c.shares && whole.base != 0u && tiles <= kFewTiles &&
+        whole_units((uint32_t)units, (uint64_t)(units * tiles), (uint32_t)tiles, (uint32_t)c.n_ctas, whole)) {
+        c.shares = false;
+        c.n_ctas = ctas(units);
+    }
+    if (c.forced) {
         const int want = std::atoi(env);
         c.shares = want > 0;
         c.n_ctas = std::max(std::min(want > 0 ? want : c.n_ctas, sms), 1);
@@ -554,7 +561,10 @@ static int chunk_attention(Form form, const void* q, int64_t q_stride, const int
             tiles = std::min<int64_t>(tiles, p.window_tiles);
         }
         const bool fast_single = kv_type == KVATTN_KV_F16 && head_dim == 128 && cell_plan == nullptr;
-        const Cut c = cut_of(units, tiles, head_dim, true, false, form == Form::plain ? 0u : cut_cost(n_tok, n_seq, fast_single));
+        const bool windowed = form == Form::window;
+        auto rule = [&](bool merged) { return windowed ? whole_rule(n_tok, n_seq, fast_single, merged, device_sms()) : WholeRule{}; };
+        const Cut c = cut_of(units, tiles, head_dim, true, false, rule(false));
+        if (!c.forced) p.whole = rule(true);
         if (ws_bytes < c.total) return KVATTN_ERR_WORKSPACE;
         shares = c.shares;
         n_ctas = c.n_ctas;
