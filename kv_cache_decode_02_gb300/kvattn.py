@@ -809,7 +809,8 @@ def _weight(w, name, n):
 def norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, layout="half", q_out=None, k_out=None,
               stream=None):
     """:func:`rope` of heads that are normed first, in the same pass: ``q_weight`` / ``k_weight`` half
-    [D] (None: that side is not normed), ``eps`` beside the mean square."""
+    [D] (None: that side is not normed), ``eps`` beside the mean square.  ``positions`` as there: a row of
+    tokens for each axis, [axes][T]."""
     if _torch is None:
         _bind_torch()
     code = KVATTN_ROPE_HALF if layout == "half" else {"interleaved": KVATTN_ROPE_INTERLEAVED}[layout]
@@ -840,6 +841,8 @@ def norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6,
         ka = (k.data_ptr(), st, h, k_out.data_ptr(), so)
     turns, axis, n_axes, n_rot = table.turns, table.axis, table.n_axes, table.n_rot
     at = _ints(positions, "positions", T * n_axes)
+    if n_axes > 1 and tuple(positions.shape) != (n_axes, T):   # (not [T][axes], which holds as many)
+        raise ValueError(f"positions: [axes][T] is wanted, {n_axes} rows of {T} tokens")
     d = _here(k if q is None else q, "k" if q is None else "q")
     if (positions.get_device() != d or turns.get_device() != d or _off(k, d) or _off(q_out, d) or _off(k_out, d)
             or _off(q_weight, d) or _off(k_weight, d) or _off(axis, d)):
