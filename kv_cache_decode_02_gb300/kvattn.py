@@ -866,8 +866,9 @@ def norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6,
 class StepMaps:
     """What :func:`step_maps` makes: int32 ``offsets`` [S + 1], ``seq_lens`` [S], ``positions`` [T],
     ``slots`` [T] and ``n_free`` [1]; made by :func:`step_maps_buffers`, and written by any number of
-    steps."""
-    __slots__ = ("_all", "_at")
+    steps.  A step without a free list leaves ``n_free`` as it is: 0 in new buffers, None in what
+    :func:`step_maps` made for such a step."""
+    __slots__ = ("_all", "_at", "_no_count")
 
     def __init__(self, n_seq, n_tok, device):
         import torch
@@ -880,17 +881,20 @@ class StepMaps:
             at += -(-n // 4) * 4
         self._all = tuple(views)
         self._at = (n_seq, n_tok, room.get_device()) + tuple(room.data_ptr() + 4 * x.storage_offset() for x in views)
+        self._no_count = False
 
     offsets = property(lambda self: self._all[0])
     seq_lens = property(lambda self: self._all[1])
     positions = property(lambda self: self._all[2])
     slots = property(lambda self: self._all[3])
-    n_free = property(lambda self: self._all[4])
+    n_free = property(lambda self: None if self._no_count else self._all[4])
 
 
 def step_maps_buffers(n_seq, n_tok, device="cuda"):
     """A StepMaps for steps of ``n_seq`` sequences and at most ``n_tok`` tokens."""
-    return StepMaps(n_seq, n_tok, device)
+    made = StepMaps(n_seq, n_tok, device)
+    made.n_free.zero_()
+    return made
 
 
 def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells, n_cells, n_tok=None, plan=None,
@@ -912,6 +916,7 @@ def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells
                 out = StepMaps(lens.numel(), n_tok, lens.device)
         else:
             out = StepMaps(lens.numel(), n_tok, lens.device)
+        out._no_count = True   # (until a step counts)
     S, T, d, offsets, seq_lens, positions, slots, left = out._at
     if n_tok is not None and n_tok != T:
         raise ValueError("n_tok: out has other rows")
@@ -937,6 +942,8 @@ def step_maps(lens, n_new, tables, free_blocks=None, n_free=None, *, block_cells
         raise ValueError("free_blocks and n_free go together")
     else:
         left = None
+    if left is not None:
+        out._no_count = False
     _check(lib.kvattn_step_maps(a, b, S, tab, shape[1], block_cells, free, n_list, count, n_cells, T, offsets, seq_lens, positions,
                                 slots, left, pl, stride, 1 if whole_plan else 0, _raw(status), _stream(stream)), "kvattn_step_maps")
     return out
