@@ -22,7 +22,7 @@ namespace kvattn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBlocksPerSm = 8;    // 64 registers: 67 us for the prompt below, 72 without the bound, 92 at ten
+constexpr int kBlocksPerSm = 8;    // 64 registers: 67 us for the prompt above, 72 without the bound, 92 at ten
 // A token is split among warps until there are this many for an SM: 8192 tokens of 32 / 8 heads of 128
 // 28.0 us at 16, 27.5 at 64, 31.5 at 128 (every warp makes the token's angles).
 constexpr int kWarpsPerSm = 64;

@@ -31,8 +31,10 @@
 //  * loader (warps 8-11): fills a ring of 32 KB slots, each 128 cells x 128 dims of K or V in
 //    two 128-byte-swizzled planes.  f16: warp 8 issues a TMA box for each slot whose cells are
 //    one physical run (holes and the end of a sequence included); warps 9-11 mend V slots that
-//    need it afterwards, and copy the slots of tiles that are no run.  Quantised: warps 14 and 15 bring the codes (TMA)
-//    and scales (cp.async) of K and of V into a ring of raw bytes, and these four turn them into f16.
+//    need it afterwards, and copy the slots of tiles that are no run.  Quantised: warps 14 and 15
+//    bring the codes and scales of K and of V into a ring of raw bytes, and these four turn them into f16.
+//    Codes of a run come by TMA, its scales too when it has no holes, lies in one piece and the heads'
+//    scales are whole 16-byte pieces; the others by cp.async.
 //  * MMA (warp 12): one elected lane issues tcgen05.mma.  The 512 TMEM columns hold two buffers
 //    of S, over which p is written, and O (2 x 128 columns, or 256).  With both row groups at
 //    work each has a buffer, and a group's products run under the other's softmax; with one (256,
@@ -510,7 +512,8 @@ __device__ __forceinline__ int32_t unit_tiles(const PrefillParams& p, const Sequ
 // (With f16 rows and no plan a tile for one row group of two takes about 0.55 of one for both,
 // 1900 clocks to 3450: a last block of one group counts 5 / 8 (units of 1 to 256 tokens over 8192
 // to 65536 cells: 243 -> 229 us).  Through a plan, or from quantised rows, it waits for its loader
-// and counts as a whole one: 5 / 8 there took 267 -> 302 us.)
+// and counts as a whole one: 5 / 8 there took 267 -> 302 us.  Behind a shared prefix, whose units are
+// mostly of single tokens, it counts 4 / 8, and 5 / 8 through a plan: launch_attention has the figures.)
 // Length of a tile of a block of n tokens in the line.
 __device__ __forceinline__ int32_t tile_length(const PrefillParams& p, int32_t n_tok) {
     return n_tok <= p.group_tokens ? p.single_length : 8;

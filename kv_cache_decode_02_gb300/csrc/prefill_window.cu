@@ -6,7 +6,9 @@
 // sequence.  What differs from the plain form: where a unit's places lie; a second bound in the masks,
 // which are applied in registers (a third of the tiles have one); up to four more tiles at the front
 // that only some rows see whole, whose values that are not finite are kept apart like those at the end;
-// and shares of equal length for all units, which a window makes about equal.
+// and a line in which every unit counts as the longest that its sequence and window allow.  Units of equal
+// length are often better dealt out whole than cut: the schedulers decide, from the lengths (whole_units in
+// line.cuh).
 //
 // What bounds it: single tokens the bytes of whole tiles and the rounds of units (64 tokens, window 1024
 // and 4 first tokens, 32 / 8 heads of 128: 51 us, 74 % of the copy rate for the cells that they see);
