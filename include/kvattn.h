@@ -670,7 +670,10 @@ size_t kvattn_prefill_chunk_shared_workspace_bytes(int64_t n_tok, int n_seq, int
  * cells: the first prefix_cells logical positions of every sequence hold the same K and V (the same
  * entries in every row of a cell plan, or copies in the sequences' own caches).  They are read once, for
  * the new tokens of all sequences together, and each sequence's other cells for its own tokens; the
- * result is kvattn_prefill_chunk's.
+ * result is kvattn_prefill_chunk's.  It pays for few new tokens of each sequence (64 single tokens behind 8192
+ * cells 334 -> 54 us, 16 x 16 tokens 98 -> 62); where a sequence's tokens fill rows alone, n_head / n_head_kv of
+ * them a token and 128 a group, kvattn_prefill_chunk is faster (32 x 32 tokens 182 us against 204, 32 x 128 461
+ * against 764, 32 / 8 heads of 128).
  *  prefix_cells  any value >= 0 (INVALID_ARG otherwise).  It counts in whole tiles of 128 cells, as far
  *           as every sequence that has new tokens holds them in front of those; what is left is read as
  *           the sequences' own.  The shared cells are read through the first sequence that has tokens.

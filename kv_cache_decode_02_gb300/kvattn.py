@@ -1059,8 +1059,9 @@ def prefill_chunk(q, offsets, k_cache, v_cache, seq_lens, *, max_len=None, n_cel
     a ``cell_plan`` (int32 [S][stride]), a per-sequence [S][N][Hk][D] cache, or one [cells][Hk][D]
     whose ``n_cells`` are each sequence's.  With a ``window`` a token sees its sequence's last ``window``
     cells (its own among them) and the first ``sinks``; with ``shared`` the sequences' first ``shared``
-    cells hold the same and are read once for all of them (one or the other).  Returns (out half
-    [T][H][D], lse: the given tensor or None)."""
+    cells hold the same and are read once for all of them (one or the other), which pays for steps of a few
+    tokens each and not for prompts (see kvattn_prefill_chunk_shared).  Returns (out half [T][H][D],
+    lse: the given tensor or None)."""
     if _torch is None:
         _bind_torch()
     if (out is None or ws is None) and _other_stream(stream):
